@@ -649,7 +649,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       if (i > 0 && !wait(B_ODONE, (uint32_t)(i - 1) & 1u)) break;
       tc_fence_after();
       if (pend && !flush()) break;
-      if (rescale && !first) {
+      // the tensor-memory accesses are warp-wide: the whole warp rescales when one
+      // of its rows has to (the others by 1)
+      if (__any_sync(kFull, rescale) && !first) {
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
           uint32_t v[32];
