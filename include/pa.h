@@ -76,6 +76,8 @@ typedef enum pa_status {
 #define PA_DEVERR_QLEN_RANGE 0x8u    /* q_len < 0, q_len > context_len (causal, or context 0), or cu_seqlens_q inconsistent */
 #define PA_DEVERR_PIPE_TIMEOUT 0x10u /* an asynchronous copy did not land within its time limit */
 #define PA_DEVERR_PLAN_OVERFLOW 0x20u /* work list larger than the launch was sized for */
+#define PA_DEVERR_TREE_RANGE 0x40u   /* a tree parent or an accepted path outside its rules */
+#define PA_DEVERR_BUDGET_RANGE 0x80u /* an eviction budget outside its rules */
 
 /* Problem shape, passed by pointer (host memory) to every call. */
 typedef struct pa_shape {
@@ -401,6 +403,154 @@ int pa_decode_cascade_ex(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16
  * policy (0 if the arguments are invalid). */
 size_t pa_decode_cascade_workspace_size(const pa_shape* shape, int num_groups, int num_members,
                                         int max_group_size, int max_prefix_len);
+
+/* Pool formats of the calls below that take any of the library's pools. */
+#define PA_KV_BF16 0 /* the bf16 pool: [num_blocks][num_kv_heads][block_size][head_dim] */
+#define PA_KV_INT8 1 /* the int8 pool: [num_blocks][num_kv_heads][PA_INT8_TILE_BYTES] */
+#define PA_KV_FP8 2  /* the FP8 pool, same tiles */
+
+/*
+ * Speculative decoding with a tree of drafted tokens ("S20 - The Complete
+ * Engine", "Core idea": step 3 PROPOSE, step 5 verify). A sequence's window of
+ * Lq query tokens (cu_seqlens_q, as in pa_decode_varlen) is a tree: its K and V
+ * rows are the last Lq positions of the context, in the order of the window,
+ * and a token attends to the cached context before the window and to its own
+ * ancestors. A step is: pa_reshape_and_cache of the window's rows,
+ * pa_tree_mask (once per tree), pa_decode_tree (per layer), the caller's
+ * choice of a path, pa_commit_path (per layer).
+ *
+ * pa_tree_mask -- the ancestor bits of every window token.
+ *
+ *   parents       [num_q_tokens] int32: the parent's index in the same window, or
+ *                 -1 for a token that follows the cached context directly; a
+ *                 parent comes before its children (-1 <= parents[j] < j)
+ *   cu_seqlens_q  [num_seqs + 1] int32, as in pa_decode_varlen
+ *   max_q_len     an upper bound of the q_lens (host), <= 32 * mask_words
+ *   tree_mask     [num_q_tokens][mask_words] uint32: bit i % 32 of word i / 32 of
+ *                 row j is set if i == j or i is an ancestor of j, every other
+ *                 bit of the row is cleared
+ *   depths        [num_q_tokens] int32, the number of ancestors (a token's
+ *                 position is context_len - Lq + depth); may be NULL
+ * A parent outside its range sets PA_DEVERR_TREE_RANGE and its node counts as
+ * one with parent -1; a window longer than max_q_len or outside the rows sets
+ * PA_DEVERR_QLEN_RANGE and its rows are left as they were.
+ */
+int pa_tree_mask(const int32_t* parents, const int32_t* cu_seqlens_q, int num_seqs,
+                 int64_t num_q_tokens, int max_q_len, uint32_t* tree_mask, int mask_words,
+                 int32_t* depths, void* stream);
+
+/*
+ * pa_decode_tree -- pa_decode_varlen with a mask inside the window: query j of
+ * a window sees every key before the window (positions 0 .. c - Lq - 1) and
+ * window key i (position c - Lq + i) if bit i of its mask row is set. The mask
+ * may be any bits (pa_tree_mask makes a tree's); bits at and past Lq are not
+ * read as keys. A query that sees no key at all gives out = 0 and lse = -inf.
+ * A key that a query does not see never reaches its result, whatever its K
+ * and V hold (infinities and NaNs included).
+ *
+ *   tree_mask, mask_words, max_q_len   as in pa_tree_mask; the other arguments
+ *                 as in pa_decode_varlen
+ *   workspace     at least pa_decode_tree_workspace_size(...) bytes, 256-byte
+ *                 aligned; clobbered
+ * Built for any group of 1 to 128 query heads per KV head (bf16 pool). Softmax
+ * statistics and sums are fp32; the softmax weights are rounded to bf16 for
+ * the product with V, as in pa_decode_varlen. A window needs 0 <= Lq <= c and
+ * Lq <= 32 * mask_words; another one sets PA_DEVERR_QLEN_RANGE and produces no
+ * rows.
+ */
+int pa_decode_tree(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
+                   const int32_t* block_tables, const int32_t* context_lens,
+                   const int32_t* cu_seqlens_q, const uint32_t* tree_mask, int mask_words,
+                   int64_t num_q_tokens, int max_q_len, float scale, pa_bf16* out, float* lse,
+                   const pa_shape* shape, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t pa_decode_tree_workspace_size(const pa_shape* shape, int64_t num_q_tokens, int max_q_len);
+
+/*
+ * pa_commit_path -- keep the accepted path of each window: row path[s][i] of
+ * sequence s's window moves to row i of the window (K and V, every KV head;
+ * byte copies), so that the path's tokens follow the context directly.
+ *
+ *   kv_format     PA_KV_BF16, PA_KV_INT8 or PA_KV_FP8; k_cache and v_cache in
+ *                 place, 16-byte aligned
+ *   path          [S][max_path_len] int32: strictly increasing window indices;
+ *                 the first path_lens[s] entries of a row are read
+ *   path_lens     [S] int32, 0 <= path_lens[s] <= min(Lq, max_path_len)
+ *   new_lens      [S] int32: context_len - Lq + path_len; may be context_lens
+ *                 itself, else must not overlap it
+ * Window rows past the path keep whatever they hold (the next tokens are
+ * written over them). Blocks of the window must belong to one sequence alone.
+ * A path that breaks the rules sets PA_DEVERR_TREE_RANGE; its sequence's rows
+ * stay as they are and new_lens[s] is context_lens[s].
+ */
+int pa_commit_path(void* k_cache, void* v_cache, int kv_format, const int32_t* block_tables,
+                   const int32_t* context_lens, const int32_t* cu_seqlens_q, const int32_t* path,
+                   const int32_t* path_lens, int max_path_len, int32_t* new_lens,
+                   const pa_shape* shape, void* stream);
+
+/*
+ * pa_accumulate_weights -- how much attention each cached position has drawn
+ * (curriculum row "Memory & KV Cache": a cache that keeps what is used). For
+ * every position p < c of sequence s and every KV head h:
+ *   sum[p] = sum over the window's queries j with p <= c - Lq + j and the group's
+ *            heads g of exp(scale * q[j][h*G+g].k[h][p] - lse[j][h*G+g])
+ *   weights[s][h][p] = sum[p]                     if p >= c - Lq (the window's
+ *                      own rows) or accumulate == 0
+ *                    = weights[s][h][p] + sum[p]  otherwise.
+ * So a cache that grows by accumulating calls needs no clearing: a position's
+ * weight begins with the call whose window holds it.
+ *
+ *   q, lse        [num_q_tokens][Hq][D] bf16 and [num_q_tokens][Hq] fp32: the
+ *                 queries of an attention call (pa_decode, pa_decode_varlen with
+ *                 causal = 1) and the log-sum-exp it returned, same scale; a
+ *                 -inf row draws nothing
+ *   k_cache       the pool's K array, in kv_format (8-bit rows dequantised)
+ *   cu_seqlens_q  [S+1] as in pa_decode_varlen, or NULL: one query per sequence
+ *                 (num_q_tokens == S)
+ *   max_q_len     an upper bound of the q_lens (host)
+ *   weights       [S][Hkv][weights_len] fp32, in place; positions at and past c
+ *                 are left as they were. context_lens[s] <= weights_len.
+ * Scores and sums are fp32, products exact; a position's sum has one order, so
+ * equal calls give equal bits. Any group size. A window that is not inside its
+ * context or the rows sets PA_DEVERR_QLEN_RANGE and leaves its sequence's
+ * weights as they were.
+ */
+int pa_accumulate_weights(const pa_bf16* q, const void* k_cache, int kv_format, const float* lse,
+                          const int32_t* block_tables, const int32_t* context_lens,
+                          const int32_t* cu_seqlens_q, int64_t num_q_tokens, int max_q_len,
+                          float scale, int accumulate, float* weights, int64_t weights_len,
+                          const pa_shape* shape, void* stream);
+
+/*
+ * pa_evict -- shrink each sequence's cache to a budget. Per KV head the first
+ * num_sinks and the last num_recent positions stay, and of those between the
+ * budgets[s] - num_sinks - num_recent with the largest weight (equal weights:
+ * the lowest positions; -0 equals 0, a NaN is below every number). What stays
+ * moves together in order: position i of the new cache holds position
+ * kept[s][h][i] of the old one, its K and V rows (byte copies) and its weight.
+ * A sequence with context_len <= budgets[s] stays as it is.
+ *
+ *   kv_format, k_cache, v_cache   as in pa_commit_path
+ *   weights       [S][Hkv][weights_len] fp32 (pa_accumulate_weights), in place;
+ *                 entries at and past new_lens[s] are unspecified afterwards, as
+ *                 are the cached rows
+ *   budgets       [S] int32, num_sinks + num_recent <= budgets[s] <= max_budget
+ *   kept          [S][Hkv][max_budget] int32, written: the positions that stay,
+ *                 increasing, then -1
+ *   new_lens      [S] int32, min(context_len, budget); must not overlap
+ *                 context_lens or budgets
+ * Heads keep different positions, so a position of the new cache holds different
+ * tokens in different heads; attention does not mind, since keys carry their
+ * own position encoding. Blocks of an evicted sequence must belong to it alone
+ * from the first moved position on. A budget outside its range sets
+ * PA_DEVERR_BUDGET_RANGE, a context longer than the table or weights_len
+ * PA_DEVERR_CONTEXT_RANGE: the sequence stays as it is, its kept entries are
+ * -1 and new_lens[s] is context_lens[s].
+ */
+int pa_evict(void* k_cache, void* v_cache, int kv_format, const int32_t* block_tables,
+             const int32_t* context_lens, float* weights, int64_t weights_len,
+             const int32_t* budgets, int max_budget, int num_sinks, int num_recent, int32_t* kept,
+             int32_t* new_lens, const pa_shape* shape, void* stream);
 
 /*
  * pa_splitk_reduce -- merge of split-K partial softmax results (course

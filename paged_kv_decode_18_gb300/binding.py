@@ -31,6 +31,13 @@ PA_DEVERR_CONTEXT_RANGE = 0x4
 PA_DEVERR_QLEN_RANGE = 0x8
 PA_DEVERR_PIPE_TIMEOUT = 0x10
 PA_DEVERR_PLAN_OVERFLOW = 0x20
+PA_DEVERR_TREE_RANGE = 0x40
+PA_DEVERR_BUDGET_RANGE = 0x80
+
+# pool formats of the calls that take any of the library's pools
+PA_KV_BF16 = 0
+PA_KV_INT8 = 1
+PA_KV_FP8 = 2
 
 # every symbol include/pa.h declares
 EXPORTED = (
@@ -50,6 +57,12 @@ EXPORTED = (
     "pa_decode_cascade",
     "pa_decode_cascade_ex",
     "pa_decode_cascade_workspace_size",
+    "pa_tree_mask",
+    "pa_decode_tree",
+    "pa_decode_tree_workspace_size",
+    "pa_commit_path",
+    "pa_accumulate_weights",
+    "pa_evict",
     "pa_splitk_reduce",
     "pa_status_string",
     "pa_debug_read_error",
@@ -128,6 +141,20 @@ def load(path: str | None = None):
                                              V, V, S, i32, V, sz, V]
         lib.pa_decode_cascade_workspace_size.restype = sz
         lib.pa_decode_cascade_workspace_size.argtypes = [S, i32, i32, i32, i32]
+        lib.pa_tree_mask.restype = i32
+        lib.pa_tree_mask.argtypes = [V, V, i32, i64, i32, V, i32, V, V]
+        lib.pa_decode_tree.restype = i32
+        lib.pa_decode_tree.argtypes = [V, V, V, V, V, V, V, i32, i64, i32, f32, V, V, S, V, sz,
+                                       V]
+        lib.pa_decode_tree_workspace_size.restype = sz
+        lib.pa_decode_tree_workspace_size.argtypes = [S, i64, i32]
+        lib.pa_commit_path.restype = i32
+        lib.pa_commit_path.argtypes = [V, V, i32, V, V, V, V, V, i32, V, S, V]
+        lib.pa_accumulate_weights.restype = i32
+        lib.pa_accumulate_weights.argtypes = [V, V, i32, V, V, V, V, i64, i32, f32, i32, V, i64,
+                                              S, V]
+        lib.pa_evict.restype = i32
+        lib.pa_evict.argtypes = [V, V, i32, V, V, V, i64, V, i32, i32, i32, V, V, S, V]
         lib.pa_splitk_reduce.restype = i32
         lib.pa_splitk_reduce.argtypes = [V, V, i64, i32, i32, i32, V, V, V]
         lib.pa_status_string.restype = ctypes.c_char_p
@@ -518,6 +545,258 @@ def pa_decode_varlen(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens
                                    int(max_q_len), 1 if causal else 0, float(scale), _ptr(out),
                                    _ptr(lse), ctypes.byref(sh), _ptr(workspace), ws_bytes,
                                    _stream(stream)), "pa_decode_varlen")
+
+# ---------------------------------------------------------------------------
+# speculative decoding with a tree of drafted tokens
+# ---------------------------------------------------------------------------
+
+def _here(*tensors):
+    """All tensors on the current CUDA device: the library works on it alone."""
+    now = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != now:
+            raise ValueError(f"tensor on {t.device}, but the current CUDA device is {now}")
+
+
+def _max_q_len(max_q_len, num_words):
+    if not 0 <= int(max_q_len) <= 32 * num_words:
+        raise ValueError(f"max_q_len {max_q_len} needs 0 .. 32 * mask words ({32 * num_words})")
+    return int(max_q_len)
+
+
+def prepare_tree_mask(parents, cu_seqlens_q, max_q_len, tree_mask, depths=None, stream=None):
+    """pa_tree_mask with its arguments checked and marshalled now (see
+    prepare_decode)."""
+    _need(parents, "parents", torch.int32, 1)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    _need(tree_mask, "tree_mask", torch.int32, 2)
+    if depths is not None:
+        _need(depths, "depths", torch.int32, 1)
+        if depths.shape != parents.shape:
+            raise ValueError("depths shape != parents shape")
+    if tree_mask.shape[0] != parents.shape[0]:
+        raise ValueError("tree_mask rows != number of tokens")
+    if cu_seqlens_q.shape[0] < 1:
+        raise ValueError("cu_seqlens_q needs num_seqs + 1 entries")
+    _here(parents, cu_seqlens_q, tree_mask, depths)
+    words = tree_mask.shape[1]
+    args = (_ptr(parents), _ptr(cu_seqlens_q), ctypes.c_int(cu_seqlens_q.shape[0] - 1),
+            ctypes.c_int64(parents.shape[0]), ctypes.c_int(_max_q_len(max_q_len, words)),
+            _ptr(tree_mask), ctypes.c_int(words), _ptr(depths))
+    keep = (parents, cu_seqlens_q, tree_mask, depths)
+    return _prepared(load().pa_tree_mask, args, stream, "pa_tree_mask", keep)
+
+
+def pa_tree_mask(parents, cu_seqlens_q, max_q_len, tree_mask, depths=None, stream=None) -> None:
+    """Ancestor bits of a window's tokens from their parents: parents [Tq] int32
+    (-1: follows the cached context), tree_mask [Tq, words] int32 (bit patterns),
+    depths [Tq] int32."""
+    prepare_tree_mask(parents, cu_seqlens_q, max_q_len, tree_mask, depths, stream)()
+
+
+def pa_decode_tree_workspace_size(shape: pa_shape, num_q_tokens: int, max_q_len: int) -> int:
+    return int(load().pa_decode_tree_workspace_size(ctypes.byref(shape), int(num_q_tokens),
+                                                    int(max_q_len)))
+
+
+def prepare_decode_tree(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens_q, tree_mask,
+                        max_q_len, scale, out, lse=None, workspace=None, stream=None):
+    """pa_decode_tree with its arguments checked and marshalled now (see
+    prepare_decode)."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    _need(tree_mask, "tree_mask", torch.int32, 2)
+    _need(out, "out", torch.bfloat16, 3)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2)
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse shape != q rows x heads")
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k / v cache shapes differ")
+    sh = shape_of(q, k_cache, block_tables)
+    if q.shape[2] != sh.head_dim:
+        raise ValueError("q head_dim != the cache's")
+    if context_lens.shape[0] != sh.num_seqs or cu_seqlens_q.shape[0] != sh.num_seqs + 1:
+        raise ValueError("context_lens / cu_seqlens_q length mismatch")
+    if out.shape != q.shape:
+        raise ValueError("out shape != q shape")
+    if tree_mask.shape[0] != q.shape[0]:
+        raise ValueError("tree_mask rows != number of query tokens")
+    _here(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens_q, tree_mask, out, lse,
+          workspace)
+    words = tree_mask.shape[1]
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
+            _ptr(cu_seqlens_q), _ptr(tree_mask), ctypes.c_int(words),
+            ctypes.c_int64(q.shape[0]), ctypes.c_int(_max_q_len(max_q_len, words)),
+            ctypes.c_float(scale), _ptr(out), _ptr(lse), ctypes.byref(sh), _ptr(workspace),
+            ctypes.c_size_t(ws_bytes))
+    keep = (q, k_cache, v_cache, block_tables, context_lens, cu_seqlens_q, tree_mask, out, lse,
+            workspace, sh)
+    return _prepared(load().pa_decode_tree, args, stream, "pa_decode_tree", keep)
+
+
+def pa_decode_tree(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens_q, tree_mask,
+                   max_q_len, scale, out, lse=None, workspace=None, stream=None) -> None:
+    """Attention for a window whose queries see the cached context before it and
+    the window keys of their mask row (pa_tree_mask)."""
+    prepare_decode_tree(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens_q, tree_mask,
+                        max_q_len, scale, out, lse, workspace, stream)()
+
+
+def _pool_pair(k_cache, v_cache):
+    """Checks of a pool pair whose rows are moved; its format."""
+    if k_cache.dim() == 3:
+        _need(k_cache, "k_cache", torch.uint8, 3)
+        _need(v_cache, "v_cache", torch.uint8, 3)
+        fmt = PA_KV_INT8  # the FP8 pool's rows are the same bytes
+    else:
+        _need(k_cache, "k_cache", torch.bfloat16, 4)
+        _need(v_cache, "v_cache", torch.bfloat16, 4)
+        fmt = PA_KV_BF16
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k / v cache shapes differ")
+    return fmt
+
+
+def _pool_shape(k_cache, block_tables) -> pa_shape:
+    """shape_of for calls without queries (one query head per KV head)."""
+    return shape_of(torch.empty((0, k_cache.shape[1], 0)), k_cache, block_tables)
+
+
+def prepare_commit_path(k_cache, v_cache, block_tables, context_lens, cu_seqlens_q, path,
+                        path_lens, new_lens, stream=None):
+    """pa_commit_path with its arguments checked and marshalled now (see
+    prepare_decode)."""
+    fmt = _pool_pair(k_cache, v_cache)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    _need(path, "path", torch.int32, 2)
+    _need(path_lens, "path_lens", torch.int32, 1)
+    _need(new_lens, "new_lens", torch.int32, 1)
+    sh = _pool_shape(k_cache, block_tables)
+    S = sh.num_seqs
+    if (context_lens.shape[0] != S or path.shape[0] != S or path_lens.shape[0] != S or
+            new_lens.shape[0] != S or cu_seqlens_q.shape[0] != S + 1):
+        raise ValueError("a per-sequence tensor does not have one entry per sequence")
+    _here(k_cache, v_cache, block_tables, context_lens, cu_seqlens_q, path, path_lens, new_lens)
+    args = (_ptr(k_cache), _ptr(v_cache), ctypes.c_int(fmt), _ptr(block_tables),
+            _ptr(context_lens), _ptr(cu_seqlens_q), _ptr(path), _ptr(path_lens),
+            ctypes.c_int(path.shape[1]), _ptr(new_lens), ctypes.byref(sh))
+    keep = (k_cache, v_cache, block_tables, context_lens, cu_seqlens_q, path, path_lens,
+            new_lens, sh)
+    return _prepared(load().pa_commit_path, args, stream, "pa_commit_path", keep)
+
+
+def pa_commit_path(k_cache, v_cache, block_tables, context_lens, cu_seqlens_q, path, path_lens,
+                   new_lens, stream=None) -> None:
+    """Move the accepted path's cached rows to the front of their window: path
+    [S, max_path] int32 increasing window indices, path_lens [S]; new_lens [S]
+    receives context_len - Lq + path_len (it may be context_lens itself)."""
+    prepare_commit_path(k_cache, v_cache, block_tables, context_lens, cu_seqlens_q, path,
+                        path_lens, new_lens, stream)()
+
+
+# ---------------------------------------------------------------------------
+# eviction by accumulated attention weight
+# ---------------------------------------------------------------------------
+
+def prepare_accumulate_weights(q, k_cache, lse, block_tables, context_lens, scale, weights,
+                               cu_seqlens_q=None, max_q_len: int = 1, accumulate: bool = True,
+                               kv_format: int | None = None, stream=None):
+    """pa_accumulate_weights with its arguments checked and marshalled now (see
+    prepare_decode)."""
+    _need(q, "q", torch.bfloat16, 3)
+    if k_cache.dim() == 3:
+        _need(k_cache, "k_cache", torch.uint8, 3)
+        if kv_format not in (PA_KV_INT8, PA_KV_FP8):
+            raise ValueError("an 8-bit pool needs kv_format PA_KV_INT8 or PA_KV_FP8")
+    else:
+        _need(k_cache, "k_cache", torch.bfloat16, 4)
+        if kv_format not in (None, PA_KV_BF16):
+            raise ValueError("a bf16 pool has kv_format PA_KV_BF16")
+        kv_format = PA_KV_BF16
+    _need(lse, "lse", torch.float32, 2)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    _need(weights, "weights", torch.float32, 3)
+    sh = shape_of(q, k_cache, block_tables)
+    if q.shape[2] != sh.head_dim:
+        raise ValueError("q head_dim != the cache's")
+    if lse.shape != q.shape[:2]:
+        raise ValueError("lse shape != q rows x heads")
+    if context_lens.shape[0] != sh.num_seqs:
+        raise ValueError("context_lens length != number of sequences")
+    if weights.shape[:2] != (sh.num_seqs, sh.num_kv_heads):
+        raise ValueError("weights must be [num_seqs, num_kv_heads, positions]")
+    if cu_seqlens_q is None:
+        if q.shape[0] != sh.num_seqs:
+            raise ValueError("without cu_seqlens_q there is one query per sequence")
+    else:
+        _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+        if cu_seqlens_q.shape[0] != sh.num_seqs + 1:
+            raise ValueError("cu_seqlens_q needs num_seqs + 1 entries")
+    _here(q, k_cache, lse, block_tables, context_lens, weights, cu_seqlens_q)
+    args = (_ptr(q), _ptr(k_cache), ctypes.c_int(kv_format), _ptr(lse), _ptr(block_tables),
+            _ptr(context_lens), _ptr(cu_seqlens_q), ctypes.c_int64(q.shape[0]),
+            ctypes.c_int(int(max_q_len)), ctypes.c_float(scale),
+            ctypes.c_int(1 if accumulate else 0), _ptr(weights),
+            ctypes.c_int64(weights.shape[2]), ctypes.byref(sh))
+    keep = (q, k_cache, lse, block_tables, context_lens, weights, cu_seqlens_q, sh)
+    return _prepared(load().pa_accumulate_weights, args, stream, "pa_accumulate_weights", keep)
+
+
+def pa_accumulate_weights(q, k_cache, lse, block_tables, context_lens, scale, weights,
+                          cu_seqlens_q=None, max_q_len: int = 1, accumulate: bool = True,
+                          kv_format: int | None = None, stream=None) -> None:
+    """Attention weight that each cached position draws from these queries, added
+    to weights [S, Hkv, positions] fp32 (or written: accumulate=False); lse is
+    what the attention call over the same queries returned."""
+    prepare_accumulate_weights(q, k_cache, lse, block_tables, context_lens, scale, weights,
+                               cu_seqlens_q, max_q_len, accumulate, kv_format, stream)()
+
+
+def prepare_evict(k_cache, v_cache, block_tables, context_lens, weights, budgets, num_sinks,
+                  num_recent, kept, new_lens, stream=None):
+    """pa_evict with its arguments checked and marshalled now (see
+    prepare_decode)."""
+    fmt = _pool_pair(k_cache, v_cache)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    _need(weights, "weights", torch.float32, 3)
+    _need(budgets, "budgets", torch.int32, 1)
+    _need(kept, "kept", torch.int32, 3)
+    _need(new_lens, "new_lens", torch.int32, 1)
+    sh = _pool_shape(k_cache, block_tables)
+    S = sh.num_seqs
+    if context_lens.shape[0] != S or budgets.shape[0] != S or new_lens.shape[0] != S:
+        raise ValueError("a per-sequence tensor does not have one entry per sequence")
+    if weights.shape[:2] != (S, sh.num_kv_heads):
+        raise ValueError("weights must be [num_seqs, num_kv_heads, positions]")
+    if kept.shape[:2] != (S, sh.num_kv_heads):
+        raise ValueError("kept must be [num_seqs, num_kv_heads, max_budget]")
+    _here(k_cache, v_cache, block_tables, context_lens, weights, budgets, kept, new_lens)
+    args = (_ptr(k_cache), _ptr(v_cache), ctypes.c_int(fmt), _ptr(block_tables),
+            _ptr(context_lens), _ptr(weights), ctypes.c_int64(weights.shape[2]), _ptr(budgets),
+            ctypes.c_int(kept.shape[2]), ctypes.c_int(int(num_sinks)),
+            ctypes.c_int(int(num_recent)), _ptr(kept), _ptr(new_lens), ctypes.byref(sh))
+    keep = (k_cache, v_cache, block_tables, context_lens, weights, budgets, kept, new_lens, sh)
+    return _prepared(load().pa_evict, args, stream, "pa_evict", keep)
+
+
+def pa_evict(k_cache, v_cache, block_tables, context_lens, weights, budgets, num_sinks,
+             num_recent, kept, new_lens, stream=None) -> None:
+    """Shrink each sequence's cache to budgets[s] positions per KV head: the
+    first num_sinks, the last num_recent and the heaviest between them stay and
+    move together in order, with their weights. kept [S, Hkv, max_budget]
+    receives their old positions, new_lens [S] the new lengths."""
+    prepare_evict(k_cache, v_cache, block_tables, context_lens, weights, budgets, num_sinks,
+                  num_recent, kept, new_lens, stream)()
 
 
 def pa_splitk_reduce(part_out, part_lse, out, lse=None, stream=None) -> None:

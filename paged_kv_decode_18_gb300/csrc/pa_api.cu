@@ -22,6 +22,9 @@ extern "C" int pa_debug_read_error(void* stream) {
   word |= pa::take_error_word_varlen(st, &rc);
   word |= pa::take_error_word_prefill(st, &rc);
   word |= pa::take_error_word_cascade(st, &rc);
+  word |= pa::take_error_word_tree(st, &rc);
+  word |= pa::take_error_word_weights(st, &rc);
+  word |= pa::take_error_word_evict(st, &rc);
   if (rc != PA_OK) return rc;
   return static_cast<int>(word);
 }

@@ -184,6 +184,48 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a
 }
 
 // ---------------------------------------------------------------------------
+// tree masks: row of 32-bit words, bit i of word i / 32 = window key i is seen
+// ---------------------------------------------------------------------------
+
+// The 32 bits from bit i0 >= 0 of a mask row of `words` words; bits past the
+// row are 0.
+__device__ __forceinline__ uint32_t mask_window32(const uint32_t* __restrict__ row, int words,
+                                                  int i0) {
+  const int w = i0 >> 5;
+  const uint32_t lo = w < words ? __ldg(row + w) : 0u;
+  const uint32_t hi = w + 1 < words ? __ldg(row + w + 1) : 0u;
+  return __funnelshift_r(lo, hi, i0 & 31);
+}
+
+// Visibility of 32 consecutive keys whose first is window key i0 (i0 < 0: the
+// first -i0 of them lie before the window and are seen) as bits; only the
+// first `valid` of them (<= 0: none) lie inside the context.
+__device__ __forceinline__ uint32_t tree_visible32(const uint32_t* __restrict__ row, int words,
+                                                   int i0, int valid) {
+  uint32_t vis;
+  if (i0 >= 0)
+    vis = mask_window32(row, words, i0);
+  else if (i0 <= -32)
+    vis = 0xffffffffu;
+  else
+    vis = ((1u << -i0) - 1u) | (mask_window32(row, words, 0) << -i0);
+  if (valid >= 32) return vis;
+  return valid <= 0 ? 0u : vis & ((1u << valid) - 1u);
+}
+
+// Whether a pair of bf16 values holds an infinity or a NaN (all exponent bits set).
+__device__ __forceinline__ bool bf2_nonfinite(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// The pair with infinities and NaNs replaced by zero.
+__device__ __forceinline__ uint32_t bf2_finite_part(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// ---------------------------------------------------------------------------
 // Work plan.
 //
 // The batch is a list of (sequence, query tile) pairs; pair p needs n_p K/V
@@ -216,6 +258,9 @@ struct PlanInputs {
   int key_tile = kBlock;       // keys per flat tile (a multiple of the block size)
   int min_lq = 0;              // sequences whose q_len lies outside [min_lq, max_lq]
   int max_lq = 0x7fffffff;     // belong to another kernel: no tiles here (not an error)
+  // > 0 (non-causal): a query window is the last lq positions of its context
+  // and holds at most this many (the bits of a tree mask row)
+  int max_window = 0;
   // decode only: every sequence is cut into `parts` near-equal block ranges,
   // one pair each (pair s * parts + j holds blocks part_begin(j) ..), the
   // split-K partitions; 1 = one pair per sequence
@@ -260,6 +305,14 @@ __device__ __forceinline__ int pair_tiles(int c, int lq, int qt, int qtile, int 
   return (kv_end + key_tile - 1) / key_tile;
 }
 
+// Whether a window of lq queries starting at row q0, over a context of c keys,
+// is one the plan refuses: a causal (or tree) window lies inside its context;
+// other queries see the whole (non-empty) context whatever their number.
+__device__ __forceinline__ bool bad_window(const PlanInputs& in, int lq, int q0, int c) {
+  return lq < 0 || (lq > c && (in.causal || in.max_window > 0 || c == 0)) || q0 < 0 ||
+         (in.max_window > 0 && lq > in.max_window) || (int64_t)q0 + lq > in.num_q_rows;
+}
+
 // Build the plan in shared memory. All threads of the CTA must call it; it
 // ends with a CTA barrier. Invalid lengths are clamped (and flagged) so that
 // every later access stays inside the caller's buffers.
@@ -280,10 +333,7 @@ __device__ inline void build_plan(const PlanInputs& in, PlanSmem& P, int* /*scra
     if (varlen) {
       const int q0 = in.cu_seqlens_q[s];
       int lq = in.cu_seqlens_q[s + 1] - q0;
-      // causal: a query window cannot be longer than its context; non-causal
-      // queries see the whole (non-empty) context whatever their number
-      if (lq < 0 || (lq > c && (in.causal || c == 0)) || q0 < 0 ||
-          (int64_t)q0 + lq > in.num_q_rows) {
+      if (bad_window(in, lq, q0, c)) {
         flag_error(PA_DEVERR_QLEN_RANGE);
         lq = 0;  // the sequence produces no rows
       }
@@ -331,9 +381,7 @@ __device__ inline void build_plan(const PlanInputs& in, PlanSmem& P, int* /*scra
       const int c = P.ctx[s];
       const int q0 = in.cu_seqlens_q[s];
       int lq = in.cu_seqlens_q[s + 1] - q0;
-      if (lq < 0 || (lq > c && (in.causal || c == 0)) || q0 < 0 ||
-          (int64_t)q0 + lq > in.num_q_rows)
-        lq = 0;
+      if (bad_window(in, lq, q0, c)) lq = 0;
       if (lq < in.min_lq || lq > in.max_lq) lq = 0;
       for (int p = p0; p < p1; ++p)
         P.pair_off[p] = in.Hkv * pair_tiles(c, lq, p - p0, in.qtile, in.causal, in.key_tile);

@@ -196,11 +196,27 @@ int launch_prefill_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf1
                       const int32_t* row_map = nullptr, int parts = 3, int split = 0);
 // parts: bit 0 launches the attention grid, bit 1 its merge grid.
 
+// The same tile for tree windows (pa_decode_tree): every sequence of the batch,
+// any group of up to kTcRows query heads per KV head, visibility inside a
+// window from the mask rows.
+constexpr int kTcRows = 128;
+int tree_tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len,
+                     PrefillTcGeometry* g);
+int launch_tree_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf16* k_cache,
+                   const pa_bf16* v_cache, const int32_t* block_tables,
+                   const int32_t* context_lens, const int32_t* cu_seqlens_q,
+                   const uint32_t* tree_mask, int mask_words, int64_t num_q_tokens, float scale,
+                   pa_bf16* out, float* lse, const pa_shape* sh, void* workspace,
+                   cudaStream_t st);
+
 // Each TU that owns kernels exposes the reader of its device error word.
 unsigned take_error_word_cache(cudaStream_t stream, int* rc);
 unsigned take_error_word_decode(cudaStream_t stream, int* rc);
 unsigned take_error_word_varlen(cudaStream_t stream, int* rc);
 unsigned take_error_word_prefill(cudaStream_t stream, int* rc);
 unsigned take_error_word_cascade(cudaStream_t stream, int* rc);
+unsigned take_error_word_tree(cudaStream_t stream, int* rc);
+unsigned take_error_word_weights(cudaStream_t stream, int* rc);
+unsigned take_error_word_evict(cudaStream_t stream, int* rc);
 
 }  // namespace pa

@@ -55,6 +55,8 @@ constexpr int kOffBar = kOffKV + 2 * 2 * kOpBytes;
 constexpr int kNumBars = 20;
 constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
 constexpr int kOffAbort = kOffTmemSlot + 4;
+constexpr int kOffBadV = kOffAbort + 4;
+static_assert(kOffBadV + 4 <= kOffBar + 256, "barrier area");
 constexpr int kOffLx = kOffBar + 256;       // [2 pieces][2 halves][128 rows] x (m, l)
 constexpr int kOffPlan = kOffLx + 2 * 2 * kRowsT * 8;
 // a segment start weighs as much as one key tile in the cut between CTAs
@@ -97,6 +99,10 @@ struct TcArgs {
   float* part_lse;  // [NW * 2][128 rows]
   RowsOut rows;     // fp32 row output instead of out / lse (rows.o set)
   const int32_t* row_map;  // rows mode: query token i -> output token row_map[i]
+  // tree windows: mask rows, and V for the elements that the product leaves out
+  const uint32_t* mask = nullptr;
+  int mask_words = 0;
+  const uint16_t* v_cache = nullptr;
 };
 
 // Output row (token * Hq + head) of query token qtok, head hd; -1 when the
@@ -251,6 +257,7 @@ __device__ __forceinline__ void plan_inputs(const TcArgs& a, PlanInputs& in) {
   in.num_q_rows = a.num_q_tokens;
   in.key_tile = kKeysT;
   in.min_lq = a.min_lq;
+  in.max_window = a.mask_words * 32;  // 0: not a tree
 }
 
 __device__ __forceinline__ void plan_view(unsigned char* base, const TcArgs& a, PlanSmem& P) {
@@ -282,6 +289,9 @@ __device__ __forceinline__ int prefill_workers(const TcArgs& a, unsigned char* p
   return min(a.num_workers, K);
 }
 
+// TREE: the window's visibility comes from a.mask, and any group size is taken
+// (rows past QTb x G of a tile are padding whose results nothing reads).
+template <bool TREE>
 __global__ void __launch_bounds__(kThreadsT, 1)
     paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq,
                             const __grid_constant__ CUtensorMap tmk,
@@ -293,6 +303,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffAbort);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffTmemSlot);
+  // TREE: a window row of V held an infinity or a NaN (set once, kept)
+  volatile int* bad_v = reinterpret_cast<volatile int*>(smem + kOffBadV);
   const int S = a.S, Hkv = a.Hkv, G = a.G, QTb = a.QTb;
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
 
@@ -304,6 +316,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       mbar_init(bar(i), all ? (uint32_t)(kSoftmaxWarps * 32) : 1u);
     }
     *abort_flag = 0;
+    *bad_v = 0;
     mbar_fence_init();
   }
   if (tid == 32) {
@@ -376,7 +389,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         if (lane == 0) {
           const int z = P.qstart[t.s] + t.qt * QTb;  // first query token of the tile
           const uint32_t qd = smem_addr(smem + kOffQ + qs * kOpBytes);
-          mbar_arrive_expect_tx(bar(B_QFULL + qs), kOpBytes);
+          mbar_arrive_expect_tx(bar(B_QFULL + qs),
+                                TREE ? (uint32_t)(QTb * G) * 256u : (uint32_t)kOpBytes);
           tma_load_3d(qd, &tmq, 0, t.h * G, z, bar(B_QFULL + qs));
           tma_load_3d(qd + kHalfT, &tmq, 64, t.h * G, z, bar(B_QFULL + qs));
         }
@@ -492,6 +506,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     float m_ref = neg_inf(), l = 0.f;
     int lim = 0, c = 0, lq = 0, tok = 0, piece_b0 = 0, np = 0;
     bool valid = false, piece_first = true;
+    const uint32_t* mrow = nullptr;  // TREE: this row's mask words
+    int pend_s = 0, pend_h = 0, pend_k0 = 0, pend_k1 = 0;
     // A finished piece's O stays in TMEM until the next tile's exponentials
     // are done (its last PV completes meanwhile); then it is written out.
     bool pend = false, pend_complete = false, pend_valid = false;
@@ -523,6 +539,32 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           o[j] = fmaf(__uint_as_float(u0[j]), c0, __uint_as_float(u1[j]) * c1);
+        if constexpr (TREE) {
+          // infinities and NaNs of window rows entered the product as zeros
+          // (they must not reach queries that do not see their row): they join
+          // the rows that see them here
+          if (*bad_v && pend_valid) {
+            const int lqp = P.qstart[pend_s + 1] - P.qstart[pend_s];
+            const int p0 = P.ctx[pend_s] - lqp;
+            const uint32_t* mr = a.mask + (pend_orow / a.Hq) * a.mask_words;
+            const int i1 = min(lqp, pend_k1 - p0);  // the piece's window keys
+            for (int i = max(0, pend_k0 - p0); i < i1; ++i) {
+              if (!((__ldg(mr + (i >> 5)) >> (i & 31)) & 1u)) continue;
+              const int phys =
+                  a.block_tables[(size_t)pend_s * a.max_blocks + (p0 + i) / kBlock];
+              if (phys < 0 || (int64_t)phys >= a.num_blocks) continue;
+              const uint32_t* vr = reinterpret_cast<const uint32_t*>(
+                  a.v_cache +
+                  ((((int64_t)phys * Hkv + pend_h) * kBlock) + (p0 + i) % kBlock) * kHeadDim + d0);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const uint32_t wv = __ldg(vr + j), fin = bf2_finite_part(wv);
+                if ((wv ^ fin) & 0x7f80u) o[2 * j] += bf_lo(wv);
+                if ((wv ^ fin) & 0x7f800000u) o[2 * j + 1] += bf_hi(wv);
+              }
+            }
+          }
+        }
         if (pend_complete && a.rows.o) {
           if (pend_valid) {
             float4* dst = reinterpret_cast<float4*>(
@@ -570,6 +612,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         lq = P.qstart[t.s + 1] - P.qstart[t.s];
         tok = t.qt * QTb + r / G;
         valid = tok < lq;
+        if constexpr (TREE) {
+          valid = valid && r < QTb * G;
+          mrow = a.mask + ((int64_t)P.qstart[t.s] + (valid ? tok : 0)) * a.mask_words;
+        }
         lim = valid ? (a.causal ? c - lq + tok + 1 : c) : 0;
         m_ref = neg_inf();
         l = 0.f;
@@ -597,7 +643,22 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                        make_float2(sc, sc));
       }
       const int kb = t.b * kKeysT + hf * 64;  // first key of this half
-      if (kb + 64 > lim) {  // the causal diagonal or the end of the context
+      if constexpr (TREE) {
+        if (kb + 64 > c - lq) {  // the half reaches into the window
+          const int i0 = kb - (c - lq);
+          const uint32_t vis0 =
+              valid ? tree_visible32(mrow, a.mask_words, i0, c - kb) : 0u;
+          const uint32_t vis1 =
+              valid ? tree_visible32(mrow, a.mask_words, i0 + 32, c - kb - 32) : 0u;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (!((vis0 >> (2 * j)) & 1u)) x[j].x = neg_inf();
+            if (!((vis0 >> (2 * j + 1)) & 1u)) x[j].y = neg_inf();
+            if (!((vis1 >> (2 * j)) & 1u)) x[16 + j].x = neg_inf();
+            if (!((vis1 >> (2 * j + 1)) & 1u)) x[16 + j].y = neg_inf();
+          }
+        }
+      } else if (kb + 64 > lim) {  // the causal diagonal or the end of the context
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           if (kb + 2 * j >= lim) x[j].x = neg_inf();
@@ -668,13 +729,41 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       // keys past the context may hold anything (even NaN): zero their V rows
       // so that P = 0 never meets them (thread (r, hf) clears half hf of key row r)
       const int key0 = t.b * kKeysT;
-      if (key0 + kKeysT > c && key0 + r >= c) {
+      const int vsafe = TREE ? c - lq : c;  // rows before it enter the product as they are
+      if (key0 + kKeysT > vsafe && key0 + r >= vsafe) {
         if (!wait(B_VFULL + sb, (uint32_t)(i >> 1) & 1u)) break;
         unsigned char* vrow = smem + kOffKV + sb * 2 * kOpBytes + kOpBytes + hf * kHalfT + r * 128;
+        bool write = true;
+        if constexpr (TREE) {
+          if (key0 + r < c) {  // a window row: only its infinities and NaNs are left out
+            bool bad = false;
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch)
-          *reinterpret_cast<uint4*>(vrow + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
+            for (int ch = 0; ch < 8; ++ch) {
+              const uint4 x4 = *reinterpret_cast<const uint4*>(vrow + ch * 16);
+              bad = bad || bf2_nonfinite(x4.x) || bf2_nonfinite(x4.y) || bf2_nonfinite(x4.z) ||
+                    bf2_nonfinite(x4.w);
+            }
+            write = false;
+            if (bad) {
+              *bad_v = 1;
+              for (int ch = 0; ch < 8; ++ch) {
+                uint4 x4 = *reinterpret_cast<const uint4*>(vrow + ch * 16);
+                x4.x = bf2_finite_part(x4.x);
+                x4.y = bf2_finite_part(x4.y);
+                x4.z = bf2_finite_part(x4.z);
+                x4.w = bf2_finite_part(x4.w);
+                *reinterpret_cast<uint4*>(vrow + ch * 16) = x4;
+              }
+              fence_proxy_async_smem();
+            }
+          }
+        }
+        if (write) {
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch)
+            *reinterpret_cast<uint4*>(vrow + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+        }
       }
       tc_fence_before();
       mbar_arrive(bar(B_PFULL));
@@ -693,6 +782,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         pend_complete = (piece_b0 == 0) && (t.b == t.nt - 1);
         pend_orow = valid ? out_row(a, (int64_t)P.qstart[t.s] + tok, t.h * G + r % G) : 0;
         pend_valid = valid && pend_orow >= 0;
+        pend_s = t.s;
+        pend_h = t.h;
+        pend_k0 = piece_b0 * kKeysT;
+        pend_k1 = (t.b + 1) * kKeysT;
         pend_slot = (size_t)w * 2 + (piece_first ? 0 : 1);
       }
       if (idx + 1 < R1) advance(P, S, Hkv, t);
@@ -747,7 +840,7 @@ __global__ void __launch_bounds__(kFixThreads)
   const int r = blockIdx.y * kFixRowsPerCta + warp * 4 + (lane >> 3);
   const int d0 = (lane & 7) * 16;
   const int tok = job.qt * a.QTb + r / a.G;
-  if (tok >= lq) return;
+  if (r >= a.QTb * a.G || tok >= lq) return;  // padding rows
   // online merge over the pieces, four at a time with all their loads in flight
   float m = neg_inf(), sum = 0.f;
   float acc[16];
@@ -832,12 +925,12 @@ size_t plan_bytes(int S, int npairs_cap, int workers) {
 
 }  // namespace
 
-int prefill_tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len,
-                        PrefillTcGeometry* g, int min_q_len, int max_ctas) {
+static int tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len,
+                       PrefillTcGeometry* g, int min_q_len, int max_ctas, bool tree) {
   DeviceInfo dev;
   if (!current_device_info(&dev)) return PA_ERR_CUDA;
   const int G = sh->num_q_heads / sh->num_kv_heads;
-  if (G > kRowsT || kRowsT % G != 0 || max_q_len < min_q_len || max_q_len < 1) {
+  if (G > kRowsT || (kRowsT % G != 0 && !tree) || max_q_len < min_q_len || max_q_len < 1) {
     g->enabled = false;
     g->ws_bytes = 0;
     return PA_OK;
@@ -857,7 +950,8 @@ int prefill_tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len,
   g->fixup_smem = plan_bytes(S, g->npairs_cap, g->workers);
   if (g->smem > (size_t)dev.max_smem_optin || g->fixup_smem > (size_t)dev.max_smem_optin)
     return PA_ERR_UNSUPPORTED;
-  if (!raise_smem_limit(reinterpret_cast<const void*>(paged_prefill_tc_kernel)))
+  if (!raise_smem_limit(tree ? reinterpret_cast<const void*>(paged_prefill_tc_kernel<true>)
+                             : reinterpret_cast<const void*>(paged_prefill_tc_kernel<false>)))
     return PA_ERR_CUDA;
   if (g->fixup_smem > 48 * 1024 &&
       !raise_smem_limit(reinterpret_cast<const void*>(prefill_tc_fixup_kernel)))
@@ -868,24 +962,25 @@ int prefill_tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len,
   return PA_OK;
 }
 
-int launch_prefill_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf16* k_cache,
-                      const pa_bf16* v_cache, const int32_t* block_tables,
-                      const int32_t* context_lens, const int32_t* cu_seqlens_q,
-                      int64_t num_q_tokens, int causal, float scale, pa_bf16* out, float* lse,
-                      const pa_shape* sh, void* workspace, cudaStream_t st, int min_q_len,
-                      const RowsOut* rows, const int32_t* row_map, int parts, int split) {
+int prefill_tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len,
+                        PrefillTcGeometry* g, int min_q_len, int max_ctas) {
+  return tc_geometry(sh, num_q_tokens, max_q_len, g, min_q_len, max_ctas, false);
+}
+
+int tree_tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len,
+                     PrefillTcGeometry* g) {
+  return tc_geometry(sh, num_q_tokens, max_q_len, g, 1, 0, true);
+}
+
+static int launch_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf16* k_cache,
+                     const pa_bf16* v_cache, TcArgs a, int64_t num_q_tokens, float scale,
+                     const pa_shape* sh, void* workspace, cudaStream_t st, int parts) {
   const int G = sh->num_q_heads / sh->num_kv_heads;
   CUtensorMap tmq, tmk, tmv;
   const int64_t pool_rows = sh->num_blocks * sh->num_kv_heads * kBlock;
   if (!make_q_map(&tmq, q, num_q_tokens, sh->num_q_heads, G, g.QTb) ||
       !make_pool_map(&tmk, k_cache, pool_rows) || !make_pool_map(&tmv, v_cache, pool_rows))
     return PA_ERR_CUDA;
-  TcArgs a;
-  a.block_tables = block_tables;
-  a.context_lens = context_lens;
-  a.cu_seqlens_q = cu_seqlens_q;
-  a.out = out;
-  a.lse = lse;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.S = sh->num_seqs;
   a.Hq = sh->num_q_heads;
@@ -895,23 +990,65 @@ int launch_prefill_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf1
   a.max_blocks = sh->max_blocks_per_seq;
   a.num_blocks = sh->num_blocks;
   a.num_q_tokens = num_q_tokens;
-  a.causal = causal ? 1 : 0;
   a.npairs_cap = g.npairs_cap;
   a.num_workers = g.workers;
-  a.split = split > 0 ? g.grid : 0;
-  a.min_lq = min_q_len;
-  if (rows) a.rows = *rows;
-  a.row_map = row_map;
   char* ws = static_cast<char*>(workspace);
   a.part_lse = reinterpret_cast<float*>(ws);
   a.part_o = reinterpret_cast<float*>(ws + g.ws_lse);
-  if ((parts & 1) && launch_dependent(paged_prefill_tc_kernel, dim3(g.grid), dim3(kThreadsT),
-                                      g.smem, st, tmq, tmk, tmv, a) != cudaSuccess)
-    return PA_ERR_CUDA;
+  if (parts & 1) {
+    const cudaError_t e =
+        a.mask ? launch_dependent(paged_prefill_tc_kernel<true>, dim3(g.grid), dim3(kThreadsT),
+                                  g.smem, st, tmq, tmk, tmv, a)
+               : launch_dependent(paged_prefill_tc_kernel<false>, dim3(g.grid), dim3(kThreadsT),
+                                  g.smem, st, tmq, tmk, tmv, a);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+  }
   if ((parts & 2) && launch_dependent(prefill_tc_fixup_kernel, dim3(g.workers, kRowsT / kFixRowsPerCta),
                        dim3(kFixThreads), g.fixup_smem, st, a) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;
+}
+
+int launch_prefill_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf16* k_cache,
+                      const pa_bf16* v_cache, const int32_t* block_tables,
+                      const int32_t* context_lens, const int32_t* cu_seqlens_q,
+                      int64_t num_q_tokens, int causal, float scale, pa_bf16* out, float* lse,
+                      const pa_shape* sh, void* workspace, cudaStream_t st, int min_q_len,
+                      const RowsOut* rows, const int32_t* row_map, int parts, int split) {
+  TcArgs a;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.out = out;
+  a.lse = lse;
+  a.causal = causal ? 1 : 0;
+  a.split = split > 0 ? g.grid : 0;
+  a.min_lq = min_q_len;
+  if (rows) a.rows = *rows;
+  a.row_map = row_map;
+  return launch_tc(g, q, k_cache, v_cache, a, num_q_tokens, scale, sh, workspace, st, parts);
+}
+
+int launch_tree_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf16* k_cache,
+                   const pa_bf16* v_cache, const int32_t* block_tables,
+                   const int32_t* context_lens, const int32_t* cu_seqlens_q,
+                   const uint32_t* tree_mask, int mask_words, int64_t num_q_tokens, float scale,
+                   pa_bf16* out, float* lse, const pa_shape* sh, void* workspace,
+                   cudaStream_t st) {
+  TcArgs a;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.out = out;
+  a.lse = lse;
+  a.causal = 0;
+  a.split = 0;
+  a.min_lq = 1;
+  a.row_map = nullptr;
+  a.mask = tree_mask;
+  a.mask_words = mask_words;
+  a.v_cache = v_cache;
+  return launch_tc(g, q, k_cache, v_cache, a, num_q_tokens, scale, sh, workspace, st, 3);
 }
 
 unsigned take_error_word_prefill(cudaStream_t stream, int* rc) {

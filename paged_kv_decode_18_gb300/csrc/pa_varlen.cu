@@ -68,6 +68,10 @@ struct VarlenArgs {
   // `split` CTAs (overlap_split); this grid works on the other SMs' share of
   // its CTAs, the first ones launched
   int split;
+  // tree windows (pa_decode_tree): row t of the mask says which keys of its
+  // window query t sees; every earlier key is seen by all
+  const uint32_t* mask = nullptr;
+  int mask_words = 0;
 };
 
 // byte offset of (row, 16-byte chunk) inside a 16 x 128 B box written by TMA
@@ -82,7 +86,9 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   return r;
 }
 
-template <int NWARPS, int NSTAGE>
+// TREE: the window's visibility comes from a mask (a.mask), and any group size
+// up to 16 is taken (rows past QT x G of a tile are padding).
+template <int NWARPS, int NSTAGE, bool TREE>
 __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtensorMap& tmv,
                                             const VarlenArgs& a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -125,6 +131,7 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
   in.npairs_cap = a.npairs_cap;
   in.num_q_rows = a.num_q_tokens;
   in.max_lq = a.max_lq;
+  if constexpr (TREE) in.max_window = a.mask_words * 32;
   build_plan(in, P, scratch);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -219,6 +226,13 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
   float o[16][4];
   float m_r[2], l_r[2];
   int lim[2] = {0, 0}, lim_min = 0, lq = 0, ctx = 0;
+  const uint32_t* mrow[2] = {nullptr, nullptr};  // TREE: mask rows (null: padding)
+  // query token of tile row r (padding rows: past every window)
+  auto token_of = [&](int qt, int r) -> int {
+    if constexpr (TREE)
+      if (r >= QT * G) return 0x7fffffff;
+    return qt * QT + r / G;
+  };
   int piece_b0 = 0;
   bool piece_first = true;
 
@@ -245,7 +259,7 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
         const int rws[2] = {r0, r1};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int tok = cp.qt * QT + rws[i] / G;
+          const int tok = token_of(cp.qt, rws[i]);
           if (tok < lq)
             qrow[i] = reinterpret_cast<const uint32_t*>(
                 a.q + (((int64_t)P.qstart[cp.s] + tok) * Hq + (int64_t)cp.h * G + rws[i] % G) *
@@ -269,15 +283,17 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
       int lv[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int tok = cp.qt * QT + rows[i] / G;
+        const int tok = token_of(cp.qt, rows[i]);
         const bool valid = tok < lq;
+        if constexpr (TREE)
+          mrow[i] = valid ? a.mask + ((int64_t)P.qstart[cp.s] + tok) * a.mask_words : nullptr;
         lim[i] = valid ? (a.causal ? ctx - lq + tok + 1 : ctx) : 0x7fffffff;
         lv[i] = valid ? lim[i] : 0x7fffffff;
       }
       int mn = min(lv[0], lv[1]);
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) mn = min(mn, __shfl_xor_sync(kFull, mn, off));
-      lim_min = mn;
+      lim_min = TREE ? ctx - lq : mn;
       piece_b0 = cp.b;
       piece_first = (idx == R0);
     }
@@ -327,14 +343,26 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
     }
     // ---- mask, online softmax ----------------------------------------------------
     const bool need_mask = key0 + kBlock > lim_min;
+    uint32_t vis[2] = {0xffffu, 0xffffu};  // TREE: the tile's keys that each row sees
+    if constexpr (TREE) {
+      if (need_mask) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (mrow[i]) vis[i] = tree_visible32(mrow[i], a.mask_words, key0 - lim_min, ctx - key0);
+      }
+    }
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float v = s[n][e] * a.scale_log2;
         if (need_mask) {
-          const int key = key0 + n * 8 + quad * 2 + (e & 1);
-          if (key >= lim[e >> 1]) v = neg_inf();
+          if constexpr (TREE) {
+            if (!((vis[e >> 1] >> (n * 8 + quad * 2 + (e & 1))) & 1u)) v = neg_inf();
+          } else {
+            const int key = key0 + n * 8 + quad * 2 + (e & 1);
+            if (key >= lim[e >> 1]) v = neg_inf();
+          }
         }
         s[n][e] = v;
       }
@@ -369,6 +397,43 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
         o[n][1] *= alpha[0];
         o[n][2] *= alpha[1];
         o[n][3] *= alpha[1];
+      }
+    }
+    if constexpr (TREE) {
+      // a window row that only some queries see may hold an infinity or a NaN,
+      // which the product would spread to all of them (0 x NaN): such elements
+      // join the rows that see them here and enter the product as zeros
+      if (need_mask) {
+        uint32_t badk = 0u;  // keys of this tile with such an element
+        const int nk = min(kBlock, ctx - key0);
+        for (int kk = max(0, lim_min - key0); kk < nk; ++kk) {
+          const uint2 w = *reinterpret_cast<const uint2*>(
+              st + 2 * kHalfBytes + (lane >> 4) * kHalfBytes + swz(kk, (lane & 15) >> 1) +
+              (lane & 1) * 8);
+          if (__any_sync(kFull, bf2_nonfinite(w.x) || bf2_nonfinite(w.y))) badk |= 1u << kk;
+        }
+        while (badk) {
+          const int kk = __ffs(badk) - 1;
+          badk &= badk - 1;
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                st + 2 * kHalfBytes + (n >> 3) * kHalfBytes + swz(kk, n & 7) + quad * 4);
+            const uint32_t f = bf2_finite_part(w);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!((vis[i] >> kk) & 1u)) continue;
+              if ((w ^ f) & 0x7f80u) o[n][2 * i] += bf_lo(w);
+              if ((w ^ f) & 0x7f800000u) o[n][2 * i + 1] += bf_hi(w);
+            }
+          }
+          __syncwarp();
+          uint2* wp = reinterpret_cast<uint2*>(st + 2 * kHalfBytes + (lane >> 4) * kHalfBytes +
+                                               swz(kk, (lane & 15) >> 1) + (lane & 1) * 8);
+          *wp = make_uint2(bf2_finite_part(wp->x), bf2_finite_part(wp->y));
+          __syncwarp();
+          asm volatile("" ::: "memory");
+        }
       }
     }
     // ---- O += P V ----------------------------------------------------------------------
@@ -408,7 +473,7 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
       if (complete) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int tok = cp.qt * QT + rows[i] / G;
+          const int tok = token_of(cp.qt, rows[i]);
           if (tok >= lq) continue;
           const int g = rows[i] % G;
           const int64_t orow = ((int64_t)P.qstart[cp.s] + tok) * Hq + (int64_t)cp.h * G + g;
@@ -441,11 +506,11 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
   }
 }
 
-template <int NWARPS, int NSTAGE>
+template <int NWARPS, int NSTAGE, bool TREE>
 __global__ void __launch_bounds__(NWARPS * 32)
     paged_varlen_kernel(const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv, const VarlenArgs a) {
-  varlen_body<NWARPS, NSTAGE>(tmk, tmv, a);
+  varlen_body<NWARPS, NSTAGE, TREE>(tmk, tmv, a);
   // late: thread 0 of each CTA waits for the grid ahead on the way out, so
   // this grid never completes before it
   if (a.late && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -479,7 +544,7 @@ __global__ void __launch_bounds__(kFixWarps * 32)
   const int d0 = (lane & 7) * 16;
   const int q0 = cu_seqlens_q[s], lq = cu_seqlens_q[s + 1] - q0;
   const int tok = qt * QT + r / G;
-  if (tok >= lq) return;
+  if (r >= QT * G || tok >= lq) return;  // padding rows
   const int npieces = last - w + 2;  // workers w-1 .. last
   float m = neg_inf(), sum = 0.f;
   float acc[16];
@@ -543,7 +608,7 @@ struct VarlenGeometry {
 };
 
 int varlen_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len,
-                    VarlenGeometry* g) {
+                    VarlenGeometry* g, bool tree = false) {
   DeviceInfo dev;
   if (!current_device_info(&dev)) return PA_ERR_CUDA;
   const int S = sh->num_seqs;
@@ -556,7 +621,9 @@ int varlen_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len,
   const size_t plan = sizeof(int) * ((size_t)g->npairs_cap + 1 + 3 * (size_t)S + 2 + 40);
   g->smem = 1024 + (size_t)kWarps * kStages * kStageBytes + (size_t)kWarps * kStages * 8 + plan;
   if (g->smem > (size_t)dev.max_smem_optin) return PA_ERR_UNSUPPORTED;
-  const void* kern = reinterpret_cast<const void*>(paged_varlen_kernel<kWarps, kStages>);
+  const void* kern =
+      tree ? reinterpret_cast<const void*>(paged_varlen_kernel<kWarps, kStages, true>)
+           : reinterpret_cast<const void*>(paged_varlen_kernel<kWarps, kStages, false>);
   int per_sm = 0;
   if (!kernel_occupancy(kern, kWarps * 32, g->smem, &per_sm) || per_sm <= 0) return PA_ERR_CUDA;
   g->grid = dev.num_sms * per_sm;
@@ -577,6 +644,25 @@ int check_varlen_args(const pa_shape* shape, int64_t num_q_tokens, int max_q_len
   if (num_q_tokens > 0x3fffffff) return PA_ERR_ARG;
   if (shape->num_blocks * shape->num_kv_heads * kBlock > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   return PA_OK;
+}
+
+// Tree windows: any group of up to 128 query heads per KV head.
+int check_tree_args(const pa_shape* shape, int64_t num_q_tokens, int max_q_len) {
+  int rc = check_shape_common(shape);
+  if (rc != PA_OK) return rc;
+  if (shape->num_q_heads / shape->num_kv_heads > kTcRows) return PA_ERR_UNSUPPORTED;
+  if (num_q_tokens < 0 || max_q_len < 0) return PA_ERR_ARG;
+  if (num_q_tokens > 0x3fffffff) return PA_ERR_ARG;
+  if (shape->num_blocks * shape->num_kv_heads * kBlock > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+// The kernel of a tree call: the warp tile of 16 rows while a window's rows of
+// a KV head (query tokens x group) fit one such tile, so that the cache is
+// read once; else the tcgen05 tile of 128 rows.
+bool tree_on_tc(const pa_shape* shape, int max_q_len) {
+  const int G = shape->num_q_heads / shape->num_kv_heads;
+  return G > kRows || max_q_len > kRows / G;
 }
 
 }  // namespace
@@ -709,7 +795,7 @@ extern "C" int pa_decode_varlen(const pa_bf16* q, const pa_bf16* k_cache, const 
                            /*split=*/overlap ? 1 : 0);
     if (rc != PA_OK) return rc;
   }
-  if (launch_dependent(paged_varlen_kernel<kWarps, kStages>, dim3(g.grid), dim3(kWarps * 32),
+  if (launch_dependent(paged_varlen_kernel<kWarps, kStages, false>, dim3(g.grid), dim3(kWarps * 32),
                        g.smem, st, tmk, tmv, a) != cudaSuccess)
     return PA_ERR_CUDA;
   if (overlap) {
@@ -718,6 +804,99 @@ extern "C" int pa_decode_varlen(const pa_bf16* q, const pa_bf16* k_cache, const 
                            kTcMinQLen, nullptr, nullptr, /*parts=*/2, /*split=*/1);
     if (rc != PA_OK) return rc;
   }
+  if (launch_dependent(varlen_fixup_kernel, dim3(g.workers), dim3(kFixWarps * 32), 0, st,
+                       (const int*)a.desc, (const float*)a.part_o, (const float*)a.part_lse,
+                       cu_seqlens_q, g.workers, a.Hq, a.G, a.QT, (uint16_t*)out,
+                       lse) != cudaSuccess)
+    return PA_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+  return PA_OK;
+}
+
+extern "C" size_t pa_decode_tree_workspace_size(const pa_shape* shape, int64_t num_q_tokens,
+                                                int max_q_len) {
+  if (check_tree_args(shape, num_q_tokens, max_q_len) != PA_OK) return 0;
+  if (shape->num_seqs == 0 || num_q_tokens == 0 || max_q_len == 0) return 0;
+  if (tree_on_tc(shape, max_q_len)) {
+    PrefillTcGeometry tg;
+    return tree_tc_geometry(shape, num_q_tokens, max_q_len, &tg) == PA_OK ? tg.ws_bytes : 0;
+  }
+  VarlenGeometry g;
+  return varlen_geometry(shape, num_q_tokens, max_q_len, &g, true) == PA_OK ? g.ws_bytes : 0;
+}
+
+extern "C" int pa_decode_tree(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
+                              const int32_t* block_tables, const int32_t* context_lens,
+                              const int32_t* cu_seqlens_q, const uint32_t* tree_mask,
+                              int mask_words, int64_t num_q_tokens, int max_q_len, float scale,
+                              pa_bf16* out, float* lse, const pa_shape* shape, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  pa::NvtxRange nvtx_range("pa_decode_tree");
+  int rc = check_tree_args(shape, num_q_tokens, max_q_len);
+  if (rc != PA_OK) return rc;
+  if (mask_words < 0 || mask_words > (1 << 20) || max_q_len > (int64_t)mask_words * 32)
+    return PA_ERR_ARG;
+  if (shape->num_seqs == 0 || num_q_tokens == 0) return PA_OK;
+  if (max_q_len == 0) return PA_ERR_ARG;  // rows, but no window may hold one
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_seqlens_q ||
+      !tree_mask || !out)
+    return PA_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(cu_seqlens_q, 4) ||
+      !aligned(tree_mask, 4) || (lse && !aligned(lse, 4)))
+    return PA_ERR_ARG;
+  if (!(scale == scale)) return PA_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (tree_on_tc(shape, max_q_len)) {
+    PrefillTcGeometry tg;
+    rc = tree_tc_geometry(shape, num_q_tokens, max_q_len, &tg);
+    if (rc != PA_OK) return rc;
+    if (!workspace || workspace_bytes < tg.ws_bytes || !aligned(workspace, 256))
+      return PA_ERR_WORKSPACE;
+    return launch_tree_tc(tg, q, k_cache, v_cache, block_tables, context_lens, cu_seqlens_q,
+                          tree_mask, mask_words, num_q_tokens, scale, out, lse, shape, workspace,
+                          st);
+  }
+  VarlenGeometry g;
+  rc = varlen_geometry(shape, num_q_tokens, max_q_len, &g, true);
+  if (rc != PA_OK) return rc;
+  if (!workspace || workspace_bytes < g.ws_bytes || !aligned(workspace, 256))
+    return PA_ERR_WORKSPACE;
+  const int64_t rows = shape->num_blocks * shape->num_kv_heads * kBlock;
+  CUtensorMap tmk, tmv;
+  if (!make_pool_map(&tmk, k_cache, rows) || !make_pool_map(&tmv, v_cache, rows))
+    return PA_ERR_CUDA;
+  VarlenArgs a;
+  a.q = q;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.out = out;
+  a.lse = lse;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.S = shape->num_seqs;
+  a.Hq = shape->num_q_heads;
+  a.Hkv = shape->num_kv_heads;
+  a.G = a.Hq / a.Hkv;
+  a.QT = kRows / a.G;
+  a.max_blocks = shape->max_blocks_per_seq;
+  a.num_blocks = shape->num_blocks;
+  a.num_q_tokens = num_q_tokens;
+  a.causal = 0;
+  a.npairs_cap = g.npairs_cap;
+  a.num_workers = g.workers;
+  a.max_lq = 0x7fffffff;
+  a.late = 0;
+  a.split = 0;
+  a.mask = tree_mask;
+  a.mask_words = mask_words;
+  char* ws = static_cast<char*>(workspace);
+  a.desc = reinterpret_cast<int*>(ws);
+  a.part_lse = reinterpret_cast<float*>(ws + g.ws_desc);
+  a.part_o = reinterpret_cast<float*>(ws + g.ws_desc + g.ws_lse);
+  if (launch_dependent(paged_varlen_kernel<kWarps, kStages, true>, dim3(g.grid),
+                       dim3(kWarps * 32), g.smem, st, tmk, tmv, a) != cudaSuccess)
+    return PA_ERR_CUDA;
   if (launch_dependent(varlen_fixup_kernel, dim3(g.workers), dim3(kFixWarps * 32), 0, st,
                        (const int*)a.desc, (const float*)a.part_o, (const float*)a.part_lse,
                        cu_seqlens_q, g.workers, a.Hq, a.G, a.QT, (uint16_t*)out,
