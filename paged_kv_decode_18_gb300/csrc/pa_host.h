@@ -168,6 +168,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // 2-D view of one pool array: [num_blocks * Hkv * 16 rows][128] bf16, boxes of
 // 16 rows x 64 dims, 128-byte swizzle.
 bool make_pool_map(CUtensorMap* map, const void* pool, int64_t rows);
+// 3-D view of q (pa_prefill_tc.cu): boxes of QTb tokens x G heads x 64 dims.
+bool make_q_map(CUtensorMap* map, const void* q, int64_t num_q_tokens, int Hq, int G, int QTb);
 
 // ---------------------------------------------------------------------------
 // tcgen05 prefill path (pa_prefill_tc.cu): sequences with q_len >= this go
@@ -217,6 +219,7 @@ unsigned take_error_word_prefill(cudaStream_t stream, int* rc);
 unsigned take_error_word_cascade(cudaStream_t stream, int* rc);
 unsigned take_error_word_tree(cudaStream_t stream, int* rc);
 unsigned take_error_word_weights(cudaStream_t stream, int* rc);
+unsigned take_error_word_weights_tc(cudaStream_t stream, int* rc);
 unsigned take_error_word_evict(cudaStream_t stream, int* rc);
 
 }  // namespace pa

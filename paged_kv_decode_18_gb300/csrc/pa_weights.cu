@@ -14,50 +14,13 @@
 // the fragment's two k pairs of a step are neighbouring pairs of the piece.
 #include "pa_device.cuh"
 #include "pa_host.h"
+#include "pa_weights.cuh"
 
 namespace pa {
 namespace {
 
 constexpr int kWgtWarps = 8;
-
-struct WeightArgs {
-  const uint16_t* q;
-  const uint8_t* k_cache;
-  const float* lse;
-  const int32_t* block_tables;
-  const int32_t* context_lens;
-  const int32_t* cu_seqlens_q;  // null: one query per sequence
-  int64_t num_q_tokens;
-  int accumulate;
-  float scale_log2;
-  float* weights;
-  int64_t weights_len;
-  int S, Hq, Hkv, G, max_blocks;
-  int64_t num_blocks;
-};
-
-// Two one-byte codes (low 16 bits of c) as an exact bf16 pair.
-// int8: 128 + the low seven bits, less 128 or (sign bit set) 256; both are
-// bf16 bit patterns 0x43xx, and the difference, at most 8 bits, is exact.
-__device__ __forceinline__ uint32_t int8x2_to_bf16x2(uint32_t c) {
-  const uint32_t spread = __byte_perm(c, 0u, 0x4140);  // bytes c0, 0, c1, 0
-  const uint32_t hi = (spread & 0x007f007fu) | 0x43004300u;
-  const uint32_t lo = (spread & 0x00800080u) | 0x43004300u;
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(hi), "r"(lo));
-  return r;
-}
-// E4M3: the hardware's exact f16 pair, then fp32, whose upper halves are the
-// bf16 values (4 significant bits, exponents -9 .. 8: exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  float lo, hi;
-  asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}"
-      : "=f"(lo), "=f"(hi)
-      : "r"(h));
-  return (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xffff0000u);
-}
+constexpr int kWgtTcRows = 16;  // windows with more query rows a KV head go to the tcgen05 kernel
 
 // One warp's K tile as loaded: two rows per lane. bf16: four 16-byte pieces a
 // row (dims (4i + quad) * 8 ..); 8-bit: two (dims (4i + quad) * 16 ..) and the
@@ -108,10 +71,8 @@ __device__ __forceinline__ void fragments(const KTile<FMT>& t, uint32_t (&f)[8][
       } else {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          f[4 * j + u][i] = FMT == PA_KV_INT8 ? int8x2_to_bf16x2(w[u] & 0xffffu)
-                                              : e4m3x2_to_bf16x2(w[u] & 0xffffu);
-          f[4 * j + u][2 + i] = FMT == PA_KV_INT8 ? int8x2_to_bf16x2(w[u] >> 16)
-                                                  : e4m3x2_to_bf16x2(w[u] >> 16);
+          f[4 * j + u][i] = codes_to_bf16x2<FMT>(w[u] & 0xffffu);
+          f[4 * j + u][2 + i] = codes_to_bf16x2<FMT>(w[u] >> 16);
         }
       }
     }
@@ -344,6 +305,12 @@ extern "C" int pa_accumulate_weights(const pa_bf16* q, const void* k_cache, int 
   a.G = a.Hq / a.Hkv;
   a.max_blocks = shape->max_blocks_per_seq;
   a.num_blocks = shape->num_blocks;
+  if (num_q_tokens > 0 && (int64_t)max_q_len * a.G > kWgtTcRows) {
+    WeightsTcGeometry g;
+    rc = weights_tc_geometry(shape, max_q_len, kv_format, &g);
+    if (rc != PA_OK) return rc;
+    if (g.enabled) return launch_weights_tc(g, a, kv_format, static_cast<cudaStream_t>(stream));
+  }
   auto kernel = kv_format == PA_KV_BF16   ? accumulate_weights_kernel<PA_KV_BF16>
                 : kv_format == PA_KV_INT8 ? accumulate_weights_kernel<PA_KV_INT8>
                                           : accumulate_weights_kernel<PA_KV_FP8>;

@@ -1,0 +1,624 @@
+// pa_weights_tc.cu -- pa_accumulate_weights for windows of many queries on the
+// fifth-generation tensor cores (tcgen05 + tensor memory) of sm_103a.
+//
+//   w[s][h][p] (+)= sum_j sum_g exp(scale q_jg . k_p - lse_jg)
+//
+// S^T = K Q^T with the keys as the rows of the product: a thread of the
+// epilogue owns one key (one tensor-memory lane) and sums its exponentials over
+// the query columns in its own registers, with no reduction between threads
+// but one of two column halves at the end. A work item is (sequence, KV head,
+// 128 keys) with all of the window's query tiles, so a weight has one writer
+// and its sum one order. One CTA per SM, warp-specialised:
+//   warp 0     K producer: eight 16-key pool blocks a tile through the block
+//              table (bf16: 2-D TMA with the 128-byte swizzle; 8-bit: bulk
+//              copies of the raw tiles);
+//   warp 10    query tiles of 128 rows ((128/G) tokens x G heads, 3-D TMA) and
+//              their columns' log-sum-exps and causal limits;
+//   warp 1     tensor memory and, from one thread, the products: 128 keys x up
+//              to 128 columns into one of four accumulators;
+//   warps 2-9  the epilogue: two threads a key, one for the even and one for
+//              the odd groups of 32 columns;
+//   warps 11-14 (8-bit pools) turn the raw codes into a swizzled bf16 tile
+//              (exact); the row scales multiply the scores in the epilogue.
+// Bound: a 128 x 128 tile is 16 k exponentials, 1 k cycles at 16 a clock on the
+// SM's special-function units, against 32 KB of K (0.7 us of the SM's share of
+// HBM) and 0.5 k cycles of tensor time; windows of up to 128 rows are bound by
+// the K stream and the exponentials together, longer ones by the exponentials.
+#include <cudaTypedefs.h>
+
+#include "pa_device.cuh"
+#include "pa_host.h"
+#include "pa_tcgen05.cuh"
+#include "pa_weights.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kKeys = 128;                    // keys per item (MMA M)
+constexpr int kCols = 128;                    // query rows per tile (MMA N, at most)
+constexpr int kBlocksK = kKeys / kBlock;
+constexpr int kHalfB = 128 * 128;             // 64 dims of a 128-row bf16 operand
+constexpr int kOperand = 2 * kHalfB;
+constexpr int kRawTile = kBlocksK * kInt8TileBytes;  // the raw codes and scales of an item
+constexpr int kRawStages = 4;
+constexpr int kDBufs = 4;                     // accumulators in tensor memory
+constexpr int kScaleSlots = 8;                // items whose row scales are kept (see below)
+constexpr int kEpiWarps = 8;
+constexpr int kQWarp = 2 + kEpiWarps;
+constexpr int kConvWarps = 4;
+
+constexpr int kNumBarsMax = 32;
+
+template <int FMT>
+struct Lay {
+  static constexpr bool q8 = FMT != PA_KV_BF16;
+  static constexpr int kStages = q8 ? 2 : 4;  // bf16 K tiles
+  static constexpr int q = 0;                 // two query tiles
+  static constexpr int k = q + 2 * kOperand;
+  static constexpr int raw = k + kStages * kOperand;
+  static constexpr int bars = raw + (q8 ? kRawStages * kRawTile : 0);
+  static constexpr int misc = bars + kNumBarsMax * 8;  // tmem slot, abort flag
+  static constexpr int l2 = misc + 16;              // [2][128] log-sum-exp, log2 units
+  static constexpr int last = l2 + 2 * kCols * 4;   // [2][128] last key seen; -1: no query
+  static constexpr int clean = last + 2 * kCols * 4;  // [2] all 128 columns are queries
+  static constexpr int xch = clean + 16;            // [2][128] sums of the odd groups
+  static constexpr int scale = xch + 2 * kKeys * 4;  // [kScaleSlots][128] row scales
+  static constexpr int plan = scale + (q8 ? kScaleSlots * kKeys * 4 : 0);
+  static constexpr int threads = 32 * (kQWarp + 1 + (q8 ? kConvWarps : 0));
+};
+
+enum : int {
+  B_KFULL = 0, B_KEMPTY = 4, B_QFULL = 8, B_QEMPTY = 10, B_DFULL = 12, B_DEMPTY = 16,
+  B_RFULL = 20, B_REMPTY = 24, B_XFULL = 28, B_XEMPTY = 30, kNumBars = 32
+};
+
+static_assert(kNumBars <= kNumBarsMax, "barrier area");
+
+struct TcWeightArgs {
+  WeightArgs w;
+  int QTb;
+};
+
+// Per sequence, in shared memory: items and cost before it, lengths.
+struct WPlan {
+  int* cost;   // [S + 1] (query tiles + 1) summed over the items of earlier sequences
+  int* item;   // [S + 1]
+  int* ctx;    // [S]
+  int* q0;     // [S]
+  int* lq;     // [S]
+};
+
+// Query tiles that key tile kt of a window meets: those from the first token
+// that sees a key of it.
+__device__ __forceinline__ int first_tile(int kt, int c, int lq, int QTb) {
+  return max(0, kt * kKeys - (c - lq)) / QTb;
+}
+
+struct Item {
+  int s, h, i, nt;
+};
+
+__device__ __forceinline__ Item item_at(const WPlan& P, int S, int Hkv, int x) {
+  Item t;
+  t.s = upper_index(P.item, 0, S, x);
+  t.nt = (P.item[t.s + 1] - P.item[t.s]) / Hkv;
+  const int local = x - P.item[t.s];
+  t.h = local / t.nt;
+  t.i = local - t.h * t.nt;
+  return t;
+}
+__device__ __forceinline__ void next_item(const WPlan& P, int Hkv, Item& t) {
+  if (++t.i < t.nt) return;
+  t.i = 0;
+  if (++t.h < Hkv) return;
+  t.h = 0;
+  do {
+    ++t.s;
+  } while (P.item[t.s + 1] == P.item[t.s]);
+  t.nt = (P.item[t.s + 1] - P.item[t.s]) / Hkv;
+}
+// Key tiles from both ends in turn: under the causal mask of a long window an
+// early tile meets many query tiles and a late one few, so neighbours even out.
+__device__ __forceinline__ int key_tile(const Item& t) {
+  return (t.i & 1) ? t.nt - 1 - (t.i >> 1) : t.i >> 1;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(Lay<FMT>::threads, 1)
+    weights_tc_kernel(const __grid_constant__ CUtensorMap tmq,
+                      const __grid_constant__ CUtensorMap tmk, const TcWeightArgs arg) {
+  using L = Lay<FMT>;
+  const WeightArgs& a = arg.w;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t rawp = smem_addr(smem_raw);
+  unsigned char* smem = smem_raw + (((rawp + 1023u) & ~1023u) - rawp);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
+  auto bar = [&](int i) { return smem_addr(&bars[i]); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc + 4);
+  float* col_l2 = reinterpret_cast<float*>(smem + L::l2);
+  int* col_last = reinterpret_cast<int*>(smem + L::last);
+  volatile int* col_clean = reinterpret_cast<volatile int*>(smem + L::clean);
+  const int S = a.S, Hkv = a.Hkv, G = a.G, QTb = arg.QTb;
+
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(B_KFULL + i), L::q8 ? kConvWarps * 32u : 1u);
+      mbar_init(bar(B_KEMPTY + i), 1u);
+      mbar_init(bar(B_DFULL + i), 2u);  // the issuing thread and its commit
+      mbar_init(bar(B_DEMPTY + i), kEpiWarps * 32u);
+      mbar_init(bar(B_RFULL + i), 1u);
+      mbar_init(bar(B_REMPTY + i), kConvWarps * 32u);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_QFULL + i), 33u);  // warp 10's lanes and the expected bytes
+      mbar_init(bar(B_QEMPTY + i), 1u + kEpiWarps * 32u);
+      mbar_init(bar(B_XFULL + i), kEpiWarps * 16u);
+      mbar_init(bar(B_XEMPTY + i), kEpiWarps * 16u);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (tid == 32) {
+    prefetch_tensormap(&tmq);
+    if (!L::q8) prefetch_tensormap(&tmk);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- plan ---------------------------------------------------------------------
+  WPlan P;
+  P.cost = reinterpret_cast<int*>(smem + L::plan);
+  P.item = P.cost + (S + 1);
+  P.ctx = P.item + (S + 1);
+  P.q0 = P.ctx + S;
+  P.lq = P.q0 + S;
+  const int max_ctx = (int)min((int64_t)a.max_blocks * kBlock, a.weights_len);
+  for (int s = tid; s < S; s += blockDim.x) {
+    int c = a.context_lens[s];
+    if (c < 0 || c > max_ctx) {
+      flag_error(PA_DEVERR_CONTEXT_RANGE);
+      c = c < 0 ? 0 : max_ctx;
+    }
+    const int q0 = a.cu_seqlens_q ? a.cu_seqlens_q[s] : s;
+    const int lq = a.cu_seqlens_q ? a.cu_seqlens_q[s + 1] - q0 : (c > 0 ? 1 : 0);
+    const bool bad = q0 < 0 || lq < 0 || lq > c || (int64_t)q0 + lq > a.num_q_tokens;
+    if (bad && c > 0) flag_error(PA_DEVERR_QLEN_RANGE);
+    // no query: nothing to add, zeros to write
+    const int nt = bad || (lq == 0 && a.accumulate) ? 0 : (c + kKeys - 1) / kKeys;
+    const int nq = lq > 0 ? (lq + QTb - 1) / QTb : 0;
+    int cost = 0;
+    for (int kt = 0; kt < nt; ++kt)
+      cost += 1 + (nq > 1 ? nq - first_tile(kt, c, lq, QTb) : nq);
+    P.ctx[s] = c;
+    P.q0[s] = q0;
+    P.lq[s] = bad ? 0 : lq;
+    P.item[s] = Hkv * nt;
+    P.cost[s] = Hkv * cost;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int n = warp0_exclusive_scan(P.item, S);
+    if (lane == 0) P.item[S] = n;
+    const int n2 = warp0_exclusive_scan(P.cost, S);
+    if (lane == 0) P.cost[S] = n2;
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int total = P.item[S], cost_total = P.cost[S];
+  // CTA w begins at the item in which its share of the cost begins
+  auto begin_of = [&](int w) -> int {
+    if (w >= (int)gridDim.x) return total;
+    const int T = (int)((long long)w * cost_total / gridDim.x);
+    const int s = upper_index(P.cost, 0, S, T);
+    const int items = P.item[s + 1] - P.item[s], cost = P.cost[s + 1] - P.cost[s];
+    if (cost <= 0) return total;
+    return P.item[s] + (int)((long long)(T - P.cost[s]) * items / cost);
+  };
+  if (total == 0) return;
+  const int I0 = begin_of((int)blockIdx.x), I1 = begin_of((int)blockIdx.x + 1);
+  if (I0 >= I1) return;  // the whole CTA
+
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto wait = [&](int b, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (!mbar_wait_bounded(bar(b), parity)) {
+      *abort_flag = 1;
+      return false;
+    }
+    return true;
+  };
+  // Query tiles of the window: one stays for all key tiles of a head, several
+  // are loaded for each key tile again.
+  auto tiles_of = [&](const Item& t) { return (P.lq[t.s] + QTb - 1) / QTb; };
+  auto fresh_q = [&](const Item& t, int nq, int x) { return nq > 1 || t.i == 0 || x == I0; };
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- K producer
+    Item t = item_at(P, S, Hkv, I0);
+    auto blocks_of = [&](const Item& it, int kt) {
+      return min(kBlocksK, (P.ctx[it.s] + kBlock - 1) / kBlock - kt * kBlocksK);
+    };
+    auto fetch = [&](const Item& it) -> int {
+      const int kt = key_tile(it);
+      return lane < blocks_of(it, kt)
+                 ? a.block_tables[(size_t)it.s * a.max_blocks + kt * kBlocksK + lane]
+                 : 0;
+    };
+    int ids = fetch(t), n = 0;  // n: items with queries so far
+    for (int x = I0; x < I1; ++x) {
+      const Item cur = t;
+      const int nb = blocks_of(cur, key_tile(cur));
+      int id = ids;
+      if (x + 1 < I1) {
+        next_item(P, Hkv, t);
+        ids = fetch(t);
+      }
+      if (P.lq[cur.s] == 0) continue;
+      if (lane < nb && (id < 0 || (int64_t)id >= a.num_blocks)) {
+        flag_error(PA_DEVERR_BLOCK_RANGE);
+        id = 0;
+      }
+      constexpr int kRing = L::q8 ? kRawStages : L::kStages;
+      const int st = n % kRing;
+      const uint32_t full = bar((L::q8 ? B_RFULL : B_KFULL) + st);
+      if (n >= kRing &&
+          !wait((L::q8 ? B_REMPTY : B_KEMPTY) + st, (uint32_t)((n / kRing) - 1) & 1u))
+        break;
+      if (lane == 0)
+        mbar_arrive_expect_tx(full, (uint32_t)nb * (uint32_t)(L::q8 ? kInt8TileBytes : kTileBytes));
+      __syncwarp();
+      if (lane < nb) {
+        if constexpr (L::q8) {
+          bulk_copy_g2s(smem_addr(smem + L::raw + st * kRawTile + lane * kInt8TileBytes),
+                        a.k_cache + ((int64_t)id * Hkv + cur.h) * kInt8TileBytes, kInt8TileBytes,
+                        full);
+        } else {
+          const int y = (int)(((int64_t)id * Hkv + cur.h) * kBlock);
+          const uint32_t d = smem_addr(smem + L::k + st * kOperand + lane * (kBlock * 128));
+          tma_load_2d(d, &tmk, 0, y, full);
+          tma_load_2d(d + kHalfB, &tmk, 64, y, full);
+        }
+      }
+      __syncwarp();
+      ++n;
+    }
+  } else if (warp == kQWarp) {
+    // -------------------------------------------------------------- query tiles
+    Item t = item_at(P, S, Hkv, I0);
+    int qn = 0;
+    bool ok = true;
+    for (int x = I0; ok && x < I1; ++x) {
+      const int c = P.ctx[t.s], lq = P.lq[t.s], q0 = P.q0[t.s], nq = tiles_of(t);
+      if (fresh_q(t, nq, x)) {
+        for (int qt = nq > 1 ? first_tile(key_tile(t), c, lq, QTb) : 0; qt < nq; ++qt, ++qn) {
+          const int b = qn & 1;
+          if (qn >= 2 && !wait(B_QEMPTY + b, (uint32_t)((qn >> 1) - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(B_QFULL + b), (uint32_t)(QTb * G) * 256u);
+            const uint32_t d = smem_addr(smem + L::q + b * kOperand);
+            tma_load_3d(d, &tmq, 0, t.h * G, q0 + qt * QTb, bar(B_QFULL + b));
+            tma_load_3d(d + kHalfB, &tmq, 64, t.h * G, q0 + qt * QTb, bar(B_QFULL + b));
+          }
+          bool all = true;
+#pragma unroll
+          for (int i = 0; i < kCols / 32; ++i) {
+            const int col = i * 32 + lane, tok = qt * QTb + col / G;
+            float l = neg_inf();
+            if (col < QTb * G && tok < lq)
+              l = a.lse[((int64_t)q0 + tok) * a.Hq + t.h * G + col % G];
+            const bool draws = l != neg_inf();  // a query that saw nothing draws nothing
+            col_l2[b * kCols + col] = draws ? l * kLog2e : 0.f;
+            col_last[b * kCols + col] = draws ? c - lq + tok : -1;
+            all = all && draws;
+          }
+          all = __all_sync(kFull, all);
+          if (lane == 0) col_clean[b] = all;
+          __syncwarp();
+          mbar_arrive(bar(B_QFULL + b));
+        }
+      }
+      if (x + 1 < I1) next_item(P, Hkv, t);
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- products
+    if (lane == 0) {
+      Item t = item_at(P, S, Hkv, I0);
+      int n = 0, qn = 0, dn = 0;
+      bool ok = true;
+      for (int x = I0; ok && x < I1; ++x) {
+        const int c = P.ctx[t.s], lq = P.lq[t.s], nq = tiles_of(t);
+        if (lq > 0) {
+          const int st = n % L::kStages;
+          if (!wait(B_KFULL + st, (uint32_t)(n / L::kStages) & 1u)) break;
+          const bool fresh = fresh_q(t, nq, x);
+          for (int qt = nq > 1 ? first_tile(key_tile(t), c, lq, QTb) : 0; qt < nq; ++qt, ++dn) {
+            if (fresh) {
+              if (!wait(B_QFULL + (qn & 1), (uint32_t)(qn >> 1) & 1u)) {
+                ok = false;
+                break;
+              }
+              ++qn;
+            }
+            const int qb = (qn - 1) & 1, db = dn % kDBufs;
+            if (dn >= kDBufs && !wait(B_DEMPTY + db, (uint32_t)((dn / kDBufs) - 1) & 1u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const int cols = min(kCols, min(QTb, lq - qt * QTb) * G);
+            const uint32_t idesc = f16_idesc(kKeys, (cols + 15) & ~15, 0);
+            const uint32_t sQ = smem_addr(smem + L::q + qb * kOperand);
+            const uint32_t sK = smem_addr(smem + L::k + st * kOperand);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t off = (uint32_t)(k >> 2) * kHalfB + (uint32_t)(k & 3) * 32u;
+              tc_mma(tmem + (uint32_t)db * kCols, sw128_desc(sK + off, 16, 1024),
+                     sw128_desc(sQ + off, 16, 1024), idesc, k > 0);
+            }
+            tc_commit(bar(B_DFULL + db));
+            mbar_arrive(bar(B_DFULL + db));
+            // the query tile is done with after its last product
+            const bool last_use = nq > 1 || t.i == t.nt - 1 || x + 1 == I1;
+            if (last_use) tc_commit(bar(B_QEMPTY + qb));
+          }
+          tc_commit(bar(B_KEMPTY + st));
+          ++n;
+        }
+        if (x + 1 < I1) next_item(P, Hkv, t);
+      }
+    }
+    __syncwarp();
+  } else if (warp < kQWarp) {
+    // -------------------------------------------------------------- epilogue
+    const int q4 = warp & 3, hf = (warp - 2) >> 2;
+    const int r = q4 * 32 + lane;  // this thread's key (tensor-memory lane)
+    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    float* xch = reinterpret_cast<float*>(smem + L::xch);
+    const float* kscale = reinterpret_cast<const float*>(smem + L::scale);
+    Item t = item_at(P, S, Hkv, I0);
+    int n = 0, qn = 0, dn = 0;
+    bool ok = true;
+    for (int x = I0; x < I1; ++x) {
+      const int c = P.ctx[t.s], lq = P.lq[t.s], nq = tiles_of(t), kt = key_tile(t);
+      const int key = kt * kKeys + r;
+      float* dst = a.weights + ((int64_t)t.s * Hkv + t.h) * a.weights_len + key;
+      float old = 0.f;
+      if (hf == 0 && a.accumulate && key < c - lq) old = *dst;
+      float2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+      if (lq > 0) {
+        const bool fresh = fresh_q(t, nq, x);
+        for (int qt = nq > 1 ? first_tile(kt, c, lq, QTb) : 0; qt < nq; ++qt, ++dn) {
+          if (fresh) {
+            if (!wait(B_QFULL + (qn & 1), (uint32_t)(qn >> 1) & 1u)) {
+              ok = false;
+              break;
+            }
+            ++qn;
+          }
+          const int qb = (qn - 1) & 1, db = dn % kDBufs;
+          const int cols = min(kCols, min(QTb, lq - qt * QTb) * G);
+          if (!wait(B_DFULL + db, (uint32_t)(dn / kDBufs) & 1u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          uint32_t v0[32], v1[32];
+          const uint32_t ta = tmem + lane_base + (uint32_t)db * kCols + (uint32_t)hf * 32u;
+          const bool two = (hf + 2) * 32 < cols;  // uniform
+          tmem_ld32_async(ta, v0);
+          if (two) tmem_ld32_async(ta + 64u, v1);
+          tmem_wait_ld(v0);
+          if (two) tmem_tie(v1);
+          tc_fence_before();
+          mbar_arrive(bar(B_DEMPTY + db));
+          float sc = a.scale_log2;
+          if constexpr (L::q8) sc *= kscale[(n % kScaleSlots) * kKeys + r];
+          const float2 sc2 = make_float2(sc, sc);
+          // every key of the tile is seen by every column, and all are queries
+          const bool clean = col_clean[qb] && kt * kKeys + kKeys <= c - lq + qt * QTb + 1;
+          auto group = [&](const uint32_t (&v)[32], int c0) {
+            const float* l2 = col_l2 + qb * kCols + c0;
+            if (clean) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float4 l = *reinterpret_cast<const float4*>(l2 + 4 * j);
+                const float2 z0 = __ffma2_rn(
+                    make_float2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), sc2,
+                    make_float2(-l.x, -l.y));
+                const float2 z1 = __ffma2_rn(
+                    make_float2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), sc2,
+                    make_float2(-l.z, -l.w));
+                acc[(2 * j) & 3] = __fadd2_rn(acc[(2 * j) & 3], make_float2(ex2(z0.x), ex2(z0.y)));
+                acc[(2 * j + 1) & 3] =
+                    __fadd2_rn(acc[(2 * j + 1) & 3], make_float2(ex2(z1.x), ex2(z1.y)));
+              }
+            } else {
+              const int* last = col_last + qb * kCols + c0;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float2 l = *reinterpret_cast<const float2*>(l2 + 2 * j);
+                const int2 e = *reinterpret_cast<const int2*>(last + 2 * j);
+                const float z0 = fmaf(__uint_as_float(v[2 * j]), sc, -l.x);
+                const float z1 = fmaf(__uint_as_float(v[2 * j + 1]), sc, -l.y);
+                acc[j & 3].x += key <= e.x ? ex2(z0) : 0.f;
+                acc[j & 3].y += key <= e.y ? ex2(z1) : 0.f;
+              }
+            }
+          };
+          if (hf * 32 < cols) group(v0, hf * 32);
+          if (two) group(v1, hf * 32 + 64);
+          if (nq > 1 || t.i == t.nt - 1 || x + 1 == I1) mbar_arrive(bar(B_QEMPTY + qb));
+        }
+        if (!ok) break;
+      }
+      const float2 s2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+      const float sum = s2.x + s2.y;
+      // the odd groups' thread hands its sum to the even groups', which writes
+      const int i = x - I0, xb = i & 1;
+      if (hf == 1) {
+        if (i >= 2 && !wait(B_XEMPTY + xb, (uint32_t)((i >> 1) - 1) & 1u)) break;
+        xch[xb * kKeys + r] = sum;
+        mbar_arrive(bar(B_XFULL + xb));
+      } else {
+        if (!wait(B_XFULL + xb, (uint32_t)(i >> 1) & 1u)) break;
+        const float other = xch[xb * kKeys + r];
+        mbar_arrive(bar(B_XEMPTY + xb));
+        if (key < c) *dst = old + (sum + other);
+      }
+      if (lq > 0) ++n;
+      if (x + 1 < I1) next_item(P, Hkv, t);
+    }
+  } else if constexpr (L::q8) {
+    // -------------------------------------------------------------- codes to bf16
+    // thread = key row: 128 codes from the raw tile to two 128-byte swizzled
+    // halves. The chunk order is rotated by the lane, so a quarter-warp's reads
+    // fall into different banks. Row scales go to slot n mod 8: by the time
+    // slot n is written again, item n + 8's, the epilogue is at least past item
+    // n + 2 (two K stages and four accumulators lie between them).
+    const int r = tid - 32 * (kQWarp + 1);
+    float* kscale = reinterpret_cast<float*>(smem + L::scale);
+    Item t = item_at(P, S, Hkv, I0);
+    int n = 0;
+    for (int x = I0; x < I1; ++x) {
+      if (P.lq[t.s] > 0) {
+        const int rs = n % kRawStages, st = n % L::kStages;
+        if (!wait(B_RFULL + rs, (uint32_t)(n / kRawStages) & 1u)) break;
+        const unsigned char* raw =
+            smem + L::raw + rs * kRawTile + (r / kBlock) * kInt8TileBytes;
+        const bool here = r < P.ctx[t.s] - key_tile(t) * kKeys;
+        uint4 x16[8];
+        float scale = 0.f;
+        if (here) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x16[i] = *reinterpret_cast<const uint4*>(raw + (r % kBlock) * kHeadDim +
+                                                     ((i + lane) & 7) * 16);
+          scale = *reinterpret_cast<const float*>(raw + kBlock * kHeadDim + (r % kBlock) * 4);
+        }
+        mbar_arrive(bar(B_REMPTY + rs));
+        if (n >= L::kStages &&
+            !wait(B_KEMPTY + st, (uint32_t)((n / L::kStages) - 1) & 1u))
+          break;
+        kscale[(n % kScaleSlots) * kKeys + r] = scale;
+        if (here) {
+          unsigned char* row = smem + L::k + st * kOperand + r * 128;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int ch = (i + lane) & 7;  // 16 codes: dims 16 ch .. 16 ch + 15
+            const uint32_t w[4] = {x16[i].x, x16[i].y, x16[i].z, x16[i].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              o[2 * u] = codes_to_bf16x2<FMT>(w[u] & 0xffffu);
+              o[2 * u + 1] = codes_to_bf16x2<FMT>(w[u] >> 16);
+            }
+            unsigned char* half = row + (ch >> 2) * kHalfB;
+            const int c2 = (ch & 3) * 2;
+            *reinterpret_cast<uint4*>(half + ((c2 ^ (r & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(half + (((c2 + 1) ^ (r & 7)) << 4)) =
+                make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(B_KFULL + st));
+        ++n;
+      }
+      if (x + 1 < I1) next_item(P, Hkv, t);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+}
+
+template <int FMT>
+size_t smem_bytes(int S) {
+  return 1024 + (size_t)Lay<FMT>::plan + sizeof(int) * (5 * (size_t)S + 2);
+}
+
+const void* kernel_of(int fmt) {
+  return fmt == PA_KV_BF16   ? reinterpret_cast<const void*>(weights_tc_kernel<PA_KV_BF16>)
+         : fmt == PA_KV_INT8 ? reinterpret_cast<const void*>(weights_tc_kernel<PA_KV_INT8>)
+                             : reinterpret_cast<const void*>(weights_tc_kernel<PA_KV_FP8>);
+}
+
+}  // namespace
+
+int weights_tc_geometry(const pa_shape* sh, int max_q_len, int kv_format, WeightsTcGeometry* g) {
+  g->enabled = false;
+  const int G = sh->num_q_heads / sh->num_kv_heads;
+  if (G > kCols || max_q_len < 1) return PA_OK;
+  DeviceInfo dev;
+  if (!current_device_info(&dev)) return PA_ERR_CUDA;
+  g->QTb = kCols / G;
+  g->smem = kv_format == PA_KV_BF16 ? smem_bytes<PA_KV_BF16>(sh->num_seqs)
+                                    : smem_bytes<PA_KV_INT8>(sh->num_seqs);
+  if (g->smem > (size_t)dev.max_smem_optin) return PA_OK;
+  // costs are summed in 32 bits, and K's rows are 32-bit coordinates
+  const int64_t tiles = (int64_t)sh->max_blocks_per_seq / kBlocksK + 1;
+  const int64_t steps = (int64_t)(max_q_len + g->QTb - 1) / g->QTb + 1;
+  if (steps > (int64_t(1) << 30) / sh->num_seqs / sh->num_kv_heads / tiles) return PA_OK;
+  if (kv_format == PA_KV_BF16 && sh->num_blocks * sh->num_kv_heads * kBlock > 0x7fffffff)
+    return PA_OK;
+  if (!raise_smem_limit(kernel_of(kv_format))) return PA_ERR_CUDA;
+  g->grid = dev.num_sms;
+  g->enabled = true;
+  return PA_OK;
+}
+
+int launch_weights_tc(const WeightsTcGeometry& g, const WeightArgs& a, int kv_format,
+                      cudaStream_t st) {
+  CUtensorMap tmq, tmk;
+  if (!make_q_map(&tmq, a.q, a.num_q_tokens, a.Hq, a.G, g.QTb)) return PA_ERR_CUDA;
+  tmk = tmq;  // unused by the 8-bit pools
+  if (kv_format == PA_KV_BF16 &&
+      !make_pool_map(&tmk, a.k_cache, a.num_blocks * a.Hkv * kBlock))
+    return PA_ERR_CUDA;
+  TcWeightArgs t;
+  t.w = a;
+  t.QTb = g.QTb;
+  cudaError_t e;
+  if (kv_format == PA_KV_BF16)
+    e = launch_dependent(weights_tc_kernel<PA_KV_BF16>, dim3(g.grid),
+                         dim3(Lay<PA_KV_BF16>::threads), g.smem, st, tmq, tmk, t);
+  else if (kv_format == PA_KV_INT8)
+    e = launch_dependent(weights_tc_kernel<PA_KV_INT8>, dim3(g.grid),
+                         dim3(Lay<PA_KV_INT8>::threads), g.smem, st, tmq, tmk, t);
+  else
+    e = launch_dependent(weights_tc_kernel<PA_KV_FP8>, dim3(g.grid),
+                         dim3(Lay<PA_KV_FP8>::threads), g.smem, st, tmq, tmk, t);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+unsigned take_error_word_weights_tc(cudaStream_t stream, int* rc) {
+  unsigned v = 0, zero = 0;
+  if (cudaStreamSynchronize(stream) != cudaSuccess ||
+      cudaMemcpyFromSymbol(&v, g_pa_error_word, sizeof v) != cudaSuccess ||
+      cudaMemcpyToSymbol(g_pa_error_word, &zero, sizeof zero) != cudaSuccess) {
+    *rc = PA_ERR_CUDA;
+    return 0;
+  }
+  return v;
+}
+
+}  // namespace pa
