@@ -344,7 +344,7 @@ __device__ inline void build_plan(const PlanInputs& in, PlanSmem& P, int* /*scra
     } else if (in.parts <= 1) {
       P.qstart[s] = s;
       P.seq_pair[s] = s;
-      P.pair_off[s] = in.Hkv * ((c + kBlock - 1) / kBlock);
+      P.pair_off[s] = in.Hkv * ((c + in.key_tile - 1) / in.key_tile);
       if (s == S - 1) {
         P.qstart[S] = S;
         P.seq_pair[S] = S;

@@ -570,7 +570,7 @@ int weights_tc_geometry(const pa_shape* sh, int max_q_len, int kv_format, Weight
   if (G > kCols || max_q_len < 1) return PA_OK;
   DeviceInfo dev;
   if (!current_device_info(&dev)) return PA_ERR_CUDA;
-  g->QTb = kCols / G;
+  g->QTb = kCols / G < max_q_len ? kCols / G : max_q_len;
   g->smem = kv_format == PA_KV_BF16 ? smem_bytes<PA_KV_BF16>(sh->num_seqs)
                                     : smem_bytes<PA_KV_INT8>(sh->num_seqs);
   if (g->smem > (size_t)dev.max_smem_optin) return PA_OK;
