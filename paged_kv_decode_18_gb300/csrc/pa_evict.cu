@@ -4,13 +4,17 @@
 // `recent` positions stay, and of those between the ones that have drawn the
 // most weight; what stays is moved together in order, in place.
 //
-// Selection is a radix select: four passes over the weights' 32-bit keys, each
-// a 256-bin histogram of one byte among the keys that match the bytes found so
-// far, give the key of the last position that stays and how many of its equals
-// do (the lowest positions first). One ordered scan then lists the positions.
+// A cluster of CTAs serves one (sequence, KV head), each a slice of the
+// positions, read once into shared memory. Selection is a radix select: three
+// passes over the weights' 32-bit keys, each a histogram of the next 11, 11 and
+// 10 bits among the keys that match the bits found so far, summed over the
+// cluster through distributed shared memory; they give the key of the last
+// position that stays and how many of its equals do (the lowest positions
+// first). An ordered scan then lists the positions.
 // Moving: the i-th row that stays comes from a position kept[i] >= i, and kept
-// increases, so groups of rows that are read before any of them is written,
-// group after group, never read a row that is already overwritten.
+// increases. So the rows go in waves of as many as the cluster's shared memory
+// holds: all CTAs read their rows of a wave, the cluster meets, all write. A
+// wave's writes fall before every later wave's sources.
 #include "pa_device.cuh"
 #include "pa_host.h"
 #include "pa_rows.cuh"
@@ -20,7 +24,16 @@ namespace {
 
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kMoveRows = 4;  // rows a warp holds between reading and writing
+constexpr int kMaxCluster = 8;
+constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;
+constexpr int kArea = 96 * 1024;  // the slice's weights, then a wave's rows: two CTAs an SM
+constexpr int kEvictSmem = kArea + (2 * kBins + 3 * kEvictWarps + 4) * 4;
+constexpr int kSliceMax = kArea / 4;  // weights of a slice that fit; a longer one is read again
+template <bool Q8>
+constexpr int kRowBytes = Q8 ? 2 * kHeadDim : 4 * kHeadDim;  // a row's K and V (8-bit: the codes)
+// rows of a wave a CTA: data, and 16 bytes for the weight and the 8-bit scales
+template <bool Q8>
+constexpr int kWaveRows = kArea / (kRowBytes<Q8> + 16) / kEvictWarps * kEvictWarps;
 
 struct EvictArgs {
   uint8_t* k_cache;
@@ -46,15 +59,51 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of the cluster meet; what they wrote (shared and global memory)
+// is seen by all afterwards.
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The int at this CTA's shared address `p`, in CTA `rank` of the cluster.
+__device__ __forceinline__ int cluster_load(const int* p, uint32_t rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  int v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <bool Q8>
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int warp_tot[kEvictWarps];
-  __shared__ int found[2];  // digit, how many are still needed inside it
+__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs a) {
+  extern __shared__ __align__(128) unsigned char area[];
+  int(*hist)[kBins] = reinterpret_cast<int(*)[kBins]>(area + kArea);
+  int* warp_tot = hist[2];                 // [kEvictWarps]
+  int* run_tot = warp_tot + kEvictWarps;   // [2][kEvictWarps] keys above the last one, equal to it
+  int* found = run_tot + 2 * kEvictWarps;  // digit, how many are still needed inside it
+  int* counts = found + 2;                 // run_tot summed over this CTA
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int h = blockIdx.x, s = blockIdx.y;
+  const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
+  const int h = (int)blockIdx.x / ctas, s = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gtid = rank * kEvictThreads + tid, gthreads = ctas * kEvictThreads;
   const int c = a.context_lens[s];
   const int budget = a.budgets[s];
   int32_t* kept = a.kept + ((int64_t)s * a.Hkv + h) * a.max_budget;
@@ -62,39 +111,65 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
   const bool bad_ctx = c < 0 || c > max_ctx;
   const bool bad_budget = budget > a.max_budget || budget < a.sinks + a.recent;
   if (bad_ctx || bad_budget) {  // the sequence stays as it is
-    if (tid == 0 && h == 0) {
+    if (gtid == 0 && h == 0) {
       flag_error(bad_ctx ? PA_DEVERR_CONTEXT_RANGE : PA_DEVERR_BUDGET_RANGE);
       a.new_lens[s] = c;
     }
-    for (int i = tid; i < a.max_budget; i += kEvictThreads) kept[i] = -1;
+    for (int i = gtid; i < a.max_budget; i += gthreads) kept[i] = -1;
     return;
   }
   const int n = min(c, budget);
-  if (tid == 0 && h == 0) a.new_lens[s] = n;
+  if (gtid == 0 && h == 0) a.new_lens[s] = n;
   if (c <= budget) {
-    for (int i = tid; i < a.max_budget; i += kEvictThreads) kept[i] = i < c ? i : -1;
+    for (int i = gtid; i < a.max_budget; i += gthreads) kept[i] = i < c ? i : -1;
     return;
   }
   float* w = a.weights + ((int64_t)s * a.Hkv + h) * a.weights_len;
-  const int lo = a.sinks, hi = c - a.recent;  // positions to choose among
-  int need = budget - a.sinks - a.recent;     // how many of them stay, < hi - lo
-  // ---- the key of the last one that stays --------------------------------------
-  uint32_t prefix = 0u;
-  for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0;
-    __syncthreads();
-    const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int p = lo + tid; p < hi; p += kEvictThreads) {
-      const uint32_t key = weight_key(w[p]);
-      if ((key & above) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      // lane l owns bins 255 - 8l .. 248 - 8l: running counts from the top
-      int cnt[8], sum = 0;
+  // ---- this CTA's slice of the positions to choose among --------------------------
+  const int lo = a.sinks, hi = c - a.recent;
+  const int per = (hi - lo + ctas - 1) / ctas;
+  const int p0 = min(hi, lo + rank * per), p1 = min(hi, p0 + per), len = p1 - p0;
+  const bool held = per <= kSliceMax;
+  float* slice = reinterpret_cast<float*>(area);
+  if (held) {
+    for (int i = tid; i < len; i += 4 * kEvictThreads) {
+      float x[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        cnt[i] = hist[255 - lane * 8 - i];
+      for (int u = 0; u < 4; ++u)
+        if (i + u * kEvictThreads < len) x[u] = w[p0 + i + u * kEvictThreads];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + u * kEvictThreads < len) slice[i + u * kEvictThreads] = x[u];
+    }
+  }
+  auto key_of = [&](int i) { return weight_key(held ? slice[i] : w[p0 + i]); };
+  // ---- the key of the last one that stays -----------------------------------------
+  int need = budget - a.sinks - a.recent;  // how many of the middle stay, < hi - lo
+  const bool some = need > 0;
+  uint32_t prefix = 0u;
+  if (some) {
+    int shift = 32;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int bits = pass < 2 ? kDigitBits : 32 - 2 * kDigitBits, bins = 1 << bits;
+      int* hs = hist[pass & 1];
+      for (int i = tid; i < bins; i += kEvictThreads) hs[i] = 0;
+      __syncthreads();
+      const uint32_t above = shift == 32 ? 0u : 0xffffffffu << shift;
+      shift -= bits;
+      for (int i = tid; i < len; i += kEvictThreads) {
+        const uint32_t key = key_of(i);
+        if ((key & above) == prefix) atomicAdd(&hs[(key >> shift) & (uint32_t)(bins - 1)], 1);
+      }
+      cluster_meet();
+      // thread t owns bins from the top: bins - 1 - 4 t .. (bins / 512 of them)
+      const int mine = bins / kEvictThreads;  // 4, 4, 2
+      int cnt[4], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        cnt[i] = 0;
+        if (i < mine)
+          for (int r = 0; r < ctas; ++r)
+            cnt[i] += cluster_load(&hs[bins - 1 - tid * mine - i], (uint32_t)r);
         sum += cnt[i];
       }
       int x = sum;
@@ -103,71 +178,87 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
         const int y = __shfl_up_sync(kFull, x, o);
         if (lane >= o) x += y;
       }
+      if (lane == 31) warp_tot[warp] = x;
+      __syncthreads();
       int run = x - sum;  // keys in higher bins
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (run < need && run + cnt[i] >= need) {
-          found[0] = 255 - lane * 8 - i;
+      for (int i = 0; i < kEvictWarps; ++i)
+        if (i < warp) run += warp_tot[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < mine && run < need && run + cnt[i] >= need) {
+          found[0] = bins - 1 - tid * mine - i;
           found[1] = need - run;
         }
         run += cnt[i];
       }
+      __syncthreads();
+      prefix |= (uint32_t)found[0] << shift;
+      need = found[1];
     }
-    __syncthreads();
-    prefix |= (uint32_t)found[0] << shift;
-    need = found[1];
   }
-  // ---- the positions that stay, in order ---------------------------------------
-  // need: how many keys equal to prefix stay (0: nothing of the middle does)
-  const bool some = budget > a.sinks + a.recent;
-  int run_gt = 0, run_eq = 0;
-  for (int p0 = 0; p0 < c; p0 += kEvictThreads) {
-    const int p = p0 + tid;
-    int gt = 0, eq = 0;
-    if (p < c) {
-      if (p < lo || p >= hi) {
-        gt = 1;
-      } else if (some) {
-        const uint32_t key = weight_key(w[p]);
-        gt = key > prefix;
-        eq = key == prefix;
-      }
+  // ---- the positions that stay, in order ------------------------------------------
+  // need: how many keys equal to prefix stay. A warp scans a run of the slice.
+  const int wlen = (len + kEvictWarps - 1) / kEvictWarps;
+  const int i0 = min(len, warp * wlen), i1 = min(len, i0 + wlen);
+  int gt = 0, eq = 0;  // of this warp's run
+  if (some) {
+    for (int i = i0; i < i1; i += 32) {
+      const uint32_t key = i + lane < i1 ? key_of(i + lane) : 0u;
+      const bool in = i + lane < i1;
+      gt += __popc(__ballot_sync(kFull, in && key > prefix));
+      eq += __popc(__ballot_sync(kFull, in && key == prefix));
     }
-    const unsigned bg = __ballot_sync(kFull, gt), be = __ballot_sync(kFull, eq);
-    if (lane == 0) warp_tot[warp] = __popc(bg) | (__popc(be) << 16);
+  }
+  int before_gt = 0, before_eq = 0;
+  {
+    if (lane == 0) {
+      run_tot[warp] = gt;
+      run_tot[kEvictWarps + warp] = eq;
+    }
     __syncthreads();
-    int before = 0, total = 0;
-#pragma unroll
+    int tg = 0, te = 0;
     for (int i = 0; i < kEvictWarps; ++i) {
-      const int t = warp_tot[i];
-      if (i < warp) before += t;
-      total += t;
+      if (i < warp) {
+        before_gt += run_tot[i];
+        before_eq += run_tot[kEvictWarps + i];
+      }
+      tg += run_tot[i];
+      te += run_tot[kEvictWarps + i];
     }
-    __syncthreads();
-    const unsigned below = (1u << lane) - 1u;
-    const int ig = run_gt + (before & 0xffff) + __popc(bg & below);
-    const int ie = run_eq + (before >> 16) + __popc(be & below);
-    if (gt || (eq && ie < need)) kept[ig + min(ie, need)] = p;
-    run_gt += total & 0xffff;
-    run_eq += total >> 16;
-  }
-  for (int i = n + tid; i < a.max_budget; i += kEvictThreads) kept[i] = -1;
-  __syncthreads();
-  // ---- weights, then rows ---------------------------------------------------------
-  for (int i0 = 0; i0 < n; i0 += 4 * kEvictThreads) {
-    float x[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * kEvictThreads + tid;
-      if (i < n) x[u] = w[kept[i]];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * kEvictThreads + tid;
-      if (i < n) w[i] = x[u];
+    if (tid == 0) {
+      counts[0] = tg;
+      counts[1] = te;
     }
   }
+  cluster_meet();
+  for (int r = 0; r < rank; ++r) {
+    before_gt += cluster_load(&counts[0], (uint32_t)r);
+    before_eq += cluster_load(&counts[1], (uint32_t)r);
+  }
+  if (some) {
+    for (int i = i0; i < i1; i += 32) {
+      const bool in = i + lane < i1;
+      const uint32_t key = in ? key_of(i + lane) : 0u;
+      const unsigned bg = __ballot_sync(kFull, in && key > prefix);
+      const unsigned be = __ballot_sync(kFull, in && key == prefix);
+      const unsigned below = (1u << lane) - 1u;
+      const int ig = before_gt + __popc(bg & below), ie = before_eq + __popc(be & below);
+      if (((bg >> lane) & 1u) || (((be >> lane) & 1u) && ie < need))
+        kept[lo + ig + min(ie, need)] = p0 + i + lane;
+      before_gt += __popc(bg);
+      before_eq += __popc(be);
+    }
+  }
+  for (int i = gtid; i < lo; i += gthreads) kept[i] = i;
+  for (int i = gtid; i < a.recent; i += gthreads) kept[n - a.recent + i] = hi + i;
+  for (int i = n + gtid; i < a.max_budget; i += gthreads) kept[i] = -1;
+  cluster_meet();  // the list is complete, and nobody reads the weights by slices any more
+  // ---- weights and rows, wave by wave ---------------------------------------------
+  constexpr int kRows = kWaveRows<Q8>, kRow = kRowBytes<Q8>, kMine = kRows / kEvictWarps;
+  static_assert(kMine <= 32, "a lane a row");
+  unsigned char* data = area + (size_t)warp * kMine * kRow;            // this warp's rows
+  unsigned char* aux = area + (size_t)kRows * kRow + (size_t)warp * kMine * 16;
   PoolView pool;
   pool.k = a.k_cache;
   pool.v = a.v_cache;
@@ -175,29 +266,66 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
   pool.num_blocks = a.num_blocks;
   pool.Hkv = a.Hkv;
   pool.h = h;
-  for (int i0 = 0; i0 < n; i0 += kMoveRows * kEvictWarps) {
-    uint4 x[kMoveRows];
-    uint8_t* to[kMoveRows];
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      to[u] = nullptr;
-      const int i = i0 + u * kEvictWarps + warp;
-      if (i >= n) continue;
-      const int src = kept[i];
-      if (src == i) continue;
-      RowPlace from, dst;
-      const bool ok1 = pool.place(src, &from), ok2 = pool.place(i, &dst);
-      if (!ok1 || !ok2) {
-        if (lane == 0) flag_error(PA_DEVERR_BLOCK_RANGE);
-        continue;
+  for (int base = 0; base < n; base += ctas * kRows) {
+    // lane j looks up row j of the warp's: where it comes from and goes to
+    const int first = base + rank * kRows + warp * kMine;
+    const int i = first + lane;
+    RowPlace from{0, 0}, to{0, 0};
+    int src = -1;
+    if (lane < kMine && i < n) {
+      src = kept[i];
+      if (src == i) {
+        src = -1;
+      } else {
+        const bool ok1 = pool.place(src, &from), ok2 = pool.place(i, &to);
+        if (!ok1 || !ok2) {
+          flag_error(PA_DEVERR_BLOCK_RANGE);
+          src = -1;
+        }
       }
-      x[u] = load_chunk<Q8>(row_chunk<Q8>(pool, from, lane), lane);
-      to[u] = row_chunk<Q8>(pool, dst, lane);
     }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u)
-      if (to[u]) store_chunk<Q8>(to[u], lane, x[u]);
+    const unsigned moving = __ballot_sync(kFull, src >= 0);
+    for (unsigned m = moving; m; m &= m - 1) {
+      const int j = __ffs(m) - 1;
+      RowPlace f;
+      f.tile = __shfl_sync(kFull, from.tile, j);
+      f.off = __shfl_sync(kFull, from.off, j);
+      const int sp = __shfl_sync(kFull, src, j);
+      const uint32_t d = smem_addr(data + j * kRow), x = smem_addr(aux + j * 16);
+      if constexpr (Q8) {
+        if (lane < 16)
+          copy16_async(d + lane * 16, row_chunk<Q8>(pool, f, lane));
+        else if (lane < 18)
+          copy4_async(x + (lane - 16) * 4, row_chunk<Q8>(pool, f, lane));
+        else if (lane == 18)
+          copy4_async(x + 8, w + sp);
+      } else {
+        copy16_async(d + lane * 16, row_chunk<Q8>(pool, f, lane));
+        if (lane == 18) copy4_async(x + 8, w + sp);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    cluster_meet();  // every row of the wave has been read
+    for (unsigned m = moving; m; m &= m - 1) {
+      const int j = __ffs(m) - 1;
+      RowPlace t;
+      t.tile = __shfl_sync(kFull, to.tile, j);
+      t.off = __shfl_sync(kFull, to.off, j);
+      if constexpr (Q8) {
+        if (lane < 16)
+          *reinterpret_cast<uint4*>(row_chunk<Q8>(pool, t, lane)) =
+              *reinterpret_cast<const uint4*>(data + j * kRow + lane * 16);
+        else if (lane < 18)
+          *reinterpret_cast<uint32_t*>(row_chunk<Q8>(pool, t, lane)) =
+              *reinterpret_cast<const uint32_t*>(aux + j * 16 + (lane - 16) * 4);
+      } else {
+        *reinterpret_cast<uint4*>(row_chunk<Q8>(pool, t, lane)) =
+            *reinterpret_cast<const uint4*>(data + j * kRow + lane * 16);
+      }
+      if (lane == 18) w[first + j] = *reinterpret_cast<const float*>(aux + j * 16 + 8);
+    }
+    __syncwarp();  // the rows' shared memory is read before the next wave's copies
   }
 }
 
@@ -260,10 +388,21 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, int kv_format, const int32
   a.max_blocks = shape->max_blocks_per_seq;
   a.Hkv = shape->num_kv_heads;
   a.num_blocks = shape->num_blocks;
-  auto kernel = kv_format == PA_KV_BF16 ? evict_kernel<false> : evict_kernel<true>;
-  if (launch_dependent(kernel, dim3((unsigned)a.Hkv, (unsigned)shape->num_seqs),
-                       dim3(kEvictThreads), 0, static_cast<cudaStream_t>(stream),
-                       a) != cudaSuccess)
+  DeviceInfo dev;
+  if (!current_device_info(&dev)) return PA_ERR_CUDA;
+  const bool q8 = kv_format != PA_KV_BF16;
+  auto kernel = q8 ? evict_kernel<true> : evict_kernel<false>;
+  if (!raise_smem_limit(reinterpret_cast<const void*>(kernel))) return PA_ERR_CUDA;
+  // clusters as large as leave every (sequence, KV head) resident at two CTAs an
+  // SM, but no larger than a slice of 1024 positions calls for
+  const int64_t heads = (int64_t)shape->num_seqs * a.Hkv;
+  const int64_t most = (int64_t)a.max_blocks * kBlock / 1024;
+  int cluster = 1;
+  while (cluster < kMaxCluster && heads * cluster * 2 <= 2 * dev.num_sms && cluster * 2 <= most)
+    cluster *= 2;
+  if (launch_dependent_cluster(kernel, dim3((unsigned)(a.Hkv * cluster), (unsigned)shape->num_seqs),
+                               dim3(kEvictThreads), kEvictSmem, cluster,
+                               static_cast<cudaStream_t>(stream), a) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;
 }
