@@ -5,12 +5,16 @@
 // most weight; what stays is moved together in order, in place.
 //
 // A cluster of CTAs serves one (sequence, KV head), each a slice of the
-// positions, read once into shared memory. Selection is a radix select: three
-// passes over the weights' 32-bit keys, each a histogram of the next 11, 11 and
-// 10 bits among the keys that match the bits found so far, summed over the
+// positions, read once into shared memory. Selection is a radix select: four
+// passes over the weights' 32-bit keys, each a 256-bin histogram of the next
+// byte among the keys that match the bits found so far, summed over the
 // cluster through distributed shared memory; they give the key of the last
 // position that stays and how many of its equals do (the lowest positions
-// first). An ordered scan then lists the positions.
+// first). The first eight bits are a sign and an exponent, which most weights
+// share: that histogram has a column a lane, so that no two lanes of a warp add
+// to one word. (Longer digits make fewer passes, but 4096 bins read from every
+// CTA of the cluster cost more than a pass: 102 us against 54 us at 8 x 32k.)
+// An ordered scan then lists the positions.
 // Moving: the i-th row that stays comes from a position kept[i] >= i, and kept
 // increases. So the rows go in waves of as many as the cluster's shared memory
 // holds: all CTAs read their rows of a wave, the cluster meets, all write. A
@@ -25,15 +29,19 @@ namespace {
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;
-constexpr int kArea = 96 * 1024;  // the slice's weights, then a wave's rows: two CTAs an SM
-constexpr int kEvictSmem = kArea + (2 * kBins + 3 * kEvictWarps + 4) * 4;
-constexpr int kSliceMax = kArea / 4;  // weights of a slice that fit; a longer one is read again
+// Shared memory: the first pass's histogram, two of a CTA's sums, the slice's
+// weights; later a wave's rows. Two CTAs an SM.
+constexpr int kBins = 256;
+constexpr int kOffB = kBins * 32 * 4;
+constexpr int kOffSlice = kOffB + 2 * kBins * 4;
+constexpr int kArea = 112 * 1024;
+constexpr int kSliceMax = (kArea - kOffSlice) / 4;  // a longer slice is read again each time
+constexpr int kEvictSmem = kArea + (3 * kEvictWarps + 4) * 4;
 template <bool Q8>
 constexpr int kRowBytes = Q8 ? 2 * kHeadDim : 4 * kHeadDim;  // a row's K and V (8-bit: the codes)
-// rows of a wave a CTA: data, and 16 bytes for the weight and the 8-bit scales
+// rows of a wave a warp: data, and 16 bytes for the weight and the 8-bit scales
 template <bool Q8>
-constexpr int kWaveRows = kArea / (kRowBytes<Q8> + 16) / kEvictWarps * kEvictWarps;
+constexpr int kWarpRows = kArea / (kRowBytes<Q8> + 16) / kEvictWarps / 2 * 2;
 
 struct EvictArgs {
   uint8_t* k_cache;
@@ -93,8 +101,7 @@ __device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
 template <bool Q8>
 __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs a) {
   extern __shared__ __align__(128) unsigned char area[];
-  int(*hist)[kBins] = reinterpret_cast<int(*)[kBins]>(area + kArea);
-  int* warp_tot = hist[2];                 // [kEvictWarps]
+  int* warp_tot = reinterpret_cast<int*>(area + kArea);  // [kEvictWarps]
   int* run_tot = warp_tot + kEvictWarps;   // [2][kEvictWarps] keys above the last one, equal to it
   int* found = run_tot + 2 * kEvictWarps;  // digit, how many are still needed inside it
   int* counts = found + 2;                 // run_tot summed over this CTA
@@ -130,7 +137,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   const int per = (hi - lo + ctas - 1) / ctas;
   const int p0 = min(hi, lo + rank * per), p1 = min(hi, p0 + per), len = p1 - p0;
   const bool held = per <= kSliceMax;
-  float* slice = reinterpret_cast<float*>(area);
+  float* slice = reinterpret_cast<float*>(area + kOffSlice);
   if (held) {
     for (int i = tid; i < len; i += 4 * kEvictThreads) {
       float x[4];
@@ -148,30 +155,42 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   const bool some = need > 0;
   uint32_t prefix = 0u;
   if (some) {
-    int shift = 32;
-    for (int pass = 0; pass < 3; ++pass) {
-      const int bits = pass < 2 ? kDigitBits : 32 - 2 * kDigitBits, bins = 1 << bits;
-      int* hs = hist[pass & 1];
-      for (int i = tid; i < bins; i += kEvictThreads) hs[i] = 0;
-      __syncthreads();
-      const uint32_t above = shift == 32 ? 0u : 0xffffffffu << shift;
-      shift -= bits;
-      for (int i = tid; i < len; i += kEvictThreads) {
-        const uint32_t key = key_of(i);
-        if ((key & above) == prefix) atomicAdd(&hs[(key >> shift) & (uint32_t)(bins - 1)], 1);
+    // clearing and adding up the columns pays from some thousand weights on
+    const bool columns = per > 2048;
+    for (int i = (columns ? 0 : kOffB / 16) + tid; i < kOffSlice / 16; i += kEvictThreads)
+      reinterpret_cast<int4*>(area)[i] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    for (int pass = 0, shift = 24; pass < 4; ++pass, shift -= 8) {
+      int* hs = reinterpret_cast<int*>(area + kOffB) + (pass & 1) * kBins;
+      if (pass == 0 && columns) {
+        int* ha = reinterpret_cast<int*>(area);
+        for (int i = tid; i < len; i += kEvictThreads)
+          atomicAdd(&ha[(key_of(i) >> 24) * 32 + lane], 1);
+        __syncthreads();
+        // two threads a bin, sixteen columns each, beginning at their own so that
+        // a warp's reads fall into different banks
+        int sum = 0;
+        const int* col = ha + (tid >> 1) * 32 + (tid & 1) * 16;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum += col[(i + (lane >> 1)) & 15];
+        sum += __shfl_xor_sync(kFull, sum, 1);
+        if (!(tid & 1)) hs[tid >> 1] = sum;
+      } else {
+        if (pass >= 2) {  // read by the cluster two passes ago: all have met since
+          if (tid < kBins) hs[tid] = 0;
+          __syncthreads();
+        }
+        const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
+        for (int i = tid; i < len; i += kEvictThreads) {
+          const uint32_t key = key_of(i);
+          if ((key & above) == prefix) atomicAdd(&hs[(key >> shift) & 255u], 1);
+        }
       }
       cluster_meet();
-      // thread t owns bins from the top: bins - 1 - 4 t .. (bins / 512 of them)
-      const int mine = bins / kEvictThreads;  // 4, 4, 2
-      int cnt[4], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        cnt[i] = 0;
-        if (i < mine)
-          for (int r = 0; r < ctas; ++r)
-            cnt[i] += cluster_load(&hs[bins - 1 - tid * mine - i], (uint32_t)r);
-        sum += cnt[i];
-      }
+      // thread t owns bin 255 - t
+      int sum = 0;
+      if (tid < kBins)
+        for (int r = 0; r < ctas; ++r) sum += cluster_load(&hs[kBins - 1 - tid], (uint32_t)r);
       int x = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -184,13 +203,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
 #pragma unroll
       for (int i = 0; i < kEvictWarps; ++i)
         if (i < warp) run += warp_tot[i];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i < mine && run < need && run + cnt[i] >= need) {
-          found[0] = bins - 1 - tid * mine - i;
-          found[1] = need - run;
-        }
-        run += cnt[i];
+      if (run < need && run + sum >= need) {
+        found[0] = kBins - 1 - tid;
+        found[1] = need - run;
       }
       __syncthreads();
       prefix |= (uint32_t)found[0] << shift;
@@ -255,10 +270,12 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   for (int i = n + gtid; i < a.max_budget; i += gthreads) kept[i] = -1;
   cluster_meet();  // the list is complete, and nobody reads the weights by slices any more
   // ---- weights and rows, wave by wave ---------------------------------------------
-  constexpr int kRows = kWaveRows<Q8>, kRow = kRowBytes<Q8>, kMine = kRows / kEvictWarps;
+  constexpr int kMine = kWarpRows<Q8>, kRow = kRowBytes<Q8>, kRows = kMine * kEvictWarps;
   static_assert(kMine <= 32, "a lane a row");
-  unsigned char* data = area + (size_t)warp * kMine * kRow;            // this warp's rows
-  unsigned char* aux = area + (size_t)kRows * kRow + (size_t)warp * kMine * 16;
+  unsigned char* data = area + (size_t)warp * kMine * kRow;  // this warp's rows
+  const uint32_t aux = smem_addr(area + (size_t)kRows * kRow + ((size_t)warp * kMine + lane) * 16);
+  const float* auxf = reinterpret_cast<const float*>(area + (size_t)kRows * kRow) +
+                      ((size_t)warp * kMine + lane) * 4;
   PoolView pool;
   pool.k = a.k_cache;
   pool.v = a.v_cache;
@@ -266,66 +283,77 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   pool.num_blocks = a.num_blocks;
   pool.Hkv = a.Hkv;
   pool.h = h;
-  for (int base = 0; base < n; base += ctas * kRows) {
-    // lane j looks up row j of the warp's: where it comes from and goes to
-    const int first = base + rank * kRows + warp * kMine;
-    const int i = first + lane;
-    RowPlace from{0, 0}, to{0, 0};
-    int src = -1;
+  // 16-byte chunks of a row: bf16 one row of 16 + 16 (K, V), 8-bit two rows of 8 + 8
+  constexpr int kAtOnce = Q8 ? 2 : 1, kHalfChunks = Q8 ? 8 : 16;
+  const int sub = Q8 ? lane >> 4 : 0, chunk = lane & (2 * kHalfChunks - 1);
+  uint8_t* mybase = (chunk < kHalfChunks ? a.k_cache : a.v_cache) + (chunk & (kHalfChunks - 1)) * 16;
+  auto row_at = [&](const RowPlace& p) -> int64_t {  // byte offset of a row's data in K and V
+    return Q8 ? p.tile * kInt8TileBytes + p.off * kHeadDim
+              : (p.tile * kBlock + p.off) * (kHeadDim * 2);
+  };
+  // lane j looks up row j of the warp's: where it comes from and goes to (-1: stays)
+  struct Move {
+    int64_t from, to;
+    int64_t scale_from, scale_to;  // 8-bit: byte offsets of the scales
+    int src;
+  };
+  auto look_up = [&](int base) -> Move {
+    Move m{-1, -1, 0, 0, 0};
+    const int i = base + rank * kRows + warp * kMine + lane;
     if (lane < kMine && i < n) {
-      src = kept[i];
-      if (src == i) {
-        src = -1;
-      } else {
-        const bool ok1 = pool.place(src, &from), ok2 = pool.place(i, &to);
-        if (!ok1 || !ok2) {
+      m.src = kept[i];
+      RowPlace from, to;
+      if (m.src != i) {
+        const bool ok1 = pool.place(m.src, &from), ok2 = pool.place(i, &to);
+        if (ok1 && ok2) {
+          m.from = row_at(from);
+          m.to = row_at(to);
+          if (Q8) {
+            m.scale_from = from.tile * kInt8TileBytes + kBlock * kHeadDim + from.off * 4;
+            m.scale_to = to.tile * kInt8TileBytes + kBlock * kHeadDim + to.off * 4;
+          }
+        } else {
           flag_error(PA_DEVERR_BLOCK_RANGE);
-          src = -1;
         }
       }
     }
-    const unsigned moving = __ballot_sync(kFull, src >= 0);
-    for (unsigned m = moving; m; m &= m - 1) {
-      const int j = __ffs(m) - 1;
-      RowPlace f;
-      f.tile = __shfl_sync(kFull, from.tile, j);
-      f.off = __shfl_sync(kFull, from.off, j);
-      const int sp = __shfl_sync(kFull, src, j);
-      const uint32_t d = smem_addr(data + j * kRow), x = smem_addr(aux + j * 16);
-      if constexpr (Q8) {
-        if (lane < 16)
-          copy16_async(d + lane * 16, row_chunk<Q8>(pool, f, lane));
-        else if (lane < 18)
-          copy4_async(x + (lane - 16) * 4, row_chunk<Q8>(pool, f, lane));
-        else if (lane == 18)
-          copy4_async(x + 8, w + sp);
-      } else {
-        copy16_async(d + lane * 16, row_chunk<Q8>(pool, f, lane));
-        if (lane == 18) copy4_async(x + 8, w + sp);
+    return m;
+  };
+  Move mv = look_up(0);
+  for (int base = 0; base < n; base += ctas * kRows) {
+    if (mv.from >= 0) {
+      copy4_async(aux + 8, w + mv.src);
+      if (Q8) {
+        copy4_async(aux, a.k_cache + mv.scale_from);
+        copy4_async(aux + 4, a.v_cache + mv.scale_from);
       }
     }
+    const uint32_t d = smem_addr(data) + lane * 16;
+#pragma unroll
+    for (int j = 0; j < kMine; j += kAtOnce) {
+      const int64_t f = __shfl_sync(kFull, mv.from, j + sub);
+      if (f >= 0) copy16_async(d + j * kRow, mybase + f);
+    }
+    const Move next = look_up(base + ctas * kRows);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     cluster_meet();  // every row of the wave has been read
-    for (unsigned m = moving; m; m &= m - 1) {
-      const int j = __ffs(m) - 1;
-      RowPlace t;
-      t.tile = __shfl_sync(kFull, to.tile, j);
-      t.off = __shfl_sync(kFull, to.off, j);
-      if constexpr (Q8) {
-        if (lane < 16)
-          *reinterpret_cast<uint4*>(row_chunk<Q8>(pool, t, lane)) =
-              *reinterpret_cast<const uint4*>(data + j * kRow + lane * 16);
-        else if (lane < 18)
-          *reinterpret_cast<uint32_t*>(row_chunk<Q8>(pool, t, lane)) =
-              *reinterpret_cast<const uint32_t*>(aux + j * 16 + (lane - 16) * 4);
-      } else {
-        *reinterpret_cast<uint4*>(row_chunk<Q8>(pool, t, lane)) =
+#pragma unroll
+    for (int j = 0; j < kMine; j += kAtOnce) {
+      const int64_t to = __shfl_sync(kFull, mv.to, j + sub);
+      if (to >= 0)
+        *reinterpret_cast<uint4*>(mybase + to) =
             *reinterpret_cast<const uint4*>(data + j * kRow + lane * 16);
+    }
+    if (mv.from >= 0) {
+      w[base + rank * kRows + warp * kMine + lane] = auxf[2];
+      if (Q8) {
+        *reinterpret_cast<float*>(a.k_cache + mv.scale_to) = auxf[0];
+        *reinterpret_cast<float*>(a.v_cache + mv.scale_to) = auxf[1];
       }
-      if (lane == 18) w[first + j] = *reinterpret_cast<const float*>(aux + j * 16 + 8);
     }
     __syncwarp();  // the rows' shared memory is read before the next wave's copies
+    mv = next;
   }
 }
 
