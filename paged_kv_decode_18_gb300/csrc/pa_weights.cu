@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kWarpsOf<FMT> * 32, kCtasOf<FMT>)
     // nothing writes, so the blocks need no branch between them
     auto block = [&](int u, auto few) {
       uint32_t f[8][4];
-      float kscale[2] = {1.f, 1.f};
+      [[maybe_unused]] float kscale[2] = {1.f, 1.f};
       if constexpr (FMT == PA_KV_BF16) {
         // ldmatrix leaves a step's fragment in four registers in a row (taking
         // whole 16-byte pieces instead costs 32 register moves a block); the

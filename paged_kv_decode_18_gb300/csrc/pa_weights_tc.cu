@@ -5,8 +5,8 @@
 //
 // S^T = K Q^T with the keys as the rows of the product: a thread of the
 // epilogue owns one key (one tensor-memory lane) and sums its exponentials over
-// the query columns in its own registers, with no reduction between threads
-// but one of two column halves at the end. A work item is (sequence, KV head,
+// the query columns in its own registers, with no reduction between threads.
+// A work item is (sequence, KV head,
 // 128 keys) with all of the window's query tiles, so a weight has one writer
 // and its sum one order. One CTA per SM, warp-specialised:
 //   warp 0     K producer: eight 16-key pool blocks a tile through the block
@@ -14,11 +14,15 @@
 //              copies of the raw tiles);
 //   warp 10    query tiles of 128 rows ((128/G) tokens x G heads, 3-D TMA) and
 //              their columns' log-sum-exps and causal limits;
-//   warp 1     tensor memory and, from one thread, the products: 128 keys x up
-//              to 128 columns into one of four accumulators;
-//   warps 2-9  the epilogue: two threads a key, one for the even and one for
-//              the odd groups of 32 columns;
-//   warps 11-14 (8-bit pools) turn the raw codes into a swizzled bf16 tile
+//   warps 1,11 tensor memory and, from one thread each, the products: 128 keys x
+//              up to 128 columns into one of four accumulators; they take the
+//              items in turn (one thread alone spends 2,000 cycles an item on
+//              waits, issue and commits, more than anything else of it takes);
+//   warps 2-9  the epilogue: two groups of four warps that take the items in
+//              turn, so that one's exponentials hide the other's waits (two
+//              threads a key with half the columns each, who met at every
+//              item's end, took 45 us where this takes 38);
+//   warps 12-15 (8-bit pools) turn the raw codes into a swizzled bf16 tile
 //              (exact); the row scales multiply the scores in the epilogue.
 // Bound: a 128 x 128 tile is 16 k exponentials, 1 k cycles at 16 a clock on the
 // SM's special-function units, against 32 KB of K (0.7 us of the SM's share of
@@ -45,6 +49,7 @@ constexpr int kDBufs = 4;                     // accumulators in tensor memory
 constexpr int kScaleSlots = 8;                // items whose row scales are kept (see below)
 constexpr int kEpiWarps = 8;
 constexpr int kQWarp = 2 + kEpiWarps;
+constexpr int kMma2Warp = kQWarp + 1;
 constexpr int kConvWarps = 4;
 
 constexpr int kNumBarsMax = 32;
@@ -58,18 +63,17 @@ struct Lay {
   static constexpr int raw = k + kStages * kOperand;
   static constexpr int bars = raw + (q8 ? kRawStages * kRawTile : 0);
   static constexpr int misc = bars + kNumBarsMax * 8;  // tmem slot, abort flag
-  static constexpr int l2 = misc + 16;              // [2][128] log-sum-exp, log2 units
+  static constexpr int l2 = misc + 16;              // [2][128] -log-sum-exp, log2 units
   static constexpr int last = l2 + 2 * kCols * 4;   // [2][128] last key seen; -1: no query
   static constexpr int clean = last + 2 * kCols * 4;  // [2] all 128 columns are queries
-  static constexpr int xch = clean + 16;            // [2][128] sums of the odd groups
-  static constexpr int scale = xch + 2 * kKeys * 4;  // [kScaleSlots][128] row scales
+  static constexpr int scale = clean + 16;          // [kScaleSlots][128] row scales
   static constexpr int plan = scale + (q8 ? kScaleSlots * kKeys * 4 : 0);
-  static constexpr int threads = 32 * (kQWarp + 1 + (q8 ? kConvWarps : 0));
+  static constexpr int threads = 32 * (kMma2Warp + 1 + (q8 ? kConvWarps : 0));
 };
 
 enum : int {
   B_KFULL = 0, B_KEMPTY = 4, B_QFULL = 8, B_QEMPTY = 10, B_DFULL = 12, B_DEMPTY = 16,
-  B_RFULL = 20, B_REMPTY = 24, B_XFULL = 28, B_XEMPTY = 30, kNumBars = 32
+  B_RFULL = 20, B_REMPTY = 24, kNumBars = 28
 };
 
 static_assert(kNumBars <= kNumBarsMax, "barrier area");
@@ -147,15 +151,13 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
       mbar_init(bar(B_KFULL + i), L::q8 ? kConvWarps * 32u : 1u);
       mbar_init(bar(B_KEMPTY + i), 1u);
       mbar_init(bar(B_DFULL + i), 2u);  // the issuing thread and its commit
-      mbar_init(bar(B_DEMPTY + i), kEpiWarps * 32u);
+      mbar_init(bar(B_DEMPTY + i), kEpiWarps * 16u);  // the group that reads it
       mbar_init(bar(B_RFULL + i), 1u);
       mbar_init(bar(B_REMPTY + i), kConvWarps * 32u);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_QFULL + i), 33u);  // warp 10's lanes and the expected bytes
-      mbar_init(bar(B_QEMPTY + i), 1u + kEpiWarps * 32u);
-      mbar_init(bar(B_XFULL + i), kEpiWarps * 16u);
-      mbar_init(bar(B_XEMPTY + i), kEpiWarps * 16u);
+      mbar_init(bar(B_QEMPTY + i), 2u + kEpiWarps * 32u);
     }
     *abort_flag = 0;
     mbar_fence_init();
@@ -232,6 +234,7 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
   const uint32_t tmem = *tmem_slot;
 
   auto wait = [&](int b, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar(b), parity)) return true;
     if (*abort_flag) return false;
     if (!mbar_wait_bounded(bar(b), parity)) {
       *abort_flag = 1;
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
             if (col < QTb * G && tok < lq)
               l = a.lse[((int64_t)q0 + tok) * a.Hq + t.h * G + col % G];
             const bool draws = l != neg_inf();  // a query that saw nothing draws nothing
-            col_l2[b * kCols + col] = draws ? l * kLog2e : 0.f;
+            col_l2[b * kCols + col] = draws ? -(l * kLog2e) : 0.f;
             col_last[b * kCols + col] = draws ? c - lq + tok : -1;
             all = all && draws;
           }
@@ -334,18 +337,35 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
       }
       if (x + 1 < I1) next_item(P, Hkv, t);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == kMma2Warp) {
     // -------------------------------------------------------------- products
     if (lane == 0) {
+      const int me = warp == 1 ? 0 : 1;
+      // one thread issues for the whole CTA: what does not change within a
+      // sequence or at all is kept out of its loop (built anew for each item it
+      // cost 1,700 cycles, more than the item's exponentials)
+      const uint64_t desc_q = sw128_desc(smem_addr(smem + L::q), 16, 1024);
+      const uint64_t desc_k = sw128_desc(smem_addr(smem + L::k), 16, 1024);
       Item t = item_at(P, S, Hkv, I0);
-      int n = 0, qn = 0, dn = 0;
-      bool ok = true;
+      int n = 0, qn = 0, dn = 0, c = 0, lq = 0, nq = 0;
+      uint32_t idesc_last = 0;  // of the window's last tile
+      bool ok = true, begun = false;
       for (int x = I0; ok && x < I1; ++x) {
-        const int c = P.ctx[t.s], lq = P.lq[t.s], nq = tiles_of(t);
+        if (!begun || t.i == 0) {
+          begun = true;
+          c = P.ctx[t.s];
+          lq = P.lq[t.s];
+          nq = tiles_of(t);
+          const int cols = min(kCols, (lq - (nq - 1) * QTb) * G);
+          idesc_last = f16_idesc(kKeys, (cols + 15) & ~15, 0);
+        }
         if (lq > 0) {
           const int st = n % L::kStages;
-          if (!wait(B_KFULL + st, (uint32_t)(n / L::kStages) & 1u)) break;
+          const bool mine = (n & 1) == me;
+          if (mine && !wait(B_KFULL + st, (uint32_t)(n / L::kStages) & 1u)) break;
           const bool fresh = fresh_q(t, nq, x);
+          const bool last_use = nq > 1 || t.i == t.nt - 1 || x + 1 == I1;
+          const uint64_t dk = desc_k + (uint64_t)(st * (kOperand >> 4));
           for (int qt = nq > 1 ? first_tile(key_tile(t), c, lq, QTb) : 0; qt < nq; ++qt, ++dn) {
             if (fresh) {
               if (!wait(B_QFULL + (qn & 1), (uint32_t)(qn >> 1) & 1u)) {
@@ -355,54 +375,65 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
               ++qn;
             }
             const int qb = (qn - 1) & 1, db = dn % kDBufs;
+            if (!mine) {  // the other's; this one's products with the tile come first
+              if (last_use) tc_commit(bar(B_QEMPTY + qb));
+              continue;
+            }
             if (dn >= kDBufs && !wait(B_DEMPTY + db, (uint32_t)((dn / kDBufs) - 1) & 1u)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const int cols = min(kCols, min(QTb, lq - qt * QTb) * G);
-            const uint32_t idesc = f16_idesc(kKeys, (cols + 15) & ~15, 0);
-            const uint32_t sQ = smem_addr(smem + L::q + qb * kOperand);
-            const uint32_t sK = smem_addr(smem + L::k + st * kOperand);
+            const uint32_t idesc =
+                qt == nq - 1 ? idesc_last : f16_idesc(kKeys, (QTb * G + 15) & ~15, 0);
+            const uint64_t dq = desc_q + (uint64_t)(qb * (kOperand >> 4));
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const uint32_t off = (uint32_t)(k >> 2) * kHalfB + (uint32_t)(k & 3) * 32u;
-              tc_mma(tmem + (uint32_t)db * kCols, sw128_desc(sK + off, 16, 1024),
-                     sw128_desc(sQ + off, 16, 1024), idesc, k > 0);
+              const uint64_t off = (uint64_t)((k >> 2) * kHalfB + (k & 3) * 32) >> 4;
+              tc_mma(tmem + (uint32_t)db * kCols, dk + off, dq + off, idesc, k > 0);
             }
             tc_commit(bar(B_DFULL + db));
             mbar_arrive(bar(B_DFULL + db));
             // the query tile is done with after its last product
-            const bool last_use = nq > 1 || t.i == t.nt - 1 || x + 1 == I1;
             if (last_use) tc_commit(bar(B_QEMPTY + qb));
           }
-          tc_commit(bar(B_KEMPTY + st));
+          if (mine) tc_commit(bar(B_KEMPTY + st));
           ++n;
         }
         if (x + 1 < I1) next_item(P, Hkv, t);
       }
     }
     __syncwarp();
-  } else if (warp < kQWarp) {
+  } else if (warp < kQWarp) {  // warps 2 .. 9
     // -------------------------------------------------------------- epilogue
-    const int q4 = warp & 3, hf = (warp - 2) >> 2;
+    const int q4 = warp & 3, group = (warp - 2) >> 2;
     const int r = q4 * 32 + lane;  // this thread's key (tensor-memory lane)
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
-    float* xch = reinterpret_cast<float*>(smem + L::xch);
     const float* kscale = reinterpret_cast<const float*>(smem + L::scale);
     Item t = item_at(P, S, Hkv, I0);
     int n = 0, qn = 0, dn = 0;
-    bool ok = true;
-    for (int x = I0; x < I1; ++x) {
-      const int c = P.ctx[t.s], lq = P.lq[t.s], nq = tiles_of(t), kt = key_tile(t);
-      const int key = kt * kKeys + r;
-      float* dst = a.weights + ((int64_t)t.s * Hkv + t.h) * a.weights_len + key;
+    int c = 0, lq = 0, nq = 0;
+    float* row = nullptr;  // weights of the item's sequence and head
+    bool ok = true, begun = false;
+    for (int x = I0; ok && x < I1; ++x) {
+      if (!begun || t.i == 0) {
+        begun = true;
+        c = P.ctx[t.s];
+        lq = P.lq[t.s];
+        nq = tiles_of(t);
+        row = a.weights + ((int64_t)t.s * Hkv + t.h) * a.weights_len;
+      }
+      const int kt = key_tile(t), key = kt * kKeys + r;
+      const int mine = lq > 0 ? n & 1 : 0;  // the group that this item falls to
       float old = 0.f;
-      if (hf == 0 && a.accumulate && key < c - lq) old = *dst;
+      if (mine == group && a.accumulate && key < c - lq) old = row[key];
       float2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
       if (lq > 0) {
         const bool fresh = fresh_q(t, nq, x);
+        const bool last_use = nq > 1 || t.i == t.nt - 1 || x + 1 == I1;
         for (int qt = nq > 1 ? first_tile(kt, c, lq, QTb) : 0; qt < nq; ++qt, ++dn) {
+          // both groups wait for a new query tile and release it, so that neither
+          // runs a tile ahead
           if (fresh) {
             if (!wait(B_QFULL + (qn & 1), (uint32_t)(qn >> 1) & 1u)) {
               ok = false;
@@ -411,76 +442,79 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
             ++qn;
           }
           const int qb = (qn - 1) & 1, db = dn % kDBufs;
-          const int cols = min(kCols, min(QTb, lq - qt * QTb) * G);
-          if (!wait(B_DFULL + db, (uint32_t)(dn / kDBufs) & 1u)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          uint32_t v0[32], v1[32];
-          const uint32_t ta = tmem + lane_base + (uint32_t)db * kCols + (uint32_t)hf * 32u;
-          const bool two = (hf + 2) * 32 < cols;  // uniform
-          tmem_ld32_async(ta, v0);
-          if (two) tmem_ld32_async(ta + 64u, v1);
-          tmem_wait_ld(v0);
-          if (two) tmem_tie(v1);
-          tc_fence_before();
-          mbar_arrive(bar(B_DEMPTY + db));
-          float sc = a.scale_log2;
-          if constexpr (L::q8) sc *= kscale[(n % kScaleSlots) * kKeys + r];
-          const float2 sc2 = make_float2(sc, sc);
-          // every key of the tile is seen by every column, and all are queries
-          const bool clean = col_clean[qb] && kt * kKeys + kKeys <= c - lq + qt * QTb + 1;
-          auto group = [&](const uint32_t (&v)[32], int c0) {
-            const float* l2 = col_l2 + qb * kCols + c0;
-            if (clean) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float4 l = *reinterpret_cast<const float4*>(l2 + 4 * j);
-                const float2 z0 = __ffma2_rn(
-                    make_float2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), sc2,
-                    make_float2(-l.x, -l.y));
-                const float2 z1 = __ffma2_rn(
-                    make_float2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), sc2,
-                    make_float2(-l.z, -l.w));
-                acc[(2 * j) & 3] = __fadd2_rn(acc[(2 * j) & 3], make_float2(ex2(z0.x), ex2(z0.y)));
-                acc[(2 * j + 1) & 3] =
-                    __fadd2_rn(acc[(2 * j + 1) & 3], make_float2(ex2(z1.x), ex2(z1.y)));
-              }
-            } else {
-              const int* last = col_last + qb * kCols + c0;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float2 l = *reinterpret_cast<const float2*>(l2 + 2 * j);
-                const int2 e = *reinterpret_cast<const int2*>(last + 2 * j);
-                const float z0 = fmaf(__uint_as_float(v[2 * j]), sc, -l.x);
-                const float z1 = fmaf(__uint_as_float(v[2 * j + 1]), sc, -l.y);
-                acc[j & 3].x += key <= e.x ? ex2(z0) : 0.f;
-                acc[j & 3].y += key <= e.y ? ex2(z1) : 0.f;
-              }
+          if (mine == group) {
+            const int cols = min(kCols, min(QTb, lq - qt * QTb) * G);
+            if (!wait(B_DFULL + db, (uint32_t)(dn / kDBufs) & 1u)) {
+              ok = false;
+              break;
             }
-          };
-          if (hf * 32 < cols) group(v0, hf * 32);
-          if (two) group(v1, hf * 32 + 64);
-          if (nq > 1 || t.i == t.nt - 1 || x + 1 == I1) mbar_arrive(bar(B_QEMPTY + qb));
+            tc_fence_after();
+            float sc = a.scale_log2;
+            if constexpr (L::q8) sc *= kscale[(n % kScaleSlots) * kKeys + r];
+            const float2 sc2 = make_float2(sc, sc);
+            const uint32_t ta = tmem + lane_base + (uint32_t)db * kCols;
+            // every key of the tile is seen by every column, and all are queries
+            const bool clean = col_clean[qb] && kt * kKeys + kKeys <= c - lq + qt * QTb + 1;
+            auto columns = [&](const uint32_t (&v)[32], int c0) {
+              const float* l2 = col_l2 + qb * kCols + c0;
+              if (clean) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const float4 l = *reinterpret_cast<const float4*>(l2 + 4 * j);
+                  const float2 z0 = __ffma2_rn(
+                      make_float2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), sc2,
+                      make_float2(l.x, l.y));
+                  const float2 z1 = __ffma2_rn(
+                      make_float2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])),
+                      sc2, make_float2(l.z, l.w));
+                  acc[(2 * j) & 3] =
+                      __fadd2_rn(acc[(2 * j) & 3], make_float2(ex2(z0.x), ex2(z0.y)));
+                  acc[(2 * j + 1) & 3] =
+                      __fadd2_rn(acc[(2 * j + 1) & 3], make_float2(ex2(z1.x), ex2(z1.y)));
+                }
+              } else {
+                const int* last = col_last + qb * kCols + c0;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float2 l = *reinterpret_cast<const float2*>(l2 + 2 * j);
+                  const int2 e = *reinterpret_cast<const int2*>(last + 2 * j);
+                  const float z0 = fmaf(__uint_as_float(v[2 * j]), sc, l.x);
+                  const float z1 = fmaf(__uint_as_float(v[2 * j + 1]), sc, l.y);
+                  acc[j & 3] = __fadd2_rn(acc[j & 3], make_float2(ex2(key <= e.x ? z0 : neg_inf()),
+                                                                  ex2(key <= e.y ? z1 : neg_inf())));
+                }
+              }
+            };
+            // 32 columns at a time, the next ones on their way
+            uint32_t v0[32], v1[32];
+            tmem_ld32_async(ta, v0);
+            tmem_wait_ld(v0);
+            if (cols > 32) tmem_ld32_async(ta + 32u, v1);
+            columns(v0, 0);
+            if (cols > 32) {
+              tmem_wait_ld(v1);
+              if (cols > 64) tmem_ld32_async(ta + 64u, v0);
+              columns(v1, 32);
+            }
+            if (cols > 64) {
+              tmem_wait_ld(v0);
+              if (cols > 96) tmem_ld32_async(ta + 96u, v1);
+              columns(v0, 64);
+            }
+            if (cols > 96) tmem_wait_ld(v1);
+            tc_fence_before();
+            mbar_arrive(bar(B_DEMPTY + db));
+            if (cols > 96) columns(v1, 96);
+          }
+          if (last_use) mbar_arrive(bar(B_QEMPTY + qb));
         }
         if (!ok) break;
+        ++n;
       }
-      const float2 s2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-      const float sum = s2.x + s2.y;
-      // the odd groups' thread hands its sum to the even groups', which writes
-      const int i = x - I0, xb = i & 1;
-      if (hf == 1) {
-        if (i >= 2 && !wait(B_XEMPTY + xb, (uint32_t)((i >> 1) - 1) & 1u)) break;
-        xch[xb * kKeys + r] = sum;
-        mbar_arrive(bar(B_XFULL + xb));
-      } else {
-        if (!wait(B_XFULL + xb, (uint32_t)(i >> 1) & 1u)) break;
-        const float other = xch[xb * kKeys + r];
-        mbar_arrive(bar(B_XEMPTY + xb));
-        if (key < c) *dst = old + (sum + other);
+      if (mine == group && key < c) {
+        const float2 s2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+        row[key] = old + (s2.x + s2.y);
       }
-      if (lq > 0) ++n;
       if (x + 1 < I1) next_item(P, Hkv, t);
     }
   } else if constexpr (L::q8) {
@@ -488,9 +522,10 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
     // thread = key row: 128 codes from the raw tile to two 128-byte swizzled
     // halves. The chunk order is rotated by the lane, so a quarter-warp's reads
     // fall into different banks. Row scales go to slot n mod 8: by the time
-    // slot n is written again, item n + 8's, the epilogue is at least past item
-    // n + 2 (two K stages and four accumulators lie between them).
-    const int r = tid - 32 * (kQWarp + 1);
+    // slot n is written again, item n + 8's, the accumulator of item n + 2 has been
+    // read (two K stages and four accumulators lie between), by the group that
+    // took item n before it.
+    const int r = tid - 32 * (kMma2Warp + 1);
     float* kscale = reinterpret_cast<float*>(smem + L::scale);
     Item t = item_at(P, S, Hkv, I0);
     int n = 0;
