@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   const uint32_t tmem = *tmem_slot;
 
   auto wait = [&](int b, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar(b), parity)) return true;
     if (*abort_flag) return false;
     if (!mbar_wait_bounded(bar(b), parity)) {
       *abort_flag = 1;
@@ -301,6 +302,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const uint32_t idS = f16_idesc(kRowsT, kKeysT, 0);
       const uint32_t idPV = f16_idesc(kRowsT, 128, 1);
       int qn = 0, qs = 0;  // query tiles seen; buffer of the current one
+      // operand descriptors differ by their address alone (16-byte units)
+      const uint64_t desc_q = sw128_desc(smem_addr(smem + kOffQ), 16, 1024);
+      const uint64_t desc_k = sw128_desc(smem_addr(smem + kOffKV), 16, 1024);
+      const uint64_t desc_v = sw128_desc(smem_addr(smem + kOffKV + kOpBytes), kHalfT, 1024);
       auto issue_S = [&](int i, bool first) -> bool {
         if (first) {
           qs = qn & 1;
@@ -312,13 +317,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         // the S/P buffer is free once the PV that read P of tile i-2 is done
         if (i >= 2 && !wait(B_SFREE + st, (uint32_t)((i >> 1) - 1) & 1u)) return false;
         tc_fence_after();
-        const uint32_t sQ = smem_addr(smem + kOffQ + qs * kOpBytes);
-        const uint32_t sK = smem_addr(smem + kOffKV + st * 2 * kOpBytes);
+        const uint64_t dq = desc_q + (uint64_t)(qs * (kOpBytes >> 4));
+        const uint64_t dk = desc_k + (uint64_t)(st * (2 * kOpBytes >> 4));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {  // head_dim 128 = 8 steps of 16
-          const uint32_t off = (uint32_t)(k >> 2) * kHalfT + (uint32_t)(k & 3) * 32u;
-          tc_mma(tmem + (uint32_t)st * 128u, sw128_desc(sQ + off, 16, 1024),
-                 sw128_desc(sK + off, 16, 1024), idS, k > 0);
+          const uint64_t off = (uint64_t)((k >> 2) * kHalfT + (k & 3) * 32) >> 4;
+          tc_mma(tmem + (uint32_t)st * 128u, dq + off, dk + off, idS, k > 0);
         }
         tc_commit(bar(B_SFULL + st));
         tc_commit(bar(B_KEMPTY + st));
@@ -329,9 +333,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       if (ok && (R0 + 1 >= R1 || t.b == t.nt - 1)) tc_commit(bar(B_QEMPTY + qs));
       for (int idx = R0, i = 0; ok && idx < R1; ++idx, ++i) {
         const bool first = (idx == R0) || (t.b == 0);
+        TilePos tn = t;
         if (idx + 1 < R1) {
           // the next tile's S first: the tensor core computes it during softmax
-          TilePos tn = t;
           advance(P, S, Hkv, tn);
           if (!issue_S(i + 1, tn.b == 0)) {
             ok = false;
@@ -345,7 +349,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t sV = smem_addr(smem + kOffKV + st * 2 * kOpBytes + kOpBytes);
+        const uint64_t dv = desc_v + (uint64_t)(st * (2 * kOpBytes >> 4));
         // O_hf += P[:, keys of half hf] V[keys of half hf, :]: one accumulator per
         // key half; P (bf16 pairs) sits in columns st*128 + hf*64 .. +31 of TMEM
 #pragma unroll
@@ -354,12 +358,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           for (int k = 0; k < 4; ++k)
             tc_mma_ts(tmem + kColO + (uint32_t)hf * 128u,
                       tmem + (uint32_t)st * 128u + (uint32_t)hf * 64u + (uint32_t)k * 8u,
-                      sw128_desc(sV + (uint32_t)(hf * 4 + k) * 2048u, kHalfT, 1024), idPV,
+                      dv + (uint64_t)((hf * 4 + k) * (2048 >> 4)), idPV,
                       (k > 0 || !first) ? 1u : 0u);
         tc_commit(bar(B_VEMPTY + st));
         tc_commit(bar(B_SFREE + st));
         tc_commit(bar(B_ODONE));
-        if (idx + 1 < R1) advance(P, S, Hkv, t);
+        t = tn;
       }
     }
     __syncwarp();
