@@ -190,6 +190,12 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // 2-D view of one pool array: [num_blocks * Hkv * 16 rows][128] bf16, boxes of
 // 16 rows x 64 dims, 128-byte swizzle.
 bool make_pool_map(CUtensorMap* map, const void* pool, int64_t rows);
+// The same rows as [groups of 8 rows][64-dim halves][8 rows][64 dims], boxes of
+// one 16-row tile: a single copy lands the whole tile as four 1 KB swizzle atoms,
+// (group, half) = (0,0) (0,1) (1,0) (1,1), so that 8-row groups follow one
+// another every 2 KB in a tile and from tile to tile. (Two 2 KB boxes a tile, the
+// map above, held the tcgen05 kernels to 44 GB/s an SM.)
+bool make_block_map(CUtensorMap* map, const void* pool, int64_t rows);
 // 3-D view of q (pa_prefill_tc.cu): boxes of QTb tokens x G heads x 64 dims.
 bool make_q_map(CUtensorMap* map, const void* q, int64_t num_q_tokens, int Hq, int G, int QTb);
 

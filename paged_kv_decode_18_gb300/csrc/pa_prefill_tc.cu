@@ -14,8 +14,8 @@
 // tensor memory. One CTA per SM, warp-specialised (11 warps):
 //   warp 0    TMA producer for the query tiles (3-D tensor map over q; two
 //             buffers, so the next piece's tile lands early) and for K, as
-//             eight 16-key pool blocks per 128-key tile found through the
-//             block table (ids fetched one tile ahead);
+//             eight 16-key pool blocks per 128-key tile, one copy each, found
+//             through the block table (ids fetched one tile ahead);
 //   warp 10   TMA producer for V; K and V stages have their own full/empty
 //             mbarriers, so a K stage refills as soon as its S is done;
 //   warp 1    allocates 512 TMEM columns and, from one thread, issues the
@@ -282,17 +282,14 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         if (is_k) flag_error(PA_DEVERR_BLOCK_RANGE);
         my_id = 0;
       }
-      const int y = (int)(((int64_t)my_id * Hkv + t.h) * kBlock);
+      const int group = (int)(((int64_t)my_id * Hkv + t.h) * (kBlock / 8));
       // the stage is free once the S (K) or the PV (V) of tile i-2 is done
       if (i >= 2 && !wait(b_empty + st, (uint32_t)((i >> 1) - 1) & 1u)) break;
       if (lane == 0) mbar_arrive_expect_tx(bar(b_full + st), (uint32_t)nb * (uint32_t)kTileBytes);
       __syncwarp();
       const uint32_t d = smem_addr(smem + kOffKV + st * 2 * kOpBytes + (is_k ? 0 : kOpBytes) +
-                                   lane * (kBlock * 128));
-      if (lane < nb) {
-        tma_load_2d(d, map, 0, y, bar(b_full + st));
-        tma_load_2d(d + kHalfT, map, 64, y, bar(b_full + st));
-      }
+                                   lane * kTileBytes);
+      if (lane < nb) tma_load_block(d, map, group, bar(b_full + st));
       __syncwarp();
       if (idx + 1 < R1) advance(P, S, Hkv, t);
     }
@@ -304,8 +301,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       int qn = 0, qs = 0;  // query tiles seen; buffer of the current one
       // operand descriptors differ by their address alone (16-byte units)
       const uint64_t desc_q = sw128_desc(smem_addr(smem + kOffQ), 16, 1024);
-      const uint64_t desc_k = sw128_desc(smem_addr(smem + kOffKV), 16, 1024);
-      const uint64_t desc_v = sw128_desc(smem_addr(smem + kOffKV + kOpBytes), kHalfT, 1024);
+      // K and V: 8-row groups every 2 KB, each the two 64-dim halves' 1 KB atoms
+      const uint64_t desc_k = sw128_desc(smem_addr(smem + kOffKV), 16, 2048);
+      const uint64_t desc_v = sw128_desc(smem_addr(smem + kOffKV + kOpBytes), 1024, 2048);
       auto issue_S = [&](int i, bool first) -> bool {
         if (first) {
           qs = qn & 1;
@@ -321,8 +319,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const uint64_t dk = desc_k + (uint64_t)(st * (2 * kOpBytes >> 4));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {  // head_dim 128 = 8 steps of 16
-          const uint64_t off = (uint64_t)((k >> 2) * kHalfT + (k & 3) * 32) >> 4;
-          tc_mma(tmem + (uint32_t)st * 128u, dq + off, dk + off, idS, k > 0);
+          tc_mma(tmem + (uint32_t)st * 128u, dq + (uint64_t)(((k >> 2) * kHalfT + (k & 3) * 32) >> 4),
+                 dk + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4), idS, k > 0);
         }
         tc_commit(bar(B_SFULL + st));
         tc_commit(bar(B_KEMPTY + st));
@@ -358,7 +356,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           for (int k = 0; k < 4; ++k)
             tc_mma_ts(tmem + kColO + (uint32_t)hf * 128u,
                       tmem + (uint32_t)st * 128u + (uint32_t)hf * 64u + (uint32_t)k * 8u,
-                      dv + (uint64_t)((hf * 4 + k) * (2048 >> 4)), idPV,
+                      dv + (uint64_t)((hf * 4 + k) * (4096 >> 4)), idPV,
                       (k > 0 || !first) ? 1u : 0u);
         tc_commit(bar(B_VEMPTY + st));
         tc_commit(bar(B_SFREE + st));
@@ -609,7 +607,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const int vsafe = TREE ? c - lq : c;  // rows before it enter the product as they are
       if (key0 + kKeysT > vsafe && key0 + r >= vsafe) {
         if (!wait(B_VFULL + sb, (uint32_t)(i >> 1) & 1u)) break;
-        unsigned char* vrow = smem + kOffKV + sb * 2 * kOpBytes + kOpBytes + hf * kHalfT + r * 128;
+        unsigned char* vrow = smem + kOffKV + sb * 2 * kOpBytes + kOpBytes + (r >> 3) * 2048 +
+                              hf * 1024 + (r & 7) * 128;
         bool write = true;
         if constexpr (TREE) {
           if (key0 + r < c) {  // a window row: only its infinities and NaNs are left out
@@ -856,7 +855,7 @@ static int launch_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf16
   CUtensorMap tmq, tmk, tmv;
   const int64_t pool_rows = sh->num_blocks * sh->num_kv_heads * kBlock;
   if (!make_q_map(&tmq, q, num_q_tokens, sh->num_q_heads, G, g.QTb) ||
-      !make_pool_map(&tmk, k_cache, pool_rows) || !make_pool_map(&tmv, v_cache, pool_rows))
+      !make_block_map(&tmk, k_cache, pool_rows) || !make_block_map(&tmv, v_cache, pool_rows))
     return PA_ERR_CUDA;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.S = sh->num_seqs;

@@ -10,7 +10,7 @@
 // 128 keys) with all of the window's query tiles, so a weight has one writer
 // and its sum one order. One CTA per SM, warp-specialised:
 //   warp 0     K producer: eight 16-key pool blocks a tile through the block
-//              table (bf16: 2-D TMA with the 128-byte swizzle; 8-bit: bulk
+//              table (bf16: 4-D TMA with the 128-byte swizzle; 8-bit: bulk
 //              copies of the raw tiles);
 //   warp 10    query tiles of 128 rows ((128/G) tokens x G heads, 3-D TMA) and
 //              their columns' log-sum-exps and causal limits;
@@ -288,10 +288,9 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
                         a.k_cache + ((int64_t)id * Hkv + cur.h) * kInt8TileBytes, kInt8TileBytes,
                         full);
         } else {
-          const int y = (int)(((int64_t)id * Hkv + cur.h) * kBlock);
-          const uint32_t d = smem_addr(smem + L::k + st * kOperand + lane * (kBlock * 128));
-          tma_load_2d(d, &tmk, 0, y, full);
-          tma_load_2d(d + kHalfB, &tmk, 64, y, full);
+          const int group = (int)(((int64_t)id * Hkv + cur.h) * (kBlock / 8));
+          tma_load_block(smem_addr(smem + L::k + st * kOperand + lane * kTileBytes), &tmk, group,
+                         full);
         }
       }
       __syncwarp();
@@ -345,7 +344,8 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
       // sequence or at all is kept out of its loop (built anew for each item it
       // cost 1,700 cycles, more than the item's exponentials)
       const uint64_t desc_q = sw128_desc(smem_addr(smem + L::q), 16, 1024);
-      const uint64_t desc_k = sw128_desc(smem_addr(smem + L::k), 16, 1024);
+      // K: 8-row groups every 2 KB, each the two halves' 1 KB atoms
+      const uint64_t desc_k = sw128_desc(smem_addr(smem + L::k), 16, 2048);
       Item t = item_at(P, S, Hkv, I0);
       int n = 0, qn = 0, dn = 0, c = 0, lq = 0, nq = 0;
       uint32_t idesc_last = 0;  // of the window's last tile
@@ -389,8 +389,8 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
             const uint64_t dq = desc_q + (uint64_t)(qb * (kOperand >> 4));
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const uint64_t off = (uint64_t)((k >> 2) * kHalfB + (k & 3) * 32) >> 4;
-              tc_mma(tmem + (uint32_t)db * kCols, dk + off, dq + off, idesc, k > 0);
+              tc_mma(tmem + (uint32_t)db * kCols, dk + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4),
+                     dq + (uint64_t)(((k >> 2) * kHalfB + (k & 3) * 32) >> 4), idesc, k > 0);
             }
             tc_commit(bar(B_DFULL + db));
             mbar_arrive(bar(B_DFULL + db));
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
           break;
         kscale[(n % kScaleSlots) * kKeys + r] = scale;
         if (here) {
-          unsigned char* row = smem + L::k + st * kOperand + r * 128;
+          unsigned char* row = smem + L::k + st * kOperand + (r >> 3) * 2048 + (r & 7) * 128;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int ch = (i + lane) & 7;  // 16 codes: dims 16 ch .. 16 ch + 15
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
               o[2 * u] = codes_to_bf16x2<FMT>(w[u] & 0xffffu);
               o[2 * u + 1] = codes_to_bf16x2<FMT>(w[u] >> 16);
             }
-            unsigned char* half = row + (ch >> 2) * kHalfB;
+            unsigned char* half = row + (ch >> 2) * 1024;
             const int c2 = (ch & 3) * 2;
             *reinterpret_cast<uint4*>(half + ((c2 ^ (r & 7)) << 4)) =
                 make_uint4(o[0], o[1], o[2], o[3]);
@@ -627,7 +627,7 @@ int launch_weights_tc(const WeightsTcGeometry& g, const WeightArgs& a, int kv_fo
   if (!make_q_map(&tmq, a.q, a.num_q_tokens, a.Hq, a.G, g.QTb)) return PA_ERR_CUDA;
   tmk = tmq;  // unused by the 8-bit pools
   if (kv_format == PA_KV_BF16 &&
-      !make_pool_map(&tmk, a.k_cache, a.num_blocks * a.Hkv * kBlock))
+      !make_block_map(&tmk, a.k_cache, a.num_blocks * a.Hkv * kBlock))
     return PA_ERR_CUDA;
   TcWeightArgs t;
   t.w = a;
