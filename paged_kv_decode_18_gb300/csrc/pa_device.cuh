@@ -553,12 +553,12 @@ __device__ inline PieceCut build_piece_cut(const PlanSmem& P, int Hkv, int max_w
 // threads of the CTA call it (two CTA barriers); red: two 8-byte-aligned
 // words of shared memory. Returns 0 (no prefill work) .. N (no verify work).
 // A prefill tile beside the HBM-bound verify grid takes longer than alone
-// (1.46 us: its K/V loads from L2 wait behind the verify stream); a sweep of
-// this constant on the mixed batch (48 verify windows + two 512-token chunks)
-// put the best split at 2.25-3.0 us per tile (176-179 us per call against
-// 193 us with the grids in turn) and a cliff below it (2.0 us: 188 us), so the
-// constant sits on the safe side.
-constexpr long long kSplitTileNs = 2500;
+// (1.3 us: its K/V loads from L2 wait behind the verify stream); a sweep of this
+// constant on the mixed batch (48 verify windows + two 512-token chunks) put the
+// best split at 2.0-2.25 us per tile (188 us per eager call; 2.5 us: 191 us) and
+// a cliff below it (1.75 us: 191 us, 1.5 us: 206 us), so the constant sits on the
+// safe side.
+constexpr long long kSplitTileNs = 2150;
 constexpr long long kSplitBytesPerUs = 5900000;  // verify grid on all SMs (HBM)
 
 __device__ inline int overlap_split(const int32_t* cu_seqlens_q, const int32_t* context_lens,

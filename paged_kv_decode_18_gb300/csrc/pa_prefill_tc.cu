@@ -11,18 +11,20 @@
 //
 // A prefill chunk gives each KV head (128/G) x G query rows that share every
 // K/V tile: a real matrix product, so it runs on tcgen05 with accumulators in
-// tensor memory. One CTA per SM, warp-specialised (11 warps):
+// tensor memory. One CTA per SM, warp-specialised (12 warps):
 //   warp 0    TMA producer for the query tiles (3-D tensor map over q; two
 //             buffers, so the next piece's tile lands early) and for K, as
 //             eight 16-key pool blocks per 128-key tile, one copy each, found
 //             through the block table (ids fetched one tile ahead);
 //   warp 10   TMA producer for V; K and V stages have their own full/empty
 //             mbarriers, so a K stage refills as soon as its S is done;
-//   warp 1    allocates 512 TMEM columns and, from one thread, issues the
-//             MMAs: S = Q K^T into one of two S buffers (the next tile's S is
-//             computed while softmax works on this one), then O_h += P_h V_h
-//             for the two 64-key halves, with P read from tensor memory; each
-//             finished group is signalled by tcgen05.commit on an mbarrier;
+//   warp 1    allocates 512 TMEM columns and, from one thread, issues
+//             S = Q K^T into one of two S buffers (the next tile's S is computed
+//             while softmax works on this one);
+//   warp 11   issues, from one thread, O_h += P_h V_h for the two 64-key halves,
+//             with P read from tensor memory (a thread that issued both spent
+//             its time on the other product's waits); each finished group of
+//             either is signalled by tcgen05.commit on an mbarrier;
 //   warps 2-9 softmax, two threads per query row, one per 64-key half, each
 //             with its own running max, sum and O accumulator: read the S
 //             half from TMEM, mask, exp2, write P (bf16 pairs) back over the S
@@ -66,7 +68,8 @@ constexpr int kOffPlan = kOffLx + 2 * 2 * kRowsT * 8;
 constexpr int kPieceCost4 = 4;
 constexpr int kSoftmaxWarps = 8;            // warps 2-9, two per SM sub-partition
 constexpr int kVWarp = 2 + kSoftmaxWarps;   // the V producer
-constexpr int kThreadsT = 96 + kSoftmaxWarps * 32;
+constexpr int kPvWarp = kVWarp + 1;         // issues O += P V
+constexpr int kThreadsT = 128 + kSoftmaxWarps * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;             // S/P buffers at columns 0 and 128; O halves at 256, 384
 constexpr float kRescaleLog2 = 8.f;         // lazy O rescale threshold (log2 units)
@@ -104,6 +107,9 @@ struct TcArgs {
   const uint32_t* mask = nullptr;
   int mask_words = 0;
   const uint16_t* v_cache = nullptr;
+  // 1: CTAs 2p and 2p + 1 take the same key ranges for neighbouring query tiles
+  // (the plan's unit is two tiles), so the second's K and V come from L2
+  int pair = 0;
 };
 
 // Output row (token * Hq + head) of query token qtok, head hd; -1 when the
@@ -124,7 +130,7 @@ __device__ __forceinline__ void plan_inputs(const TcArgs& a, PlanInputs& in) {
   in.S = a.S;
   in.Hkv = a.Hkv;
   in.max_ctx = a.max_blocks * kBlock;
-  in.qtile = a.QTb;
+  in.qtile = a.QTb << a.pair;
   in.causal = a.causal;
   in.npairs_cap = a.npairs_cap;
   in.num_q_rows = a.num_q_tokens;
@@ -205,10 +211,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   PlanInputs in;
   plan_inputs(a, in);
   build_plan(in, P, nullptr);  // ends with a CTA barrier
-  const PieceCut cut = build_piece_cut(P, Hkv, max_workers, kPieceCost4, cut_view(smem + kOffPlan, a));
+  const PieceCut cut = build_piece_cut(P, Hkv, max_workers >> a.pair, kPieceCost4,
+                                       cut_view(smem + kOffPlan, a));
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int w = blockIdx.x;
+  const int w = blockIdx.x >> a.pair;
+  const int odd = blockIdx.x & a.pair;  // which tile of a unit of two
   if (w >= cut.nw) return;  // the whole CTA is idle (uniform)
   const int R0 = cut.start(w), R1 = cut.start(w + 1);
   if (R0 >= R1) return;
@@ -261,7 +269,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const int qs = qn & 1;
         if (qn >= 2 && !wait(B_QEMPTY + qs, (uint32_t)((qn >> 1) - 1) & 1u)) break;
         if (lane == 0) {
-          const int z = P.qstart[t.s] + t.qt * QTb;  // first query token of the tile
+          // first query token of the tile (past the rows for the missing second
+          // tile of a unit: zeros)
+          const int z = P.qstart[t.s] + ((t.qt << a.pair) + odd) * QTb;
           const uint32_t qd = smem_addr(smem + kOffQ + qs * kOpBytes);
           mbar_arrive_expect_tx(bar(B_QFULL + qs),
                                 TREE ? (uint32_t)(QTb * G) * 256u : (uint32_t)kOpBytes);
@@ -294,16 +304,14 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       if (idx + 1 < R1) advance(P, S, Hkv, t);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------------ MMA issuer, S = Q K^T
     if (lane == 0) {
       const uint32_t idS = f16_idesc(kRowsT, kKeysT, 0);
-      const uint32_t idPV = f16_idesc(kRowsT, 128, 1);
       int qn = 0, qs = 0;  // query tiles seen; buffer of the current one
       // operand descriptors differ by their address alone (16-byte units)
       const uint64_t desc_q = sw128_desc(smem_addr(smem + kOffQ), 16, 1024);
-      // K and V: 8-row groups every 2 KB, each the two 64-dim halves' 1 KB atoms
+      // K: 8-row groups every 2 KB, each the two 64-dim halves' 1 KB atoms
       const uint64_t desc_k = sw128_desc(smem_addr(smem + kOffKV), 16, 2048);
-      const uint64_t desc_v = sw128_desc(smem_addr(smem + kOffKV + kOpBytes), 1024, 2048);
       auto issue_S = [&](int i, bool first) -> bool {
         if (first) {
           qs = qn & 1;
@@ -327,25 +335,24 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         return true;
       };
       TilePos t = locate(P, S, Hkv, R0);
-      bool ok = issue_S(0, true);
-      if (ok && (R0 + 1 >= R1 || t.b == t.nt - 1)) tc_commit(bar(B_QEMPTY + qs));
-      for (int idx = R0, i = 0; ok && idx < R1; ++idx, ++i) {
+      for (int idx = R0, i = 0; idx < R1; ++idx, ++i) {
+        if (!issue_S(i, (idx == R0) || (t.b == 0))) break;
+        if (idx + 1 >= R1 || t.b == t.nt - 1) tc_commit(bar(B_QEMPTY + qs));
+        if (idx + 1 < R1) advance(P, S, Hkv, t);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kPvWarp) {
+    // ------------------------------------------------------------------ MMA issuer, O += P V
+    if (lane == 0) {
+      const uint32_t idPV = f16_idesc(kRowsT, 128, 1);
+      // V: 8-row groups every 2 KB, each the two 64-dim halves' 1 KB atoms
+      const uint64_t desc_v = sw128_desc(smem_addr(smem + kOffKV + kOpBytes), 1024, 2048);
+      TilePos t = locate(P, S, Hkv, R0);
+      for (int idx = R0, i = 0; idx < R1; ++idx, ++i) {
         const bool first = (idx == R0) || (t.b == 0);
-        TilePos tn = t;
-        if (idx + 1 < R1) {
-          // the next tile's S first: the tensor core computes it during softmax
-          advance(P, S, Hkv, tn);
-          if (!issue_S(i + 1, tn.b == 0)) {
-            ok = false;
-            break;
-          }
-          if (idx + 2 >= R1 || tn.b == tn.nt - 1) tc_commit(bar(B_QEMPTY + qs));
-        }
         const int st = i & 1;
-        if (!wait(B_PFULL, (uint32_t)i & 1u) || !wait(B_VFULL + st, (uint32_t)(i >> 1) & 1u)) {
-          ok = false;
-          break;
-        }
+        if (!wait(B_VFULL + st, (uint32_t)(i >> 1) & 1u) || !wait(B_PFULL, (uint32_t)i & 1u)) break;
         tc_fence_after();
         const uint64_t dv = desc_v + (uint64_t)(st * (2 * kOpBytes >> 4));
         // O_hf += P[:, keys of half hf] V[keys of half hf, :]: one accumulator per
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         tc_commit(bar(B_VEMPTY + st));
         tc_commit(bar(B_SFREE + st));
         tc_commit(bar(B_ODONE));
-        t = tn;
+        if (idx + 1 < R1) advance(P, S, Hkv, t);
       }
     }
     __syncwarp();
@@ -485,7 +492,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       if (first) {
         c = P.ctx[t.s];
         lq = P.qstart[t.s + 1] - P.qstart[t.s];
-        tok = t.qt * QTb + r / G;
+        tok = ((t.qt << a.pair) + odd) * QTb + r / G;
         valid = tok < lq;
         if constexpr (TREE) {
           valid = valid && r < QTb * G;
@@ -662,7 +669,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         pend_h = t.h;
         pend_k0 = piece_b0 * kKeysT;
         pend_k1 = (t.b + 1) * kKeysT;
-        pend_slot = (size_t)w * 2 + (piece_first ? 0 : 1);
+        pend_slot = (size_t)blockIdx.x * 2 + (piece_first ? 0 : 1);
       }
       if (idx + 1 < R1) advance(P, S, Hkv, t);
     }
@@ -701,8 +708,9 @@ __global__ void __launch_bounds__(kFixThreads)
   plan_inputs(a, in);
   const int max_workers = prefill_workers(a, fx_smem);
   build_plan(in, P, nullptr);
-  const PieceCut cut = build_piece_cut(P, a.Hkv, max(max_workers, 1), kPieceCost4, cut_view(fx_smem, a));
-  const int w = blockIdx.x;
+  const PieceCut cut = build_piece_cut(P, a.Hkv, max(max_workers >> a.pair, 1), kPieceCost4,
+                                       cut_view(fx_smem, a));
+  const int w = blockIdx.x >> a.pair, odd = blockIdx.x & a.pair;
   const MergeJob job = merge_job_of(P, a.S, a.Hkv, w, cut.nw, cut);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!job.valid) return;
@@ -710,12 +718,12 @@ __global__ void __launch_bounds__(kFixThreads)
   const int q0 = P.qstart[job.s], lq = P.qstart[job.s + 1] - q0;
   const int npieces = job.last - w + 2;  // workers w-1 .. last
   auto slot_of = [&](int i) -> size_t {
-    return (size_t)(w - 1 + i) * 2 + (i == 0 ? job.slot_prev : 0);
+    return (size_t)(((w - 1 + i) << a.pair) + odd) * 2 + (i == 0 ? job.slot_prev : 0);
   };
   // a warp merges four rows at once: eight lanes per row, sixteen dims per lane
   const int r = blockIdx.y * kFixRowsPerCta + warp * 4 + (lane >> 3);
   const int d0 = (lane & 7) * 16;
-  const int tok = job.qt * a.QTb + r / a.G;
+  const int tok = ((job.qt << a.pair) + odd) * a.QTb + r / a.G;
   if (r >= a.QTb * a.G || tok >= lq) return;  // padding rows
   // online merge over the pieces, four at a time with all their loads in flight
   float m = neg_inf(), sum = 0.f;
@@ -924,6 +932,9 @@ int launch_tree_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf16* 
   a.mask = tree_mask;
   a.mask_words = mask_words;
   a.v_cache = v_cache;
+  // windows of two tiles and more, on average nearly: the second tile of a unit
+  // is seldom missing
+  a.pair = num_q_tokens * (sh->num_q_heads / sh->num_kv_heads) > (int64_t)kRowsT * 3 / 2 * sh->num_seqs;
   return launch_tc(g, q, k_cache, v_cache, a, num_q_tokens, scale, sh, workspace, st, 3);
 }
 
