@@ -183,6 +183,10 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _need(t, name, dtype, ndim=None):
     if t is None:
         raise ValueError(f"{name} is required")
@@ -403,7 +407,9 @@ def _prepared(cfn, args, stream, what, keep):
     """A zero-argument callable that makes one C-ABI call with arguments that
     were checked and converted once (the tensors in `keep` stay referenced).
     The stream goes last: fixed now when one was given, else the current
-    torch stream at each call (so the call can also be captured in a graph)."""
+    torch stream of the tensors' device at each call (so the call can also be
+    captured in a graph), taken as a raw handle: torch's stream object costs
+    2.8 us, half of a small call."""
     if stream is not None:
         full = args + (_stream(stream),)
 
@@ -412,8 +418,10 @@ def _prepared(cfn, args, stream, what, keep):
             if rc != PA_OK:
                 raise PAError(rc, what)
     else:
+        device = keep[0].device.index
+
         def call():
-            rc = cfn(*args, _stream(None))
+            rc = cfn(*args, _raw_stream(device))
             if rc != PA_OK:
                 raise PAError(rc, what)
     call.keep = keep

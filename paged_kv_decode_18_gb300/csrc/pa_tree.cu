@@ -73,7 +73,9 @@ __global__ void __launch_bounds__(kMaskThreads)
 // pa_commit_path. One CTA per sequence, one warp per KV head at a time. A path
 // of increasing window indices has path[i] >= i, so a warp that reads a group
 // of rows before it writes any of them, group after group, never reads a row
-// that it has already written.
+// that it has already written. The call is a chain of dependent reads -- the
+// lengths and the path, the block table, the rows -- so lane i looks up row i
+// of 32 at once.
 // ---------------------------------------------------------------------------
 constexpr int kCommitWarps = 8;
 constexpr int kCommitGroup = 8;  // rows a warp holds between reading and writing
@@ -89,64 +91,88 @@ __global__ void __launch_bounds__(kCommitWarps * 32)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int s = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t* row = path + (int64_t)s * max_path_len;
+  // path entries base + lane - 1 and base + lane (-1 before the first)
+  auto entry = [&](int base, int& before) -> int {
+    const int i = base + lane;
+    const int x = i < max_path_len ? row[i] : 0;
+    before = __shfl_up_sync(kFull, x, 1);
+    if (lane == 0) before = base > 0 ? row[base - 1] : -1;
+    return x;
+  };
+  int before;
+  const int x0 = entry(0, before);  // read beside the lengths, whether used or not
   const int c = context_lens[s], n = path_lens[s];
   const int lq = cu[s + 1] - cu[s];
   const bool bad_ctx = c < 0 || c > max_blocks * kBlock;
   const bool bad_len = lq < 0 || lq > c;
   bool bad_path = n < 0 || n > max_path_len || n > lq;
-  const int32_t* row = path + (int64_t)s * max_path_len;
   if (!bad_ctx && !bad_len && !bad_path) {
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-      const int x = row[i];
-      if (x < 0 || x >= lq || (i > 0 && x <= row[i - 1])) bad_path = true;
+    // increasing from -1 and below lq; every warp checks the whole path
+    bad_path = lane < n && (x0 <= before || x0 >= lq);
+    for (int base = 32; base < n; base += 32) {
+      const int x = entry(base, before);
+      bad_path = bad_path || (base + lane < n && (x <= before || x >= lq));
     }
-  }
-  // also the barrier between the reads of context_lens above and the write of
-  // new_lens below, which may be the same array
-  bad_path = __syncthreads_or(bad_path);
-  if (bad_ctx || bad_len || bad_path) {  // the sequence stays as it is
-    if (threadIdx.x == 0) {
-      flag_error(bad_ctx ? PA_DEVERR_CONTEXT_RANGE
-                         : (bad_len ? PA_DEVERR_QLEN_RANGE : PA_DEVERR_TREE_RANGE));
-      new_lens[s] = c;
-    }
-    return;
+    bad_path = __any_sync(kFull, bad_path);
   }
   const int p0 = c - lq;
-  if (threadIdx.x == 0) new_lens[s] = p0 + n;
-  PoolView pool;
-  pool.k = k_cache;
-  pool.v = v_cache;
-  pool.table = block_tables + (int64_t)s * max_blocks;
-  pool.num_blocks = num_blocks;
-  pool.Hkv = Hkv;
-  for (int h = warp; h < Hkv; h += kCommitWarps) {
-    pool.h = h;
-    for (int i0 = 0; i0 < n; i0 += kCommitGroup) {
-      uint4 x[kCommitGroup];
-      uint8_t* to[kCommitGroup];
-#pragma unroll
-      for (int u = 0; u < kCommitGroup; ++u) {
-        to[u] = nullptr;
-        const int i = i0 + u;
-        if (i >= n) continue;
-        const int src = row[i];
-        if (src == i) continue;
-        RowPlace from, dst;
-        const bool ok1 = pool.place(p0 + src, &from), ok2 = pool.place(p0 + i, &dst);
+  if (bad_ctx || bad_len || bad_path) {  // the sequence stays as it is
+    if (threadIdx.x == 0)
+      flag_error(bad_ctx ? PA_DEVERR_CONTEXT_RANGE
+                         : (bad_len ? PA_DEVERR_QLEN_RANGE : PA_DEVERR_TREE_RANGE));
+  } else {
+    PoolView pool;
+    pool.k = k_cache;
+    pool.v = v_cache;
+    pool.table = block_tables + (int64_t)s * max_blocks;
+    pool.num_blocks = num_blocks;
+    pool.Hkv = Hkv;
+    for (int base = 0; base < n; base += 32) {
+      const int src = base == 0 ? x0 : entry(base, before);
+      const int i = base + lane;
+      // tiles of head 0 and rows of where lane's row comes from and goes to
+      bool moves = i < n && src != i;
+      RowPlace from{0, 0}, to{0, 0};
+      pool.h = 0;
+      if (moves) {
+        const bool ok1 = pool.place(p0 + src, &from), ok2 = pool.place(p0 + i, &to);
         if (!ok1 || !ok2) {
-          if (lane == 0) flag_error(PA_DEVERR_BLOCK_RANGE);
-          continue;
+          if (warp == 0) flag_error(PA_DEVERR_BLOCK_RANGE);
+          moves = false;
         }
-        x[u] = load_chunk<Q8>(row_chunk<Q8>(pool, from, lane), lane);
-        to[u] = row_chunk<Q8>(pool, dst, lane);
       }
-      __syncwarp();
+      const unsigned moving = __ballot_sync(kFull, moves);
+      for (int h = warp; h < Hkv; h += kCommitWarps) {
+        unsigned m = moving;
+        while (m) {
+          uint4 x[kCommitGroup];
+          uint8_t* dst[kCommitGroup];
 #pragma unroll
-      for (int u = 0; u < kCommitGroup; ++u)
-        if (to[u]) store_chunk<Q8>(to[u], lane, x[u]);
+          for (int u = 0; u < kCommitGroup; ++u) {
+            dst[u] = nullptr;
+            if (!m) continue;
+            const int j = __ffs(m) - 1;
+            m &= m - 1;
+            RowPlace f, d;
+            f.tile = __shfl_sync(kFull, from.tile, j) + h;
+            f.off = __shfl_sync(kFull, from.off, j);
+            d.tile = __shfl_sync(kFull, to.tile, j) + h;
+            d.off = __shfl_sync(kFull, to.off, j);
+            x[u] = load_chunk<Q8>(row_chunk<Q8>(pool, f, lane), lane);
+            dst[u] = row_chunk<Q8>(pool, d, lane);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < kCommitGroup; ++u)
+            if (dst[u]) store_chunk<Q8>(dst[u], lane, x[u]);
+        }
+      }
     }
   }
+  // new_lens may be context_lens: every warp has read it
+  __syncthreads();
+  if (threadIdx.x == 0) new_lens[s] = bad_ctx || bad_len || bad_path ? c : p0 + n;
 }
 
 }  // namespace
