@@ -17,8 +17,9 @@
 // An ordered scan then lists the positions.
 // Moving: the i-th row that stays comes from a position kept[i] >= i, and kept
 // increases. So the rows go in waves of as many as the cluster's shared memory
-// holds: all CTAs read their rows of a wave, the cluster meets, all write. A
-// wave's writes fall before every later wave's sources.
+// holds twice over: all CTAs read their rows of a wave, the cluster meets, all
+// write. A wave's writes fall before every later wave's sources, so the next
+// wave's reads begin before the cluster has met.
 #include "pa_device.cuh"
 #include "pa_host.h"
 #include "pa_rows.cuh"
@@ -39,9 +40,10 @@ constexpr int kSliceMax = (kArea - kOffSlice) / 4;  // a longer slice is read ag
 constexpr int kEvictSmem = kArea + (3 * kEvictWarps + 4) * 4;
 template <bool Q8>
 constexpr int kRowBytes = Q8 ? 2 * kHeadDim : 4 * kHeadDim;  // a row's K and V (8-bit: the codes)
-// rows of a wave a warp: data, and 16 bytes for the weight and the 8-bit scales
+// rows of a wave a warp (two waves' rows are in shared memory): data, and 16
+// bytes for the weight and the 8-bit scales
 template <bool Q8>
-constexpr int kWarpRows = kArea / (kRowBytes<Q8> + 16) / kEvictWarps / 2 * 2;
+constexpr int kWarpRows = kArea / 2 / (kRowBytes<Q8> + 16) / kEvictWarps / (Q8 ? 2 : 1) * (Q8 ? 2 : 1);
 
 struct EvictArgs {
   uint8_t* k_cache;
@@ -137,19 +139,31 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   const int per = (hi - lo + ctas - 1) / ctas;
   const int p0 = min(hi, lo + rank * per), p1 = min(hi, p0 + per), len = p1 - p0;
   const bool held = per <= kSliceMax;
-  float* slice = reinterpret_cast<float*>(area + kOffSlice);
+  uint32_t* slice = reinterpret_cast<uint32_t*>(area + kOffSlice);  // keys
   if (held) {
-    for (int i = tid; i < len; i += 4 * kEvictThreads) {
-      float x[4];
+    for (int i = tid; i < len; i += 8 * kEvictThreads) {
+      float x[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 8; ++u)
         if (i + u * kEvictThreads < len) x[u] = w[p0 + i + u * kEvictThreads];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + u * kEvictThreads < len) slice[i + u * kEvictThreads] = x[u];
+      for (int u = 0; u < 8; ++u)
+        if (i + u * kEvictThreads < len) slice[i + u * kEvictThreads] = weight_key(x[u]);
     }
   }
-  auto key_of = [&](int i) { return weight_key(held ? slice[i] : w[p0 + i]); };
+  auto key_of = [&](int i) { return held ? slice[i] : weight_key(w[p0 + i]); };
+  // every key of [i, end) in steps of `step`, several reads on their way at once
+  auto each_key = [&](int i, int end, int step, auto&& use) {
+    for (; i + 3 * step < end; i += 4 * step) {
+      const uint32_t k0 = key_of(i), k1 = key_of(i + step), k2 = key_of(i + 2 * step),
+                     k3 = key_of(i + 3 * step);
+      use(k0);
+      use(k1);
+      use(k2);
+      use(k3);
+    }
+    for (; i < end; i += step) use(key_of(i));
+  };
   // ---- the key of the last one that stays -----------------------------------------
   int need = budget - a.sinks - a.recent;  // how many of the middle stay, < hi - lo
   const bool some = need > 0;
@@ -164,8 +178,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
       int* hs = reinterpret_cast<int*>(area + kOffB) + (pass & 1) * kBins;
       if (pass == 0 && columns) {
         int* ha = reinterpret_cast<int*>(area);
-        for (int i = tid; i < len; i += kEvictThreads)
-          atomicAdd(&ha[(key_of(i) >> 24) * 32 + lane], 1);
+        each_key(tid, len, kEvictThreads,
+                 [&](uint32_t key) { atomicAdd(&ha[(key >> 24) * 32 + lane], 1); });
         __syncthreads();
         // two threads a bin, sixteen columns each, beginning at their own so that
         // a warp's reads fall into different banks
@@ -181,10 +195,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
           __syncthreads();
         }
         const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
-        for (int i = tid; i < len; i += kEvictThreads) {
-          const uint32_t key = key_of(i);
+        each_key(tid, len, kEvictThreads, [&](uint32_t key) {
           if ((key & above) == prefix) atomicAdd(&hs[(key >> shift) & 255u], 1);
-        }
+        });
       }
       cluster_meet();
       // thread t owns bin 255 - t
@@ -199,10 +212,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
       }
       if (lane == 31) warp_tot[warp] = x;
       __syncthreads();
-      int run = x - sum;  // keys in higher bins
-#pragma unroll
-      for (int i = 0; i < kEvictWarps; ++i)
-        if (i < warp) run += warp_tot[i];
+      // keys in higher bins
+      const int run = x - sum + __reduce_add_sync(kFull, lane < warp ? warp_tot[lane] : 0);
       if (run < need && run + sum >= need) {
         found[0] = kBins - 1 - tid;
         found[1] = need - run;
@@ -218,12 +229,12 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   const int i0 = min(len, warp * wlen), i1 = min(len, i0 + wlen);
   int gt = 0, eq = 0;  // of this warp's run
   if (some) {
-    for (int i = i0; i < i1; i += 32) {
-      const uint32_t key = i + lane < i1 ? key_of(i + lane) : 0u;
-      const bool in = i + lane < i1;
-      gt += __popc(__ballot_sync(kFull, in && key > prefix));
-      eq += __popc(__ballot_sync(kFull, in && key == prefix));
-    }
+    each_key(i0 + lane, i1, 32, [&](uint32_t key) {
+      gt += key > prefix;
+      eq += key == prefix;
+    });
+    gt = __reduce_add_sync(kFull, gt);
+    eq = __reduce_add_sync(kFull, eq);
   }
   int before_gt = 0, before_eq = 0;
   {
@@ -232,15 +243,11 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
       run_tot[kEvictWarps + warp] = eq;
     }
     __syncthreads();
-    int tg = 0, te = 0;
-    for (int i = 0; i < kEvictWarps; ++i) {
-      if (i < warp) {
-        before_gt += run_tot[i];
-        before_eq += run_tot[kEvictWarps + i];
-      }
-      tg += run_tot[i];
-      te += run_tot[kEvictWarps + i];
-    }
+    const int g = lane < kEvictWarps ? run_tot[lane] : 0;
+    const int e = lane < kEvictWarps ? run_tot[kEvictWarps + lane] : 0;
+    before_gt = __reduce_add_sync(kFull, lane < warp ? g : 0);
+    before_eq = __reduce_add_sync(kFull, lane < warp ? e : 0);
+    const int tg = __reduce_add_sync(kFull, g), te = __reduce_add_sync(kFull, e);
     if (tid == 0) {
       counts[0] = tg;
       counts[1] = te;
@@ -272,10 +279,11 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   // ---- weights and rows, wave by wave ---------------------------------------------
   constexpr int kMine = kWarpRows<Q8>, kRow = kRowBytes<Q8>, kRows = kMine * kEvictWarps;
   static_assert(kMine <= 32, "a lane a row");
-  unsigned char* data = area + (size_t)warp * kMine * kRow;  // this warp's rows
-  const uint32_t aux = smem_addr(area + (size_t)kRows * kRow + ((size_t)warp * kMine + lane) * 16);
-  const float* auxf = reinterpret_cast<const float*>(area + (size_t)kRows * kRow) +
-                      ((size_t)warp * kMine + lane) * 4;
+  // this warp's rows in each half of the area
+  unsigned char* data = area + (size_t)warp * kMine * kRow;
+  unsigned char* aux = area + (size_t)kRows * kRow + ((size_t)warp * kMine + lane) * 16;
+  constexpr int kHalfArea = kRows * (kRow + 16);
+  static_assert(2 * kHalfArea <= kArea, "two waves");
   PoolView pool;
   pool.k = a.k_cache;
   pool.v = a.v_cache;
@@ -319,41 +327,53 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
     }
     return m;
   };
-  Move mv = look_up(0);
-  for (int base = 0; base < n; base += ctas * kRows) {
-    if (mv.from >= 0) {
-      copy4_async(aux + 8, w + mv.src);
+  auto read_rows = [&](const Move& m, int half) {
+    const uint32_t x = smem_addr(aux + half * kHalfArea);
+    if (m.from >= 0) {
+      copy4_async(x + 8, w + m.src);
       if (Q8) {
-        copy4_async(aux, a.k_cache + mv.scale_from);
-        copy4_async(aux + 4, a.v_cache + mv.scale_from);
+        copy4_async(x, a.k_cache + m.scale_from);
+        copy4_async(x + 4, a.v_cache + m.scale_from);
       }
     }
-    const uint32_t d = smem_addr(data) + lane * 16;
+    const uint32_t d = smem_addr(data + half * kHalfArea) + lane * 16;
 #pragma unroll
     for (int j = 0; j < kMine; j += kAtOnce) {
-      const int64_t f = __shfl_sync(kFull, mv.from, j + sub);
+      const int64_t f = __shfl_sync(kFull, m.from, j + sub);
       if (f >= 0) copy16_async(d + j * kRow, mybase + f);
     }
-    const Move next = look_up(base + ctas * kRows);
+  };
+  const int step = ctas * kRows;
+  Move mv = look_up(0);
+  read_rows(mv, 0);
+  Move next = look_up(step);
+  for (int base = 0, half = 0; base < n; base += step, half ^= 1) {
+    // this wave's rows are here; while the others' land too, the next wave's set
+    // out (their sources lie behind everything that this wave writes)
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
-    cluster_meet();  // every row of the wave has been read
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    read_rows(next, half ^ 1);
+    const Move after = look_up(base + 2 * step);
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
     for (int j = 0; j < kMine; j += kAtOnce) {
       const int64_t to = __shfl_sync(kFull, mv.to, j + sub);
       if (to >= 0)
         *reinterpret_cast<uint4*>(mybase + to) =
-            *reinterpret_cast<const uint4*>(data + j * kRow + lane * 16);
+            *reinterpret_cast<const uint4*>(data + half * kHalfArea + j * kRow + lane * 16);
     }
     if (mv.from >= 0) {
-      w[base + rank * kRows + warp * kMine + lane] = auxf[2];
+      const float* x = reinterpret_cast<const float*>(aux + half * kHalfArea);
+      w[base + rank * kRows + warp * kMine + lane] = x[2];
       if (Q8) {
-        *reinterpret_cast<float*>(a.k_cache + mv.scale_to) = auxf[0];
-        *reinterpret_cast<float*>(a.v_cache + mv.scale_to) = auxf[1];
+        *reinterpret_cast<float*>(a.k_cache + mv.scale_to) = x[0];
+        *reinterpret_cast<float*>(a.v_cache + mv.scale_to) = x[1];
       }
     }
-    __syncwarp();  // the rows' shared memory is read before the next wave's copies
+    __syncwarp();  // this half is read before the copies of the wave after next
     mv = next;
+    next = after;
   }
 }
 
