@@ -208,7 +208,7 @@ constexpr int kTcMinQLen = 32;
 struct PrefillTcGeometry {
   bool enabled = false;
   int grid = 0, workers = 0, npairs_cap = 0, QTb = 0;
-  size_t smem = 0, fixup_smem = 0, ws_lse = 0, ws_o = 0, ws_bytes = 0;
+  size_t smem = 0, ws_lse = 0, ws_o = 0, ws_bytes = 0;
 };
 
 // min_q_len: sequences with a shorter query window are left to another kernel.

@@ -72,6 +72,7 @@ constexpr int kPvWarp = kVWarp + 1;         // issues O += P V
 constexpr int kThreadsT = 128 + kSoftmaxWarps * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;             // S/P buffers at columns 0 and 128; O halves at 256, 384
+constexpr int kDescInts = 8;
 constexpr float kRescaleLog2 = 8.f;         // lazy O rescale threshold (log2 units)
 
 enum : int {
@@ -101,6 +102,7 @@ struct TcArgs {
   int min_lq;
   float* part_o;    // [NW * 2][128 rows][128]
   float* part_lse;  // [NW * 2][128 rows]
+  int* desc;        // [NW][kDescInts] the merge that each worker boundary owns
   RowsOut rows;     // fp32 row output instead of out / lse (rows.o set)
   const int32_t* row_map;  // rows mode: query token i -> output token row_map[i]
   // tree windows: mask rows, and V for the elements that the product leaves out
@@ -206,8 +208,14 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   // launched as a programmatic dependent of the previous grid
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int max_workers = prefill_workers(a, smem + kOffPlan);
+  const int w = blockIdx.x >> a.pair;
+  const int odd = blockIdx.x & a.pair;  // which tile of a unit of two
+  int* desc = a.desc + (size_t)w * kDescInts;
   // beside a verify grid: the CTAs past the split leave now, freeing their SMs
-  if ((int)blockIdx.x >= max_workers) return;
+  if ((int)blockIdx.x >= max_workers) {
+    if (tid == 0 && odd == 0) desc[0] = -1;
+    return;
+  }
   PlanInputs in;
   plan_inputs(a, in);
   build_plan(in, P, nullptr);  // ends with a CTA barrier
@@ -215,8 +223,20 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                                        cut_view(smem + kOffPlan, a));
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int w = blockIdx.x >> a.pair;
-  const int odd = blockIdx.x & a.pair;  // which tile of a unit of two
+  if (tid == 32 * kPvWarp && odd == 0) {  // a warp whose own work begins last
+    // what the merge grid needs of the plan (rebuilding it there, after this
+    // grid has left its SMs, took most of that grid's time)
+    const MergeJob j = merge_job_of(P, S, Hkv, w, cut.nw, cut);
+    desc[0] = j.valid ? j.s : -1;
+    if (j.valid) {
+      desc[1] = j.qt;
+      desc[2] = j.h;
+      desc[3] = j.last;
+      desc[4] = j.slot_prev;
+      desc[5] = P.qstart[j.s];
+      desc[6] = P.qstart[j.s + 1] - P.qstart[j.s];
+    }
+  }
   if (w >= cut.nw) return;  // the whole CTA is idle (uniform)
   const int R0 = cut.start(w), R1 = cut.start(w + 1);
   if (R0 >= R1) return;
@@ -691,8 +711,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 // Merge the pieces of (sequence, query tile, KV head) segments cut between
 // CTAs. Grid (CTA boundary, quarter of the tile's rows); eight lanes per
 // query row, so each piece's row is one coalesced 512-byte read and a warp has
-// four rows' loads in flight. The plan is rebuilt (the prefill grid does not
-// change it) before the wait for that grid.
+// four rows' loads in flight.
 constexpr int kFixRowsPerCta = 32;
 constexpr int kFixThreads = 256;
 
@@ -701,29 +720,21 @@ __global__ void __launch_bounds__(kFixThreads)
   // the next grid in the stream may start its own preparation now; it waits
   // for this grid before it reads anything this grid writes
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  extern __shared__ __align__(16) unsigned char fx_smem[];
-  PlanSmem P;
-  plan_view(fx_smem, a, P);
-  PlanInputs in;
-  plan_inputs(a, in);
-  const int max_workers = prefill_workers(a, fx_smem);
-  build_plan(in, P, nullptr);
-  const PieceCut cut = build_piece_cut(P, a.Hkv, max(max_workers >> a.pair, 1), kPieceCost4,
-                                       cut_view(fx_smem, a));
-  const int w = blockIdx.x >> a.pair, odd = blockIdx.x & a.pair;
-  const MergeJob job = merge_job_of(P, a.S, a.Hkv, w, cut.nw, cut);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!job.valid) return;
+  const int w = blockIdx.x >> a.pair, odd = blockIdx.x & a.pair;
+  const int4* d = reinterpret_cast<const int4*>(a.desc + (size_t)w * kDescInts);
+  const int4 d0 = __ldcg(d), d1 = __ldcg(d + 1);
+  if (d0.x < 0) return;
+  const int qt = d0.y, h = d0.z, last = d0.w, slot_prev = d1.x, q0 = d1.y, lq = d1.z;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int q0 = P.qstart[job.s], lq = P.qstart[job.s + 1] - q0;
-  const int npieces = job.last - w + 2;  // workers w-1 .. last
+  const int npieces = last - w + 2;  // workers w-1 .. last
   auto slot_of = [&](int i) -> size_t {
-    return (size_t)(((w - 1 + i) << a.pair) + odd) * 2 + (i == 0 ? job.slot_prev : 0);
+    return (size_t)(((w - 1 + i) << a.pair) + odd) * 2 + (i == 0 ? slot_prev : 0);
   };
   // a warp merges four rows at once: eight lanes per row, sixteen dims per lane
   const int r = blockIdx.y * kFixRowsPerCta + warp * 4 + (lane >> 3);
-  const int d0 = (lane & 7) * 16;
-  const int tok = ((job.qt << a.pair) + odd) * a.QTb + r / a.G;
+  const int dim0 = (lane & 7) * 16;
+  const int tok = ((qt << a.pair) + odd) * a.QTb + r / a.G;
   if (r >= a.QTb * a.G || tok >= lq) return;  // padding rows
   // online merge over the pieces, four at a time with all their loads in flight
   float m = neg_inf(), sum = 0.f;
@@ -741,7 +752,7 @@ __global__ void __launch_bounds__(kFixThreads)
         const size_t sl = slot_of(i0 + u);
         li[u] = a.part_lse[sl * kRowsT + r];
         const float4* src =
-            reinterpret_cast<const float4*>(a.part_o + (sl * kRowsT + r) * kHeadDim + d0);
+            reinterpret_cast<const float4*>(a.part_o + (sl * kRowsT + r) * kHeadDim + dim0);
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[u][k] = src[k];
       }
@@ -770,17 +781,17 @@ __global__ void __launch_bounds__(kFixThreads)
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] *= inv;
   const float LSE = sum > 0.f ? m + lg2(sum) * kLn2 : neg_inf();
-  const int64_t orow = out_row(a, (int64_t)q0 + tok, job.h * a.G + r % a.G);
+  const int64_t orow = out_row(a, (int64_t)q0 + tok, h * a.G + r % a.G);
   if (orow < 0) return;
   if (a.rows.o) {
-    float4* dst = reinterpret_cast<float4*>(a.rows.o + (orow * a.rows.stride + a.rows.slot) * kHeadDim + d0);
+    float4* dst = reinterpret_cast<float4*>(a.rows.o + (orow * a.rows.stride + a.rows.slot) * kHeadDim + dim0);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       dst[k] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
     if ((lane & 7) == 0) a.rows.lse[orow * a.rows.stride + a.rows.slot] = LSE;
     return;
   }
-  uint4* dst = reinterpret_cast<uint4*>(a.out + orow * kHeadDim + d0);
+  uint4* dst = reinterpret_cast<uint4*>(a.out + orow * kHeadDim + dim0);
   dst[0] = make_uint4(cvt_bf16x2(acc[0], acc[1]), cvt_bf16x2(acc[2], acc[3]),
                       cvt_bf16x2(acc[4], acc[5]), cvt_bf16x2(acc[6], acc[7]));
   dst[1] = make_uint4(cvt_bf16x2(acc[8], acc[9]), cvt_bf16x2(acc[10], acc[11]),
@@ -831,18 +842,13 @@ static int tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len,
   g->grid = max_ctas > 0 && max_ctas < dev.num_sms ? max_ctas : dev.num_sms;
   g->workers = g->grid;
   g->smem = 1024 + kOffPlan + round_up(plan_bytes(S, g->npairs_cap, g->workers), 16);
-  g->fixup_smem = plan_bytes(S, g->npairs_cap, g->workers);
-  if (g->smem > (size_t)dev.max_smem_optin || g->fixup_smem > (size_t)dev.max_smem_optin)
-    return PA_ERR_UNSUPPORTED;
+  if (g->smem > (size_t)dev.max_smem_optin) return PA_ERR_UNSUPPORTED;
   if (!raise_smem_limit(tree ? reinterpret_cast<const void*>(paged_prefill_tc_kernel<true>)
                              : reinterpret_cast<const void*>(paged_prefill_tc_kernel<false>)))
     return PA_ERR_CUDA;
-  if (g->fixup_smem > 48 * 1024 &&
-      !raise_smem_limit(reinterpret_cast<const void*>(prefill_tc_fixup_kernel)))
-    return PA_ERR_CUDA;
   g->ws_lse = round_up(sizeof(float) * 2 * kRowsT * (size_t)g->workers, 256);
   g->ws_o = round_up(sizeof(float) * 2 * kRowsT * kHeadDim * (size_t)g->workers, 256);
-  g->ws_bytes = g->ws_lse + g->ws_o;
+  g->ws_bytes = g->ws_lse + g->ws_o + round_up(sizeof(int) * kDescInts * (size_t)g->workers, 256);
   return PA_OK;
 }
 
@@ -879,6 +885,7 @@ static int launch_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf16
   char* ws = static_cast<char*>(workspace);
   a.part_lse = reinterpret_cast<float*>(ws);
   a.part_o = reinterpret_cast<float*>(ws + g.ws_lse);
+  a.desc = reinterpret_cast<int*>(ws + g.ws_lse + g.ws_o);
   if (parts & 1) {
     const cudaError_t e =
         a.mask ? launch_dependent(paged_prefill_tc_kernel<true>, dim3(g.grid), dim3(kThreadsT),
@@ -888,7 +895,7 @@ static int launch_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf16
     if (e != cudaSuccess) return PA_ERR_CUDA;
   }
   if ((parts & 2) && launch_dependent(prefill_tc_fixup_kernel, dim3(g.workers, kRowsT / kFixRowsPerCta),
-                       dim3(kFixThreads), g.fixup_smem, st, a) != cudaSuccess)
+                       dim3(kFixThreads), 0, st, a) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;
 }
