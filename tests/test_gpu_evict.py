@@ -126,6 +126,50 @@ def test_weights(fmt, hq, hkv, ctx, ql):
         assert same_bits(one, got)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("hq,hkv,ql", [(16, 8, 1), (8, 8, 2), (16, 8, 7), (16, 8, 64), (4, 4, 300)])
+def test_weights_of_large_batches(fmt, hq, hkv, ql):
+    # sizes at which every ring of stages wraps, against 64-bit matrix products on
+    # the GPU; two sequences have windows of their own lengths
+    ctx = [4100, 2500, 311, 6007, 900, 1]
+    lens = [min(ql, c) for c in ctx]
+    lens[1], lens[4] = max(1, lens[1] // 2), 0
+    w = W.build("large", 44, ctx, lens, pool_factor=1.1, num_q_heads=hq, num_kv_heads=hkv,
+                outlier_frac=0.02, outlier_gain=2.5)
+    db = batch(w, fmt)
+    rows = rows_of(db.kc, fmt, w.block_tables, w.context_lens)
+    G = hq // hkv
+    old = torch.rand((len(ctx), hkv, 6007), generator=torch.Generator().manual_seed(3)) * 0.01
+    lse = torch.zeros((w.num_q_tokens, hq))
+    ref, tol = old.double(), torch.zeros(old.shape, dtype=torch.float64)
+    for s, c in enumerate(ctx):
+        a, L = int(w.cu_seqlens_q[s]), lens[s]
+        hidden = (torch.arange(c) > (c - L + torch.arange(L))[:, None]).cuda()
+        for h in range(hkv if L else 0):
+            k = rows(s, h).cuda()
+            x = w.q[a:a + L, h * G:(h + 1) * G].cuda().double().transpose(0, 1)
+            z = (w.scale * x @ k.T).masked_fill(hidden, float("-inf"))
+            l = torch.logsumexp(z, -1).float()
+            lse[a:a + L, h * G:(h + 1) * G] = l.T.cpu()
+            l = l.double()[..., None]
+            p = torch.exp(z - l)
+            err = p * (140 * R.U32 * (w.scale * x.abs() @ k.abs().T) + 8 * R.U32 *
+                       (z.masked_fill(hidden, 0).abs() + l.abs()) + 2.0 ** -20)
+            tot, e = p.sum((0, 1)).cpu(), err.sum((0, 1)).cpu()
+            before = old[s, h, :c].double()
+            before[c - L:] = 0
+            ref[s, h, :c] = before + tot
+            tol[s, h, :c] = 2 * e + L * G * R.U32 * tot + 2 * R.U32 * (before + tot) + 1e-37
+    got = old.cuda()
+    weights_call(db, w, fmt, lse, got, True)
+    ok()
+    d = (got.cpu().double() - ref).abs()
+    assert (d <= tol).all(), float((d - tol).max())
+    again = old.cuda()
+    weights_call(db, w, fmt, lse, again, True)
+    assert same_bits(again, got)
+
+
 @pytest.mark.parametrize("mq", [1, 512])
 def test_weights_bad_windows_are_flagged_and_keep_theirs(mq):
     ctx, ql = [60, 100, 30], [8, 8, 8]
@@ -257,9 +301,7 @@ def test_evict_ties_and_odd_weights(kind):
     else:
         x = -x
     # 1e-42 is below fp32's normal range; a key is its bits, so it counts as it is
-    check_evict("bf16", [700, 300, 513], [333, 17, 512], 400 if kind != "equal" else 512, 2, 5,
-                x, hkv=2) if kind == "equal" else \
-        check_evict("bf16", [700, 300, 400], [333, 17, 399], 400, 2, 5, x, hkv=2)
+    check_evict("bf16", [700, 300, 513], [333, 17, 512], 512, 2, 5, x, hkv=2)
 
 
 def test_evict_to_nothing_and_protected_only():
@@ -272,6 +314,22 @@ def test_evict_long_context():
     g = torch.Generator().manual_seed(37)
     check_evict("bf16", [20011, 9000], [4096, 8999], 8999, 4, 512, heavy(g, 2, 1, 20016), hkv=1)
     check_evict("fp8", [12345], [12000], 12000, 0, 0, heavy(g, 1, 2, 12352), hkv=2)
+
+
+def test_evict_many_heads():
+    # more (sequence, KV head) pairs than fill the GPU: one CTA each, many waves
+    g = torch.Generator().manual_seed(45)
+    ctx = [900 - 11 * i for i in range(20)]
+    for fmt in ("bf16", "int8"):
+        check_evict(fmt, ctx, [c - 200 + 7 * (i % 5) for i, c in enumerate(ctx)], 800, 2, 100,
+                    heavy(g, 20, 8, 912))
+
+
+def test_evict_slices_longer_than_shared_memory():
+    g = torch.Generator().manual_seed(46)
+    x = heavy(g, 1, 1, 170011)
+    x[0, 0, ::3] = 0.25
+    check_evict("bf16", [170011], [60001], 60001, 4, 1000, x, hkv=1)
 
 
 def test_evict_bad_values_are_flagged_and_change_nothing():

@@ -385,3 +385,89 @@ def test_rows_past_four_gigabytes():
     ok()
     assert same_bits(kc[-64:], kref) and new.tolist() == [434, 329]
     assert math.prod(kc.shape) * 2 > 1 << 32
+
+
+# ---------------------------------------------------------------------------
+# sizes at which every ring of stages wraps and segments are cut, against 64-bit
+# matrix products on the GPU
+# ---------------------------------------------------------------------------
+
+def dense_reference(w, kc, vc, mask):
+    """tree_attention's results and tolerances as matrix products in 64 bits."""
+    Tq, Hq, D = w.q.shape
+    Hkv = w.num_kv_heads
+    G = Hq // Hkv
+    out = torch.zeros(Tq, Hq, D, dtype=torch.float64)
+    tol, lse, ltol = torch.zeros_like(out), torch.zeros(Tq, Hq).double(), torch.zeros(Tq, Hq).double()
+    q = w.q.cuda().double()
+    for s in range(w.num_seqs):
+        a, b, c = int(w.cu_seqlens_q[s]), int(w.cu_seqlens_q[s + 1]), int(w.context_lens[s])
+        L = b - a
+        if L == 0:
+            continue
+        hidden = torch.zeros(L, c, dtype=torch.bool)
+        for j in range(L):
+            hidden[j, c - L:] = ~R.bits_to_bool(mask[a + j].numpy(), L)
+        hidden = hidden.cuda()
+        ids = w.block_tables[s, :(c + 15) // 16].long().cuda()
+        for h in range(Hkv):
+            k = kc[ids, h].reshape(-1, D)[:c].double()
+            v = vc[ids, h].reshape(-1, D)[:c].double()
+            x = q[a:b, h * G:(h + 1) * G].transpose(0, 1)
+            z = (w.scale * x @ k.T).masked_fill(hidden, float("-inf"))
+            big = (w.scale * x.abs() @ k.abs().T).masked_fill(hidden, 0).amax(-1, keepdim=True)
+            p = torch.softmax(z, -1)
+            o, spread = p @ v, p @ v.abs()
+            ez = 136 * R.U32 * big + 2.0 ** -21
+            out[a:b, h * G:(h + 1) * G] = o.transpose(0, 1).cpu()
+            tol[a:b, h * G:(h + 1) * G] = (R.UBF * (1 + R.UBF) * (o.abs() + spread)
+                                           + 4 * ez * spread + 2.0 ** -30).transpose(0, 1).cpu()
+            l = torch.logsumexp(z, -1)
+            lse[a:b, h * G:(h + 1) * G] = l.T.cpu()
+            ltol[a:b, h * G:(h + 1) * G] = (2 * ez[..., 0] + 4 * R.U32 * l.abs()).T.cpu()
+    return out, lse, tol, ltol
+
+
+@pytest.mark.parametrize("hq,hkv,ctx,ql", [
+    (16, 8, [6001, 3333, 128, 5000, 40, 4097], [64, 40, 33, 64, 7, 64]),      # a tile a window
+    (32, 4, [9000, 5555, 2500], [64, 61, 50]),                                # four: pairs of CTAs
+    (24, 4, [4000, 8191, 700], [64, 64, 22]),                                 # groups of 6, two padding rows
+    (16, 8, [8000, 3001, 17, 6400, 5], [8, 5, 8, 1, 3]),                      # warp tiles
+    (16, 8, [300 + 37 * i for i in range(40)], [1 + i % 8 for i in range(40)]),
+])
+def test_large_batches(hq, hkv, ctx, ql):
+    w = W.build("large", 20, ctx, ql, pool_factor=1.1, num_q_heads=hq, num_kv_heads=hkv,
+                outlier_frac=0.01)
+    g = torch.Generator().manual_seed(21)
+    mask = torch.from_numpy(R.tree_mask(R.random_parents(g, ql), w.cu_seqlens_q, 2)[0])
+    db = DeviceBatch(w)
+    ref = dense_reference(w, db.kc, db.vc, mask)
+    out, lse = tree_call(db, mask.cuda())
+    ok()
+    R.assert_tree_close(out, lse, ref, f"large {hq}/{hkv}")
+    out2, lse2 = tree_call(db, mask.cuda(), fill=0)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+def test_two_streams_at_once():
+    # two batches, each call with its own workspace, interleaved on two streams
+    ql = [[64, 40], [8, 3]]
+    ws, dbs, masks = [], [], []
+    for i in range(2):
+        w = W.build("two", 22 + i, [3000, 1500], ql[i], pool_factor=1.1)
+        g = torch.Generator().manual_seed(24)
+        dbs.append(DeviceBatch(w))
+        masks.append(torch.from_numpy(R.tree_mask(R.random_parents(g, ql[i]), w.cu_seqlens_q, 2)[0]))
+        ws.append(w)
+    refs = [dense_reference(w, db.kc, db.vc, m) for w, db, m in zip(ws, dbs, masks)]
+    dm = [m.cuda() for m in masks]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i] = tree_call(dbs[i], dm[i])
+    ok()
+    for i in range(2):
+        R.assert_tree_close(*got[i], refs[i], f"stream {i}")
