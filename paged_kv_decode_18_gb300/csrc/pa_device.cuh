@@ -194,6 +194,45 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a
 }
 
 // ---------------------------------------------------------------------------
+// merge of many pieces: groups of warps each merge every GROUPS-th round of a
+// row's pieces and leave (maximum, sum, 16 dims a lane) in shared memory, from
+// which the first group takes the row
+// ---------------------------------------------------------------------------
+constexpr int kMergeRow = kHeadDim + 4;  // floats: the dims, then maximum and sum
+
+__device__ __forceinline__ void merge_store(float* row, int d0, float m, float sum,
+                                            const float (&acc)[16]) {
+  float4* dst = reinterpret_cast<float4*>(row + d0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    dst[k] = make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+  if (d0 == 0) {
+    row[kHeadDim] = m;
+    row[kHeadDim + 1] = sum;
+  }
+}
+
+__device__ __forceinline__ void merge_take(const float* row, int d0, float& m, float& sum,
+                                           float (&acc)[16]) {
+  const float mo = row[kHeadDim], so = row[kHeadDim + 1];
+  if (mo == neg_inf()) return;
+  if (mo != mo) m = sum = mo;  // a NaN stays one
+  const float mn = fmaxf(m, mo);
+  const float mine = m == neg_inf() ? 0.f : ex2((m - mn) * kLog2e), other = ex2((mo - mn) * kLog2e);
+  sum = sum * mine + so * other;
+  const float4* src = reinterpret_cast<const float4*>(row + d0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 x = src[k];
+    acc[4 * k + 0] = fmaf(x.x, other, acc[4 * k + 0] * mine);
+    acc[4 * k + 1] = fmaf(x.y, other, acc[4 * k + 1] * mine);
+    acc[4 * k + 2] = fmaf(x.z, other, acc[4 * k + 2] * mine);
+    acc[4 * k + 3] = fmaf(x.w, other, acc[4 * k + 3] * mine);
+  }
+  m = mn;
+}
+
+// ---------------------------------------------------------------------------
 // tree masks: row of 32-bit words, bit i of word i / 32 = window key i is seen
 // ---------------------------------------------------------------------------
 

@@ -442,7 +442,8 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, int kv_format, const int32
   auto kernel = q8 ? evict_kernel<true> : evict_kernel<false>;
   if (!raise_smem_limit(reinterpret_cast<const void*>(kernel))) return PA_ERR_CUDA;
   // clusters as large as leave every (sequence, KV head) resident at two CTAs an
-  // SM, but no larger than a slice of 1024 positions calls for
+  // SM (twice as large, in two rounds: 41 us against 28.6 us at 8 x 32k), but no
+  // larger than a slice of 1024 positions calls for
   const int64_t heads = (int64_t)shape->num_seqs * a.Hkv;
   const int64_t most = (int64_t)a.max_blocks * kBlock / 1024;
   int cluster = 1;

@@ -426,9 +426,11 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const float a_me = pend_m == neg_inf() ? 0.f : ex2(pend_m - M);
       const float a_o = m_o == neg_inf() ? 0.f : ex2(m_o - M);
       const float lt = pend_l * a_me + l_o * a_o;
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;
+      // (TREE: a NaN score's NaN goes on into the row's results)
+      const bool any_weight = TREE ? lt != 0.f : lt > 0.f;
+      const float inv = any_weight ? 1.f / lt : 0.f;
       const float c0 = (hf == 0 ? a_me : a_o) * inv, c1 = (hf == 0 ? a_o : a_me) * inv;
-      const float lse_v = lt > 0.f ? (M + lg2(lt)) * kLn2 : neg_inf();
+      const float lse_v = any_weight ? (M + lg2(lt)) * kLn2 : neg_inf();
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         const int d0 = hf * 64 + cc * 32;  // output dims d0 .. d0+31
@@ -712,9 +714,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 // CTAs. Grid (CTA boundary, quarter of the tile's rows); eight lanes per
 // query row, so each piece's row is one coalesced 512-byte read and a warp has
 // four rows' loads in flight.
+// GROUPS > 1: that many groups of the CTA's warps share its rows' pieces.
 constexpr int kFixRowsPerCta = 32;
 constexpr int kFixThreads = 256;
+constexpr int kFixGroupsT = 4;
 
+template <int GROUPS>
 __global__ void __launch_bounds__(kFixThreads)
     prefill_tc_fixup_kernel(const TcArgs a) {
   // the next grid in the stream may start its own preparation now; it waits
@@ -732,16 +737,20 @@ __global__ void __launch_bounds__(kFixThreads)
     return (size_t)(((w - 1 + i) << a.pair) + odd) * 2 + (i == 0 ? slot_prev : 0);
   };
   // a warp merges four rows at once: eight lanes per row, sixteen dims per lane
-  const int r = blockIdx.y * kFixRowsPerCta + warp * 4 + (lane >> 3);
+  constexpr int kRowWarps = kFixThreads / 32 / GROUPS;
+  const int group = warp / kRowWarps, rl = (warp % kRowWarps) * 4 + (lane >> 3);
+  const int r = blockIdx.y * (kFixRowsPerCta / GROUPS) + rl;
   const int dim0 = (lane & 7) * 16;
   const int tok = ((qt << a.pair) + odd) * a.QTb + r / a.G;
-  if (r >= a.QTb * a.G || tok >= lq) return;  // padding rows
+  const bool live = r < a.QTb * a.G && tok < lq;  // not a padding row
+  if (GROUPS == 1 && !live) return;
   // online merge over the pieces, four at a time with all their loads in flight
   float m = neg_inf(), sum = 0.f;
+  bool nan = false;  // a piece with a NaN score: the row's results are NaNs
   float acc[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-  for (int i0 = 0; i0 < npieces; i0 += 4) {
+  for (int i0 = 4 * group; live && i0 < npieces; i0 += 4 * GROUPS) {
     float li[4];
     float4 x[4][4];
 #pragma unroll
@@ -758,6 +767,8 @@ __global__ void __launch_bounds__(kFixThreads)
       }
     }
     const float mn = fmaxf(fmaxf(m, fmaxf(li[0], li[1])), fmaxf(li[2], li[3]));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) nan = nan || li[u] != li[u];
     if (mn == neg_inf()) continue;
     const float shrink = m == neg_inf() ? 0.f : ex2((m - mn) * kLog2e);
     sum *= shrink;
@@ -777,10 +788,18 @@ __global__ void __launch_bounds__(kFixThreads)
     }
     m = mn;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  if (nan) m = sum = __int_as_float(0x7fc00000);
+  if constexpr (GROUPS > 1) {
+    __shared__ __align__(16) float left[GROUPS - 1][kFixRowsPerCta / GROUPS][kMergeRow];
+    if (group > 0 && live) merge_store(left[group - 1][rl], dim0, m, sum, acc);
+    __syncthreads();
+    if (group > 0 || !live) return;
+    for (int g = 0; g < GROUPS - 1; ++g) merge_take(left[g][rl], dim0, m, sum, acc);
+  }
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] *= inv;
-  const float LSE = sum > 0.f ? m + lg2(sum) * kLn2 : neg_inf();
+  const float LSE = sum != 0.f ? m + lg2(sum) * kLn2 : neg_inf();
   const int64_t orow = out_row(a, (int64_t)q0 + tok, h * a.G + r % a.G);
   if (orow < 0) return;
   if (a.rows.o) {
@@ -894,9 +913,14 @@ static int launch_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf16
                                   g.smem, st, tmq, tmk, tmv, a);
     if (e != cudaSuccess) return PA_ERR_CUDA;
   }
-  if ((parts & 2) && launch_dependent(prefill_tc_fixup_kernel, dim3(g.workers, kRowsT / kFixRowsPerCta),
-                       dim3(kFixThreads), 0, st, a) != cudaSuccess)
-    return PA_ERR_CUDA;
+  if (parts & 2) {
+    // trees over few contexts: more than eight pieces to a segment on average
+    const bool many = a.mask && (int64_t)g.workers > 8 * (int64_t)a.S * a.Hkv;
+    const dim3 grid(g.workers, kRowsT / kFixRowsPerCta * (many ? kFixGroupsT : 1));
+    if (launch_dependent(many ? prefill_tc_fixup_kernel<kFixGroupsT> : prefill_tc_fixup_kernel<1>,
+                         grid, dim3(kFixThreads), 0, st, a) != cudaSuccess)
+      return PA_ERR_CUDA;
+  }
   return PA_OK;
 }
 
@@ -939,9 +963,9 @@ int launch_tree_tc(const PrefillTcGeometry& g, const pa_bf16* q, const pa_bf16* 
   a.mask = tree_mask;
   a.mask_words = mask_words;
   a.v_cache = v_cache;
-  // windows of two tiles and more, on average nearly: the second tile of a unit
-  // is seldom missing
-  a.pair = num_q_tokens * (sh->num_q_heads / sh->num_kv_heads) > (int64_t)kRowsT * 3 / 2 * sh->num_seqs;
+  // windows of more than one tile on average: the second tile of a unit is seldom
+  // missing (and costs nothing of the bandwidth that bounds the call where it is)
+  a.pair = num_q_tokens * (sh->num_q_heads / sh->num_kv_heads) > (int64_t)kRowsT * 17 / 16 * sh->num_seqs;
   return launch_tc(g, q, k_cache, v_cache, a, num_q_tokens, scale, sh, workspace, st, 3);
 }
 

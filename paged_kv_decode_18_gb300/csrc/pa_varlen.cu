@@ -230,6 +230,9 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
   float m_r[2], l_r[2];
   int lim[2] = {0, 0}, lim_min = 0, lq = 0, ctx = 0;
   const uint32_t* mrow[2] = {nullptr, nullptr};  // TREE: mask rows (null: padding)
+  // a row's sum of weights is no empty one (TREE: a NaN score's NaN goes on into
+  // the row's results)
+  auto any_weight = [](float l) { return TREE ? l != 0.f : l > 0.f; };
   // query token of tile row r (padding rows: past every window)
   auto token_of = [&](int qt, int r) -> int {
     if constexpr (TREE)
@@ -480,20 +483,20 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
           if (tok >= lq) continue;
           const int g = rows[i] % G;
           const int64_t orow = ((int64_t)P.qstart[cp.s] + tok) * Hq + (int64_t)cp.h * G + g;
-          const float inv = lt[i] > 0.f ? 1.f / lt[i] : 0.f;
+          const float inv = any_weight(lt[i]) ? 1.f / lt[i] : 0.f;
           uint16_t* dst = a.out + orow * kHeadDim + quad * 2;
 #pragma unroll
           for (int n = 0; n < 16; ++n)
             *reinterpret_cast<uint32_t*>(dst + n * 8) =
                 cvt_bf16x2(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
           if (a.lse && quad == 0)
-            a.lse[orow] = lt[i] > 0.f ? (m_r[i] + lg2(lt[i])) * kLn2 : neg_inf();
+            a.lse[orow] = any_weight(lt[i]) ? (m_r[i] + lg2(lt[i])) * kLn2 : neg_inf();
         }
       } else {
         const size_t slot = (size_t)w * 2 + (piece_first ? 0 : 1);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float inv = lt[i] > 0.f ? 1.f / lt[i] : 0.f;
+          const float inv = any_weight(lt[i]) ? 1.f / lt[i] : 0.f;
           float* dst = a.part_o + (slot * kRows + rows[i]) * kHeadDim + quad * 2;
 #pragma unroll
           for (int n = 0; n < 16; ++n)
@@ -501,7 +504,7 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
                 make_float2(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
           if (quad == 0)
             a.part_lse[slot * kRows + rows[i]] =
-                lt[i] > 0.f ? (m_r[i] + lg2(lt[i])) * kLn2 : neg_inf();
+                any_weight(lt[i]) ? (m_r[i] + lg2(lt[i])) * kLn2 : neg_inf();
         }
       }
     }
@@ -524,9 +527,14 @@ __global__ void __launch_bounds__(NWARPS * 32)
 // once (eight lanes per row, sixteen dims per lane), online over the pieces,
 // four pieces at a time with all their loads in flight. Partials are read
 // through L2 (ld.global.cg): other SMs wrote them.
+// GROUPS > 1: that many groups of warps share the pieces of a CTA's rows (few
+// segments in many pieces: a tree over one 7,000-key context, 114 pieces, spent
+// 23 of its 34 us in one group's rounds).
 constexpr int kFixWarps = kRows / 4;
+constexpr int kFixGroups = 4;
 
-__global__ void __launch_bounds__(kFixWarps * 32)
+template <int GROUPS>
+__global__ void __launch_bounds__(kFixWarps * 32 * GROUPS)
     varlen_fixup_kernel(const int* __restrict__ desc, const float* __restrict__ part_o,
                         const float* __restrict__ part_lse,
                         const int32_t* __restrict__ cu_seqlens_q, int num_workers, int Hq, int G,
@@ -543,17 +551,20 @@ __global__ void __launch_bounds__(kFixWarps * 32)
   const int qt = __ldcg(d + 1), h = __ldcg(d + 2), last = __ldcg(d + 3),
             slot_prev = __ldcg(d + 4);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = warp * 4 + (lane >> 3);
+  const int group = warp / kFixWarps;
+  const int r = (warp % kFixWarps) * 4 + (lane >> 3);
   const int d0 = (lane & 7) * 16;
   const int q0 = cu_seqlens_q[s], lq = cu_seqlens_q[s + 1] - q0;
   const int tok = qt * QT + r / G;
-  if (r >= QT * G || tok >= lq) return;  // padding rows
+  const bool live = r < QT * G && tok < lq;  // not a padding row
+  if (GROUPS == 1 && !live) return;
   const int npieces = last - w + 2;  // workers w-1 .. last
   float m = neg_inf(), sum = 0.f;
+  bool nan = false;  // a piece with a NaN score: the row's results are NaNs
   float acc[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-  for (int i0 = 0; i0 < npieces; i0 += 4) {
+  for (int i0 = 4 * group; live && i0 < npieces; i0 += 4 * GROUPS) {
     float li[4];
     float4 x[4][4];
 #pragma unroll
@@ -569,6 +580,8 @@ __global__ void __launch_bounds__(kFixWarps * 32)
       }
     }
     const float mn = fmaxf(fmaxf(m, fmaxf(li[0], li[1])), fmaxf(li[2], li[3]));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) nan = nan || li[u] != li[u];
     if (mn == neg_inf()) continue;
     const float shrink = m == neg_inf() ? 0.f : ex2((m - mn) * kLog2e);
     sum *= shrink;
@@ -588,8 +601,16 @@ __global__ void __launch_bounds__(kFixWarps * 32)
     }
     m = mn;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const float LSE = sum > 0.f ? m + lg2(sum) * kLn2 : neg_inf();
+  if (nan) m = sum = __int_as_float(0x7fc00000);
+  if constexpr (GROUPS > 1) {
+    __shared__ __align__(16) float left[GROUPS - 1][kRows][kMergeRow];
+    if (group > 0 && live) merge_store(left[group - 1][r], d0, m, sum, acc);
+    __syncthreads();
+    if (group > 0 || !live) return;
+    for (int g = 0; g < GROUPS - 1; ++g) merge_take(left[g][r], d0, m, sum, acc);
+  }
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  const float LSE = sum != 0.f ? m + lg2(sum) * kLn2 : neg_inf();
   const int64_t orow = ((int64_t)q0 + tok) * Hq + (int64_t)h * G + r % G;
   uint4* dst = reinterpret_cast<uint4*>(out + orow * kHeadDim + d0);
   dst[0] = make_uint4(cvt_bf16x2(acc[0] * inv, acc[1] * inv), cvt_bf16x2(acc[2] * inv, acc[3] * inv),
@@ -662,10 +683,20 @@ int check_tree_args(const pa_shape* shape, int64_t num_q_tokens, int max_q_len) 
 
 // The kernel of a tree call: the warp tile of 16 rows while a window's rows of
 // a KV head (query tokens x group) fit one such tile, so that the cache is
-// read once; else the tcgen05 tile of 128 rows.
+// read once; else the tcgen05 tile of 128 rows -- unless two warp tiles hold the
+// rows and the whole call is surely no more than kSmallTree tiles of 16 rows x 16
+// keys, whose start costs less than a tcgen05 grid's (3 sequences of 100..422
+// keys, 20 rows: 14 us against 19 us; with three row tiles, 21 sequences of
+// 56..88 keys and 40 rows, it is 16 us against 13 us the other way).
+constexpr int64_t kSmallTree = 2048;
+
 bool tree_on_tc(const pa_shape* shape, int max_q_len) {
   const int G = shape->num_q_heads / shape->num_kv_heads;
-  return G > kRows || max_q_len > kRows / G;
+  if (G > kRows) return true;
+  const int64_t row_tiles = (max_q_len + kRows / G - 1) / (kRows / G);
+  return row_tiles > 2 ||
+         (row_tiles == 2 && 2LL * shape->num_seqs * shape->num_kv_heads *
+                                    shape->max_blocks_per_seq > kSmallTree);
 }
 
 }  // namespace
@@ -819,7 +850,7 @@ extern "C" int pa_decode_varlen(const pa_bf16* q, const pa_bf16* k_cache, const 
                            kTcMinQLen, nullptr, nullptr, /*parts=*/2, /*split=*/1);
     if (rc != PA_OK) return rc;
   }
-  if (launch_dependent(varlen_fixup_kernel, dim3(g.workers), dim3(kFixWarps * 32), 0, st,
+  if (launch_dependent(varlen_fixup_kernel<1>, dim3(g.workers), dim3(kFixWarps * 32), 0, st,
                        (const int*)a.desc, (const float*)a.part_o, (const float*)a.part_lse,
                        cu_seqlens_q, g.workers, a.Hq, a.G, a.QT, (uint16_t*)out,
                        lse) != cudaSuccess)
@@ -912,10 +943,13 @@ extern "C" int pa_decode_tree(const pa_bf16* q, const pa_bf16* k_cache, const pa
   if (launch_dependent(paged_varlen_kernel<kWarps, kStages, true>, dim3(g.grid),
                        dim3(kWarps * 32), g.smem, st, tmk, tmv, a) != cudaSuccess)
     return PA_ERR_CUDA;
-  if (launch_dependent(varlen_fixup_kernel, dim3(g.workers), dim3(kFixWarps * 32), 0, st,
-                       (const int*)a.desc, (const float*)a.part_o, (const float*)a.part_lse,
-                       cu_seqlens_q, g.workers, a.Hq, a.G, a.QT, (uint16_t*)out,
-                       lse) != cudaSuccess)
+  // a worker boundary a piece: more than eight to a segment on average
+  const bool many = (int64_t)g.workers > 8 * (int64_t)a.S * a.Hkv;
+  const int fix_threads = kFixWarps * 32 * (many ? kFixGroups : 1);
+  if (launch_dependent(many ? varlen_fixup_kernel<kFixGroups> : varlen_fixup_kernel<1>,
+                       dim3(g.workers), dim3(fix_threads), 0, st, (const int*)a.desc,
+                       (const float*)a.part_o, (const float*)a.part_lse, cu_seqlens_q, g.workers,
+                       a.Hq, a.G, a.QT, (uint16_t*)out, lse) != cudaSuccess)
     return PA_ERR_CUDA;
   if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
   return PA_OK;

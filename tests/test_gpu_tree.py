@@ -187,7 +187,8 @@ def test_a_chain_equals_the_causal_window():
 
 
 @pytest.mark.parametrize("ctx,ql", [([40, 21], [8, 3]), ([700, 64, 150], [64, 64, 20]),
-                                    ([16, 130], [8, 8])])
+                                    ([16, 130], [8, 8]), ([3000, 1000], [8, 6]),
+                                    ([3000, 1000], [64, 40])])
 def test_infinities_and_nans_reach_only_those_who_see_them(ctx, ql):
     w = W.build("poison", 11, ctx, ql, pool_factor=1.2)
     g = torch.Generator().manual_seed(12)
@@ -215,7 +216,7 @@ def test_infinities_and_nans_reach_only_those_who_see_them(ctx, ql):
     sees_nan = torch.isnan(ref[0]).all(-1)
     assert sees_nan.any() and not sees_nan.all()
     got = out.cpu().double()
-    assert not torch.isfinite(got[sees_nan]).any()
+    assert torch.isnan(got[sees_nan]).all() and torch.isnan(lse.cpu()[sees_nan]).all()
     rest = ~sees_nan
     R.assert_tree_close(got[rest], lse.cpu()[rest], tuple(x[rest] for x in ref), "poison")
 
