@@ -20,6 +20,10 @@
 // holds twice over: all CTAs read their rows of a wave, the cluster meets, all
 // write. A wave's writes fall before every later wave's sources, so the next
 // wave's reads begin before the cluster has met.
+// Bound: HBM for large moves, the chain of passes and meetings for small ones.
+// 8 contexts of 30,000..32,768 positions, 8 KV heads, int8, cut to 4096: 28.5 us
+// for 148 MB (5.2 TB/s), about a third of it selection; 32 of 1030..1153, bf16, to
+// 1024: 25 us, of which DRAM moves 185 MB (44 us with a cold L2).
 #include "pa_device.cuh"
 #include "pa_host.h"
 #include "pa_rows.cuh"

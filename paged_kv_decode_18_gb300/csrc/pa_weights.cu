@@ -5,16 +5,21 @@
 // so one pass over K is enough (course README "Build an LLM Inference Engine
 // From Scratch", curriculum row "Memory & KV Cache": what a cache keeps).
 //
-// A warp owns 32 or 64 consecutive positions (two or four blocks) of one KV head and all of
-// their queries, so every weight has one writer and the sums have one order.
-// S^T = K Q^T on mma.sync m16n8k16: rows are positions, columns eight query
-// rows. K tiles arrive by 1-D bulk copies in a private ring of stages. The
-// contraction does not care in which order it meets the head dimensions, so a
-// lane takes whole 16-byte pieces of its two K rows and of its query column as
-// fragments: a step's two k pairs are neighbouring pairs of a piece. 8-bit
-// codes become f16 (exact), and q enters times the power of two that puts its
+// A warp owns 32 or 64 consecutive positions (two or four blocks) of one KV head
+// and all of their queries, so every weight has one writer and the sums have
+// one order. S^T = K Q^T on mma.sync m16n8k16: rows are positions, columns eight
+// query rows. K tiles arrive in a private ring of stages: bf16 by TMA with the
+// 128-byte swizzle for ldmatrix, 8-bit by 1-D bulk copies. There a lane takes
+// whole 16-byte pieces of its two rows of codes and of its query column, since
+// the contraction does not care in which order it meets the head dimensions: a
+// step's two k pairs are neighbouring pairs of a piece. The codes become f16
+// (exact), and q enters times the power of two that puts its
 // largest element in [2^14, 2^15) (exact: 8 significant bits; elements 2^-28
 // below the largest lose bits that the fp32 sum does not hold either).
+// Bound: the K stream. 8 contexts of 30,000..32,768 positions, one query: bf16
+// 86 us, 6.1 TB/s (0.90 of the measured copy rate); FP8 50 us, 5.7 TB/s (0.83). A
+// ragged step (256 sequences, log-uniform 1..4096): 51 us, 5.2 TB/s (0.77); about
+// 8 us of a call are its launch, the plan and the first copies' latency.
 #include "pa_device.cuh"
 #include "pa_host.h"
 #include "pa_weights.cuh"
@@ -24,12 +29,17 @@
 namespace pa {
 namespace {
 
-// blocks of a tile: enough to spread a tile's fixed work, few enough for ten
-// warps' stages (bf16: 2 measured better than 1 or 4; 8-bit: 4)
+// blocks of a tile: enough to spread a tile's fixed work (212 instructions a tile
+// against some 100 a block), few enough for ten warps' two stages. Ragged bf16
+// step: 52 us with two blocks, 62 us with four (six warps); 8 x 32k FP8: 57 us
+// with four, 66 us with two.
 template <int FMT>
 constexpr int kSubOf = FMT == PA_KV_BF16 ? 2 : 4;
 constexpr int kQRows = 8;                   // query rows that travel with a tile
-constexpr int kWgtTcRows = 16;  // windows with more query rows a KV head go to the tcgen05 kernel
+// Windows with more query rows a KV head go to the tcgen05 kernel. 16 contexts of
+// 1000..8192 positions, 16 / 24 rows: bf16 34 / 70 us here against 34 / 34 us
+// there, FP8 27 / 89 us against 45 / 45 us (its codes have to be widened).
+constexpr int kWgtTcRows = 16;
 
 // Four one-byte codes as two exact f16 pairs. int8: the byte with its sign bit
 // flipped is 128 + x, in the mantissa of a half it is 1024 + 128 + x.
@@ -69,12 +79,9 @@ constexpr int kOffLse = kOffQ + kQRows * kHeadDim * 2;
 constexpr int kSide = kOffLse + kQRows * 4;
 template <int FMT>
 constexpr int kStagesOf = 2;
-// CTAs per SM that the stages leave room for
-template <int FMT>
-constexpr int kCtasOf = FMT == PA_KV_BF16 ? 1 : 1;
-// warps of a CTA, at most (fewer when a large batch's plan needs the room)
-template <int FMT>
-constexpr int kWarpsOf = FMT == PA_KV_BF16 ? 10 : 10;
+// warps of a CTA (one an SM), as many as two stages each leave room for; fewer
+// when a large batch's plan needs the room
+constexpr int kWgtWarps = 10;
 
 // The B fragments of eight query rows (column = lane / 4), the lane's two
 // columns' log-sum-exps in log2 units, as a leading part and the rest, and the
@@ -160,7 +167,7 @@ __device__ __forceinline__ void load_q(const WeightArgs& a, const unsigned char*
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kWarpsOf<FMT> * 32, kCtasOf<FMT>)
+__global__ void __launch_bounds__(kWgtWarps * 32, 1)
     accumulate_weights_kernel(const __grid_constant__ CUtensorMap tmk, const WeightArgs a) {
   constexpr int kSub = kSubOf<FMT>, kTileKeys = kSub * kBlock;
   constexpr int kStages = kStagesOf<FMT>, kBytes = kTileOf<FMT>;
@@ -289,9 +296,7 @@ __global__ void __launch_bounds__(kWarpsOf<FMT> * 32, kCtasOf<FMT>)
       }
       const uint32_t d = smem_addr(ring + (stage * kSub + lane) * kBytes);
       if constexpr (FMT == PA_KV_BF16) {
-        const int y = (int)(((int64_t)phys * Hkv + pp.h) * kBlock);
-        tma_load_2d(d, &tmk, 0, y, bar);
-        tma_load_2d(d + kBlock * 128, &tmk, 64, y, bar);
+        tma_load_block(d, &tmk, (int)(((int64_t)phys * Hkv + pp.h) * (kBlock / 8)), bar);
       } else {
         bulk_copy_g2s(d, a.k_cache + ((int64_t)phys * Hkv + pp.h) * kBytes, kBytes, bar);
       }
@@ -363,7 +368,8 @@ __global__ void __launch_bounds__(kWarpsOf<FMT> * 32, kCtasOf<FMT>)
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
           const int ch = 2 * s + (mi >> 1);
-          ldsm_x4(blk + (ch >> 3) * (kBlock * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+          ldsm_x4(blk + (row >> 3) * 2048 + (ch >> 3) * 1024 + (row & 7) * 128 +
+                      (((ch & 7) ^ (row & 7)) << 4),
                   f[s][0], f[s][1], f[s][2], f[s][3]);
         }
       } else {
@@ -467,9 +473,9 @@ int launch_weights(const WeightArgs& a, const DeviceInfo& dev, cudaStream_t st) 
   CUtensorMap tmk = {};
   if (FMT == PA_KV_BF16) {
     if (a.num_blocks * a.Hkv * kBlock > 0x7fffffff) return PA_ERR_UNSUPPORTED;
-    if (!make_pool_map(&tmk, a.k_cache, a.num_blocks * a.Hkv * kBlock)) return PA_ERR_CUDA;
+    if (!make_block_map(&tmk, a.k_cache, a.num_blocks * a.Hkv * kBlock)) return PA_ERR_CUDA;
   }
-  int warps = kWarpsOf<FMT>;
+  int warps = kWgtWarps;
   while (warps > 0 && weights_smem<FMT>(a.S, warps) > (size_t)dev.max_smem_optin) --warps;
   if (warps == 0) return PA_ERR_UNSUPPORTED;
   const size_t smem = weights_smem<FMT>(a.S, warps);
