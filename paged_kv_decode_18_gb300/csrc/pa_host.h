@@ -196,6 +196,9 @@ bool make_pool_map(CUtensorMap* map, const void* pool, int64_t rows);
 // another every 2 KB in a tile and from tile to tile. (Two 2 KB boxes a tile, the
 // map above, held the tcgen05 kernels to 44 GB/s an SM.)
 bool make_block_map(CUtensorMap* map, const void* pool, int64_t rows);
+// The codes of one 8-bit pool array: [num_blocks * Hkv tiles][16 rows][128 bytes],
+// boxes of one tile, 128-byte swizzle (the row scales behind them are left out).
+bool make_code_map(CUtensorMap* map, const void* pool, int64_t tiles);
 // 3-D view of q (pa_prefill_tc.cu): boxes of QTb tokens x G heads x 64 dims.
 bool make_q_map(CUtensorMap* map, const void* q, int64_t num_q_tokens, int Hq, int G, int QTb);
 

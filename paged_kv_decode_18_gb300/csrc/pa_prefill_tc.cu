@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       }
       // P row r, keys of half hf, over the S columns this thread has read
       tmem_st32(tS, pk);
-      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tmem_wait_st();
       // keys past the context may hold anything (even NaN): zero their V rows
       // so that P = 0 never meets them (thread (r, hf) clears half hf of key row r)
       const int key0 = t.b * kKeysT;

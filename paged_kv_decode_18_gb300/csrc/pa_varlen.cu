@@ -739,6 +739,18 @@ bool make_block_map(CUtensorMap* map, const void* pool, int64_t rows) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_code_map(CUtensorMap* map, const void* pool, int64_t tiles) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)kBlock, (cuuint64_t)tiles};
+  cuuint64_t strides[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)kInt8TileBytes};
+  cuuint32_t box[3] = {(cuuint32_t)kHeadDim, (cuuint32_t)kBlock, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 unsigned take_error_word_varlen(cudaStream_t stream, int* rc) {
   unsigned v = 0, zero = 0;
   if (cudaStreamSynchronize(stream) != cudaSuccess ||

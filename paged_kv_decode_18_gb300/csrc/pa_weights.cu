@@ -38,7 +38,7 @@ constexpr int kSubOf = FMT == PA_KV_BF16 ? 2 : 4;
 constexpr int kQRows = 8;                   // query rows that travel with a tile
 // Windows with more query rows a KV head go to the tcgen05 kernel. 16 contexts of
 // 1000..8192 positions, 16 / 24 rows: bf16 34 / 70 us here against 34 / 34 us
-// there, FP8 27 / 89 us against 45 / 45 us (its codes have to be widened).
+// there, FP8 27 / 89 us against 42 / 42 us (its codes have to be widened).
 constexpr int kWgtTcRows = 16;
 
 // Four one-byte codes as two exact f16 pairs. int8: the byte with its sign bit

@@ -10,24 +10,24 @@
 // 128 keys) with all of the window's query tiles, so a weight has one writer
 // and its sum one order. One CTA per SM, warp-specialised:
 //   warp 0     K producer: eight 16-key pool blocks a tile through the block
-//              table (bf16: 4-D TMA with the 128-byte swizzle; 8-bit: bulk
-//              copies of the raw tiles);
+//              table (4-D TMA, 8-bit codes 3-D, with the 128-byte swizzle);
 //   warp 10    query tiles of 128 rows ((128/G) tokens x G heads, 3-D TMA) and
 //              their columns' log-sum-exps and causal limits;
 //   warps 1,11 tensor memory and, from one thread each, the products: 128 keys x
-//              up to 128 columns into one of four accumulators; they take the
+//              up to 128 columns into the next accumulator; they take the
 //              items in turn (one thread alone spends 2,000 cycles an item on
 //              waits, issue and commits, more than anything else of it takes);
 //   warps 2-9  the epilogue: two groups of four warps that take the items in
 //              turn, so that one's exponentials hide the other's waits (two
 //              threads a key with half the columns each, who met at every
-//              item's end, took 45 us where this takes 38);
-//   warps 12-15 (8-bit pools) turn the raw codes into a swizzled bf16 tile
-//              (exact); the row scales multiply the scores in the epilogue.
+//              item's end, took 45 us where this took 38);
+//   warps 12-15 (8-bit pools) turn the raw codes into bf16 (exact) in tensor
+//              memory, where the products take them from; the row scales
+//              multiply the scores in the epilogue.
 // Bound: windows of up to 128 rows by the K stream and the call's start: 16
 // contexts of 1000..8192 positions with 64 queries of two heads (157 MB) take
-// 37.8 us, 35.5 us with the exponentials left out and 33.9 us with all of the
-// epilogue's column work left out. Longer windows are bound by the epilogue
+// 35.5 us in bf16, 33.9 us with all of the epilogue's column work left out; FP8
+// codes (81 MB) 43.5 us, 38.7 us without their conversion. Longer windows are bound by the epilogue
 // (16 k exponentials a 128 x 128 tile) beside 0.27 us of tensor time.
 #include <cudaTypedefs.h>
 
@@ -44,25 +44,28 @@ constexpr int kCols = 128;                    // query rows per tile (MMA N, at 
 constexpr int kBlocksK = kKeys / kBlock;
 constexpr int kHalfB = 128 * 128;             // 64 dims of a 128-row bf16 operand
 constexpr int kOperand = 2 * kHalfB;
-constexpr int kRawTile = kBlocksK * kInt8TileBytes;  // the raw codes and scales of an item
-constexpr int kRawStages = 4;
-constexpr int kDBufs = 4;                     // accumulators in tensor memory
+constexpr int kCodes = kKeys * kHeadDim;      // the raw codes of an item
+constexpr int kRawTile = kCodes + 1024;       // and its row scales
 constexpr int kScaleSlots = 8;                // items whose row scales are kept (see below)
 constexpr int kEpiWarps = 8;
 constexpr int kQWarp = 2 + kEpiWarps;
 constexpr int kMma2Warp = kQWarp + 1;
 constexpr int kConvWarps = 4;
 
-constexpr int kNumBarsMax = 32;
+constexpr int kNumBarsMax = 40;
 
 template <int FMT>
 struct Lay {
   static constexpr bool q8 = FMT != PA_KV_BF16;
-  static constexpr int kStages = q8 ? 2 : 4;  // bf16 K tiles
+  // bf16 K tiles: in shared memory, or widened into tensor memory (64 columns each)
+  static constexpr int kStages = q8 ? 2 : 4;
+  static constexpr int kRawStages = 6;        // of raw 8-bit tiles
+  static constexpr int kDBufs = q8 ? 3 : 4;   // accumulators in tensor memory
+  static constexpr int kATmem = kDBufs * kCols;
+  static_assert(kATmem + (q8 ? kStages * kHeadDim / 2 : 0) <= 512, "tensor memory");
   static constexpr int q = 0;                 // two query tiles
-  static constexpr int k = q + 2 * kOperand;
-  static constexpr int raw = k + kStages * kOperand;
-  static constexpr int bars = raw + (q8 ? kRawStages * kRawTile : 0);
+  static constexpr int k = q + 2 * kOperand;  // K as it arrives
+  static constexpr int bars = k + (q8 ? kRawStages * kRawTile : kStages * kOperand);
   static constexpr int misc = bars + kNumBarsMax * 8;  // tmem slot, abort flag
   static constexpr int l2 = misc + 16;              // [2][128] -log-sum-exp, log2 units
   static constexpr int last = l2 + 2 * kCols * 4;   // [2][128] last key seen; -1: no query
@@ -74,7 +77,7 @@ struct Lay {
 
 enum : int {
   B_KFULL = 0, B_KEMPTY = 4, B_QFULL = 8, B_QEMPTY = 10, B_DFULL = 12, B_DEMPTY = 16,
-  B_RFULL = 20, B_REMPTY = 24, kNumBars = 28
+  B_RFULL = 20, B_REMPTY = 26, kNumBars = 32
 };
 
 static_assert(kNumBars <= kNumBarsMax, "barrier area");
@@ -153,6 +156,8 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
       mbar_init(bar(B_KEMPTY + i), 1u);
       mbar_init(bar(B_DFULL + i), 2u);  // the issuing thread and its commit
       mbar_init(bar(B_DEMPTY + i), kEpiWarps * 16u);  // the group that reads it
+    }
+    for (int i = 0; i < L::kRawStages; ++i) {
       mbar_init(bar(B_RFULL + i), 1u);
       mbar_init(bar(B_REMPTY + i), kConvWarps * 32u);
     }
@@ -165,7 +170,7 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
   }
   if (tid == 32) {
     prefetch_tensormap(&tmq);
-    if (!L::q8) prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmk);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
         flag_error(PA_DEVERR_BLOCK_RANGE);
         id = 0;
       }
-      constexpr int kRing = L::q8 ? kRawStages : L::kStages;
+      constexpr int kRing = L::q8 ? L::kRawStages : L::kStages;
       const int st = n % kRing;
       const uint32_t full = bar((L::q8 ? B_RFULL : B_KFULL) + st);
       if (n >= kRing &&
@@ -285,9 +290,12 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
       __syncwarp();
       if (lane < nb) {
         if constexpr (L::q8) {
-          bulk_copy_g2s(smem_addr(smem + L::raw + st * kRawTile + lane * kInt8TileBytes),
-                        a.k_cache + ((int64_t)id * Hkv + cur.h) * kInt8TileBytes, kInt8TileBytes,
-                        full);
+          // the codes with the 128-byte swizzle, the row scales behind the tile's codes
+          const int64_t tile = (int64_t)id * Hkv + cur.h;
+          unsigned char* raw = smem + L::k + st * kRawTile;
+          tma_load_3d(smem_addr(raw + lane * kBlock * kHeadDim), &tmk, 0, 0, (int)tile, full);
+          bulk_copy_g2s(smem_addr(raw + kCodes + lane * kBlock * 4),
+                        a.k_cache + tile * kInt8TileBytes + kBlock * kHeadDim, kBlock * 4, full);
         } else {
           const int group = (int)(((int64_t)id * Hkv + cur.h) * (kBlock / 8));
           tma_load_block(smem_addr(smem + L::k + st * kOperand + lane * kTileBytes), &tmk, group,
@@ -375,12 +383,12 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
               }
               ++qn;
             }
-            const int qb = (qn - 1) & 1, db = dn % kDBufs;
+            const int qb = (qn - 1) & 1, db = dn % L::kDBufs;
             if (!mine) {  // the other's; this one's products with the tile come first
               if (last_use) tc_commit(bar(B_QEMPTY + qb));
               continue;
             }
-            if (dn >= kDBufs && !wait(B_DEMPTY + db, (uint32_t)((dn / kDBufs) - 1) & 1u)) {
+            if (dn >= L::kDBufs && !wait(B_DEMPTY + db, (uint32_t)((dn / L::kDBufs) - 1) & 1u)) {
               ok = false;
               break;
             }
@@ -390,8 +398,13 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
             const uint64_t dq = desc_q + (uint64_t)(qb * (kOperand >> 4));
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              tc_mma(tmem + (uint32_t)db * kCols, dk + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4),
-                     dq + (uint64_t)(((k >> 2) * kHalfB + (k & 3) * 32) >> 4), idesc, k > 0);
+              const uint64_t dqk = dq + (uint64_t)(((k >> 2) * kHalfB + (k & 3) * 32) >> 4);
+              if constexpr (L::q8)
+                tc_mma_ts(tmem + (uint32_t)db * kCols,
+                          tmem + L::kATmem + st * (kHeadDim / 2) + k * 8, dqk, idesc, k > 0);
+              else
+                tc_mma(tmem + (uint32_t)db * kCols,
+                       dk + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4), dqk, idesc, k > 0);
             }
             tc_commit(bar(B_DFULL + db));
             mbar_arrive(bar(B_DFULL + db));
@@ -442,10 +455,10 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
             }
             ++qn;
           }
-          const int qb = (qn - 1) & 1, db = dn % kDBufs;
+          const int qb = (qn - 1) & 1, db = dn % L::kDBufs;
           if (mine == group) {
             const int cols = min(kCols, min(QTb, lq - qt * QTb) * G);
-            if (!wait(B_DFULL + db, (uint32_t)(dn / kDBufs) & 1u)) {
+            if (!wait(B_DFULL + db, (uint32_t)(dn / L::kDBufs) & 1u)) {
               ok = false;
               break;
             }
@@ -486,26 +499,18 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
                 }
               }
             };
-            // 32 columns at a time, the next ones on their way
-            uint32_t v0[32], v1[32];
-            tmem_ld32_async(ta, v0);
-            tmem_wait_ld(v0);
-            if (cols > 32) tmem_ld32_async(ta + 32u, v1);
-            columns(v0, 0);
-            if (cols > 32) {
-              tmem_wait_ld(v1);
-              if (cols > 64) tmem_ld32_async(ta + 64u, v0);
-              columns(v1, 32);
+            // 32 columns at a time; the other group's exponentials fill the wait for
+            // them. (With the next 32 on their way during these, an epilogue warp
+            // keeps its scheduler to itself: 37.9 us instead of 35.5 in bf16, 51
+            // instead of 43.5 in FP8, where the codes' conversion waits for it.)
+            uint32_t v0[32];
+#pragma unroll 1
+            for (int c0 = 0; c0 < cols; c0 += 32) {
+              tmem_ld32(ta + (uint32_t)c0, v0);
+              columns(v0, c0);
             }
-            if (cols > 64) {
-              tmem_wait_ld(v0);
-              if (cols > 96) tmem_ld32_async(ta + 96u, v1);
-              columns(v0, 64);
-            }
-            if (cols > 96) tmem_wait_ld(v1);
             tc_fence_before();
             mbar_arrive(bar(B_DEMPTY + db));
-            if (cols > 96) columns(v1, 96);
           }
           if (last_use) mbar_arrive(bar(B_QEMPTY + qb));
         }
@@ -520,62 +525,70 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
     }
   } else if constexpr (L::q8) {
     // -------------------------------------------------------------- codes to bf16
-    // thread = key row: 128 codes from the raw tile to two 128-byte swizzled
-    // halves. The chunk order is rotated by the lane, so a quarter-warp's reads
-    // fall into different banks. Row scales go to slot n mod 8: by the time
-    // slot n is written again, item n + 8's, the accumulator of item n + 2 has been
-    // read (two K stages and four accumulators lie between), by the group that
-    // took item n before it.
-    const int r = tid - 32 * (kMma2Warp + 1);
+    // thread = key row = tensor-memory lane: 128 codes of the swizzled raw tile to
+    // the 64 columns of a K operand, which the products read from tensor memory
+    // (a swizzled bf16
+    // tile in shared memory and the fence that it needs: 64 us instead of 61 for
+    // FP8 windows of 128 rows). The next item's codes are loaded while this one's
+    // stores end (61 -> 51 us).
+    // Row scales go to slot n mod 8: by the time slot n is written again, item
+    // n + 8's, the accumulator of item n has been read (K stages and accumulators
+    // between them hold fewer items).
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     float* kscale = reinterpret_cast<float*>(smem + L::scale);
-    Item t = item_at(P, S, Hkv, I0);
-    int n = 0;
-    for (int x = I0; x < I1; ++x) {
-      if (P.lq[t.s] > 0) {
-        const int rs = n % kRawStages, st = n % L::kStages;
-        if (!wait(B_RFULL + rs, (uint32_t)(n / kRawStages) & 1u)) break;
-        const unsigned char* raw =
-            smem + L::raw + rs * kRawTile + (r / kBlock) * kInt8TileBytes;
-        const bool here = r < P.ctx[t.s] - key_tile(t) * kKeys;
-        uint4 x16[8];
-        float scale = 0.f;
-        if (here) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            x16[i] = *reinterpret_cast<const uint4*>(raw + (r % kBlock) * kHeadDim +
-                                                     ((i + lane) & 7) * 16);
-          scale = *reinterpret_cast<const float*>(raw + kBlock * kHeadDim + (r % kBlock) * 4);
-        }
-        mbar_arrive(bar(B_REMPTY + rs));
-        if (n >= L::kStages &&
-            !wait(B_KEMPTY + st, (uint32_t)((n / L::kStages) - 1) & 1u))
-          break;
-        kscale[(n % kScaleSlots) * kKeys + r] = scale;
-        if (here) {
-          unsigned char* row = smem + L::k + st * kOperand + (r >> 3) * 2048 + (r & 7) * 128;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int ch = (i + lane) & 7;  // 16 codes: dims 16 ch .. 16 ch + 15
-            const uint32_t w[4] = {x16[i].x, x16[i].y, x16[i].z, x16[i].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              o[2 * u] = codes_to_bf16x2<FMT>(w[u] & 0xffffu);
-              o[2 * u + 1] = codes_to_bf16x2<FMT>(w[u] >> 16);
-            }
-            unsigned char* half = row + (ch >> 2) * 1024;
-            const int c2 = (ch & 3) * 2;
-            *reinterpret_cast<uint4*>(half + ((c2 ^ (r & 7)) << 4)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(half + (((c2 + 1) ^ (r & 7)) << 4)) =
-                make_uint4(o[4], o[5], o[6], o[7]);
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(B_KFULL + st));
-        ++n;
+    int m = 0;  // items with queries
+    {
+      Item t = item_at(P, S, Hkv, I0);
+      for (int x = I0; x < I1; ++x) {
+        m += P.lq[t.s] > 0;
+        if (x + 1 < I1) next_item(P, Hkv, t);
       }
-      if (x + 1 < I1) next_item(P, Hkv, t);
+    }
+    uint4 x16[8];  // 16 codes each; rows behind the context hold anything
+    float scale = 0.f;
+    auto load = [&](int n) {
+      const int rs = n % L::kRawStages;
+      const unsigned char* raw = smem + L::k + rs * kRawTile;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x16[i] = *reinterpret_cast<const uint4*>(raw + r * kHeadDim + ((i ^ (r & 7)) << 4));
+      scale = *reinterpret_cast<const float*>(raw + kCodes + r * 4);
+      mbar_arrive(bar(B_REMPTY + rs));
+    };
+    bool loaded = false;
+    for (int n = 0; n < m; ++n) {
+      const int st = n % L::kStages;
+      if (!loaded) {
+        if (!__all_sync(kFull, wait(B_RFULL + n % L::kRawStages, (uint32_t)(n / L::kRawStages) & 1u)))
+          break;
+        load(n);
+      }
+      if (n >= L::kStages &&
+          !__all_sync(kFull, wait(B_KEMPTY + st, (uint32_t)((n / L::kStages) - 1) & 1u)))
+        break;
+      tc_fence_after();
+      kscale[(n % kScaleSlots) * kKeys + r] = scale;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t o[32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = x16[half * 4 + i];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            codes_to_bf16<FMT>(w[u], o[8 * i + 2 * u], o[8 * i + 2 * u + 1]);
+        }
+        tmem_st32(tmem + lane_base + L::kATmem + st * (kHeadDim / 2) + half * 32, o);
+      }
+      // the next item's codes, if they are there, come while the stores end
+      loaded = n + 1 < m && __all_sync(kFull, mbar_test(bar(B_RFULL + (n + 1) % L::kRawStages),
+                                                            (uint32_t)((n + 1) / L::kRawStages) & 1u));
+      if (loaded) load(n + 1);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(B_KFULL + st));
     }
   }
 
@@ -614,7 +627,7 @@ int weights_tc_geometry(const pa_shape* sh, int max_q_len, int kv_format, Weight
   const int64_t tiles = (int64_t)sh->max_blocks_per_seq / kBlocksK + 1;
   const int64_t steps = (int64_t)(max_q_len + g->QTb - 1) / g->QTb + 1;
   if (steps > (int64_t(1) << 30) / sh->num_seqs / sh->num_kv_heads / tiles) return PA_OK;
-  if (kv_format == PA_KV_BF16 && sh->num_blocks * sh->num_kv_heads * kBlock > 0x7fffffff)
+  if (sh->num_blocks * sh->num_kv_heads * (kv_format == PA_KV_BF16 ? kBlock : 1) > 0x7fffffff)
     return PA_OK;
   if (!raise_smem_limit(kernel_of(kv_format))) return PA_ERR_CUDA;
   g->grid = dev.num_sms;
@@ -626,9 +639,8 @@ int launch_weights_tc(const WeightsTcGeometry& g, const WeightArgs& a, int kv_fo
                       cudaStream_t st) {
   CUtensorMap tmq, tmk;
   if (!make_q_map(&tmq, a.q, a.num_q_tokens, a.Hq, a.G, g.QTb)) return PA_ERR_CUDA;
-  tmk = tmq;  // unused by the 8-bit pools
-  if (kv_format == PA_KV_BF16 &&
-      !make_block_map(&tmk, a.k_cache, a.num_blocks * a.Hkv * kBlock))
+  if (kv_format == PA_KV_BF16 ? !make_block_map(&tmk, a.k_cache, a.num_blocks * a.Hkv * kBlock)
+                              : !make_code_map(&tmk, a.k_cache, a.num_blocks * a.Hkv))
     return PA_ERR_CUDA;
   TcWeightArgs t;
   t.w = a;
