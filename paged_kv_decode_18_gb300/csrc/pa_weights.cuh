@@ -57,6 +57,7 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t
 // batch does not fit it (group or plan size).
 struct WeightsTcGeometry {
   bool enabled = false;
+  bool split = false;  // a window may have several query tiles
   int grid = 0, QTb = 0;
   size_t smem = 0;
 };

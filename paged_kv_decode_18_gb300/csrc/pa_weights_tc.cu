@@ -26,9 +26,11 @@
 //              multiply the scores in the epilogue.
 // Bound: windows of up to 128 rows by the K stream and the call's start: 16
 // contexts of 1000..8192 positions with 64 queries of two heads (157 MB) take
-// 35.5 us in bf16, 33.9 us with all of the epilogue's column work left out; FP8
-// codes (81 MB) 43.5 us, 38.7 us without their conversion. Longer windows are bound by the epilogue
-// (16 k exponentials a 128 x 128 tile) beside 0.27 us of tensor time.
+// 36.2 us in bf16, 34.4 us with all of the epilogue's column work left out; FP8
+// codes (81 MB) 42.6 us, 4 us less without their conversion. Longer windows by the
+// chain of a tile through its two query buffers (load, product, epilogue): 1024
+// rows take 211 us, 0.83 us a tile, 157 us without the column work and still 155
+// without the queries' loads, beside 0.27 us of tensor time.
 #include <cudaTypedefs.h>
 
 #include "pa_device.cuh"
@@ -47,37 +49,44 @@ constexpr int kOperand = 2 * kHalfB;
 constexpr int kCodes = kKeys * kHeadDim;      // the raw codes of an item
 constexpr int kRawTile = kCodes + 1024;       // and its row scales
 constexpr int kScaleSlots = 8;                // items whose row scales are kept (see below)
+constexpr int kQBufs = 2;                     // query tiles in shared memory
+constexpr int kPartSlots = 8;                 // split items whose second half may wait (see below)
 constexpr int kEpiWarps = 8;
 constexpr int kQWarp = 2 + kEpiWarps;
 constexpr int kMma2Warp = kQWarp + 1;
 constexpr int kConvWarps = 4;
 
-constexpr int kNumBarsMax = 40;
+constexpr int kNumBarsMax = 48;
 
 template <int FMT>
 struct Lay {
   static constexpr bool q8 = FMT != PA_KV_BF16;
   // bf16 K tiles: in shared memory, or widened into tensor memory (64 columns each)
   static constexpr int kStages = q8 ? 2 : 4;
+  // An issuing thread waits for its own items' K only. It meets a stage at every
+  // use or never, so the phase that it waits for cannot be mistaken for an older
+  // one: the items, which the two take in turn, have to fill an even ring.
+  static_assert(kStages % 2 == 0, "a stage has one issuing thread");
   static constexpr int kRawStages = 6;        // of raw 8-bit tiles
   static constexpr int kDBufs = q8 ? 3 : 4;   // accumulators in tensor memory
   static constexpr int kATmem = kDBufs * kCols;
   static_assert(kATmem + (q8 ? kStages * kHeadDim / 2 : 0) <= 512, "tensor memory");
-  static constexpr int q = 0;                 // two query tiles
-  static constexpr int k = q + 2 * kOperand;  // K as it arrives
+  static constexpr int q = 0;                 // query tiles
+  static constexpr int k = q + kQBufs * kOperand;  // K as it arrives
   static constexpr int bars = k + (q8 ? kRawStages * kRawTile : kStages * kOperand);
   static constexpr int misc = bars + kNumBarsMax * 8;  // tmem slot, abort flag
-  static constexpr int l2 = misc + 16;              // [2][128] -log-sum-exp, log2 units
-  static constexpr int last = l2 + 2 * kCols * 4;   // [2][128] last key seen; -1: no query
-  static constexpr int clean = last + 2 * kCols * 4;  // [2] all 128 columns are queries
+  static constexpr int l2 = misc + 16;              // a query tile's 128 -log-sum-exps, log2 units
+  static constexpr int last = l2 + kQBufs * kCols * 4;   // last key seen; -1: no query
+  static constexpr int clean = last + kQBufs * kCols * 4;  // all 128 columns are queries
   static constexpr int scale = clean + 16;          // [kScaleSlots][128] row scales
-  static constexpr int plan = scale + (q8 ? kScaleSlots * kKeys * 4 : 0);
+  static constexpr int part = scale + (q8 ? kScaleSlots * kKeys * 4 : 0);
+  static constexpr int plan = part + kPartSlots * kKeys * 4;
   static constexpr int threads = 32 * (kMma2Warp + 1 + (q8 ? kConvWarps : 0));
 };
 
 enum : int {
-  B_KFULL = 0, B_KEMPTY = 4, B_QFULL = 8, B_QEMPTY = 10, B_DFULL = 12, B_DEMPTY = 16,
-  B_RFULL = 20, B_REMPTY = 26, kNumBars = 32
+  B_KFULL = 0, B_KEMPTY = 4, B_QFULL = 8, B_QEMPTY = 11, B_DFULL = 14, B_DEMPTY = 18,
+  B_RFULL = 22, B_REMPTY = 28, B_PART = 34, kNumBars = 42
 };
 
 static_assert(kNumBars <= kNumBarsMax, "barrier area");
@@ -131,7 +140,11 @@ __device__ __forceinline__ int key_tile(const Item& t) {
   return (t.i & 1) ? t.nt - 1 - (t.i >> 1) : t.i >> 1;
 }
 
-template <int FMT>
+// SPLIT: windows of several query tiles may come. Each group of the epilogue then
+// takes half the columns of all of an item's tiles, since an item's tiles fill all
+// accumulators and the other group would stand still (16 x 1000..8192 with windows
+// of 1024 rows: 232 -> 211 us; in a batch of single tiles the choice costs 1 us).
+template <int FMT, bool SPLIT>
 __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
     weights_tc_kernel(const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmk, const TcWeightArgs arg) {
@@ -155,13 +168,14 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
       mbar_init(bar(B_KFULL + i), L::q8 ? kConvWarps * 32u : 1u);
       mbar_init(bar(B_KEMPTY + i), 1u);
       mbar_init(bar(B_DFULL + i), 2u);  // the issuing thread and its commit
-      mbar_init(bar(B_DEMPTY + i), kEpiWarps * 16u);  // the group that reads it
+      mbar_init(bar(B_DEMPTY + i), kEpiWarps * 32u);
     }
     for (int i = 0; i < L::kRawStages; ++i) {
       mbar_init(bar(B_RFULL + i), 1u);
       mbar_init(bar(B_REMPTY + i), kConvWarps * 32u);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kPartSlots; ++i) mbar_init(bar(B_PART + i), kEpiWarps * 16u);
+    for (int i = 0; i < kQBufs; ++i) {
       mbar_init(bar(B_QFULL + i), 33u);  // warp 10's lanes and the expected bytes
       mbar_init(bar(B_QEMPTY + i), 2u + kEpiWarps * 32u);
     }
@@ -307,43 +321,66 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
     }
   } else if (warp == kQWarp) {
     // -------------------------------------------------------------- query tiles
-    Item t = item_at(P, S, Hkv, I0);
-    int qn = 0;
-    bool ok = true;
-    for (int x = I0; ok && x < I1; ++x) {
-      const int c = P.ctx[t.s], lq = P.lq[t.s], q0 = P.q0[t.s], nq = tiles_of(t);
-      if (fresh_q(t, nq, x)) {
-        for (int qt = nq > 1 ? first_tile(key_tile(t), c, lq, QTb) : 0; qt < nq; ++qt, ++qn) {
-          const int b = qn & 1;
-          if (qn >= 2 && !wait(B_QEMPTY + b, (uint32_t)((qn >> 1) - 1) & 1u)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(B_QFULL + b), (uint32_t)(QTb * G) * 256u);
-            const uint32_t d = smem_addr(smem + L::q + b * kOperand);
-            tma_load_3d(d, &tmq, 0, t.h * G, q0 + qt * QTb, bar(B_QFULL + b));
-            tma_load_3d(d + kHalfB, &tmq, 64, t.h * G, q0 + qt * QTb, bar(B_QFULL + b));
-          }
-          bool all = true;
+    // The log-sum-exps of the next tile are on their way while this one waits for
+    // its buffer (windows of 1024 rows: 288 -> 232 us).
+    int tok_of[kCols / 32], off[kCols / 32];
 #pragma unroll
-          for (int i = 0; i < kCols / 32; ++i) {
-            const int col = i * 32 + lane, tok = qt * QTb + col / G;
-            float l = neg_inf();
-            if (col < QTb * G && tok < lq)
-              l = a.lse[((int64_t)q0 + tok) * a.Hq + t.h * G + col % G];
-            const bool draws = l != neg_inf();  // a query that saw nothing draws nothing
-            col_l2[b * kCols + col] = draws ? -(l * kLog2e) : 0.f;
-            col_last[b * kCols + col] = draws ? c - lq + tok : -1;
-            all = all && draws;
-          }
-          all = __all_sync(kFull, all);
-          if (lane == 0) col_clean[b] = all;
-          __syncwarp();
-          mbar_arrive(bar(B_QFULL + b));
+    for (int i = 0; i < kCols / 32; ++i) {
+      const int col = i * 32 + lane;
+      tok_of[i] = col < QTb * G ? col / G : 1 << 30;
+      off[i] = col / G * a.Hq + col % G;
+    }
+    Item t = item_at(P, S, Hkv, I0);
+    int x = I0, c = 0, lq = 0, q0 = 0, nq = 0, qt = 0;
+    auto settle = [&] {  // on the first item from x on with a tile to load
+      while (x < I1) {
+        c = P.ctx[t.s], lq = P.lq[t.s], q0 = P.q0[t.s], nq = tiles_of(t);
+        if (nq > 0 && fresh_q(t, nq, x)) {
+          qt = nq > 1 ? first_tile(key_tile(t), c, lq, QTb) : 0;
+          return;
         }
+        if (++x < I1) next_item(P, Hkv, t);
       }
-      if (x + 1 < I1) next_item(P, Hkv, t);
+    };
+    float l[kCols / 32];
+    auto fetch = [&] {
+      if (x >= I1) return;
+      const float* row = a.lse + ((int64_t)q0 + qt * QTb) * a.Hq + t.h * G;
+#pragma unroll
+      for (int i = 0; i < kCols / 32; ++i)
+        l[i] = tok_of[i] < lq - qt * QTb ? row[off[i]] : neg_inf();
+    };
+    settle();
+    fetch();
+    for (int qn = 0; x < I1; ++qn) {
+      const int b = qn % kQBufs;
+      if (qn >= kQBufs &&
+          !__all_sync(kFull, wait(B_QEMPTY + b, (uint32_t)(qn / kQBufs - 1) & 1u)))
+        break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(B_QFULL + b), (uint32_t)(QTb * G) * 256u);
+        const uint32_t d = smem_addr(smem + L::q + b * kOperand);
+        tma_load_3d(d, &tmq, 0, t.h * G, q0 + qt * QTb, bar(B_QFULL + b));
+        tma_load_3d(d + kHalfB, &tmq, 64, t.h * G, q0 + qt * QTb, bar(B_QFULL + b));
+      }
+      bool all = true;
+#pragma unroll
+      for (int i = 0; i < kCols / 32; ++i) {
+        const int col = i * 32 + lane;
+        const bool draws = l[i] != neg_inf();  // a query that saw nothing draws nothing
+        col_l2[b * kCols + col] = draws ? -(l[i] * kLog2e) : 0.f;
+        col_last[b * kCols + col] = draws ? c - lq + qt * QTb + tok_of[i] : -1;
+        all = all && draws;
+      }
+      all = __all_sync(kFull, all);
+      if (lane == 0) col_clean[b] = all;
+      __syncwarp();
+      mbar_arrive(bar(B_QFULL + b));
+      if (++qt >= nq) {
+        if (++x < I1) next_item(P, Hkv, t);
+        settle();
+      }
+      fetch();
     }
   } else if (warp == 1 || warp == kMma2Warp) {
     // -------------------------------------------------------------- products
@@ -377,13 +414,13 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
           const uint64_t dk = desc_k + (uint64_t)(st * (kOperand >> 4));
           for (int qt = nq > 1 ? first_tile(key_tile(t), c, lq, QTb) : 0; qt < nq; ++qt, ++dn) {
             if (fresh) {
-              if (!wait(B_QFULL + (qn & 1), (uint32_t)(qn >> 1) & 1u)) {
+              if (!wait(B_QFULL + qn % kQBufs, (uint32_t)(qn / kQBufs) & 1u)) {
                 ok = false;
                 break;
               }
               ++qn;
             }
-            const int qb = (qn - 1) & 1, db = dn % L::kDBufs;
+            const int qb = (qn - 1) % kQBufs, db = dn % L::kDBufs;
             if (!mine) {  // the other's; this one's products with the tile come first
               if (last_use) tc_commit(bar(B_QEMPTY + qb));
               continue;
@@ -425,7 +462,8 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
     const float* kscale = reinterpret_cast<const float*>(smem + L::scale);
     Item t = item_at(P, S, Hkv, I0);
-    int n = 0, qn = 0, dn = 0;
+    float* part = reinterpret_cast<float*>(smem + L::part);
+    int n = 0, qn = 0, dn = 0, pn = 0;
     int c = 0, lq = 0, nq = 0;
     float* row = nullptr;  // weights of the item's sequence and head
     bool ok = true, begun = false;
@@ -438,7 +476,9 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
         row = a.weights + ((int64_t)t.s * Hkv + t.h) * a.weights_len;
       }
       const int kt = key_tile(t), key = kt * kKeys + r;
-      const int mine = lq > 0 ? n & 1 : 0;  // the group that this item falls to
+      // the group that a single tile falls to; the one that writes of several
+      const bool split = SPLIT && nq > 1;
+      const int mine = !SPLIT ? (lq > 0 ? n & 1 : 0) : nq == 1 ? dn & 1 : 0;
       float old = 0.f;
       if (mine == group && a.accumulate && key < c - lq) old = row[key];
       float2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
@@ -449,16 +489,16 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
           // both groups wait for a new query tile and release it, so that neither
           // runs a tile ahead
           if (fresh) {
-            if (!wait(B_QFULL + (qn & 1), (uint32_t)(qn >> 1) & 1u)) {
+            if (!__all_sync(kFull, wait(B_QFULL + qn % kQBufs, (uint32_t)(qn / kQBufs) & 1u))) {
               ok = false;
               break;
             }
             ++qn;
           }
-          const int qb = (qn - 1) & 1, db = dn % L::kDBufs;
-          if (mine == group) {
+          const int qb = (qn - 1) % kQBufs, db = dn % L::kDBufs;
+          if (split || mine == group) {
             const int cols = min(kCols, min(QTb, lq - qt * QTb) * G);
-            if (!wait(B_DFULL + db, (uint32_t)(dn / L::kDBufs) & 1u)) {
+            if (!__all_sync(kFull, wait(B_DFULL + db, (uint32_t)(dn / L::kDBufs) & 1u))) {
               ok = false;
               break;
             }
@@ -503,34 +543,49 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
             // them. (With the next 32 on their way during these, an epilogue warp
             // keeps its scheduler to itself: 37.9 us instead of 35.5 in bf16, 51
             // instead of 43.5 in FP8, where the codes' conversion waits for it.)
+            const int c_lo = split ? group * (kCols / 2) : 0;
+            const int c_hi = split ? min(cols, c_lo + kCols / 2) : cols;
             uint32_t v0[32];
 #pragma unroll 1
-            for (int c0 = 0; c0 < cols; c0 += 32) {
+            for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
               tmem_ld32(ta + (uint32_t)c0, v0);
               columns(v0, c0);
             }
             tc_fence_before();
-            mbar_arrive(bar(B_DEMPTY + db));
+            mbar_arrive_n(bar(B_DEMPTY + db), split ? 1u : 2u);
           }
           if (last_use) mbar_arrive(bar(B_QEMPTY + qb));
         }
         if (!ok) break;
         ++n;
       }
-      if (mine == group && key < c) {
-        const float2 s2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-        row[key] = old + (s2.x + s2.y);
+      const float2 s2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+      float sum = s2.x + s2.y;
+      if (split) {
+        // The second group's half goes through one of eight slots. It is less than
+        // kDBufs + 1 items ahead: a tile is written anew only after both have read it.
+        float* slot = part + (pn % kPartSlots) * kKeys + r;
+        if (group == 1) {
+          *slot = sum;
+          mbar_arrive(bar(B_PART + pn % kPartSlots));
+        } else {
+          if (!__all_sync(kFull, wait(B_PART + pn % kPartSlots,
+                                      (uint32_t)(pn / kPartSlots) & 1u)))
+            break;
+          sum += *slot;
+        }
+        ++pn;
       }
+      if (mine == group && key < c) row[key] = old + sum;
       if (x + 1 < I1) next_item(P, Hkv, t);
     }
   } else if constexpr (L::q8) {
     // -------------------------------------------------------------- codes to bf16
     // thread = key row = tensor-memory lane: 128 codes of the swizzled raw tile to
     // the 64 columns of a K operand, which the products read from tensor memory
-    // (a swizzled bf16
-    // tile in shared memory and the fence that it needs: 64 us instead of 61 for
-    // FP8 windows of 128 rows). The next item's codes are loaded while this one's
-    // stores end (61 -> 51 us).
+    // (a swizzled bf16 tile in shared memory and the fence that it needs: 64 us
+    // instead of 61 for FP8 windows of 128 rows). The next item's codes are loaded
+    // while this one's stores end (61 -> 51 us).
     // Row scales go to slot n mod 8: by the time slot n is written again, item
     // n + 8's, the accumulator of item n has been read (K stages and accumulators
     // between them hold fewer items).
@@ -605,11 +660,15 @@ size_t smem_bytes(int S) {
   return 1024 + (size_t)Lay<FMT>::plan + sizeof(int) * (5 * (size_t)S + 2);
 }
 
-const void* kernel_of(int fmt) {
-  return fmt == PA_KV_BF16   ? reinterpret_cast<const void*>(weights_tc_kernel<PA_KV_BF16>)
-         : fmt == PA_KV_INT8 ? reinterpret_cast<const void*>(weights_tc_kernel<PA_KV_INT8>)
-                             : reinterpret_cast<const void*>(weights_tc_kernel<PA_KV_FP8>);
+using Kernel = void (*)(CUtensorMap, CUtensorMap, TcWeightArgs);
+
+template <bool SPLIT>
+Kernel kernel_for(int fmt) {
+  return fmt == PA_KV_BF16   ? weights_tc_kernel<PA_KV_BF16, SPLIT>
+         : fmt == PA_KV_INT8 ? weights_tc_kernel<PA_KV_INT8, SPLIT>
+                             : weights_tc_kernel<PA_KV_FP8, SPLIT>;
 }
+Kernel kernel_of(int fmt, bool split) { return split ? kernel_for<true>(fmt) : kernel_for<false>(fmt); }
 
 }  // namespace
 
@@ -629,7 +688,9 @@ int weights_tc_geometry(const pa_shape* sh, int max_q_len, int kv_format, Weight
   if (steps > (int64_t(1) << 30) / sh->num_seqs / sh->num_kv_heads / tiles) return PA_OK;
   if (sh->num_blocks * sh->num_kv_heads * (kv_format == PA_KV_BF16 ? kBlock : 1) > 0x7fffffff)
     return PA_OK;
-  if (!raise_smem_limit(kernel_of(kv_format))) return PA_ERR_CUDA;
+  g->split = max_q_len > g->QTb;
+  if (!raise_smem_limit(reinterpret_cast<const void*>(kernel_of(kv_format, g->split))))
+    return PA_ERR_CUDA;
   g->grid = dev.num_sms;
   g->enabled = true;
   return PA_OK;
@@ -645,16 +706,9 @@ int launch_weights_tc(const WeightsTcGeometry& g, const WeightArgs& a, int kv_fo
   TcWeightArgs t;
   t.w = a;
   t.QTb = g.QTb;
-  cudaError_t e;
-  if (kv_format == PA_KV_BF16)
-    e = launch_dependent(weights_tc_kernel<PA_KV_BF16>, dim3(g.grid),
-                         dim3(Lay<PA_KV_BF16>::threads), g.smem, st, tmq, tmk, t);
-  else if (kv_format == PA_KV_INT8)
-    e = launch_dependent(weights_tc_kernel<PA_KV_INT8>, dim3(g.grid),
-                         dim3(Lay<PA_KV_INT8>::threads), g.smem, st, tmq, tmk, t);
-  else
-    e = launch_dependent(weights_tc_kernel<PA_KV_FP8>, dim3(g.grid),
-                         dim3(Lay<PA_KV_FP8>::threads), g.smem, st, tmq, tmk, t);
+  const int threads = kv_format == PA_KV_BF16 ? Lay<PA_KV_BF16>::threads : Lay<PA_KV_INT8>::threads;
+  const cudaError_t e = launch_dependent(kernel_of(kv_format, g.split), dim3(g.grid), dim3(threads),
+                                         g.smem, st, tmq, tmk, t);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -134,6 +134,17 @@ def test_weights_of_large_batches(fmt, hq, hkv, ql):
     ctx = [4100, 2500, 311, 6007, 900, 1]
     lens = [min(ql, c) for c in ctx]
     lens[1], lens[4] = max(1, lens[1] // 2), 0
+    check_large(fmt, hq, hkv, ctx, lens)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (6, 2), (8, 1)])
+def test_weights_of_windows_of_one_and_several_query_tiles(fmt, hq, hkv):
+    check_large(fmt, hq, hkv, [4100, 3000, 311, 6007, 900, 1, 513, 2048],
+                [1, 300, 64, 200, 0, 1, 513, 65])
+
+
+def check_large(fmt, hq, hkv, ctx, lens):
     w = W.build("large", 44, ctx, lens, pool_factor=1.1, num_q_heads=hq, num_kv_heads=hkv,
                 outlier_frac=0.02, outlier_gain=2.5)
     db = batch(w, fmt)
