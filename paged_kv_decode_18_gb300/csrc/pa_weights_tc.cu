@@ -62,13 +62,15 @@ template <int FMT>
 struct Lay {
   static constexpr bool q8 = FMT != PA_KV_BF16;
   // bf16 K tiles: in shared memory, or widened into tensor memory (64 columns each)
-  static constexpr int kStages = q8 ? 2 : 4;
-  // An issuing thread waits for its own items' K only. It meets a stage at every
-  // use or never, so the phase that it waits for cannot be mistaken for an older
-  // one: the items, which the two take in turn, have to fill an even ring.
-  static_assert(kStages % 2 == 0, "a stage has one issuing thread");
+  static constexpr int kStages = 4;
   static constexpr int kRawStages = 6;        // of raw 8-bit tiles
-  static constexpr int kDBufs = q8 ? 3 : 4;   // accumulators in tensor memory
+  static constexpr int kDBufs = q8 ? 2 : 4;   // accumulators in tensor memory
+  // An issuing thread waits for its own items' K only, an epilogue group for its
+  // own accumulators. Either meets a slot at every use or never, so that a phase it
+  // waits for cannot be mistaken for an older one: since the two take items and
+  // tiles in turn, the rings have to be even. (Where a window of several tiles
+  // shifts the turns, the query tile that comes next waits for all of them.)
+  static_assert(kStages % 2 == 0 && kDBufs % 2 == 0, "a slot has one thread or group");
   static constexpr int kATmem = kDBufs * kCols;
   static_assert(kATmem + (q8 ? kStages * kHeadDim / 2 : 0) <= 512, "tensor memory");
   static constexpr int q = 0;                 // query tiles
