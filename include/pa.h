@@ -46,7 +46,11 @@
  *
  * Built configuration: head_dim 128, block_size 16, and num_q_heads /
  * num_kv_heads = 2 for pa_decode (1..8 for pa_decode_varlen with
- * q tiles of 16 / group rows). Other shapes return PA_ERR_UNSUPPORTED.
+ * q tiles of 16 / group rows; 1..128 for pa_decode_tree; any group for
+ * pa_commit_path, pa_accumulate_weights and pa_evict). Other shapes return
+ * PA_ERR_UNSUPPORTED, as do batches whose plan does not fit a block's shared
+ * memory and bf16 pools of 2^31 rows (num_blocks * num_kv_heads * 16) or more
+ * in calls that read them through tensor maps.
  */
 #ifndef PA_H_
 #define PA_H_
@@ -452,7 +456,8 @@ int pa_tree_mask(const int32_t* parents, const int32_t* cu_seqlens_q, int num_se
  *                 as in pa_decode_varlen
  *   workspace     at least pa_decode_tree_workspace_size(...) bytes, 256-byte
  *                 aligned; clobbered
- * Built for any group of 1 to 128 query heads per KV head (bf16 pool). Softmax
+ * Built for any group of 1 to 128 query heads per KV head (bf16 pool; plan and
+ * pool limits as above: PA_ERR_UNSUPPORTED, workspace size 0). Softmax
  * statistics and sums are fp32; the softmax weights are rounded to bf16 for
  * the product with V, as in pa_decode_varlen. A window needs 0 <= Lq <= c and
  * Lq <= 32 * mask_words; another one sets PA_DEVERR_QLEN_RANGE and produces no
@@ -511,7 +516,9 @@ int pa_commit_path(void* k_cache, void* v_cache, int kv_format, const int32_t* b
  *   weights       [S][Hkv][weights_len] fp32, in place; positions at and past c
  *                 are left as they were. context_lens[s] <= weights_len.
  * Scores and sums are fp32, products exact; a position's sum has one order, so
- * equal calls give equal bits. Any group size. A window that is not inside its
+ * equal calls give equal bits. Any group size; plan and pool limits as above. An
+ * FP8 NaN code, which the writer never stores, gives an unspecified weight to its
+ * own position. A window that is not inside its
  * context or the rows sets PA_DEVERR_QLEN_RANGE and leaves its sequence's
  * weights as they were.
  */
@@ -545,7 +552,8 @@ int pa_accumulate_weights(const pa_bf16* q, const void* k_cache, int kv_format, 
  * from the first moved position on. A budget outside its range sets
  * PA_DEVERR_BUDGET_RANGE, a context longer than the table or weights_len
  * PA_DEVERR_CONTEXT_RANGE: the sequence stays as it is, its kept entries are
- * -1 and new_lens[s] is context_lens[s].
+ * -1 and new_lens[s] is context_lens[s]. More than 65535 sequences:
+ * PA_ERR_UNSUPPORTED.
  */
 int pa_evict(void* k_cache, void* v_cache, int kv_format, const int32_t* block_tables,
              const int32_t* context_lens, float* weights, int64_t weights_len,
