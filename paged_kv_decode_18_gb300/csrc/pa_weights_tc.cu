@@ -5,20 +5,19 @@
 //
 // S^T = K Q^T with the keys as the rows of the product: a thread of the
 // epilogue owns one key (one tensor-memory lane) and sums its exponentials over
-// the query columns in its own registers, with no reduction between threads.
-// A work item is (sequence, KV head,
-// 128 keys) with all of the window's query tiles, so a weight has one writer
-// and its sum one order. One CTA per SM, warp-specialised:
+// the query columns in its own registers. A work item is (sequence, KV head, 128
+// keys) with all of the window's query tiles, so a weight has one writer and its
+// sum one order. One CTA per SM, warp-specialised:
 //   warp 0     K producer: eight 16-key pool blocks a tile through the block
 //              table (4-D TMA, 8-bit codes 3-D, with the 128-byte swizzle);
 //   warp 10    query tiles of 128 rows ((128/G) tokens x G heads, 3-D TMA) and
 //              their columns' log-sum-exps and causal limits;
 //   warps 1,11 tensor memory and, from one thread each, the products: 128 keys x
 //              up to 128 columns into the next accumulator; they take the
-//              items in turn (one thread alone spends 2,000 cycles an item on
+//              items (windows of several query tiles: the tiles) in turn (one thread alone spends 2,000 cycles an item on
 //              waits, issue and commits, more than anything else of it takes);
 //   warps 2-9  the epilogue: two groups of four warps that take the items in
-//              turn, so that one's exponentials hide the other's waits (two
+//              turn (or half the columns each, see SPLIT), so that one's exponentials hide the other's waits (two
 //              threads a key with half the columns each, who met at every
 //              item's end, took 45 us where this took 38);
 //   warps 12-15 (8-bit pools) turn the raw codes into bf16 (exact) in tensor
@@ -28,9 +27,9 @@
 // contexts of 1000..8192 positions with 64 queries of two heads (157 MB) take
 // 36.2 us in bf16, 34.4 us with all of the epilogue's column work left out; FP8
 // codes (81 MB) 42.6 us, 4 us less without their conversion. Longer windows by the
-// chain of a tile through its two query buffers (load, product, epilogue): 1024
-// rows take 211 us, 0.83 us a tile, 157 us without the column work and still 155
-// without the queries' loads, beside 0.27 us of tensor time.
+// epilogue and the waits between its tiles: 1024 rows take 189 us, 0.75 us a tile,
+// 135 us without the column work, 132 without the queries' loads as well and 109
+// with one product in eight, beside 0.27 us of tensor time.
 #include <cudaTypedefs.h>
 
 #include "pa_device.cuh"
@@ -49,8 +48,7 @@ constexpr int kOperand = 2 * kHalfB;
 constexpr int kCodes = kKeys * kHeadDim;      // the raw codes of an item
 constexpr int kRawTile = kCodes + 1024;       // and its row scales
 constexpr int kScaleSlots = 8;                // items whose row scales are kept (see below)
-constexpr int kQBufs = 2;                     // query tiles in shared memory
-constexpr int kPartSlots = 8;                 // split items whose second half may wait (see below)
+constexpr int kPartSlots = 8;                 // items whose second half may wait (see below)
 constexpr int kEpiWarps = 8;
 constexpr int kQWarp = 2 + kEpiWarps;
 constexpr int kMma2Warp = kQWarp + 1;
@@ -58,19 +56,31 @@ constexpr int kConvWarps = 4;
 
 constexpr int kNumBarsMax = 48;
 
-template <int FMT>
+// SPLIT: windows of several query tiles may come. A tile then passes a chain of
+// query load, product and epilogue with nothing to hide behind but the next
+// tiles. So there are more query tiles in shared memory and fewer of K, the two
+// issuing threads take tiles in turn, and both groups of the epilogue take half
+// the columns of every tile (16 x 1000..8192, bf16, windows of 1024 rows: 189 us
+// where the other form takes 224; windows of 128 rows: 41 us where that takes 36).
+// Halves of columns, not every other tile: with two accumulators, all that
+// the 8-bit pools leave room for, that took 206 us instead of 194, in bf16 180.
+template <int FMT, bool SPLIT>
 struct Lay {
   static constexpr bool q8 = FMT != PA_KV_BF16;
+  static constexpr int kQBufs = SPLIT ? 4 : 2;       // query tiles in shared memory
   // bf16 K tiles: in shared memory, or widened into tensor memory (64 columns each)
-  static constexpr int kStages = 4;
-  static constexpr int kRawStages = 6;        // of raw 8-bit tiles
-  static constexpr int kDBufs = q8 ? 2 : 4;   // accumulators in tensor memory
-  // An issuing thread waits for its own items' K only, an epilogue group for its
-  // own accumulators. Either meets a slot at every use or never, so that a phase it
-  // waits for cannot be mistaken for an older one: since the two take items and
-  // tiles in turn, the rings have to be even. (Where a window of several tiles
-  // shifts the turns, the query tile that comes next waits for all of them.)
-  static_assert(kStages % 2 == 0 && kDBufs % 2 == 0, "a slot has one thread or group");
+  static constexpr int kStages = SPLIT && !q8 ? 2 : 4;
+  static constexpr int kRawStages = SPLIT ? 4 : 6;   // of raw 8-bit tiles
+  static constexpr int kDBufs = q8 ? 2 : 4;  // accumulators in tensor memory
+  // An issuing thread waits for its own accumulators, without SPLIT also for its
+  // own items' K only and an epilogue group for its own accumulators. Either meets
+  // a slot at every use or never, so that a phase it waits for cannot be mistaken
+  // for an older one: since the two take items or tiles in turn, the rings have to
+  // be even. (Should a window of several tiles come to the form without SPLIT and
+  // shift the turns, the wait for its query tile, the second after one that all
+  // have done with, keeps them together.)
+  static_assert(kDBufs % 2 == 0 && (SPLIT || (kStages % 2 == 0 && kQBufs == 2)),
+                "a slot has one thread or group");
   static constexpr int kATmem = kDBufs * kCols;
   static_assert(kATmem + (q8 ? kStages * kHeadDim / 2 : 0) <= 512, "tensor memory");
   static constexpr int q = 0;                 // query tiles
@@ -87,8 +97,8 @@ struct Lay {
 };
 
 enum : int {
-  B_KFULL = 0, B_KEMPTY = 4, B_QFULL = 8, B_QEMPTY = 11, B_DFULL = 14, B_DEMPTY = 18,
-  B_RFULL = 22, B_REMPTY = 28, B_PART = 34, kNumBars = 42
+  B_KFULL = 0, B_KEMPTY = 4, B_QFULL = 8, B_QEMPTY = 12, B_DFULL = 16, B_DEMPTY = 20,
+  B_RFULL = 24, B_REMPTY = 30, B_PART = 36, kNumBars = 44
 };
 
 static_assert(kNumBars <= kNumBarsMax, "barrier area");
@@ -142,15 +152,11 @@ __device__ __forceinline__ int key_tile(const Item& t) {
   return (t.i & 1) ? t.nt - 1 - (t.i >> 1) : t.i >> 1;
 }
 
-// SPLIT: windows of several query tiles may come. Each group of the epilogue then
-// takes half the columns of all of an item's tiles, since an item's tiles fill all
-// accumulators and the other group would stand still (16 x 1000..8192 with windows
-// of 1024 rows: 232 -> 211 us; in a batch of single tiles the choice costs 1 us).
 template <int FMT, bool SPLIT>
-__global__ void __launch_bounds__(Lay<FMT>::threads, 1)
+__global__ void __launch_bounds__((Lay<FMT, SPLIT>::threads), 1)
     weights_tc_kernel(const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmk, const TcWeightArgs arg) {
-  using L = Lay<FMT>;
+  using L = Lay<FMT, SPLIT>;
   const WeightArgs& a = arg.w;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t rawp = smem_addr(smem_raw);
@@ -168,18 +174,18 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(B_KFULL + i), L::q8 ? kConvWarps * 32u : 1u);
-      mbar_init(bar(B_KEMPTY + i), 1u);
+      mbar_init(bar(B_KEMPTY + i), SPLIT ? 2u : 1u);  // the issuing threads' commits
       mbar_init(bar(B_DFULL + i), 2u);  // the issuing thread and its commit
-      mbar_init(bar(B_DEMPTY + i), kEpiWarps * 32u);
+      mbar_init(bar(B_DEMPTY + i), kEpiWarps * (SPLIT ? 32u : 16u));  // who reads it
     }
     for (int i = 0; i < L::kRawStages; ++i) {
       mbar_init(bar(B_RFULL + i), 1u);
       mbar_init(bar(B_REMPTY + i), kConvWarps * 32u);
     }
     for (int i = 0; i < kPartSlots; ++i) mbar_init(bar(B_PART + i), kEpiWarps * 16u);
-    for (int i = 0; i < kQBufs; ++i) {
+    for (int i = 0; i < L::kQBufs; ++i) {
       mbar_init(bar(B_QFULL + i), 33u);  // warp 10's lanes and the expected bytes
-      mbar_init(bar(B_QEMPTY + i), 2u + kEpiWarps * 32u);
+      mbar_init(bar(B_QEMPTY + i), (SPLIT ? 0u : 2u) + kEpiWarps * 32u);
     }
     *abort_flag = 0;
     mbar_fence_init();
@@ -355,9 +361,9 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
     settle();
     fetch();
     for (int qn = 0; x < I1; ++qn) {
-      const int b = qn % kQBufs;
-      if (qn >= kQBufs &&
-          !__all_sync(kFull, wait(B_QEMPTY + b, (uint32_t)(qn / kQBufs - 1) & 1u)))
+      const int b = qn % L::kQBufs;
+      if (qn >= L::kQBufs &&
+          !__all_sync(kFull, wait(B_QEMPTY + b, (uint32_t)(qn / L::kQBufs - 1) & 1u)))
         break;
       if (lane == 0) {
         mbar_arrive_expect_tx(bar(B_QFULL + b), (uint32_t)(QTb * G) * 256u);
@@ -409,22 +415,24 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
         }
         if (lq > 0) {
           const int st = n % L::kStages;
-          const bool mine = (n & 1) == me;
-          if (mine && !wait(B_KFULL + st, (uint32_t)(n / L::kStages) & 1u)) break;
+          // SPLIT: the two take tiles in turn, else items
+          const bool item_mine = (n & 1) == me;
+          if ((SPLIT || item_mine) && !wait(B_KFULL + st, (uint32_t)(n / L::kStages) & 1u)) break;
           const bool fresh = fresh_q(t, nq, x);
           const bool last_use = nq > 1 || t.i == t.nt - 1 || x + 1 == I1;
           const uint64_t dk = desc_k + (uint64_t)(st * (kOperand >> 4));
           for (int qt = nq > 1 ? first_tile(key_tile(t), c, lq, QTb) : 0; qt < nq; ++qt, ++dn) {
             if (fresh) {
-              if (!wait(B_QFULL + qn % kQBufs, (uint32_t)(qn / kQBufs) & 1u)) {
+              if (!wait(B_QFULL + qn % L::kQBufs, (uint32_t)(qn / L::kQBufs) & 1u)) {
                 ok = false;
                 break;
               }
               ++qn;
             }
-            const int qb = (qn - 1) % kQBufs, db = dn % L::kDBufs;
-            if (!mine) {  // the other's; this one's products with the tile come first
-              if (last_use) tc_commit(bar(B_QEMPTY + qb));
+            const int qb = (qn - 1) % L::kQBufs, db = dn % L::kDBufs;
+            if (SPLIT ? (dn & 1) != me : !item_mine) {
+              // the other's; this one's products with the query tile come first
+              if (!SPLIT && last_use) tc_commit(bar(B_QEMPTY + qb));
               continue;
             }
             if (dn >= L::kDBufs && !wait(B_DEMPTY + db, (uint32_t)((dn / L::kDBufs) - 1) & 1u)) {
@@ -447,10 +455,11 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
             }
             tc_commit(bar(B_DFULL + db));
             mbar_arrive(bar(B_DFULL + db));
-            // the query tile is done with after its last product
-            if (last_use) tc_commit(bar(B_QEMPTY + qb));
+            // the query tile is done with after its last product (SPLIT: when both
+            // groups of the epilogue, who wait for every product, have arrived)
+            if (!SPLIT && last_use) tc_commit(bar(B_QEMPTY + qb));
           }
-          if (mine) tc_commit(bar(B_KEMPTY + st));
+          if (SPLIT || item_mine) tc_commit(bar(B_KEMPTY + st));
           ++n;
         }
         if (x + 1 < I1) next_item(P, Hkv, t);
@@ -478,9 +487,8 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
         row = a.weights + ((int64_t)t.s * Hkv + t.h) * a.weights_len;
       }
       const int kt = key_tile(t), key = kt * kKeys + r;
-      // the group that a single tile falls to; the one that writes of several
-      const bool split = SPLIT && nq > 1;
-      const int mine = !SPLIT ? (lq > 0 ? n & 1 : 0) : nq == 1 ? dn & 1 : 0;
+      // the group that the item falls to (SPLIT: that writes it)
+      const int mine = !SPLIT && lq > 0 ? n & 1 : 0;
       float old = 0.f;
       if (mine == group && a.accumulate && key < c - lq) old = row[key];
       float2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
@@ -491,14 +499,14 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
           // both groups wait for a new query tile and release it, so that neither
           // runs a tile ahead
           if (fresh) {
-            if (!__all_sync(kFull, wait(B_QFULL + qn % kQBufs, (uint32_t)(qn / kQBufs) & 1u))) {
+            if (!__all_sync(kFull, wait(B_QFULL + qn % L::kQBufs, (uint32_t)(qn / L::kQBufs) & 1u))) {
               ok = false;
               break;
             }
             ++qn;
           }
-          const int qb = (qn - 1) % kQBufs, db = dn % L::kDBufs;
-          if (split || mine == group) {
+          const int qb = (qn - 1) % L::kQBufs, db = dn % L::kDBufs;
+          if (SPLIT || mine == group) {
             const int cols = min(kCols, min(QTb, lq - qt * QTb) * G);
             if (!__all_sync(kFull, wait(B_DFULL + db, (uint32_t)(dn / L::kDBufs) & 1u))) {
               ok = false;
@@ -545,8 +553,8 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
             // them. (With the next 32 on their way during these, an epilogue warp
             // keeps its scheduler to itself: 37.9 us instead of 35.5 in bf16, 51
             // instead of 43.5 in FP8, where the codes' conversion waits for it.)
-            const int c_lo = split ? group * (kCols / 2) : 0;
-            const int c_hi = split ? min(cols, c_lo + kCols / 2) : cols;
+            const int c_lo = SPLIT ? group * (kCols / 2) : 0;
+            const int c_hi = SPLIT ? min(cols, c_lo + kCols / 2) : cols;
             uint32_t v0[32];
 #pragma unroll 1
             for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
@@ -554,7 +562,7 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
               columns(v0, c0);
             }
             tc_fence_before();
-            mbar_arrive_n(bar(B_DEMPTY + db), split ? 1u : 2u);
+            mbar_arrive(bar(B_DEMPTY + db));
           }
           if (last_use) mbar_arrive(bar(B_QEMPTY + qb));
         }
@@ -563,9 +571,9 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
       }
       const float2 s2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
       float sum = s2.x + s2.y;
-      if (split) {
-        // The second group's half goes through one of eight slots. It is less than
-        // kDBufs + 1 items ahead: a tile is written anew only after both have read it.
+      if (SPLIT && lq > 0) {
+        // The second group's half goes through one of eight slots. It is at most
+        // kDBufs items ahead: a tile is written anew only after both have read it.
         float* slot = part + (pn % kPartSlots) * kKeys + r;
         if (group == 1) {
           *slot = sum;
@@ -658,8 +666,9 @@ __global__ void __launch_bounds__(Lay<FMT>::threads, 1)
 }
 
 template <int FMT>
-size_t smem_bytes(int S) {
-  return 1024 + (size_t)Lay<FMT>::plan + sizeof(int) * (5 * (size_t)S + 2);
+size_t smem_bytes(int S, bool split) {
+  return 1024 + (size_t)(split ? Lay<FMT, true>::plan : Lay<FMT, false>::plan) +
+         sizeof(int) * (5 * (size_t)S + 2);
 }
 
 using Kernel = void (*)(CUtensorMap, CUtensorMap, TcWeightArgs);
@@ -681,8 +690,9 @@ int weights_tc_geometry(const pa_shape* sh, int max_q_len, int kv_format, Weight
   DeviceInfo dev;
   if (!current_device_info(&dev)) return PA_ERR_CUDA;
   g->QTb = kCols / G < max_q_len ? kCols / G : max_q_len;
-  g->smem = kv_format == PA_KV_BF16 ? smem_bytes<PA_KV_BF16>(sh->num_seqs)
-                                    : smem_bytes<PA_KV_INT8>(sh->num_seqs);
+  g->split = max_q_len > g->QTb;
+  g->smem = kv_format == PA_KV_BF16 ? smem_bytes<PA_KV_BF16>(sh->num_seqs, g->split)
+                                    : smem_bytes<PA_KV_INT8>(sh->num_seqs, g->split);
   if (g->smem > (size_t)dev.max_smem_optin) return PA_OK;
   // costs are summed in 32 bits, and K's rows are 32-bit coordinates
   const int64_t tiles = (int64_t)sh->max_blocks_per_seq / kBlocksK + 1;
@@ -690,7 +700,6 @@ int weights_tc_geometry(const pa_shape* sh, int max_q_len, int kv_format, Weight
   if (steps > (int64_t(1) << 30) / sh->num_seqs / sh->num_kv_heads / tiles) return PA_OK;
   if (sh->num_blocks * sh->num_kv_heads * (kv_format == PA_KV_BF16 ? kBlock : 1) > 0x7fffffff)
     return PA_OK;
-  g->split = max_q_len > g->QTb;
   if (!raise_smem_limit(reinterpret_cast<const void*>(kernel_of(kv_format, g->split))))
     return PA_ERR_CUDA;
   g->grid = dev.num_sms;
@@ -708,7 +717,7 @@ int launch_weights_tc(const WeightsTcGeometry& g, const WeightArgs& a, int kv_fo
   TcWeightArgs t;
   t.w = a;
   t.QTb = g.QTb;
-  const int threads = kv_format == PA_KV_BF16 ? Lay<PA_KV_BF16>::threads : Lay<PA_KV_INT8>::threads;
+  const int threads = kv_format == PA_KV_BF16 ? Lay<PA_KV_BF16, false>::threads : Lay<PA_KV_INT8, false>::threads;
   const cudaError_t e = launch_dependent(kernel_of(kv_format, g.split), dim3(g.grid), dim3(threads),
                                          g.smem, st, tmq, tmk, t);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
