@@ -13,13 +13,15 @@
 //   warp 10    query tiles of 128 rows ((128/G) tokens x G heads, 3-D TMA) and
 //              their columns' log-sum-exps and causal limits;
 //   warps 1,11 tensor memory and, from one thread each, the products: 128 keys x
-//              up to 128 columns into the next accumulator; they take the
-//              items (windows of several query tiles: the tiles) in turn (one thread alone spends 2,000 cycles an item on
-//              waits, issue and commits, more than anything else of it takes);
+//              up to 128 columns into the next accumulator; they take the items
+//              (windows of several query tiles: the tiles) in turn: one thread
+//              alone spends 2,000 cycles an item on waits, issue and commits,
+//              more than anything else of it takes;
 //   warps 2-9  the epilogue: two groups of four warps that take the items in
-//              turn (or half the columns each, see SPLIT), so that one's exponentials hide the other's waits (two
+//              turn, so that one's exponentials hide the other's waits (two
 //              threads a key with half the columns each, who met at every
-//              item's end, took 45 us where this took 38);
+//              item's end, took 45 us where this took 38), or in windows of
+//              several query tiles half the columns each (SPLIT below);
 //   warps 12-15 (8-bit pools) turn the raw codes into bf16 (exact) in tensor
 //              memory, where the products take them from; the row scales
 //              multiply the scores in the epilogue.
