@@ -74,11 +74,13 @@ struct Lay {
   static constexpr int kStages = SPLIT && !q8 ? 2 : 4;
   static constexpr int kRawStages = SPLIT ? 4 : 6;   // of raw 8-bit tiles
   static constexpr int kDBufs = q8 ? 2 : 4;  // accumulators in tensor memory
-  // An issuing thread waits for its own accumulators, without SPLIT also for its
-  // own items' K only and an epilogue group for its own accumulators. Either meets
-  // a slot at every use or never, so that a phase it waits for cannot be mistaken
-  // for an older one: since the two take items or tiles in turn, the rings have to
-  // be even. (Should a window of several tiles come to the form without SPLIT and
+  // A waiter knows a phase by its parity: it may neither look two phases late nor
+  // while the phase before the one it wants is still running. Whoever waits for
+  // every use of a slot has a part in emptying it (query tiles: the thread that
+  // leaves a tile to the other arrives too). An issuing thread waits for its own
+  // accumulators, without SPLIT also for its own items' K only and an epilogue group
+  // for its own accumulators. Either meets a slot at every use or never: since the
+  // two take items or tiles in turn, the rings have to be even. (Should a window of several tiles come to the form without SPLIT and
   // shift the turns, the wait for its query tile, the second after one that all
   // have done with, keeps them together.)
   static_assert(kDBufs % 2 == 0 && (SPLIT || (kStages % 2 == 0 && kQBufs == 2)),
@@ -187,7 +189,8 @@ __global__ void __launch_bounds__((Lay<FMT, SPLIT>::threads), 1)
     for (int i = 0; i < kPartSlots; ++i) mbar_init(bar(B_PART + i), kEpiWarps * 16u);
     for (int i = 0; i < L::kQBufs; ++i) {
       mbar_init(bar(B_QFULL + i), 33u);  // warp 10's lanes and the expected bytes
-      mbar_init(bar(B_QEMPTY + i), (SPLIT ? 0u : 2u) + kEpiWarps * 32u);
+      // the epilogue, and whoever of the issuing threads may still have to look for it
+      mbar_init(bar(B_QEMPTY + i), (SPLIT ? 1u : 2u) + kEpiWarps * 32u);
     }
     *abort_flag = 0;
     mbar_fence_init();
@@ -433,8 +436,17 @@ __global__ void __launch_bounds__((Lay<FMT, SPLIT>::threads), 1)
             }
             const int qb = (qn - 1) % L::kQBufs, db = dn % L::kDBufs;
             if (SPLIT ? (dn & 1) != me : !item_mine) {
-              // the other's; this one's products with the query tile come first
-              if (!SPLIT && last_use) tc_commit(bar(B_QEMPTY + qb));
+              // The other's; this one's products with the query tile come first. The
+              // epilogue answers for the thread that issues the tile's last product,
+              // nobody for the one that does not: unless its having passed QFULL
+              // counts, the buffer can be filled again before it has looked, two
+              // phases that it cannot tell from none.
+              if (last_use) {
+                if (SPLIT)
+                  mbar_arrive(bar(B_QEMPTY + qb));
+                else
+                  tc_commit(bar(B_QEMPTY + qb));
+              }
               continue;
             }
             if (dn >= L::kDBufs && !wait(B_DEMPTY + db, (uint32_t)((dn / L::kDBufs) - 1) & 1u)) {
@@ -458,7 +470,8 @@ __global__ void __launch_bounds__((Lay<FMT, SPLIT>::threads), 1)
             tc_commit(bar(B_DFULL + db));
             mbar_arrive(bar(B_DFULL + db));
             // the query tile is done with after its last product (SPLIT: when both
-            // groups of the epilogue, who wait for every product, have arrived)
+            // groups of the epilogue, who wait for every product, have arrived, and
+            // the thread without that product has passed by)
             if (!SPLIT && last_use) tc_commit(bar(B_QEMPTY + qb));
           }
           if (SPLIT || item_mine) tc_commit(bar(B_KEMPTY + st));
