@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kWgtWarps * 32, 1)
       lq = a.cu_seqlens_q[s + 1] - q0;
       P.qstart[s] = q0;
       if (q0 < 0 || lq < 0 || lq > P.ctx[s] || (int64_t)q0 + lq > a.num_q_tokens) {
-        if (P.ctx[s] > 0 && blockIdx.x == 0) flag_error(PA_DEVERR_QLEN_RANGE);
+        if (blockIdx.x == 0) flag_error(PA_DEVERR_QLEN_RANGE);
         lq = -1;
       }
     }

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__((Lay<FMT, SPLIT>::threads), 1)
     const int q0 = a.cu_seqlens_q ? a.cu_seqlens_q[s] : s;
     const int lq = a.cu_seqlens_q ? a.cu_seqlens_q[s + 1] - q0 : (c > 0 ? 1 : 0);
     const bool bad = q0 < 0 || lq < 0 || lq > c || (int64_t)q0 + lq > a.num_q_tokens;
-    if (bad && c > 0) flag_error(PA_DEVERR_QLEN_RANGE);
+    if (bad) flag_error(PA_DEVERR_QLEN_RANGE);
     // no query: nothing to add, zeros to write
     const int nt = bad || (lq == 0 && a.accumulate) ? 0 : (c + kKeys - 1) / kKeys;
     const int nq = lq > 0 ? (lq + QTb - 1) / QTb : 0;

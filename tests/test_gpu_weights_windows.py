@@ -67,3 +67,48 @@ def test_windows_of_several_tiles_many_times(fmt, lens):
     assert B.pa_debug_read_error() == 0
     for w in many:
         assert same_bits(w, first)
+
+
+@pytest.mark.parametrize("fmt", [B.PA_KV_BF16, B.PA_KV_FP8])
+@pytest.mark.parametrize("max_q", [8, 16, 700])   # mma.sync; tcgen05, one tile a window and several
+@pytest.mark.parametrize("cu", [[0, 8, 11, 19], [0, 8, 8, 16], [0, 8, 5, 13], [0, 8, 40, 48]])
+def test_windows_over_an_empty_context_are_flagged(fmt, max_q, cu):
+    # the second sequence's context is empty: a window of queries, one of fewer than
+    # none, or one outside the rows is not inside it; no query at all is
+    g = torch.Generator().manual_seed(52)
+    ctx = torch.tensor([60, 0, 33], dtype=torch.int32)
+    tab = torch.arange(12, dtype=torch.int32).reshape(3, 4).cuda()
+    q = torch.randn((19, 4, 128), generator=g).bfloat16().cuda()
+    lse = torch.full((19, 4), 5.0, device="cuda")
+    kc = pool(fmt, 12, 2, g)
+
+    def call(offsets, lens):
+        w = torch.full((3, 2, 64), 7.0, device="cuda")
+        B.pa_accumulate_weights(q, kc, lse, tab, lens.cuda(), 0.088, w,
+                                cu_seqlens_q=None if offsets is None else
+                                torch.tensor(offsets, dtype=torch.int32).cuda(),
+                                max_q_len=max_q, kv_format=fmt)
+        torch.cuda.synchronize()
+        return w, B.pa_debug_read_error()
+
+    w, err = call(cu, ctx)
+    assert err == (0 if cu[1] == cu[2] else B.PA_DEVERR_QLEN_RANGE)
+    assert (w[1] == 7).all()                       # nothing is written for it
+    assert not (w[0, :, 52:60] == 7).any() and (w[0, :, 60:] == 7).all()
+    if cu == [0, 8, 11, 19]:                       # the others are as without it
+        alone, err = call([0, 8, 8, 8], ctx)
+        assert err == 0 and same_bits(alone[0].contiguous(), w[0].contiguous())
+
+
+def test_one_query_over_an_empty_context_is_no_error():
+    g = torch.Generator().manual_seed(53)
+    q = torch.randn((2, 4, 128), generator=g).bfloat16().cuda()
+    w = torch.full((2, 2, 32), 7.0, device="cuda")
+    for max_q in (1, 700):
+        B.pa_accumulate_weights(q, pool(B.PA_KV_BF16, 4, 2, g), torch.zeros((2, 4), device="cuda"),
+                                torch.arange(4, dtype=torch.int32).reshape(2, 2).cuda(),
+                                torch.tensor([0, 20], dtype=torch.int32).cuda(), 0.088, w,
+                                max_q_len=max_q)
+        torch.cuda.synchronize()
+        assert B.pa_debug_read_error() == 0
+    assert (w[0] == 7).all() and (w[1, :, 20:] == 7).all()
