@@ -19,9 +19,9 @@ namespace {
 
 constexpr int kChunksPerRow = kHeadDim * 2 / 16;  // 16-byte chunks per (token, head) row
 
-__global__ void reshape_and_cache_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
-                                         const int64_t* __restrict__ slots, int64_t total_chunks,
-                                         int Hkv, int64_t num_slots, uint4* __restrict__ k_cache,
+__global__ void reshape_and_cache_kernel(const uint4* k, const uint4* v, const int64_t* slots,
+                                         int64_t total_chunks, int Hkv, int64_t num_slots,
+                                         uint4* __restrict__ k_cache,
                                          uint4* __restrict__ v_cache) {
   // launched as a programmatic dependent: wait for the previous grid (which may
   // produce k, v or the slots), then let a dependent grid queued behind this
@@ -43,8 +43,9 @@ __global__ void reshape_and_cache_kernel(const uint4* __restrict__ k, const uint
   }
   const int64_t blk = slot / kBlock, off = slot % kBlock;
   const int64_t dst = (((blk * Hkv + h) * kBlock + off) * kChunksPerRow) + c;
-  k_cache[dst] = k[i];
-  v_cache[dst] = v[i];
+  const uint4 xk = k[i], xv = v[i];
+  k_cache[dst] = xk;
+  v_cache[dst] = xv;
 }
 
 // Quantising write (INT8 KV): one warp per (token, KV head) row of 128 values.
@@ -104,9 +105,8 @@ __device__ __forceinline__ void quantize_row_f8_to(const uint2 x, int lane,
 
 // One warp per (token, KV head) row; FP8 selects the E4M3 codes, else int8.
 template <bool FP8>
-__global__ void reshape_and_cache_q8_kernel(const uint2* __restrict__ k,
-                                            const uint2* __restrict__ v,
-                                            const int64_t* __restrict__ slots, int64_t rows,
+__global__ void reshape_and_cache_q8_kernel(const uint2* k, const uint2* v,
+                                            const int64_t* slots, int64_t rows,
                                             int Hkv, int64_t num_slots,
                                             uint8_t* __restrict__ k_cache,
                                             uint8_t* __restrict__ v_cache) {

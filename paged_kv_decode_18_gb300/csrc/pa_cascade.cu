@@ -116,12 +116,12 @@ bool cascade_pays(const pa_shape* sh, int num_groups, int num_members, int max_p
 //   each group's prefix block table (from its first member's row);
 //   the (0, -inf) prefix partial of every sequence in no group;
 // with the consistency checks of the group description.
-__global__ void cascade_prep_kernel(const uint4* __restrict__ q, const int32_t* __restrict__ block_tables,
-                                    const int32_t* __restrict__ context_lens,
-                                    const int32_t* __restrict__ seq_group,
-                                    const int32_t* __restrict__ cu_group,
-                                    const int32_t* __restrict__ group_members,
-                                    const int32_t* __restrict__ prefix_lens, int S, int Hq,
+__global__ void cascade_prep_kernel(const uint4* q, const int32_t* block_tables,
+                                    const int32_t* context_lens,
+                                    const int32_t* seq_group,
+                                    const int32_t* cu_group,
+                                    const int32_t* group_members,
+                                    const int32_t* prefix_lens, int S, int Hq,
                                     int max_blocks, int num_groups, int num_members,
                                     int max_prefix_blocks, uint4* __restrict__ q_g,
                                     int32_t* __restrict__ prefix_bt,

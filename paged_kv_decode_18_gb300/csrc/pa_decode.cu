@@ -884,9 +884,9 @@ __global__ void __launch_bounds__(NWARPS * 32, FMT != kFmtBf16 || NWARPS <= 6 ? 
 // ends a single round of loads remains. Lane i reads piece i's lse values;
 // the partial vectors of a round are loaded together.
 __global__ void __launch_bounds__(256)
-    decode_fixup_kernel(const int32_t* __restrict__ context_lens, int S, int Hkv, int max_blocks,
-                        int num_workers, int parts, const float* __restrict__ part_o,
-                        const float* __restrict__ part_lse, int Hq, uint16_t* __restrict__ out,
+    decode_fixup_kernel(const int32_t* context_lens, int S, int Hkv, int max_blocks,
+                        int num_workers, int parts, const float* part_o,
+                        const float* part_lse, int Hq, uint16_t* __restrict__ out,
                         float* __restrict__ lse, const RowsOut rows) {
   // the next grid in the stream may start its own preparation now; it waits
   // for this grid before it reads anything this grid writes

@@ -237,20 +237,20 @@ __device__ __forceinline__ void merge_take(const float* row, int d0, float& m, f
 // ---------------------------------------------------------------------------
 
 // The 32 bits from bit i0 >= 0 of a mask row of `words` words; bits past the
-// row are 0.
-__device__ __forceinline__ uint32_t mask_window32(const uint32_t* __restrict__ row, int words,
-                                                  int i0) {
+// row are 0. (Ordinary loads, here and wherever an input may come from the grid ahead:
+// that grid may still have been writing when this one started.)
+__device__ __forceinline__ uint32_t mask_window32(const uint32_t* row, int words, int i0) {
   const int w = i0 >> 5;
-  const uint32_t lo = w < words ? __ldg(row + w) : 0u;
-  const uint32_t hi = w + 1 < words ? __ldg(row + w + 1) : 0u;
+  const uint32_t lo = w < words ? row[w] : 0u;
+  const uint32_t hi = w + 1 < words ? row[w + 1] : 0u;
   return __funnelshift_r(lo, hi, i0 & 31);
 }
 
 // Visibility of 32 consecutive keys whose first is window key i0 (i0 < 0: the
 // first -i0 of them lie before the window and are seen) as bits; only the
 // first `valid` of them (<= 0: none) lie inside the context.
-__device__ __forceinline__ uint32_t tree_visible32(const uint32_t* __restrict__ row, int words,
-                                                   int i0, int valid) {
+__device__ __forceinline__ uint32_t tree_visible32(const uint32_t* row, int words, int i0,
+                                                   int valid) {
   uint32_t vis;
   if (i0 >= 0)
     vis = mask_window32(row, words, i0);

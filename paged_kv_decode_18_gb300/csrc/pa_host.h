@@ -120,7 +120,9 @@ struct NvtxRange {
 };
 
 // Launch a kernel as a programmatic dependent of the previous grid on the
-// stream (it may start before that grid ends and waits inside).
+// stream (it may start before that grid ends and waits inside). What that grid
+// may write, a caller's inputs among it, such a kernel reads by ordinary loads
+// after the wait: the non-coherent path is for data that is constant while it runs.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t st, Args... args) {

@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
             const uint32_t* mr = a.mask + (pend_orow / a.Hq) * a.mask_words;
             const int i1 = min(lqp, pend_k1 - p0);  // the piece's window keys
             for (int i = max(0, pend_k0 - p0); i < i1; ++i) {
-              if (!((__ldg(mr + (i >> 5)) >> (i & 31)) & 1u)) continue;
+              if (!((mr[i >> 5] >> (i & 31)) & 1u)) continue;
               const int phys =
                   a.block_tables[(size_t)pend_s * a.max_blocks + (p0 + i) / kBlock];
               if (phys < 0 || (int64_t)phys >= a.num_blocks) continue;
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                   ((((int64_t)phys * Hkv + pend_h) * kBlock) + (p0 + i) % kBlock) * kHeadDim + d0);
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const uint32_t wv = __ldg(vr + j), fin = bf2_finite_part(wv);
+                const uint32_t wv = vr[j], fin = bf2_finite_part(wv);
                 if ((wv ^ fin) & 0x7f80u) o[2 * j] += bf_lo(wv);
                 if ((wv ^ fin) & 0x7f800000u) o[2 * j + 1] += bf_hi(wv);
               }

@@ -22,8 +22,8 @@ constexpr int kMaskThreads = 128;
 constexpr int kMaskStage = 8192;  // parents staged in shared memory (32 KB); longer windows read global
 
 __global__ void __launch_bounds__(kMaskThreads)
-    tree_mask_kernel(const int32_t* __restrict__ parents, const int32_t* __restrict__ cu,
-                     int64_t num_q_tokens, int max_q_len, int words, uint32_t* __restrict__ mask,
+    tree_mask_kernel(const int32_t* parents, const int32_t* cu, int64_t num_q_tokens,
+                     int max_q_len, int words, uint32_t* __restrict__ mask,
                      int32_t* __restrict__ depths) {
   extern __shared__ int32_t sp[];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -84,9 +84,9 @@ constexpr int kCommitGroup = 8;  // rows a warp holds between reading and writin
 template <bool Q8>
 __global__ void __launch_bounds__(kCommitWarps * 32)
     commit_path_kernel(uint8_t* k_cache, uint8_t* v_cache,
-                       const int32_t* __restrict__ block_tables, const int32_t* context_lens,
-                       const int32_t* __restrict__ cu, const int32_t* __restrict__ path,
-                       const int32_t* __restrict__ path_lens, int max_path_len,
+                       const int32_t* block_tables, const int32_t* context_lens,
+                       const int32_t* cu, const int32_t* path, const int32_t* path_lens,
+                       int max_path_len,
                        int32_t* new_lens, int max_blocks, int64_t num_blocks, int Hkv) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

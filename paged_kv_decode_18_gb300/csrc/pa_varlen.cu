@@ -269,10 +269,10 @@ __device__ __forceinline__ void varlen_body(const CUtensorMap& tmk, const CUtens
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const int c = kk * 8 + quad;  // 32-bit word of dims kk*16 + 2*quad
-          qa[kk][0] = qrow[0] ? __ldg(qrow[0] + c) : 0u;
-          qa[kk][1] = qrow[1] ? __ldg(qrow[1] + c) : 0u;
-          qa[kk][2] = qrow[0] ? __ldg(qrow[0] + c + 4) : 0u;
-          qa[kk][3] = qrow[1] ? __ldg(qrow[1] + c + 4) : 0u;
+          qa[kk][0] = qrow[0] ? qrow[0][c] : 0u;
+          qa[kk][1] = qrow[1] ? qrow[1][c] : 0u;
+          qa[kk][2] = qrow[0] ? qrow[0][c + 4] : 0u;
+          qa[kk][3] = qrow[1] ? qrow[1][c + 4] : 0u;
         }
       }
 #pragma unroll
@@ -535,9 +535,8 @@ constexpr int kFixGroups = 4;
 
 template <int GROUPS>
 __global__ void __launch_bounds__(kFixWarps * 32 * GROUPS)
-    varlen_fixup_kernel(const int* __restrict__ desc, const float* __restrict__ part_o,
-                        const float* __restrict__ part_lse,
-                        const int32_t* __restrict__ cu_seqlens_q, int num_workers, int Hq, int G,
+    varlen_fixup_kernel(const int* desc, const float* part_o, const float* part_lse,
+                        const int32_t* cu_seqlens_q, int num_workers, int Hq, int G,
                         int QT, uint16_t* __restrict__ out, float* __restrict__ lse) {
   // the next grid in the stream may start its own preparation now; it waits
   // for this grid before it reads anything this grid writes

@@ -155,7 +155,7 @@ __device__ __forceinline__ void load_q(const WeightArgs& a, const unsigned char*
       const int tok = (col0 + cc) / a.G;
       const float l =
           staged ? reinterpret_cast<const float*>(staged + kQRows * kHeadDim * 2)[cc]
-                 : __ldg(a.lse + (q0 + tok) * a.Hq + h * a.G + (col0 + cc) % a.G);
+                 : a.lse[(q0 + tok) * a.Hq + h * a.G + (col0 + cc) % a.G];
       if (l != neg_inf()) {  // a query that saw nothing draws nothing
         t.l2[e] = l * kLog2e;
         // what the product lost, and log2 e's own rounding
