@@ -38,11 +38,12 @@
 #include "pa_host.h"
 #include "pa_tcgen05.cuh"
 #include "pa_weights.cuh"
+#include "pa_weights_plan.h"
 
 namespace pa {
 namespace {
 
-constexpr int kKeys = 128;                    // keys per item (MMA M)
+constexpr int kKeys = kWeightKeys;            // keys per item (MMA M)
 constexpr int kCols = 128;                    // query rows per tile (MMA N, at most)
 constexpr int kBlocksK = kKeys / kBlock;
 constexpr int kHalfB = 128 * 128;             // 64 dims of a 128-row bf16 operand
@@ -120,12 +121,6 @@ struct WPlan {
   int* q0;     // [S]
   int* lq;     // [S]
 };
-
-// Query tiles that key tile kt of a window meets: those from the first token
-// that sees a key of it.
-__device__ __forceinline__ int first_tile(int kt, int c, int lq, int QTb) {
-  return max(0, kt * kKeys - (c - lq)) / QTb;
-}
 
 struct Item {
   int s, h, i, nt;
@@ -221,15 +216,11 @@ __global__ void __launch_bounds__((Lay<FMT, SPLIT>::threads), 1)
     if (bad) flag_error(PA_DEVERR_QLEN_RANGE);
     // no query: nothing to add, zeros to write
     const int nt = bad || (lq == 0 && a.accumulate) ? 0 : (c + kKeys - 1) / kKeys;
-    const int nq = lq > 0 ? (lq + QTb - 1) / QTb : 0;
-    int cost = 0;
-    for (int kt = 0; kt < nt; ++kt)
-      cost += 1 + (nq > 1 ? nq - first_tile(kt, c, lq, QTb) : nq);
     P.ctx[s] = c;
     P.q0[s] = q0;
     P.lq[s] = bad ? 0 : lq;
     P.item[s] = Hkv * nt;
-    P.cost[s] = Hkv * cost;
+    P.cost[s] = window_cost(nt, c, lq, QTb, Hkv, S);
   }
   __syncthreads();
   if (warp == 0) {
