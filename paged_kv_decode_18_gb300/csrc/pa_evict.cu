@@ -21,9 +21,11 @@
 // write. A wave's writes fall before every later wave's sources, so the next
 // wave's reads begin before the cluster has met.
 // Bound: HBM for large moves, the chain of passes and meetings for small ones.
-// 8 contexts of 30,000..32,768 positions, 8 KV heads, int8, cut to 4096: 28.5 us
-// for 148 MB (5.2 TB/s), about a third of it selection; 32 of 1030..1153, bf16, to
-// 1024: 25 us, of which DRAM moves 185 MB (44 us with a cold L2).
+// Calls one after another, each on caches and weights of its own that no call has
+// touched since they left L2: 8 contexts of 30,000..32,768 positions, 8 KV heads,
+// int8, cut to 4096: 51 us, weights of 8 MB read and 4080 rows a head moved, 149 MB
+// or 2.9 TB/s; 32 of 1030..1153, bf16, to 1024: 46 us for 785 rows a head, 210 MB or
+// 4.5 TB/s. (A call on a cache that is still in L2 is faster: 25 us for the second.)
 #include "pa_device.cuh"
 #include "pa_host.h"
 #include "pa_rows.cuh"
@@ -353,7 +355,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictArgs
   Move next = look_up(step);
   for (int base = 0, half = 0; base < n; base += step, half ^= 1) {
     // this wave's rows are here; while the others' land too, the next wave's set
-    // out (their sources lie behind everything that this wave writes)
+    // out (their sources lie behind everything that this wave writes). Relaxed: the
+    // meeting keeps reads before others' writes, and these reads have ended; an
+    // arrival that also waits for this CTA's last writes costs 2 to 5 % of a call.
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -446,8 +450,10 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, int kv_format, const int32
   auto kernel = q8 ? evict_kernel<true> : evict_kernel<false>;
   if (!raise_smem_limit(reinterpret_cast<const void*>(kernel))) return PA_ERR_CUDA;
   // clusters as large as leave every (sequence, KV head) resident at two CTAs an
-  // SM (twice as large, in two rounds: 41 us against 28.6 us at 8 x 32k), but no
-  // larger than a slice of 1024 positions calls for
+  // SM (twice as large, in two rounds: 41 us against 28.6 us at 8 x 32k in L2), but
+  // no larger than a slice of 1024 positions calls for in the longest context that
+  // the table has room for -- the host knows no other bound. With a table of 32768
+  // positions the 32 contexts of 1030..1153 take the same 46 us.
   const int64_t heads = (int64_t)shape->num_seqs * a.Hkv;
   const int64_t most = (int64_t)a.max_blocks * kBlock / 1024;
   int cluster = 1;

@@ -29,9 +29,11 @@
 // contexts of 1000..8192 positions with 64 queries of two heads (157 MB) take
 // 36.2 us in bf16, 34.4 us with all of the epilogue's column work left out; FP8
 // codes (81 MB) 42.6 us, 4 us less without their conversion. Longer windows by the
-// epilogue and the waits between its tiles: 1024 rows take 189 us, 0.75 us a tile,
-// 135 us without the column work, 132 without the queries' loads as well and 109
-// with one product in eight, beside 0.27 us of tensor time.
+// epilogue and the waits between its tiles: 1024 rows take 187 us, 0.75 us a tile
+// (135 us without the column work, 132 without the queries' loads as well and 109
+// with one product in eight). No unit is near its limit meanwhile: tensor pipe 35 %,
+// exponentials 35 %, issue 46 % of one a clock and SM quarter; windows of 128 FP8
+// rows 20, 20 and 49 %. A tile is a chain of waits.
 #include <cudaTypedefs.h>
 
 #include "pa_device.cuh"
@@ -372,6 +374,10 @@ __global__ void __launch_bounds__((Lay<FMT, SPLIT>::threads), 1)
       for (int i = 0; i < kCols / 32; ++i) {
         const int col = i * 32 + lane;
         const bool draws = l[i] != neg_inf();  // a query that saw nothing draws nothing
+        // rounded once, to half a step of lse log2 e: exp is off by 2^-24 |lse| of
+        // itself, about what the fp32 score is off by; its low part, which the warp
+        // kernel carries, would take a second addition a column here (64 queries over
+        // 1000..8192 keys: 5.2e-7 off the 64-bit sums, a plain fp32 form 2.8e-7)
         col_l2[b * kCols + col] = draws ? -(l[i] * kLog2e) : 0.f;
         col_last[b * kCols + col] = draws ? c - lq + qt * QTb + tok_of[i] : -1;
         all = all && draws;
