@@ -477,7 +477,8 @@ size_t pa_decode_tree_workspace_size(const pa_shape* shape, int64_t num_q_tokens
  * byte copies), so that the path's tokens follow the context directly.
  *
  *   kv_format     PA_KV_BF16, PA_KV_INT8 or PA_KV_FP8; k_cache and v_cache in
- *                 place, 16-byte aligned
+ *                 place, 16-byte aligned (pa_decode_tree reads bf16 pools alone: an
+ *                 8-bit pool is for a caller whose window is verified by other means)
  *   path          [S][max_path_len] int32: strictly increasing window indices;
  *                 the first path_lens[s] entries of a row are read
  *   path_lens     [S] int32, 0 <= path_lens[s] <= min(Lq, max_path_len)
