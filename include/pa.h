@@ -562,6 +562,134 @@ int pa_evict(void* k_cache, void* v_cache, int kv_format, const int32_t* block_t
              int32_t* new_lens, const pa_shape* shape, void* stream);
 
 /*
+ * Rotary positions (course README, curriculum row on the model layer: "RoPE";
+ * Work-log, "KV Cache > The Idea": the cache holds keys that carry their own
+ * position). A rotation turns pair i of a head's first rot_dim dimensions,
+ * (x[a], x[b]), by the angle position * theta_i:
+ *   y[a] = m (x[a] cos - x[b] sin),   y[b] = m (x[b] cos + x[a] sin),
+ * with (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) where pairs are
+ * interleaved; the dimensions from rot_dim on pass unchanged. m, the magnitude,
+ * is 1 but for scalings that say otherwise.
+ *
+ * A pa_rotation is host memory that every call reads before it returns. theta_i
+ * is held as a fraction of a turn in steps of 2^-64 turns, so the product with
+ * an integer position, taken modulo 2^64, is the angle of any position without
+ * error beyond that of the fraction itself (2^-54 turns times the position);
+ * cosine and sine are fp32, off by at most 2^-19.
+ */
+typedef struct pa_rotation {
+  int rot_dim;        /* rotated dimensions of a head: even, 2 .. 128 */
+  int interleaved;    /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */
+  float magnitude;    /* factor on cosine and sine */
+  uint64_t turns[64]; /* theta_i / (2 pi) as a multiple of 2^-64; rot_dim / 2 used */
+} pa_rotation;
+
+/* Scalings of pa_rotation_init: theta_i = base^(-2i / rot_dim), changed for
+ * contexts that are `factor` times as long as the original_len tokens that the
+ * model was trained with. n_i = original_len * theta_i / (2 pi) is the number of
+ * turns of pair i over that length. */
+#define PA_ROT_PLAIN 0  /* theta_i */
+#define PA_ROT_LINEAR 1 /* theta_i / factor */
+#define PA_ROT_BASE 2   /* base * factor^(rot_dim / (rot_dim - 2)) in the place of base */
+#define PA_ROT_BANDS 3  /* theta_i where n_i >= high, theta_i / factor where n_i <= low, between
+                           them theta_i s + theta_i / factor (1 - s), s = (n_i - low) / (high - low) */
+#define PA_ROT_RAMP 4   /* theta_i (1 - s) + theta_i / factor s, s rising linearly in i from 0 at
+                           a to 1 at b: a the pair that makes `high` turns, rounded down, b the one
+                           that makes `low` turns, rounded up, both clamped to 0 .. rot_dim - 1 (a
+                           step where they meet); magnitude 0.1 ln(factor) + 1 */
+
+/*
+ * pa_rotation_init -- fill *rot (host). base > 0 (RAMP: base > 1); factor > 0
+ * (not read by PLAIN); original_len > 0 and 0 < low <= high (BANDS: low < high)
+ * are read by BANDS and RAMP alone. PA_ERR_ARG otherwise.
+ */
+int pa_rotation_init(pa_rotation* rot, int rot_dim, int interleaved, double base, int scaling,
+                     double factor, double original_len, double low, double high);
+
+/* pa_rotation_set -- fill *rot from rot_dim / 2 angles per position in radians
+ * (host, finite), for any other choice of them. */
+int pa_rotation_set(pa_rotation* rot, int rot_dim, int interleaved, const double* radians,
+                    float magnitude);
+
+/* Rows [tokens][heads][head_dim] of bf16 that need not be contiguous: row (t, h)
+ * begins at data + t * token_stride + h * head_stride (elements) and its head_dim
+ * values lie side by side. data 16-byte aligned, strides multiples of 8 and not
+ * negative. Rows that a call writes must not overlap. */
+typedef struct pa_row_view {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} pa_row_view;
+
+/*
+ * pa_rotate -- y[t][h] = x[t][h] rotated by positions[t].
+ *
+ *   positions  [num_tokens] int32, any value (a negative one turns back)
+ *   transpose  0, or 1: the transposed map (turned by -positions[t], times
+ *              the magnitude again), which is the gradient of the rotation and,
+ *              where the magnitude is 1, its inverse
+ *   y          the same rows as x (same data and strides), or rows that do not
+ *              overlap them
+ * Products and sums are fp32, rounded to bf16 once. Subnormals of rotated
+ * dimensions are read as zero; the other dimensions are copied bit by bit.
+ */
+int pa_rotate(const pa_row_view* x, const int32_t* positions, int64_t num_tokens, int num_heads,
+              int head_dim, const pa_rotation* rot, int transpose, const pa_row_view* y,
+              void* stream);
+
+/*
+ * pa_rotate_and_cache -- pa_reshape_and_cache (or its int8 or FP8 form) with the
+ * rotation on the way: for every t, k[t] rotated by positions[t] and v[t] as it
+ * is go to slot_mapping[t] of the pool, and q[t] rotated by positions[t] goes to
+ * q_out[t], in one pass over the three.
+ *
+ *   q, q_out      [num_tokens][num_q_heads], or both NULL; q_out may be q itself
+ *   k, v          [num_tokens][num_kv_heads]
+ *   positions     [num_tokens] int32; slot_mapping [num_tokens] int64, as in
+ *                 pa_reshape_and_cache: a token with slot < 0 leaves the pool as
+ *                 it is, one with a slot outside it does too and sets
+ *                 PA_DEVERR_SLOT_RANGE; the queries of both are rotated
+ *   kv_format     PA_KV_BF16, PA_KV_INT8 or PA_KV_FP8 of k_cache and v_cache
+ *   shape         uses num_q_heads (with q), num_kv_heads, head_dim, block_size,
+ *                 num_blocks
+ * The rotated key is rounded once: to bf16, or, as pa_reshape_and_cache_int8
+ * and _fp8 quantise a row, from its fp32 values to codes and a scale. v gets the
+ * bytes that those calls write.
+ */
+int pa_rotate_and_cache(const pa_row_view* q, const pa_row_view* k, const pa_row_view* v,
+                        const int32_t* positions, const int64_t* slot_mapping,
+                        int64_t num_tokens, const pa_rotation* rot, const pa_row_view* q_out,
+                        void* k_cache, void* v_cache, int kv_format, const pa_shape* shape,
+                        void* stream);
+
+/*
+ * pa_rotate_cached -- keys that are already cached and rotated are turned on to
+ * new positions, in place: when what was before them has left the cache (an
+ * eviction, a dropped prefix), so that positions stay within the range that the
+ * model knows. Exactly one of shifts and kept is given:
+ *
+ *   shifts   [S] int32: every key of sequence s from position `first` on is
+ *            turned by shifts[s] positions (negative: towards the beginning);
+ *            the first `first` positions stay
+ *   kept     [S][num_kv_heads][kept_len] int32, what pa_evict wrote: the key at
+ *            position i of KV head h, which was at position kept[s][h][i], is
+ *            turned by i - kept[s][h][i]; a negative entry, and a position from
+ *            kept_len on, stays. `first` is 0.
+ *   context_lens  [S] int32 of the cache as it is now (new_lens of pa_evict)
+ *   rot      the rotation that the keys were cached with; its magnitude is not
+ *            applied again
+ * A key turned by 0 keeps its bytes; another is rounded again (an 8-bit one is
+ * dequantised, turned and quantised anew). Blocks that hold turned keys must
+ * belong to one sequence alone. A context longer than the table sets
+ * PA_DEVERR_CONTEXT_RANGE, a block outside the pool PA_DEVERR_BLOCK_RANGE (its
+ * keys are skipped). Plan limits as above.
+ */
+int pa_rotate_cached(void* k_cache, int kv_format, const int32_t* block_tables,
+                     const int32_t* context_lens, const int32_t* shifts, int first,
+                     const int32_t* kept, int kept_len, const pa_rotation* rot,
+                     const pa_shape* shape, void* stream);
+
+/*
  * pa_splitk_reduce -- merge of split-K partial softmax results (course
  * README, "online softmax is exact; paged and split-K variants agree").
  * For each (row, head):

@@ -63,6 +63,11 @@ EXPORTED = (
     "pa_commit_path",
     "pa_accumulate_weights",
     "pa_evict",
+    "pa_rotation_init",
+    "pa_rotation_set",
+    "pa_rotate",
+    "pa_rotate_and_cache",
+    "pa_rotate_cached",
     "pa_splitk_reduce",
     "pa_status_string",
     "pa_debug_read_error",
@@ -80,6 +85,23 @@ class pa_shape(ctypes.Structure):
         ("block_size", ctypes.c_int),
         ("max_blocks_per_seq", ctypes.c_int),
         ("num_blocks", ctypes.c_int64),
+    ]
+
+
+class pa_rotation(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+        ("magnitude", ctypes.c_float),
+        ("turns", ctypes.c_uint64 * 64),
+    ]
+
+
+class pa_row_view(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
     ]
 
 
@@ -155,6 +177,17 @@ def load(path: str | None = None):
                                               S, V]
         lib.pa_evict.restype = i32
         lib.pa_evict.argtypes = [V, V, i32, V, V, V, i64, V, i32, i32, i32, V, V, S, V]
+        R, Rows, f64 = ctypes.POINTER(pa_rotation), ctypes.POINTER(pa_row_view), ctypes.c_double
+        lib.pa_rotation_init.restype = i32
+        lib.pa_rotation_init.argtypes = [R, i32, i32, f64, i32, f64, f64, f64, f64]
+        lib.pa_rotation_set.restype = i32
+        lib.pa_rotation_set.argtypes = [R, i32, i32, ctypes.POINTER(f64), f32]
+        lib.pa_rotate.restype = i32
+        lib.pa_rotate.argtypes = [Rows, V, i64, i32, i32, R, i32, Rows, V]
+        lib.pa_rotate_and_cache.restype = i32
+        lib.pa_rotate_and_cache.argtypes = [Rows, Rows, Rows, V, V, i64, R, Rows, V, V, i32, S, V]
+        lib.pa_rotate_cached.restype = i32
+        lib.pa_rotate_cached.argtypes = [V, i32, V, V, V, i32, V, i32, R, S, V]
         lib.pa_splitk_reduce.restype = i32
         lib.pa_splitk_reduce.argtypes = [V, V, i64, i32, i32, i32, V, V, V]
         lib.pa_status_string.restype = ctypes.c_char_p
@@ -805,6 +838,190 @@ def pa_evict(k_cache, v_cache, block_tables, context_lens, weights, budgets, num
     receives their old positions, new_lens [S] the new lengths."""
     prepare_evict(k_cache, v_cache, block_tables, context_lens, weights, budgets, num_sinks,
                   num_recent, kept, new_lens, stream)()
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+
+ROTATION_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+
+
+def make_rotation(rot_dim: int = 128, interleaved: bool = False, base: float = 10000.0,
+                  scaling: str = "none", factor: float = 1.0, original_len: float = 0.0,
+                  low: float = 1.0, high: float = 4.0) -> pa_rotation:
+    """A rotary-position map of a head's first rot_dim dimensions, pairs (i, i +
+    rot_dim/2) or (2i, 2i+1), with angles base^(-2i/rot_dim) per position.
+    scaling: "none", "linear", "base", "bands" or "ramp", for contexts that are
+    `factor` times the original_len tokens of training; bands and ramp change
+    between pairs that make `low` and `high` turns over that length."""
+    if scaling not in ROTATION_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROTATION_SCALINGS)}, got {scaling!r}")
+    rot = pa_rotation()
+    _check(load().pa_rotation_init(ctypes.byref(rot), int(rot_dim), 1 if interleaved else 0,
+                                   float(base), ROTATION_SCALINGS[scaling], float(factor),
+                                   float(original_len), float(low), float(high)),
+           "pa_rotation_init")
+    return rot
+
+
+def make_rotation_from(radians, interleaved: bool = False, magnitude: float = 1.0) -> pa_rotation:
+    """A rotary-position map from the angles per position of its rot_dim/2 pairs
+    (numbers, or a CPU tensor)."""
+    values = [float(x) for x in radians]
+    rot = pa_rotation()
+    _check(load().pa_rotation_set(ctypes.byref(rot), 2 * len(values), 1 if interleaved else 0,
+                                  (ctypes.c_double * max(1, len(values)))(*values),
+                                  float(magnitude)), "pa_rotation_set")
+    return rot
+
+
+def _row_view(x, name):
+    """[tokens, heads, head_dim] bf16 with any token and head strides."""
+    if x is None:
+        raise ValueError(f"{name} is required")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+    if x.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {x.dim()}")
+    if x.shape[2] > 1 and x.stride(2) != 1:
+        raise ValueError(f"{name} must hold a head's values side by side")
+    # (the stride of an axis of one entry says nothing)
+    return pa_row_view(x.data_ptr(), x.stride(0) if x.shape[0] > 1 else 0,
+                       x.stride(1) if x.shape[1] > 1 else 0)
+
+
+def _rotation(rot):
+    """A copy of the caller's map: a prepared call keeps what it was made with."""
+    if not isinstance(rot, pa_rotation):
+        raise TypeError("rotation must be a pa_rotation (make_rotation)")
+    return pa_rotation.from_buffer_copy(rot)
+
+
+def prepare_rotate(x, positions, rotation, y, transpose: bool = False, stream=None):
+    """pa_rotate with its arguments checked and marshalled now (see
+    prepare_decode)."""
+    xv, yv = _row_view(x, "x"), _row_view(y, "y")
+    _need(positions, "positions", torch.int32, 1)
+    if y.shape != x.shape:
+        raise ValueError("y shape != x shape")
+    if positions.shape[0] != x.shape[0]:
+        raise ValueError("positions length != number of tokens")
+    _here(x, positions, y)
+    rot = _rotation(rotation)
+    args = (ctypes.byref(xv), _ptr(positions), ctypes.c_int64(x.shape[0]),
+            ctypes.c_int(x.shape[1]), ctypes.c_int(x.shape[2]), ctypes.byref(rot),
+            ctypes.c_int(1 if transpose else 0), ctypes.byref(yv))
+    keep = (x, positions, y, xv, yv, rot)
+    return _prepared(load().pa_rotate, args, stream, "pa_rotate", keep)
+
+
+def pa_rotate(x, positions, rotation, y, transpose: bool = False, stream=None) -> None:
+    """y = x [T, H, 128] with row t of every head rotated by positions[t] (int32);
+    y may be x. transpose: the transposed map, the gradient of the rotation."""
+    prepare_rotate(x, positions, rotation, y, transpose, stream)()
+
+
+def _kv_format(k_cache, kv_format):
+    """The format of a pool array: 8-bit tiles do not tell int8 from FP8."""
+    if k_cache.dim() == 3:
+        _need(k_cache, "k_cache", torch.uint8, 3)
+        if kv_format not in (PA_KV_INT8, PA_KV_FP8):
+            raise ValueError("an 8-bit pool needs kv_format PA_KV_INT8 or PA_KV_FP8")
+        return kv_format
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    if kv_format not in (None, PA_KV_BF16):
+        raise ValueError("a bf16 pool has kv_format PA_KV_BF16")
+    return PA_KV_BF16
+
+
+def prepare_rotate_and_cache(k, v, positions, slot_mapping, rotation, k_cache, v_cache, q=None,
+                             q_out=None, kv_format: int | None = None, stream=None):
+    """pa_rotate_and_cache with its arguments checked and marshalled now (see
+    prepare_decode)."""
+    kv, vv = _row_view(k, "k"), _row_view(v, "v")
+    _need(positions, "positions", torch.int32, 1)
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    fmt = _kv_format(k_cache, kv_format)
+    _need(v_cache, "v_cache", k_cache.dtype, k_cache.dim())
+    if k.shape != v.shape or k_cache.shape != v_cache.shape:
+        raise ValueError("k/v or cache shapes differ")
+    T = k.shape[0]
+    if positions.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("positions / slot_mapping length != number of tokens")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    qv = ov = None
+    if q is not None:
+        qv, ov = _row_view(q, "q"), _row_view(q_out, "q_out")
+        if q.shape[0] != T or q_out.shape != q.shape:
+            raise ValueError("q / q_out rows != number of tokens")
+    sh = shape_of(k if q is None else q, k_cache, torch.empty((0, 0)))
+    if k.shape[1:] != (sh.num_kv_heads, sh.head_dim):
+        raise ValueError("k rows do not match the cache's [Hkv, D]")
+    if q is not None and q.shape[2] != sh.head_dim:
+        raise ValueError("q head_dim != the cache's")
+    _here(k, v, positions, slot_mapping, k_cache, v_cache, q, q_out)
+    rot = _rotation(rotation)
+    args = (ctypes.byref(qv) if qv else None, ctypes.byref(kv), ctypes.byref(vv),
+            _ptr(positions), _ptr(slot_mapping), ctypes.c_int64(T), ctypes.byref(rot),
+            ctypes.byref(ov) if ov else None, _ptr(k_cache), _ptr(v_cache), ctypes.c_int(fmt),
+            ctypes.byref(sh))
+    keep = (k, v, positions, slot_mapping, k_cache, v_cache, q, q_out, qv, kv, vv, ov, rot, sh)
+    return _prepared(load().pa_rotate_and_cache, args, stream, "pa_rotate_and_cache", keep)
+
+
+def pa_rotate_and_cache(k, v, positions, slot_mapping, rotation, k_cache, v_cache, q=None,
+                        q_out=None, kv_format: int | None = None, stream=None) -> None:
+    """A step's rows into the cache with the rotation on the way: k [T, Hkv, 128]
+    rotated by positions [T] int32 and v as it is go to their slots, q
+    [T, Hq, 128] rotated goes to q_out (which may be q)."""
+    prepare_rotate_and_cache(k, v, positions, slot_mapping, rotation, k_cache, v_cache, q, q_out,
+                             kv_format, stream)()
+
+
+def prepare_rotate_cached(k_cache, block_tables, context_lens, rotation, shifts=None, kept=None,
+                          first: int = 0, kv_format: int | None = None, stream=None):
+    """pa_rotate_cached with its arguments checked and marshalled now (see
+    prepare_decode)."""
+    fmt = _kv_format(k_cache, kv_format)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    sh = _pool_shape(k_cache, block_tables)
+    S = sh.num_seqs
+    if context_lens.shape[0] != S:
+        raise ValueError("context_lens length != number of sequences")
+    if (shifts is None) == (kept is None):
+        raise ValueError("one of shifts and kept is needed")
+    if shifts is not None:
+        _need(shifts, "shifts", torch.int32, 1)
+        if shifts.shape[0] != S:
+            raise ValueError("shifts length != number of sequences")
+    else:
+        _need(kept, "kept", torch.int32, 3)
+        if kept.shape[:2] != (S, sh.num_kv_heads):
+            raise ValueError("kept must be [num_seqs, num_kv_heads, positions]")
+        if first:
+            raise ValueError("first goes with shifts")
+    _here(k_cache, block_tables, context_lens, shifts, kept)
+    rot = _rotation(rotation)
+    args = (_ptr(k_cache), ctypes.c_int(fmt), _ptr(block_tables), _ptr(context_lens),
+            _ptr(shifts), ctypes.c_int(int(first)), _ptr(kept),
+            ctypes.c_int(0 if kept is None else kept.shape[2]), ctypes.byref(rot),
+            ctypes.byref(sh))
+    keep = (k_cache, block_tables, context_lens, shifts, kept, rot, sh)
+    return _prepared(load().pa_rotate_cached, args, stream, "pa_rotate_cached", keep)
+
+
+def pa_rotate_cached(k_cache, block_tables, context_lens, rotation, shifts=None, kept=None,
+                     first: int = 0, kv_format: int | None = None, stream=None) -> None:
+    """Turn cached keys on to new positions, in place: by shifts [S] int32 from
+    position `first` on, or each from the position kept [S, Hkv, n] int32
+    (pa_evict) to the one it has now."""
+    prepare_rotate_cached(k_cache, block_tables, context_lens, rotation, shifts, kept, first,
+                          kv_format, stream)()
 
 
 def pa_splitk_reduce(part_out, part_lse, out, lse=None, stream=None) -> None:

@@ -13,6 +13,7 @@
 // into the tile.
 #include "pa_device.cuh"
 #include "pa_host.h"
+#include "pa_quant.cuh"
 
 namespace pa {
 namespace {
@@ -66,10 +67,7 @@ __device__ __forceinline__ void quantize_row_to(const uint2 x, int lane, int8_t*
     const float inv = __fdiv_rn(127.f, amax);
     const float fs[4] = {f0, f1, f2, f3};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float t = fminf(fmaxf(rintf(__fmul_rn(fs[j], inv)), -127.f), 127.f);
-      packed |= ((uint32_t)(int)t & 0xffu) << (8 * j);
-    }
+    for (int j = 0; j < 4; ++j) packed |= int8_code(fs[j], inv) << (8 * j);
   }
   reinterpret_cast<uint32_t*>(dst)[lane] = packed;
   if (lane == 0) *scale_dst = amax > 0.f ? __fdiv_rn(amax, 127.f) : 0.f;
@@ -80,12 +78,6 @@ __device__ __forceinline__ void quantize_row_to(const uint2 x, int lane, int8_t*
 // fp32, code = the nearest E4M3 value of y (ties to the even code), saturated
 // to +-448 (the hardware conversion with .satfinite), scale = amax / 448. A
 // zero row stores code 0 and scale 0. The codes never hold the NaN patterns.
-__device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
-  uint16_t c;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
-  return c;
-}
-
 __device__ __forceinline__ void quantize_row_f8_to(const uint2 x, int lane,
                                                    uint8_t* __restrict__ dst,
                                                    float* __restrict__ scale_dst) {

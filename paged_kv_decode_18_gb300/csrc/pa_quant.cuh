@@ -1,0 +1,76 @@
+// pa_quant.cuh -- codes of the 8-bit pools: a row's values times 127 / amax
+// (int8) or 448 / amax (FP8 E4M3), rounded to nearest even.
+#pragma once
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+// The int8 code of one value (as its low byte), inv = 127 / amax of its row.
+__device__ __forceinline__ uint32_t int8_code(float x, float inv) {
+  const float t = fminf(fmaxf(rintf(__fmul_rn(x, inv)), -127.f), 127.f);
+  return (uint32_t)(int)t & 0xffu;
+}
+
+// The E4M3 codes of two scaled values, the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+  return c;
+}
+
+// The values of two E4M3 codes (exact in f16, and so in fp32).
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+  float2 f;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+
+// A row's largest magnitude maps to this code value.
+template <bool FP8>
+__device__ __forceinline__ float code_range() {
+  return FP8 ? 448.f : 127.f;
+}
+
+// Codes of eight consecutive values of a row as eight bytes.
+template <bool FP8>
+__device__ __forceinline__ uint2 codes_of8(const float* x, float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float* f = x + 4 * i;
+    if constexpr (FP8)
+      w[i] = e4m3x2_of(__fmul_rn(f[0], inv), __fmul_rn(f[1], inv)) |
+             (e4m3x2_of(__fmul_rn(f[2], inv), __fmul_rn(f[3], inv)) << 16);
+    else
+      w[i] = int8_code(f[0], inv) | (int8_code(f[1], inv) << 8) | (int8_code(f[2], inv) << 16) |
+             (int8_code(f[3], inv) << 24);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Values of eight codes times their row's scale.
+template <bool FP8>
+__device__ __forceinline__ void values_of8(uint2 c, float scale, float* x) {
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (FP8) {
+      const float2 lo = e4m3x2_values(w[i] & 0xffffu), hi = e4m3x2_values(w[i] >> 16);
+      x[4 * i] = lo.x * scale;
+      x[4 * i + 1] = lo.y * scale;
+      x[4 * i + 2] = hi.x * scale;
+      x[4 * i + 3] = hi.y * scale;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[4 * i + j] = (float)(int)(int8_t)((w[i] >> (8 * j)) & 0xffu) * scale;
+    }
+  }
+}
+
+}  // namespace pa
