@@ -690,6 +690,45 @@ int pa_rotate_cached(void* k_cache, int kv_format, const int32_t* block_tables,
                      const pa_shape* shape, void* stream);
 
 /*
+ * pa_decode_diff -- differential attention over the paged pool: the difference
+ * of two softmax maps, each with queries and keys of its own, over values that
+ * they share. KV heads 2p and 2p + 1 form pair p: their keys are the two maps',
+ * their values side by side one value of 2 * head_dim. With G = num_q_heads /
+ * num_kv_heads query heads per KV head, head p * G + g of the num_q_heads / 2
+ * differential heads is, for each query,
+ *   a_i = softmax(scale * q[(2p + i) * G + g] . K[2p + i]) [V[2p], V[2p + 1]]
+ *   d   = a_0 - lambdas[p * G + g] * a_1
+ *   out = out_scale * d                                        without norm_weight
+ *       = out_scale * norm_weight * d / sqrt(mean(d^2) + norm_eps)   with it.
+ *
+ *   q             [num_q_tokens][num_q_heads][D] bf16
+ *   cu_seqlens_q, num_q_tokens, max_q_len, causal   as in pa_decode_varlen; or
+ *                 cu_seqlens_q NULL, num_q_tokens == S and max_q_len 1: one query
+ *                 per sequence, which sees its whole context
+ *   lambdas       [num_q_heads / 2] fp32 (a model's learned vectors make one
+ *                 number of them before it is served)
+ *   norm_weight   [2 * D] fp32, or NULL; norm_eps >= 0
+ *   out           [num_q_tokens][num_q_heads / 2][2 * D] bf16
+ *   lse           [num_q_tokens][num_q_heads] fp32 of each map, or NULL
+ *   workspace     at least pa_decode_diff_workspace_size(...) bytes, 256-byte
+ *                 aligned; clobbered
+ * bf16 pools with an even num_kv_heads and 1 to 8 query heads per KV head
+ * (else PA_ERR_UNSUPPORTED, workspace size 0). Both maps, their difference and
+ * the norm are fp32; the softmax weights are rounded to bf16 for the product
+ * with V, as in pa_decode_varlen. A sequence of the single-query form with an
+ * empty context gives out = 0 and lse = -inf. A key that a query does not see
+ * never reaches its result, whatever its K and V hold.
+ */
+int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
+                   const int32_t* block_tables, const int32_t* context_lens,
+                   const int32_t* cu_seqlens_q, int64_t num_q_tokens, int max_q_len, int causal,
+                   float scale, const float* lambdas, const float* norm_weight, float norm_eps,
+                   float out_scale, pa_bf16* out, float* lse, const pa_shape* shape,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+size_t pa_decode_diff_workspace_size(const pa_shape* shape, int64_t num_q_tokens, int max_q_len);
+
+/*
  * pa_splitk_reduce -- merge of split-K partial softmax results (course
  * README, "online softmax is exact; paged and split-K variants agree").
  * For each (row, head):

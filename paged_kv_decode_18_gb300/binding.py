@@ -68,6 +68,8 @@ EXPORTED = (
     "pa_rotate",
     "pa_rotate_and_cache",
     "pa_rotate_cached",
+    "pa_decode_diff",
+    "pa_decode_diff_workspace_size",
     "pa_splitk_reduce",
     "pa_status_string",
     "pa_debug_read_error",
@@ -188,6 +190,11 @@ def load(path: str | None = None):
         lib.pa_rotate_and_cache.argtypes = [Rows, Rows, Rows, V, V, i64, R, Rows, V, V, i32, S, V]
         lib.pa_rotate_cached.restype = i32
         lib.pa_rotate_cached.argtypes = [V, i32, V, V, V, i32, V, i32, R, S, V]
+        lib.pa_decode_diff.restype = i32
+        lib.pa_decode_diff.argtypes = [V, V, V, V, V, V, i64, i32, i32, f32, V, V, f32, f32, V, V,
+                                       S, V, sz, V]
+        lib.pa_decode_diff_workspace_size.restype = sz
+        lib.pa_decode_diff_workspace_size.argtypes = [S, i64, i32]
         lib.pa_splitk_reduce.restype = i32
         lib.pa_splitk_reduce.argtypes = [V, V, i64, i32, i32, i32, V, V, V]
         lib.pa_status_string.restype = ctypes.c_char_p
@@ -1022,6 +1029,81 @@ def pa_rotate_cached(k_cache, block_tables, context_lens, rotation, shifts=None,
     (pa_evict) to the one it has now."""
     prepare_rotate_cached(k_cache, block_tables, context_lens, rotation, shifts, kept, first,
                           kv_format, stream)()
+
+
+# ---------------------------------------------------------------------------
+# differential attention
+# ---------------------------------------------------------------------------
+
+def pa_decode_diff_workspace_size(shape: pa_shape, num_q_tokens: int, max_q_len: int = 1) -> int:
+    return int(load().pa_decode_diff_workspace_size(ctypes.byref(shape), int(num_q_tokens),
+                                                    int(max_q_len)))
+
+
+def prepare_decode_diff(q, k_cache, v_cache, block_tables, context_lens, scale, lambdas, out,
+                        lse=None, cu_seqlens_q=None, max_q_len: int = 1, causal: bool = True,
+                        norm_weight=None, norm_eps: float = 1e-5, out_scale: float = 1.0,
+                        workspace=None, stream=None):
+    """pa_decode_diff with its arguments checked and marshalled now (see
+    prepare_decode)."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    _need(lambdas, "lambdas", torch.float32, 1)
+    _need(out, "out", torch.bfloat16, 3)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k / v cache shapes differ")
+    sh = shape_of(q, k_cache, block_tables)
+    T, Hq, D = q.shape
+    if D != sh.head_dim:
+        raise ValueError("q head_dim != the cache's")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2)
+        if lse.shape != (T, Hq):
+            raise ValueError("lse shape != q rows x heads")
+    if Hq % 2 or lambdas.shape[0] != Hq // 2:
+        raise ValueError("lambdas must have one entry per two query heads")
+    if out.shape != (T, Hq // 2, 2 * D):
+        raise ValueError("out must be [tokens, query heads / 2, 2 * head_dim]")
+    if norm_weight is not None:
+        _need(norm_weight, "norm_weight", torch.float32, 1)
+        if norm_weight.shape[0] != 2 * D:
+            raise ValueError("norm_weight must have 2 * head_dim entries")
+    if context_lens.shape[0] != sh.num_seqs:
+        raise ValueError("context_lens length != number of sequences")
+    if cu_seqlens_q is None:
+        if T != sh.num_seqs or int(max_q_len) != 1:
+            raise ValueError("without cu_seqlens_q there is one query per sequence")
+    else:
+        _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+        if cu_seqlens_q.shape[0] != sh.num_seqs + 1:
+            raise ValueError("cu_seqlens_q needs num_seqs + 1 entries")
+    _here(q, k_cache, v_cache, block_tables, context_lens, lambdas, out, lse, cu_seqlens_q,
+          norm_weight, workspace)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
+            _ptr(cu_seqlens_q), ctypes.c_int64(T), ctypes.c_int(int(max_q_len)),
+            ctypes.c_int(1 if causal else 0), ctypes.c_float(scale), _ptr(lambdas),
+            _ptr(norm_weight), ctypes.c_float(norm_eps), ctypes.c_float(out_scale), _ptr(out),
+            _ptr(lse), ctypes.byref(sh), _ptr(workspace), ctypes.c_size_t(ws_bytes))
+    keep = (q, k_cache, v_cache, block_tables, context_lens, lambdas, out, lse, cu_seqlens_q,
+            norm_weight, workspace, sh)
+    return _prepared(load().pa_decode_diff, args, stream, "pa_decode_diff", keep)
+
+
+def pa_decode_diff(q, k_cache, v_cache, block_tables, context_lens, scale, lambdas, out, lse=None,
+                   cu_seqlens_q=None, max_q_len: int = 1, causal: bool = True, norm_weight=None,
+                   norm_eps: float = 1e-5, out_scale: float = 1.0, workspace=None,
+                   stream=None) -> None:
+    """Differential attention: head p*G+g of out [T, Hq/2, 256] is the attention of
+    query head 2p*G+g over KV head 2p's keys minus lambdas[p*G+g] times that of
+    query head (2p+1)*G+g over KV head 2p+1's, both over the two heads' values side
+    by side, then (norm_weight) normed by its root mean square, times out_scale."""
+    prepare_decode_diff(q, k_cache, v_cache, block_tables, context_lens, scale, lambdas, out, lse,
+                        cu_seqlens_q, max_q_len, causal, norm_weight, norm_eps, out_scale,
+                        workspace, stream)()
 
 
 def pa_splitk_reduce(part_out, part_lse, out, lse=None, stream=None) -> None:

@@ -27,6 +27,7 @@ extern "C" int pa_debug_read_error(void* stream) {
   word |= pa::take_error_word_weights_tc(st, &rc);
   word |= pa::take_error_word_evict(st, &rc);
   word |= pa::take_error_word_rotate(st, &rc);
+  word |= pa::take_error_word_diff(st, &rc);
   if (rc != PA_OK) return rc;
   return static_cast<int>(word);
 }

@@ -1,0 +1,767 @@
+// pa_diff.cu -- differential attention over the paged pool: the difference of
+// two softmax maps over values that they share, one query per sequence or short
+// windows of them.
+//
+// Pages: course README "Build an LLM Inference Engine From Scratch", curriculum
+// rows "Memory & KV Cache" (PagedAttention, GQA) and "Batching & Scheduling"
+// (FlashAttention), and its claim that online softmax is exact and split-K
+// variants agree: both maps are softmax maps, so both are cut and merged by it.
+//
+// KV heads 2p and 2p + 1 of a block lie side by side in the pool, so their two
+// key tiles are one copy of 8 KB, and their value tiles another. K is read by
+// one map, V by both: 2 FMA for each value of K and 4 for each of V per query
+// row, which the CUDA cores could just do for one row of a map while HBM
+// delivers; from two rows on (G >= 2) they could not, so both products run on
+// the tensor cores (mma.sync m16n8k16) in tiles of 16 rows: rows 0-7 are (query
+// token, head) rows of the first map, rows 8-15 the same of the second.
+//   S: both maps' rows against either key tile; of a product with K[2p] rows 0-7
+//      are kept, of one with K[2p + 1] rows 8-15. The other half is thrown away
+//      (the tensor cores are a tenth busy), and a map never meets the other's
+//      keys, whatever they hold.
+//   O: P (16 rows x 16 keys) times V (16 keys x 256 dims), 128 accumulators a lane.
+// The two results of a row end in the same lane, so difference, norm and scale
+// cost no exchange but the sum of squares: a segment that one warp has worked
+// through alone writes its bf16 output at once.
+// A warp is a worker with its own ring of 16 KB stages and an equal range of
+// the batch's (sequence, query tile, pair, block) tiles; segments that ranges
+// cut leave fp32 partials, which diff_fixup_kernel merges.
+#include <cudaTypedefs.h>
+
+#include "pa_diff.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kMapRows = 8;                 // rows of one map in a tile
+constexpr int kDRows = 2 * kMapRows;
+constexpr int kDStage = 4 * kTileBytes;     // K[2p] K[2p+1] V[2p] V[2p+1] = 16 KB
+constexpr int kDWarps = 4;
+constexpr int kDMaxStages = 3;
+constexpr int kDDesc = 8;
+
+struct DiffArgs {
+  const uint16_t* q;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* cu_seqlens_q;  // null: one query per sequence
+  DiffOut o;
+  float scale_log2;
+  int S, Hq, Hkv, G, QT, max_blocks;
+  int64_t num_blocks;
+  int64_t num_q_tokens;
+  int causal;
+  int npairs_cap;
+  int num_workers;
+  int nstage;
+  int max_lq;       // longer windows belong to the tcgen05 kernel
+  float* part_o;    // [NW*2][16][256]
+  float* part_lse;  // [NW*2][16]
+  int* desc;        // [NW][kDDesc]
+};
+
+// byte offset of a row's 16-byte chunk (0 .. 15) in a 16 x 128 tile that came in as
+// (8-row group, 64-dim half) atoms of 1 KB with the 128-byte swizzle
+__device__ __forceinline__ uint32_t atom_at(int row, int chunk) {
+  return (uint32_t)((row >> 3) * 2048 + (chunk >> 3) * 1024 + (row & 7) * 128 +
+                    (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+__global__ void __launch_bounds__(kDWarps * 32, 1)
+    paged_diff_kernel(const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv, const DiffArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  unsigned char* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nstage = a.nstage;
+  unsigned char* wbuf = smem + warp * nstage * kDStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDWarps * nstage * kDStage) +
+                   warp * kDMaxStages;
+  const int S = a.S, Hq = a.Hq, G = a.G, QT = a.QT, Hp = a.Hkv >> 1;
+
+  PlanSmem P;
+  P.pair_off = reinterpret_cast<int*>(smem + kDWarps * nstage * kDStage +
+                                      kDWarps * kDMaxStages * 8);
+  P.seq_pair = P.pair_off + (a.npairs_cap + 1);
+  P.ctx = P.seq_pair + (S + 1);
+  P.qstart = P.ctx + S;
+
+  if (lane == 0) {
+    for (int i = 0; i < nstage; ++i) mbar_init(smem_addr(&bars[i]), 1);
+    mbar_fence_init();
+  }
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  PlanInputs in;
+  in.context_lens = a.context_lens;
+  in.cu_seqlens_q = a.cu_seqlens_q;
+  in.S = S;
+  in.Hkv = Hp;
+  in.max_ctx = a.max_blocks * kBlock;
+  in.qtile = QT;
+  in.causal = a.causal;
+  in.npairs_cap = a.npairs_cap;
+  in.num_q_rows = a.num_q_tokens;
+  in.max_lq = a.max_lq;
+  build_plan(in, P, nullptr);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // a sequence of the single-query form with an empty context has no tiles
+  if (!a.cu_seqlens_q) {
+    for (int s = blockIdx.x; s < S; s += gridDim.x) {
+      if (P.ctx[s] != 0) continue;
+      uint4* row = reinterpret_cast<uint4*>(a.o.out + (int64_t)s * (Hq / 2) * kDiffDim);
+      for (int i = threadIdx.x; i < Hq / 2 * (kDiffDim / 8); i += blockDim.x)
+        row[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.o.lse)
+        for (int i = threadIdx.x; i < Hq; i += blockDim.x) a.o.lse[(int64_t)s * Hq + i] = neg_inf();
+    }
+  }
+
+  const int W = P.total;
+  const int w = warp * (int)gridDim.x + (int)blockIdx.x;
+  const int nw = min((int)gridDim.x * kDWarps, max(1, W / 2));
+  int R0 = 0, R1 = 0;
+  if (w < nw) {
+    R0 = range_start(w, W, nw);
+    R1 = range_start(w + 1, W, nw);
+  }
+  if (lane == 0) {
+    const MergeJob j = merge_job(P, S, Hp, w, W, nw);
+    int* d = a.desc + (size_t)w * kDDesc;
+    d[0] = j.valid ? j.s : -1;
+    if (j.valid) {
+      d[1] = j.qt;
+      d[2] = j.h;
+      d[3] = j.last;
+      d[4] = j.slot_prev;
+      d[5] = P.qstart[j.s];
+      d[6] = P.qstart[j.s + 1] - P.qstart[j.s];
+    }
+  }
+  if (R0 >= R1) return;
+
+  // ---- producer --------------------------------------------------------------
+  TilePos pp = locate(P, S, Hp, R0);
+  int pidx = R0, wbase = R0;
+  // block id of flat tile idx; tiles of a window lie a few pairs past pp
+  auto load_phys = [&](int idx) -> int {
+    if (idx >= R1) return 0;
+    const TilePos t = locate_from(P, Hp, pp, idx);
+    return a.block_tables[(size_t)t.s * a.max_blocks + t.b];
+  };
+  int phys_cur = load_phys(wbase + lane);
+  int phys_next = load_phys(wbase + 32 + lane);
+
+  auto issue = [&](int stage) {
+    int phys = __shfl_sync(kFull, phys_cur, pidx - wbase);
+    if (lane == 0) {
+      if (phys < 0 || (int64_t)phys >= a.num_blocks) {
+        flag_error(PA_DEVERR_BLOCK_RANGE);
+        phys = 0;
+      }
+      const uint32_t st = smem_addr(wbuf + stage * kDStage);
+      const uint32_t bar = smem_addr(&bars[stage]);
+      fence_proxy_async_smem();
+      mbar_arrive_expect_tx(bar, kDStage);
+      const int group = (int)(((int64_t)phys * a.Hkv + 2 * pp.h) * (kBlock / 8));
+      tma_load_block(st, &tmk, group, bar);
+      tma_load_block(st + 2 * kTileBytes, &tmv, group, bar);
+    }
+    ++pidx;
+    if (pidx < R1) advance(P, S, Hp, pp);
+    if (pidx - wbase == 32) {
+      wbase += 32;
+      phys_cur = phys_next;
+      phys_next = load_phys(wbase + 32 + lane);
+    }
+  };
+  for (int i = 0; i < nstage && pidx < R1; ++i) issue(i);
+
+  // ---- consumer --------------------------------------------------------------
+  TilePos cp = locate(P, S, Hp, R0);
+  const int r = lane >> 2, quad = lane & 3;  // this lane's row of either map
+  const int mi = lane >> 3, rr = lane & 7;   // ldmatrix: matrix and row of this lane's address
+  uint32_t qa[8][4];
+  float o[32][4];
+  float m_r[2], l_r[2];
+  int lim = 0, lim_min = 0, lq = 0, ctx = 0, tok = 0;
+  bool valid = false;
+  int piece_b0 = 0;
+  bool piece_first = true;
+
+  int stage = 0;
+  uint32_t parity = 0;
+  for (int idx = R0; idx < R1; ++idx) {
+    unsigned char* st = wbuf + stage * kDStage;
+    const uint32_t sK = smem_addr(st), sV = sK + 2 * kTileBytes;
+    if (idx == R0 || cp.b == 0) {
+      ctx = P.ctx[cp.s];
+      lq = P.qstart[cp.s + 1] - P.qstart[cp.s];
+      tok = cp.qt * QT + r / G;
+      valid = r < QT * G && tok < lq;
+      // row r of a map: token r / G, head r % G of the map's KV head. Padding rows
+      // stay zero (never written out).
+      const uint32_t* q0 = nullptr;
+      if (valid)
+        q0 = reinterpret_cast<const uint32_t*>(
+            a.q + (((int64_t)P.qstart[cp.s] + tok) * Hq + (int64_t)(2 * cp.h) * G + r % G) *
+                      kHeadDim);
+      const uint32_t* q1 = q0 + (int64_t)G * (kHeadDim / 2);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const int c = kk * 8 + quad;  // 32-bit word of dims kk*16 + 2*quad
+        qa[kk][0] = valid ? q0[c] : 0u;
+        qa[kk][1] = valid ? q1[c] : 0u;
+        qa[kk][2] = valid ? q0[c + 4] : 0u;
+        qa[kk][3] = valid ? q1[c + 4] : 0u;
+      }
+#pragma unroll
+      for (int n = 0; n < 32; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      m_r[0] = m_r[1] = neg_inf();
+      l_r[0] = l_r[1] = 0.f;
+      lim = valid ? (a.causal ? ctx - lq + tok + 1 : ctx) : 0x7fffffff;
+      lim_min = lim;
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1)
+        lim_min = min(lim_min, __shfl_xor_sync(kFull, lim_min, off));
+      piece_b0 = cp.b;
+      piece_first = (idx == R0);
+    }
+    if (!mbar_wait_bounded(smem_addr(&bars[stage]), parity)) {
+      // the copies in flight land before the warp leaves
+      for (int j = idx + 1; j < pidx; ++j) {
+        if (++stage == nstage) {
+          stage = 0;
+          parity ^= 1u;
+        }
+        mbar_wait_bounded(smem_addr(&bars[stage]), parity);
+      }
+      return;
+    }
+    const int key0 = cp.b * kBlock;
+    // keys past the context may hold anything: zero those V rows so that
+    // P = 0 never meets a NaN in the product
+    if (key0 + kBlock > ctx) {
+      const int zr = ctx - key0;  // first row to clear
+      for (int i = lane; i < (kBlock - zr) * 32; i += 32) {
+        const int row = zr + (i >> 5), c = i & 31;
+        *reinterpret_cast<uint4*>(st + 2 * kTileBytes + (c >> 4) * kTileBytes +
+                                  atom_at(row, c & 15)) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      __syncwarp();
+      asm volatile("" ::: "memory");  // the ldmatrix reads below stay after the stores
+    }
+
+    // ---- S = Q K^T: rows 0-7 from the first key tile, 8-15 from the second ----------
+    float s[2][4];
+    {
+      float s0[2][4], s1[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s0[n][e] = s1[n][e] = 0.f;
+      const int key = (mi >> 1) * 8 + rr;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t at = atom_at(key, 2 * kk + (mi & 1));
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4(sK + at, b0, b1, b2, b3);
+        mma_bf16_16816(s0[0], qa[kk], b0, b1);
+        mma_bf16_16816(s0[1], qa[kk], b2, b3);
+        ldsm_x4(sK + kTileBytes + at, b0, b1, b2, b3);
+        mma_bf16_16816(s1[0], qa[kk], b0, b1);
+        mma_bf16_16816(s1[1], qa[kk], b2, b3);
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        s[n][0] = s0[n][0];
+        s[n][1] = s0[n][1];
+        s[n][2] = s1[n][2];
+        s[n][3] = s1[n][3];
+      }
+    }
+    // ---- mask, online softmax of either map ------------------------------------------
+    const bool need_mask = key0 + kBlock > lim_min;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = s[n][e] * a.scale_log2;
+        if (need_mask && key0 + n * 8 + quad * 2 + (e & 1) >= lim) v = neg_inf();
+        s[n][e] = v;
+      }
+    float alpha[2], mref[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+      const float mn = fmaxf(m_r[i], mx);
+      mref[i] = mn == neg_inf() ? 0.f : mn;
+      alpha[i] = ex2(m_r[i] - mref[i]);
+      m_r[i] = mn;
+    }
+    float rs[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p = ex2(s[n][e] - mref[e >> 1]);
+        s[n][e] = p;
+        rs[e >> 1] += p;
+      }
+    l_r[0] = l_r[0] * alpha[0] + rs[0];
+    l_r[1] = l_r[1] * alpha[1] + rs[1];
+    if (__any_sync(kFull, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+      for (int n = 0; n < 32; ++n) {
+        o[n][0] *= alpha[0];
+        o[n][1] *= alpha[0];
+        o[n][2] *= alpha[1];
+        o[n][3] *= alpha[1];
+      }
+    }
+    // a key that only some rows see may hold an infinity or a NaN, which the product
+    // would spread to all of them (0 x NaN): such elements join the rows that see
+    // them here and enter the product as zeros
+    if (need_mask) {
+      const int nk = min(kBlock, ctx - key0);
+      for (int kk = max(0, lim_min - key0); kk < nk; ++kk) {
+        uint4* at = reinterpret_cast<uint4*>(st + 2 * kTileBytes + (lane >> 4) * kTileBytes +
+                                             atom_at(kk, lane & 15));
+        const uint4 x = *at;
+        const bool bad = bf2_nonfinite(x.x) || bf2_nonfinite(x.y) || bf2_nonfinite(x.z) ||
+                         bf2_nonfinite(x.w);
+        if (!__any_sync(kFull, bad)) continue;
+        const bool sees = key0 + kk < lim;
+#pragma unroll
+        for (int n = 0; n < 32; ++n) {
+          const uint32_t wv = *reinterpret_cast<const uint32_t*>(
+              st + 2 * kTileBytes + (n >> 4) * kTileBytes + atom_at(kk, n & 15) + quad * 4);
+          const uint32_t f = bf2_finite_part(wv);
+          if (sees && ((wv ^ f) & 0x7f80u)) {
+            o[n][0] += bf_lo(wv);
+            o[n][2] += bf_lo(wv);
+          }
+          if (sees && ((wv ^ f) & 0x7f800000u)) {
+            o[n][1] += bf_hi(wv);
+            o[n][3] += bf_hi(wv);
+          }
+        }
+        __syncwarp();
+        if (bad)
+          *at = make_uint4(bf2_finite_part(x.x), bf2_finite_part(x.y), bf2_finite_part(x.z),
+                           bf2_finite_part(x.w));
+        __syncwarp();
+        asm volatile("" ::: "memory");
+      }
+    }
+    // ---- O += P V --------------------------------------------------------------------
+    // P enters the product in bf16, the type that V is stored in and the MMA takes
+    // beside it: a weight is off by at most 2^-8 of itself, each its own way. The sums
+    // of the weights, and with them lse, are of the unrounded ones.
+    uint32_t p4[4];
+    p4[0] = cvt_bf16x2(s[0][0], s[0][1]);
+    p4[1] = cvt_bf16x2(s[0][2], s[0][3]);
+    p4[2] = cvt_bf16x2(s[1][0], s[1][1]);
+    p4[3] = cvt_bf16x2(s[1][2], s[1][3]);
+    {
+      const int key = (mi & 1) * 8 + rr;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4_trans(sV + t * kTileBytes + atom_at(key, 2 * c + (mi >> 1)), b0, b1, b2, b3);
+          mma_bf16_16816(o[t * 16 + 2 * c], p4, b0, b1);
+          mma_bf16_16816(o[t * 16 + 2 * c + 1], p4, b2, b3);
+        }
+    }
+    __syncwarp();
+    if (pidx < R1) issue(stage);
+    if (++stage == nstage) {
+      stage = 0;
+      parity ^= 1u;
+    }
+
+    if (idx == R1 - 1 || cp.b == cp.nt - 1) {
+      float inv[2], lse[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = l_r[i];
+        x += __shfl_xor_sync(kFull, x, 1);
+        x += __shfl_xor_sync(kFull, x, 2);
+        // (a NaN score's NaN goes on into the row's results)
+        inv[i] = x != 0.f ? 1.f / x : 0.f;
+        lse[i] = x != 0.f ? (m_r[i] + lg2(x)) * kLn2 : neg_inf();
+      }
+      if (piece_b0 == 0 && cp.b == cp.nt - 1) {
+        const int head = cp.h * G + r % G;
+        const float lam = valid ? a.o.lambdas[head] : 0.f;
+        float squares = 0.f;
+#pragma unroll
+        for (int n = 0; n < 32; ++n) {
+          o[n][0] = diff_value(o[n][0], inv[0], o[n][2], inv[1], lam);
+          o[n][1] = diff_value(o[n][1], inv[0], o[n][3], inv[1], lam);
+          squares = fmaf(o[n][0], o[n][0], fmaf(o[n][1], o[n][1], squares));
+        }
+        squares += __shfl_xor_sync(kFull, squares, 1);
+        squares += __shfl_xor_sync(kFull, squares, 2);
+        if (valid) {
+          const float f = diff_factor(a.o, squares);
+          const int64_t qtok = (int64_t)P.qstart[cp.s] + tok;
+          uint16_t* dst = a.o.out + (qtok * (Hq / 2) + head) * kDiffDim + quad * 2;
+#pragma unroll
+          for (int n = 0; n < 32; ++n) {
+            float2 wt = make_float2(f, f);
+            if (a.o.weight) {
+              const float2 x = *reinterpret_cast<const float2*>(a.o.weight + n * 8 + quad * 2);
+              wt = make_float2(f * x.x, f * x.y);
+            }
+            *reinterpret_cast<uint32_t*>(dst + n * 8) =
+                cvt_bf16x2(o[n][0] * wt.x, o[n][1] * wt.y);
+          }
+          if (a.o.lse && quad == 0) {
+            float* l = a.o.lse + qtok * Hq + (int64_t)(2 * cp.h) * G + r % G;
+            l[0] = lse[0];
+            l[G] = lse[1];
+          }
+        }
+      } else {
+        const size_t slot = (size_t)w * 2 + (piece_first ? 0 : 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = i * kMapRows + r;
+          float* dst = a.part_o + (slot * kDRows + row) * kDiffDim + quad * 2;
+          if (valid) {
+#pragma unroll
+            for (int n = 0; n < 32; ++n)
+              *reinterpret_cast<float2*>(dst + n * 8) =
+                  make_float2(o[n][2 * i] * inv[i], o[n][2 * i + 1] * inv[i]);
+          }
+          if (quad == 0) a.part_lse[slot * kDRows + row] = lse[i];
+        }
+      }
+    }
+    if (idx + 1 < R1) advance(P, S, Hp, cp);
+  }
+}
+
+// Merge the pieces of (sequence, query tile, pair) segments cut by the equal
+// ranges, then difference, norm and scale. One CTA per worker boundary; its
+// warps are dealt out to the segment's rows, several to a row where there are
+// few, each taking every n-th round of four pieces with all their loads in
+// flight. A lane holds eight of a row's 256 dims, of both maps. Partials are
+// read through L2 (ld.global.cg): other SMs wrote them.
+constexpr int kDFixWarps = 8;
+
+struct MapSum {
+  float m, sum;
+  float acc[8];
+};
+
+// Adds (m, sum, acc) of another group.
+__device__ __forceinline__ void join(MapSum& x, float mo, float so, const float (&ao)[8]) {
+  if (mo == neg_inf()) return;
+  const float mn = fmaxf(x.m, mo);
+  const float mine = x.m == neg_inf() ? 0.f : ex2((x.m - mn) * kLog2e);
+  const float other = ex2((mo - mn) * kLog2e);
+  x.sum = x.sum * mine + so * other;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x.acc[j] = x.acc[j] * mine + ao[j] * other;
+  x.m = mn;
+  if (mo != mo) x.m = x.sum = mo;  // a NaN stays one
+}
+
+__global__ void __launch_bounds__(kDFixWarps * 32)
+    diff_fixup_kernel(const int* desc, const float* part_o, const float* part_lse, const DiffOut out,
+                      int num_workers, int Hq, int G, int QT) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int w = blockIdx.x;
+  if (w >= num_workers) return;
+  const int* d = desc + (size_t)w * kDDesc;
+  if (__ldcg(d) < 0) return;
+  const int qt = __ldcg(d + 1), h = __ldcg(d + 2), last = __ldcg(d + 3),
+            slot_prev = __ldcg(d + 4), q0 = __ldcg(d + 5), lq = __ldcg(d + 6);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int npieces = last - w + 2;                       // workers w-1 .. last
+  const int nrows = min(QT, lq - qt * QT) * G;            // 1 .. 8 of either map
+  const int per_row = kDFixWarps / nrows;                 // warps to a row
+  const int r = warp / per_row, group = warp - r * per_row;
+  const bool live = r < nrows;
+  MapSum x[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[i].m = neg_inf();
+    x[i].sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[i].acc[j] = 0.f;
+  }
+  bool nan[2] = {false, false};  // a piece with a NaN score: the row's results are NaNs
+  for (int i0 = 4 * group; live && i0 < npieces; i0 += 4 * per_row) {
+    float li[2][4];
+    float4 v[2][4][2];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        li[i][u] = neg_inf();
+        v[i][u][0] = v[i][u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + u < npieces) {
+          const size_t sl = (size_t)(w - 1 + i0 + u) * 2 + (i0 + u == 0 ? slot_prev : 0);
+          const size_t row = sl * kDRows + i * kMapRows + r;
+          li[i][u] = __ldcg(part_lse + row);
+          const float4* src = reinterpret_cast<const float4*>(part_o + row * kDiffDim + lane * 8);
+          v[i][u][0] = __ldcg(src);
+          v[i][u][1] = __ldcg(src + 1);
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float mn =
+          fmaxf(fmaxf(x[i].m, fmaxf(li[i][0], li[i][1])), fmaxf(li[i][2], li[i][3]));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) nan[i] = nan[i] || li[i][u] != li[i][u];
+      if (mn == neg_inf()) continue;
+      const float shrink = x[i].m == neg_inf() ? 0.f : ex2((x[i].m - mn) * kLog2e);
+      x[i].sum *= shrink;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i].acc[j] *= shrink;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float wt = li[i][u] == neg_inf() ? 0.f : ex2((li[i][u] - mn) * kLog2e);
+        x[i].sum += wt;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          x[i].acc[4 * k + 0] = fmaf(wt, v[i][u][k].x, x[i].acc[4 * k + 0]);
+          x[i].acc[4 * k + 1] = fmaf(wt, v[i][u][k].y, x[i].acc[4 * k + 1]);
+          x[i].acc[4 * k + 2] = fmaf(wt, v[i][u][k].z, x[i].acc[4 * k + 2]);
+          x[i].acc[4 * k + 3] = fmaf(wt, v[i][u][k].w, x[i].acc[4 * k + 3]);
+        }
+      }
+      x[i].m = mn;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (nan[i]) x[i].m = x[i].sum = __int_as_float(0x7fc00000);
+  __shared__ __align__(16) float left[kDFixWarps][2][kDiffDim];
+  __shared__ float left_ms[kDFixWarps][2][2];
+  if (per_row > 1) {
+    if (live && group > 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float4* dst = reinterpret_cast<float4*>(left[warp][i] + lane * 8);
+        dst[0] = make_float4(x[i].acc[0], x[i].acc[1], x[i].acc[2], x[i].acc[3]);
+        dst[1] = make_float4(x[i].acc[4], x[i].acc[5], x[i].acc[6], x[i].acc[7]);
+        if (lane == 0) {
+          left_ms[warp][i][0] = x[i].m;
+          left_ms[warp][i][1] = x[i].sum;
+        }
+      }
+    }
+    __syncthreads();
+    if (live && group == 0) {
+      for (int g = 1; g < per_row; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float ao[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ao[j] = left[warp + g][i][lane * 8 + j];
+          join(x[i], left_ms[warp + g][i][0], left_ms[warp + g][i][1], ao);
+        }
+    }
+  }
+  if (!live || group > 0) return;
+  const int head = h * G + r % G;
+  const float lam = out.lambdas[head];
+  const float inv0 = x[0].sum != 0.f ? 1.f / x[0].sum : 0.f;
+  const float inv1 = x[1].sum != 0.f ? 1.f / x[1].sum : 0.f;
+  float y[8], squares = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    y[j] = diff_value(x[0].acc[j], inv0, x[1].acc[j], inv1, lam);
+    squares = fmaf(y[j], y[j], squares);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) squares += __shfl_xor_sync(kFull, squares, o);
+  const float f = diff_factor(out, squares);
+  if (out.weight) {
+    const float4* wt = reinterpret_cast<const float4*>(out.weight + lane * 8);
+    const float4 w0 = wt[0], w1 = wt[1];
+    const float ws[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] *= f * ws[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] *= f;
+  }
+  const int64_t qtok = (int64_t)q0 + qt * QT + r / G;
+  *reinterpret_cast<uint4*>(out.out + (qtok * (Hq / 2) + head) * kDiffDim + lane * 8) =
+      make_uint4(cvt_bf16x2(y[0], y[1]), cvt_bf16x2(y[2], y[3]), cvt_bf16x2(y[4], y[5]),
+                 cvt_bf16x2(y[6], y[7]));
+  if (out.lse && lane == 0) {
+    float* l = out.lse + qtok * Hq + (int64_t)(2 * h) * G + r % G;
+    l[0] = x[0].sum != 0.f ? x[0].m + lg2(x[0].sum) * kLn2 : neg_inf();
+    l[G] = x[1].sum != 0.f ? x[1].m + lg2(x[1].sum) * kLn2 : neg_inf();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+// make_block_map's view with boxes of two tiles: KV heads 2p and 2p + 1 of a block.
+bool make_pair_map(CUtensorMap* map, const void* pool, int64_t rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {64, 8, 2, (cuuint64_t)(rows / 8)};
+  cuuint64_t strides[3] = {(cuuint64_t)kHeadDim * 2, 128, (cuuint64_t)kHeadDim * 2 * 8};
+  cuuint32_t box[4] = {64, 8, 2, 2 * (cuuint32_t)kBlock / 8};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct DiffGeometry {
+  int grid = 0, workers = 0, npairs_cap = 0, nstage = 0;
+  size_t smem = 0, ws_desc = 0, ws_lse = 0, ws_o = 0, ws_bytes = 0;
+};
+
+int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffGeometry* g) {
+  DeviceInfo dev;
+  if (!current_device_info(&dev)) return PA_ERR_CUDA;
+  const int S = sh->num_seqs;
+  const int G = sh->num_q_heads / sh->num_kv_heads, QT = kMapRows / G;
+  const int64_t cap1 = (int64_t)S * (((int64_t)max_q_len + QT - 1) / QT);
+  const int64_t cap2 = (num_q_tokens + QT - 1) / QT + S;
+  const int64_t cap = cap1 < cap2 ? cap1 : cap2;
+  if (cap > (1 << 22)) return PA_ERR_UNSUPPORTED;
+  g->npairs_cap = (int)(cap < S ? S : cap);
+  const size_t plan = sizeof(int) * ((size_t)g->npairs_cap + 1 + 3 * (size_t)S + 2);
+  // as many stages as leave room for the plan, two at least
+  for (g->nstage = kDMaxStages; g->nstage >= 2; --g->nstage) {
+    g->smem = 1024 + (size_t)kDWarps * g->nstage * kDStage + kDWarps * kDMaxStages * 8 + plan;
+    if (g->smem <= (size_t)dev.max_smem_optin) break;
+  }
+  if (g->nstage < 2) return PA_ERR_UNSUPPORTED;
+  if (!raise_smem_limit(reinterpret_cast<const void*>(paged_diff_kernel))) return PA_ERR_CUDA;
+  g->grid = dev.num_sms;
+  g->workers = g->grid * kDWarps;
+  g->ws_desc = round_up(sizeof(int) * kDDesc * (size_t)g->workers, 256);
+  g->ws_lse = round_up(sizeof(float) * 2 * kDRows * (size_t)g->workers, 256);
+  g->ws_o = round_up(sizeof(float) * 2 * kDRows * kDiffDim * (size_t)g->workers, 256);
+  g->ws_bytes = g->ws_desc + g->ws_lse + g->ws_o;
+  return PA_OK;
+}
+
+int check_diff_args(const pa_shape* sh, int64_t num_q_tokens, int max_q_len) {
+  const int rc = check_shape_common(sh);
+  if (rc != PA_OK) return rc;
+  if (sh->num_kv_heads % 2 != 0) return PA_ERR_UNSUPPORTED;
+  if (sh->num_q_heads / sh->num_kv_heads > kMapRows) return PA_ERR_UNSUPPORTED;
+  if (num_q_tokens < 0 || max_q_len < 0 || num_q_tokens > 0x3fffffff) return PA_ERR_ARG;
+  if (sh->num_blocks * sh->num_kv_heads * kBlock > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+}  // namespace
+
+unsigned take_error_word_diff(cudaStream_t stream, int* rc) {
+  unsigned v = 0, zero = 0;
+  if (cudaStreamSynchronize(stream) != cudaSuccess ||
+      cudaMemcpyFromSymbol(&v, g_pa_error_word, sizeof v) != cudaSuccess ||
+      cudaMemcpyToSymbol(g_pa_error_word, &zero, sizeof zero) != cudaSuccess) {
+    *rc = PA_ERR_CUDA;
+    return 0;
+  }
+  return v;
+}
+
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" size_t pa_decode_diff_workspace_size(const pa_shape* shape, int64_t num_q_tokens,
+                                                int max_q_len) {
+  if (check_diff_args(shape, num_q_tokens, max_q_len) != PA_OK) return 0;
+  if (shape->num_seqs == 0 || num_q_tokens == 0 || max_q_len == 0) return 0;
+  DiffGeometry g;
+  return diff_geometry(shape, num_q_tokens, max_q_len, &g) == PA_OK ? g.ws_bytes : 0;
+}
+
+extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
+                              const int32_t* block_tables, const int32_t* context_lens,
+                              const int32_t* cu_seqlens_q, int64_t num_q_tokens, int max_q_len,
+                              int causal, float scale, const float* lambdas,
+                              const float* norm_weight, float norm_eps, float out_scale,
+                              pa_bf16* out, float* lse, const pa_shape* shape, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  pa::NvtxRange nvtx_range("pa_decode_diff");
+  int rc = check_diff_args(shape, num_q_tokens, max_q_len);
+  if (rc != PA_OK) return rc;
+  if (!cu_seqlens_q && (num_q_tokens != shape->num_seqs || max_q_len != 1)) return PA_ERR_ARG;
+  if (!(scale == scale) || !(norm_eps >= 0.f) || !(out_scale == out_scale)) return PA_ERR_ARG;
+  if (shape->num_seqs == 0 || num_q_tokens == 0) return PA_OK;
+  if (max_q_len == 0) return PA_ERR_ARG;  // rows, but no window may hold one
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !lambdas || !out)
+    return PA_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(cu_seqlens_q, 4) ||
+      !aligned(lambdas, 4) || !aligned(norm_weight, 16) || !aligned(lse, 4))
+    return PA_ERR_ARG;
+  DiffGeometry g;
+  rc = diff_geometry(shape, num_q_tokens, max_q_len, &g);
+  if (rc != PA_OK) return rc;
+  if (!workspace || workspace_bytes < g.ws_bytes || !aligned(workspace, 256))
+    return PA_ERR_WORKSPACE;
+  const int64_t rows = shape->num_blocks * shape->num_kv_heads * kBlock;
+  CUtensorMap tmk, tmv;
+  if (!make_pair_map(&tmk, k_cache, rows) || !make_pair_map(&tmv, v_cache, rows))
+    return PA_ERR_CUDA;
+  DiffArgs a = {};
+  a.q = q;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.o.out = out;
+  a.o.lse = lse;
+  a.o.lambdas = lambdas;
+  a.o.weight = norm_weight;
+  a.o.eps = norm_eps;
+  a.o.gain = out_scale;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.S = shape->num_seqs;
+  a.Hq = shape->num_q_heads;
+  a.Hkv = shape->num_kv_heads;
+  a.G = a.Hq / a.Hkv;
+  a.QT = kMapRows / a.G;
+  a.max_blocks = shape->max_blocks_per_seq;
+  a.num_blocks = shape->num_blocks;
+  a.num_q_tokens = num_q_tokens;
+  a.causal = causal && cu_seqlens_q ? 1 : 0;
+  a.npairs_cap = g.npairs_cap;
+  a.num_workers = g.workers;
+  a.nstage = g.nstage;
+  a.max_lq = 0x7fffffff;
+  char* ws = static_cast<char*>(workspace);
+  a.desc = reinterpret_cast<int*>(ws);
+  a.part_lse = reinterpret_cast<float*>(ws + g.ws_desc);
+  a.part_o = reinterpret_cast<float*>(ws + g.ws_desc + g.ws_lse);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (launch_dependent(paged_diff_kernel, dim3(g.grid), dim3(kDWarps * 32), g.smem, st, tmk, tmv,
+                       a) != cudaSuccess)
+    return PA_ERR_CUDA;
+  if (launch_dependent(diff_fixup_kernel, dim3(g.workers), dim3(kDFixWarps * 32), 0, st,
+                       (const int*)a.desc, (const float*)a.part_o, (const float*)a.part_lse, a.o,
+                       g.workers, a.Hq, a.G, a.QT) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return PA_OK;
+}

@@ -255,5 +255,6 @@ unsigned take_error_word_weights(cudaStream_t stream, int* rc);
 unsigned take_error_word_weights_tc(cudaStream_t stream, int* rc);
 unsigned take_error_word_evict(cudaStream_t stream, int* rc);
 unsigned take_error_word_rotate(cudaStream_t stream, int* rc);
+unsigned take_error_word_diff(cudaStream_t stream, int* rc);
 
 }  // namespace pa

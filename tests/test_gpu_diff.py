@@ -1,0 +1,351 @@
+"""Differential attention over the paged cache on the GPU, against a plain
+64-bit form."""
+import math
+
+import pytest
+import torch
+
+from paged_kv_decode_18_gb300 import binding as B
+from paged_kv_decode_18_gb300 import build as libbuild
+from tests import diff_ref as R
+from tests import rotate_ref
+
+pytestmark = pytest.mark.gpu
+
+DIM, BLOCK = 128, 16
+SCALE = 1 / math.sqrt(DIM)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    libbuild.build()
+    B.load()
+
+
+@pytest.fixture(autouse=True)
+def _errors():
+    B.pa_debug_read_error()
+    yield
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert B.pa_debug_read_error() == 0
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g).to(torch.bfloat16)
+
+
+class Batch:
+    """A batch in a shuffled pool: contexts `lens`, windows `qs` (None: one query
+    per sequence), cached rows past a context and unused blocks NaN."""
+
+    def __init__(self, seed, lens, qs, hkv, G, width=0, heavy=1.0):
+        g = torch.Generator().manual_seed(seed)
+        self.lens, self.qs, self.hkv, self.G, self.hq = lens, qs, hkv, G, hkv * G
+        per = [(n + BLOCK - 1) // BLOCK for n in lens]
+        blocks = sum(per) + 2
+        ids = torch.randperm(blocks, generator=g).to(torch.int32)
+        self.tables = torch.full((len(lens), max(width, max(per), 1)), -1, dtype=torch.int32)
+        self.kc = torch.full((blocks, hkv, BLOCK, DIM), float("nan"), dtype=torch.bfloat16)
+        self.vc = self.kc.clone()
+        at = 0
+        for s, n in enumerate(lens):
+            mine = ids[at:at + per[s]]
+            self.tables[s, :per[s]] = mine
+            at += per[s]
+            for pool, gain in ((self.kc, heavy), (self.vc, 1.0)):
+                x = randn(g, n, hkv, DIM)
+                if gain != 1.0 and n:
+                    x[torch.rand((n,), generator=g) < 0.05] *= gain
+                for b in range(per[s]):
+                    part = x[b * BLOCK:(b + 1) * BLOCK]
+                    pool[int(mine[b]), :, :part.shape[0]] = part.transpose(0, 1)
+        rows = [1] * len(lens) if qs is None else qs
+        self.cu = torch.tensor([0] + rows, dtype=torch.int64).cumsum(0).to(torch.int32)
+        self.T = int(self.cu[-1])
+        self.q = randn(g, self.T, self.hq, DIM)
+        self.lambdas = torch.rand((self.hq // 2,), generator=g) * 1.2 - 0.2
+        self.weight = 1 + 0.2 * torch.randn((2 * DIM,), generator=g)
+        self.max_q = max(rows) if rows else 1
+
+    def cuda(self):
+        self.d = {n: getattr(self, n).cuda() for n in
+                  ("q", "kc", "vc", "tables", "lambdas", "weight", "cu")}
+        self.d["lens"] = torch.tensor(self.lens, dtype=torch.int32).cuda()
+        return self
+
+    def call(self, norm=True, eps=1e-5, gain=0.8, causal=True, with_lse=True, max_q=None,
+             spare=0, ws_fill=None, workspace=None):
+        d = self.d
+        out = torch.full((self.T + spare, self.hq // 2, 2 * DIM), 3.0, dtype=torch.bfloat16,
+                         device="cuda")
+        lse = torch.full((self.T + spare, self.hq), 5.0, device="cuda") if with_lse else None
+        sh = B.shape_of(d["q"], d["kc"], d["tables"])
+        n = max_q or self.max_q
+        ws = workspace
+        if ws is None:
+            ws = B.workspace(B.pa_decode_diff_workspace_size(sh, self.T, n), "cuda")
+            if ws_fill is not None:
+                ws.fill_(ws_fill)
+        B.pa_decode_diff(d["q"], d["kc"], d["vc"], d["tables"], d["lens"], SCALE, d["lambdas"],
+                         out[:self.T], None if lse is None else lse[:self.T],
+                         cu_seqlens_q=None if self.qs is None else d["cu"], max_q_len=n,
+                         causal=causal, norm_weight=d["weight"] if norm else None, norm_eps=eps,
+                         out_scale=gain, workspace=ws)
+        return out, lse
+
+    def check(self, out, lse, norm=True, eps=1e-5, gain=0.8, causal=True):
+        ref, rl, tol, ltol = R.attend(self.q, self.kc, self.vc, self.tables, self.lens, self.cu,
+                                      SCALE, self.lambdas, self.weight if norm else None, eps, gain,
+                                      causal)
+        got = out[:self.T].cpu().double()
+        assert ((got - ref).abs() <= tol).all(), float(((got - ref).abs() / tol).max())
+        # the bounds say little of a difference that is small beside its maps: all in
+        # all the error is a few roundings of random sign
+        if ref.norm() > 0:
+            assert float((got - ref).norm() / ref.norm()) < 1e-2
+        if lse is not None:
+            gl = lse[:self.T].cpu().double()
+            empty = torch.isinf(rl)
+            assert torch.equal(gl[empty], rl[empty])
+            assert ((gl - rl).abs() <= ltol)[~empty].all()
+
+
+DECODE = [
+    # contexts, KV heads, group
+    ([1], 2, 1), ([16], 2, 2), ([0, 17, 1, 15, 33, 0], 2, 1), ([300, 5, 129], 8, 2),
+    ([40, 64], 4, 3), ([65, 31], 2, 5), ([70], 6, 4), ([257, 9], 2, 8), ([33, 100], 4, 7),
+    # few segments in many pieces
+    ([5000], 2, 1), ([3000, 40], 4, 2), ([2600], 2, 8),
+]
+
+
+@pytest.mark.parametrize("lens,hkv,G", DECODE)
+@pytest.mark.parametrize("norm", [True, False])
+def test_one_query_per_sequence(lens, hkv, G, norm):
+    b = Batch(len(lens) * 100 + lens[0] + G, lens, None, hkv, G, heavy=4.0).cuda()
+    out, lse = b.call(norm=norm, spare=2, ws_fill=0xFF)
+    ok()
+    b.check(out, lse, norm=norm)
+    assert (out[b.T:] == 3).all() and (lse[b.T:] == 5).all()
+    again, _ = b.call(norm=norm, with_lse=False, ws_fill=0x11)
+    ok()
+    assert torch.equal(again[:b.T].view(torch.int16), out[:b.T].view(torch.int16))
+    for s, c in enumerate(lens):
+        if c == 0:
+            assert (out[s] == 0).all() and (lse[s] == -math.inf).all()
+
+
+WINDOWS = [
+    # contexts, windows, KV heads, group
+    ([1], [1], 2, 1), ([20, 16, 40], [5, 16, 0], 2, 2), ([64, 65, 7], [1, 33, 7], 4, 1),
+    ([100, 30], [9, 30], 2, 3), ([50], [50], 2, 8), ([129, 200, 17], [4, 8, 17], 2, 5),
+    ([900, 33], [12, 3], 4, 2), ([80, 0, 90], [20, 0, 31], 6, 4), ([210], [70], 2, 6),
+]
+
+
+@pytest.mark.parametrize("lens,qs,hkv,G", WINDOWS)
+@pytest.mark.parametrize("causal", [True, False])
+def test_windows(lens, qs, hkv, G, causal):
+    b = Batch(sum(lens) + G, lens, qs, hkv, G, heavy=4.0).cuda()
+    out, lse = b.call(causal=causal, spare=3)
+    ok()
+    b.check(out, lse, causal=causal)
+    assert (out[b.T:] == 3).all() and (lse[b.T:] == 5).all()
+    # a wider bound of the windows is the same problem
+    again, _ = b.call(causal=causal, max_q=b.max_q + 9)
+    ok()
+    b.check(again, None, causal=causal)
+
+
+def test_windows_of_one_are_single_queries():
+    lens = [37, 1, 200, 16]
+    one = Batch(5, lens, None, 4, 2).cuda()
+    win = Batch(5, lens, [1] * 4, 4, 2).cuda()
+    a, la = one.call()
+    w, lw = win.call()
+    ok()
+    one.check(a, la)
+    win.check(w, lw)
+
+
+def test_a_key_that_a_query_does_not_see_never_reaches_it():
+    # infinities and NaNs in the K and V rows of a window's later tokens
+    lens, qs = [70, 35], [20, 7]
+    b = Batch(3, lens, qs, 2, 2)
+    clean = b.kc.clone(), b.vc.clone()
+    for s, at, what in ((0, 60, float("nan")), (0, 69, float("inf")), (1, 34, float("-inf"))):
+        blk = int(b.tables[s, at // BLOCK])
+        b.kc[blk, :, at % BLOCK, 3::7] = what
+        b.vc[blk, :, at % BLOCK, 1::5] = what
+    b.cuda()
+    out, lse = b.call()
+    ok()
+    dirty = b.kc, b.vc
+    b.kc, b.vc = clean
+    ref, rl, tol, ltol = R.attend(b.q, b.kc, b.vc, b.tables, lens, b.cu, SCALE, b.lambdas, b.weight,
+                                  1e-5, 0.8)
+    got, gl = out.cpu().double(), lse.cpu().double()
+    # queries before the first bad row: window 0 from position 50, window 1 from 28
+    fine = torch.zeros(b.T, dtype=torch.bool)
+    fine[0:10] = True
+    fine[20:26] = True
+    assert ((got - ref).abs() <= tol)[fine].all()
+    assert ((gl - rl).abs() <= ltol)[fine].all()
+    assert (~torch.isfinite(got[~fine])).any()
+    b.kc, b.vc = dirty
+
+
+def test_one_maps_infinities_stay_out_of_the_other():
+    # minus infinity in a K row of the first map hides the key from it; the second sees it
+    b = Batch(9, [40], None, 2, 1)
+    b.q = b.q.abs()
+    blk = int(b.tables[0, 1])
+    b.kc[blk, 0, 4] = float("-inf")
+    b.cuda()
+    out, lse = b.call(norm=False)
+    ok()
+    a = []
+    v = torch.cat([R.rows_of(b.vc, b.tables[0], 40, h) for h in (0, 1)], 1)
+    for h in (0, 1):
+        k = R.rows_of(b.kc, b.tables[0], 40, h)
+        z = SCALE * (k @ b.q[0, h].double())
+        assert abs(float(lse[0, h]) - float(torch.logsumexp(z, 0))) < 1e-4
+        a.append(torch.softmax(z, 0) @ v)
+    ref = 0.8 * (a[0] - float(b.lambdas[0]) * a[1])
+    assert ((out[0, 0].cpu().double() - ref).abs() <= 4 * R.UBF * v.abs().amax(0)).all()
+
+
+def test_a_nan_score_reaches_its_rows_alone():
+    for lens in ([64, 48], [2500, 48]):
+        b = Batch(13, lens, None, 2, 2)
+        b.q[0, 0, 5] = float("nan")   # first map of head 0 of sequence 0
+        b.cuda()
+        out, lse = b.call()
+        ok()
+        assert torch.isnan(out[0, 0]).all() and torch.isnan(lse[0, 0])
+        assert torch.isfinite(out[0, 1]).all() and torch.isfinite(out[1]).all()
+        assert torch.isfinite(lse[0, 1:]).all()
+
+
+def test_a_difference_of_zero():
+    # equal maps and lambda 1: with an eps the norm gives 0, without one too
+    b = Batch(2, [33], None, 2, 1)
+    b.kc[:, 1] = b.kc[:, 0]
+    b.q[:, 1] = b.q[:, 0]
+    b.lambdas.fill_(1.0)
+    b.cuda()
+    for eps in (1e-5, 0.0):
+        out, _ = b.call(eps=eps)
+        ok()
+        assert (out[:b.T] == 0).all()
+
+
+def test_many_sequences_and_a_wide_table():
+    g = torch.Generator().manual_seed(1)
+    lens = [int(x) for x in torch.randint(0, 60, (400,), generator=g)]
+    b = Batch(17, lens, None, 2, 1, width=64).cuda()
+    out, lse = b.call()
+    ok()
+    b.check(out, lse)
+
+
+def test_bad_tables_contexts_and_windows_are_flagged():
+    b = Batch(6, [40, 30], [4, 3], 2, 2).cuda()
+    good, _ = b.call()
+    ok()
+    b.d["tables"][0, 1] = b.kc.shape[0]
+    out, _ = b.call()
+    torch.cuda.synchronize()
+    assert B.pa_debug_read_error() == B.PA_DEVERR_BLOCK_RANGE
+    assert torch.equal(out[4:7].view(torch.int16), good[4:7].view(torch.int16))
+    b.d["tables"][0, 1] = b.tables[0, 1]
+    b.d["lens"][0] = 3                      # a window of 4 over 3 keys
+    out, lse = b.call()
+    torch.cuda.synchronize()
+    assert B.pa_debug_read_error() == B.PA_DEVERR_QLEN_RANGE
+    assert (out[:4] == 3).all() and (lse[:4] == 5).all()
+    assert torch.equal(out[4:7].view(torch.int16), good[4:7].view(torch.int16))
+    b.d["lens"][0] = 49                     # past the table
+    b.call()
+    torch.cuda.synchronize()
+    assert B.pa_debug_read_error() & B.PA_DEVERR_CONTEXT_RANGE
+
+
+def test_two_streams_and_a_graph():
+    a = Batch(31, [700, 33, 90], None, 4, 2).cuda()
+    c = Batch(32, [50, 600], [9, 17], 4, 2).cuda()
+    wa, wc = a.call()[0], c.call()[0]
+    ok()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in (one, two):
+        st.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        with torch.cuda.stream(one):
+            got.append((a.call()[0], wa))
+        with torch.cuda.stream(two):
+            got.append((c.call()[0], wc))
+    ok()
+    for x, want in got:
+        assert torch.equal(x.view(torch.int16), want.view(torch.int16))
+    # captured and replayed on other inputs
+    d = a.d
+    out = torch.empty((a.T, a.hq // 2, 2 * DIM), dtype=torch.bfloat16, device="cuda")
+    sh = B.shape_of(d["q"], d["kc"], d["tables"])
+    ws = B.workspace(B.pa_decode_diff_workspace_size(sh, a.T), "cuda")
+    call = B.prepare_decode_diff(d["q"], d["kc"], d["vc"], d["tables"], d["lens"], SCALE,
+                                 d["lambdas"], out, norm_weight=d["weight"], out_scale=0.8,
+                                 workspace=ws)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    other = Batch(33, [100, 690, 1], None, 4, 2)
+    other.tables, other.kc, other.vc = a.tables.clone(), a.kc, a.vc
+    other.lens = [400, 20, 70]
+    d["q"].copy_(other.q)
+    d["lens"].copy_(torch.tensor(other.lens, dtype=torch.int32))
+    d["lambdas"].copy_(other.lambdas)
+    d["weight"].copy_(other.weight)
+    graph.replay()
+    ok()
+    other.check(out, None)
+
+
+def test_a_layer_rotates_caches_and_attends():
+    """Queries and keys rotated on their way into the cache, then read by
+    differential attention: a prompt's window, then a step of single queries."""
+    g = torch.Generator().manual_seed(41)
+    hq, hkv, lens = 8, 4, [37, 90]
+    per = [(n + 1 + BLOCK - 1) // BLOCK for n in lens]
+    blocks = sum(per)
+    ids = torch.randperm(blocks, generator=g).to(torch.int32)
+    tables = torch.zeros((2, max(per)), dtype=torch.int32)
+    tables[0, :per[0]], tables[1, :per[1]] = ids[:per[0]], ids[per[0]:]
+    kc = torch.zeros((blocks, hkv, BLOCK, DIM), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    rot = B.make_rotation(64, interleaved=True)
+    b = Batch(1, lens, lens, hkv, hq // hkv)
+    for new, ctx in ((lens, lens), ([1, 1], [n + 1 for n in lens])):
+        T = sum(new)
+        mixed = randn(g, T, hq + 2 * hkv, DIM).cuda()
+        seq = torch.repeat_interleave(torch.arange(2), torch.tensor(new))
+        pos = torch.cat([torch.arange(c - n, c) for n, c in zip(new, ctx)])
+        slots = (tables[seq, pos // BLOCK].long() * BLOCK + pos % BLOCK).cuda()
+        q = torch.empty((T, hq, DIM), dtype=torch.bfloat16, device="cuda")
+        B.pa_rotate_and_cache(mixed[:, hq:hq + hkv], mixed[:, hq + hkv:], pos.int().cuda(), slots,
+                              rot, kc, vc, q=mixed[:, :hq], q_out=q)
+        ref, err = rotate_ref.rotate(mixed[:, :hq].cpu(), pos[:, None], rotate_ref.theta(64)[0], True)
+        assert ((q.cpu().double() - ref).abs() <= rotate_ref.held_bf16(ref, err)).all()
+        b.lens, b.qs, b.tables, b.kc, b.vc, b.q = ctx, new, tables, kc.cpu(), vc.cpu(), q.cpu()
+        b.cu = torch.tensor([0, new[0], T], dtype=torch.int32)
+        b.T, b.max_q = T, max(new)
+        if max(new) == 1:
+            b.qs = None
+        b.cuda()
+        out, lse = b.call()
+        ok()
+        b.check(out, lse)
