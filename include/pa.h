@@ -712,7 +712,7 @@ int pa_rotate_cached(void* k_cache, int kv_format, const int32_t* block_tables,
  *   lse           [num_q_tokens][num_q_heads] fp32 of each map, or NULL
  *   workspace     at least pa_decode_diff_workspace_size(...) bytes, 256-byte
  *                 aligned; clobbered
- * bf16 pools with an even num_kv_heads and 1 to 8 query heads per KV head
+ * bf16 pools with an even num_kv_heads and 1 to 128 query heads per KV head
  * (else PA_ERR_UNSUPPORTED, workspace size 0). Both maps, their difference and
  * the norm are fp32; the softmax weights are rounded to bf16 for the product
  * with V, as in pa_decode_varlen. A sequence of the single-query form with an

@@ -28,6 +28,7 @@ extern "C" int pa_debug_read_error(void* stream) {
   word |= pa::take_error_word_evict(st, &rc);
   word |= pa::take_error_word_rotate(st, &rc);
   word |= pa::take_error_word_diff(st, &rc);
+  word |= pa::take_error_word_diff_tc(st, &rc);
   if (rc != PA_OK) return rc;
   return static_cast<int>(word);
 }

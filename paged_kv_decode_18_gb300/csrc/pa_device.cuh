@@ -310,6 +310,9 @@ struct PlanInputs {
   // > 0 (non-causal): a query window is the last lq positions of its context
   // and holds at most this many (the bits of a tree mask row)
   int max_window = 0;
+  // without cu_seqlens_q: sequences with an empty context are no pairs at all
+  // (for a cut that needs every pair to hold tiles)
+  bool skip_empty = false;
   // decode only: every sequence is cut into `parts` near-equal block ranges,
   // one pair each (pair s * parts + j holds blocks part_begin(j) ..), the
   // split-K partitions; 1 = one pair per sequence
@@ -371,7 +374,12 @@ __device__ __forceinline__ bool bad_window(const PlanInputs& in, int lq, int q0,
 __device__ inline void build_plan(const PlanInputs& in, PlanSmem& P, int* /*scratch*/) {
   const int tid = threadIdx.x, nthreads = blockDim.x;
   const int S = in.S;
-  const bool varlen = in.cu_seqlens_q != nullptr;
+  const bool varlen = in.cu_seqlens_q != nullptr || in.skip_empty;
+  // the query rows q0 .. q0 + lq - 1 of sequence s (an empty context: none)
+  auto window = [&](int s, int c, int& q0, int& lq) {
+    q0 = in.cu_seqlens_q ? in.cu_seqlens_q[s] : s;
+    lq = in.cu_seqlens_q ? in.cu_seqlens_q[s + 1] - q0 : (c > 0 ? 1 : 0);
+  };
   for (int s = tid; s < S; s += nthreads) {
     int c = in.context_lens[s];
     if (c < 0 || c > in.max_ctx) {
@@ -380,8 +388,8 @@ __device__ inline void build_plan(const PlanInputs& in, PlanSmem& P, int* /*scra
     }
     P.ctx[s] = c;
     if (varlen) {
-      const int q0 = in.cu_seqlens_q[s];
-      int lq = in.cu_seqlens_q[s + 1] - q0;
+      int q0, lq;
+      window(s, c, q0, lq);
       if (bad_window(in, lq, q0, c)) {
         flag_error(PA_DEVERR_QLEN_RANGE);
         lq = 0;  // the sequence produces no rows
@@ -389,7 +397,7 @@ __device__ inline void build_plan(const PlanInputs& in, PlanSmem& P, int* /*scra
       if (lq < in.min_lq || lq > in.max_lq) lq = 0;  // handled by another kernel
       P.qstart[s] = q0;
       P.seq_pair[s] = (lq + in.qtile - 1) / in.qtile;  // query tiles of s
-      if (s == S - 1) P.qstart[S] = in.cu_seqlens_q[S];
+      if (s == S - 1) P.qstart[S] = in.cu_seqlens_q ? in.cu_seqlens_q[S] : S;
     } else if (in.parts <= 1) {
       P.qstart[s] = s;
       P.seq_pair[s] = s;
@@ -428,8 +436,8 @@ __device__ inline void build_plan(const PlanInputs& in, PlanSmem& P, int* /*scra
       const int p0 = P.seq_pair[s], p1 = P.seq_pair[s + 1];
       if (p1 > npairs) continue;
       const int c = P.ctx[s];
-      const int q0 = in.cu_seqlens_q[s];
-      int lq = in.cu_seqlens_q[s + 1] - q0;
+      int q0, lq;
+      window(s, c, q0, lq);
       if (bad_window(in, lq, q0, c)) lq = 0;
       if (lq < in.min_lq || lq > in.max_lq) lq = 0;
       for (int p = p0; p < p1; ++p)

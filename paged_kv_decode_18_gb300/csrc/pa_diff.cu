@@ -26,6 +26,7 @@
 // the batch's (sequence, query tile, pair, block) tiles; segments that ranges
 // cut leave fp32 partials, which diff_fixup_kernel merges.
 #include <cudaTypedefs.h>
+#include <stdlib.h>
 
 #include "pa_diff.cuh"
 #include "pa_tcgen05.cuh"
@@ -36,8 +37,12 @@ namespace {
 constexpr int kMapRows = 8;                 // rows of one map in a tile
 constexpr int kDRows = 2 * kMapRows;
 constexpr int kDStage = 4 * kTileBytes;     // K[2p] K[2p+1] V[2p] V[2p+1] = 16 KB
-constexpr int kDWarps = 4;
-constexpr int kDMaxStages = 3;
+#ifndef DW
+#define DW 4
+#define DS 3
+#endif
+constexpr int kDWarps = DW;
+constexpr int kDMaxStages = DS;
 constexpr int kDDesc = 8;
 
 struct DiffArgs {
@@ -54,6 +59,7 @@ struct DiffArgs {
   int npairs_cap;
   int num_workers;
   int nstage;
+  int cost4;        // what a segment start weighs in the cut, in quarters of a tile
   int max_lq;       // longer windows belong to the tcgen05 kernel
   float* part_o;    // [NW*2][16][256]
   float* part_lse;  // [NW*2][16]
@@ -86,6 +92,9 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   P.seq_pair = P.pair_off + (a.npairs_cap + 1);
   P.ctx = P.seq_pair + (S + 1);
   P.qstart = P.ctx + S;
+  int* cut_at = P.qstart + (S + 1);  // [num_workers + 1]
+  // the epilogue's factors: lambdas [Hq / 2], then the norm's weight times the scale [256]
+  float* factors = reinterpret_cast<float*>(cut_at + a.num_workers + 1);
 
   if (lane == 0) {
     for (int i = 0; i < nstage; ++i) mbar_init(smem_addr(&bars[i]), 1);
@@ -96,6 +105,8 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     prefetch_tensormap(&tmv);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int i = threadIdx.x; i < Hq / 2 + kDiffDim; i += blockDim.x)
+    factors[i] = i < Hq / 2 ? a.o.lambdas[i] : (a.o.weight ? a.o.weight[i - Hq / 2] : 1.f);
   PlanInputs in;
   in.context_lens = a.context_lens;
   in.cu_seqlens_q = a.cu_seqlens_q;
@@ -107,7 +118,14 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   in.npairs_cap = a.npairs_cap;
   in.num_q_rows = a.num_q_tokens;
   in.max_lq = a.max_lq;
+  in.skip_empty = a.cu_seqlens_q == nullptr;
   build_plan(in, P, nullptr);
+  const int W = P.total;
+  // two tiles a warp at least: cutting a short batch further costs more in the merge
+  // than it saves
+  const PieceCut cut = build_piece_cut(P, Hp, min((int)gridDim.x * kDWarps, max(1, W / 2)),
+                                       a.cost4, cut_at);
+  const int nw = W > 0 ? cut.nw : 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // a sequence of the single-query form with an empty context has no tiles
@@ -122,16 +140,14 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     }
   }
 
-  const int W = P.total;
   const int w = warp * (int)gridDim.x + (int)blockIdx.x;
-  const int nw = min((int)gridDim.x * kDWarps, max(1, W / 2));
   int R0 = 0, R1 = 0;
   if (w < nw) {
-    R0 = range_start(w, W, nw);
-    R1 = range_start(w + 1, W, nw);
+    R0 = cut.start(w);
+    R1 = cut.start(w + 1);
   }
   if (lane == 0) {
-    const MergeJob j = merge_job(P, S, Hp, w, W, nw);
+    const MergeJob j = merge_job_of(P, S, Hp, w, nw, cut);
     int* d = a.desc + (size_t)w * kDDesc;
     d[0] = j.valid ? j.s : -1;
     if (j.valid) {
@@ -173,7 +189,19 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
       tma_load_block(st + 2 * kTileBytes, &tmv, group, bar);
     }
     ++pidx;
-    if (pidx < R1) advance(P, S, Hp, pp);
+    if (pidx < R1) {
+      advance(P, S, Hp, pp);
+      if (pp.b == 0) {
+        // a new segment: its query rows on their way to L2 before they are wanted
+        const int row = lane >> 1;  // eight rows of either map, 128 bytes a lane
+        const int n = P.qstart[pp.s + 1] - P.qstart[pp.s], rm = row & 7;
+        const int tk = pp.qt * QT + rm / G;
+        if (rm < QT * G && tk < n)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(
+              a.q + (((int64_t)P.qstart[pp.s] + tk) * Hq + (int64_t)(2 * pp.h + (row >> 3)) * G +
+                     rm % G) * kHeadDim + (lane & 1) * 64));
+      }
+    }
     if (pidx - wbase == 32) {
       wbase += 32;
       phys_cur = phys_next;
@@ -402,7 +430,7 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
       }
       if (piece_b0 == 0 && cp.b == cp.nt - 1) {
         const int head = cp.h * G + r % G;
-        const float lam = valid ? a.o.lambdas[head] : 0.f;
+        const float lam = valid ? factors[head] : 0.f;
         float squares = 0.f;
 #pragma unroll
         for (int n = 0; n < 32; ++n) {
@@ -418,13 +446,9 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
           uint16_t* dst = a.o.out + (qtok * (Hq / 2) + head) * kDiffDim + quad * 2;
 #pragma unroll
           for (int n = 0; n < 32; ++n) {
-            float2 wt = make_float2(f, f);
-            if (a.o.weight) {
-              const float2 x = *reinterpret_cast<const float2*>(a.o.weight + n * 8 + quad * 2);
-              wt = make_float2(f * x.x, f * x.y);
-            }
+            const float* x = factors + Hq / 2 + n * 8 + quad * 2;
             *reinterpret_cast<uint32_t*>(dst + n * 8) =
-                cvt_bf16x2(o[n][0] * wt.x, o[n][1] * wt.y);
+                cvt_bf16x2(o[n][0] * (f * x[0]), o[n][1] * (f * x[1]));
           }
           if (a.o.lse && quad == 0) {
             float* l = a.o.lse + qtok * Hq + (int64_t)(2 * cp.h) * G + r % G;
@@ -645,7 +669,11 @@ int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffG
   const int64_t cap = cap1 < cap2 ? cap1 : cap2;
   if (cap > (1 << 22)) return PA_ERR_UNSUPPORTED;
   g->npairs_cap = (int)(cap < S ? S : cap);
-  const size_t plan = sizeof(int) * ((size_t)g->npairs_cap + 1 + 3 * (size_t)S + 2);
+  g->grid = dev.num_sms;
+  g->workers = g->grid * kDWarps;
+  const size_t plan =
+      sizeof(int) * ((size_t)g->npairs_cap + 1 + 3 * (size_t)S + 2 + (size_t)g->workers + 1) +
+      sizeof(float) * ((size_t)sh->num_q_heads / 2 + kDiffDim);
   // as many stages as leave room for the plan, two at least
   for (g->nstage = kDMaxStages; g->nstage >= 2; --g->nstage) {
     g->smem = 1024 + (size_t)kDWarps * g->nstage * kDStage + kDWarps * kDMaxStages * 8 + plan;
@@ -653,8 +681,6 @@ int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffG
   }
   if (g->nstage < 2) return PA_ERR_UNSUPPORTED;
   if (!raise_smem_limit(reinterpret_cast<const void*>(paged_diff_kernel))) return PA_ERR_CUDA;
-  g->grid = dev.num_sms;
-  g->workers = g->grid * kDWarps;
   g->ws_desc = round_up(sizeof(int) * kDDesc * (size_t)g->workers, 256);
   g->ws_lse = round_up(sizeof(float) * 2 * kDRows * (size_t)g->workers, 256);
   g->ws_o = round_up(sizeof(float) * 2 * kDRows * kDiffDim * (size_t)g->workers, 256);
@@ -662,11 +688,41 @@ int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffG
   return PA_OK;
 }
 
+// The kernels of a call. A window whose rows of a KV head (query tokens x group) are
+// fewer than kTcMinRows goes through warp tiles of eight rows, the others through
+// tcgen05 tiles of 256; more than eight query heads to a KV head always do.
+constexpr int kMaxGroup = 128;
+constexpr int kTcMinRows = 64;
+
+struct DiffPlan {
+  bool warp = false;  // some window may be short
+  DiffGeometry g;
+  DiffTcGeometry tc;
+  size_t ws_bytes = 0;
+};
+
+int diff_plan(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffPlan* p) {
+  const int G = sh->num_q_heads / sh->num_kv_heads;
+  const int min_rows = getenv("PA_MINROWS") ? atoi(getenv("PA_MINROWS")) : kTcMinRows;
+  const int min_lq = G > kMapRows ? 1 : (min_rows + G - 1) / G;
+  int rc = diff_tc_geometry(sh, num_q_tokens, max_q_len, min_lq, &p->tc);
+  if (rc != PA_OK) return rc;
+  // as many rows as windows of max_q_len hold: every window has that length
+  p->warp = G <= kMapRows &&
+            !(p->tc.enabled && num_q_tokens == (int64_t)sh->num_seqs * max_q_len);
+  if (p->warp) {
+    rc = diff_geometry(sh, num_q_tokens, max_q_len, &p->g);
+    if (rc != PA_OK) return rc;
+  }
+  p->ws_bytes = (p->warp ? p->g.ws_bytes : 0) + p->tc.ws_bytes;
+  return PA_OK;
+}
+
 int check_diff_args(const pa_shape* sh, int64_t num_q_tokens, int max_q_len) {
   const int rc = check_shape_common(sh);
   if (rc != PA_OK) return rc;
   if (sh->num_kv_heads % 2 != 0) return PA_ERR_UNSUPPORTED;
-  if (sh->num_q_heads / sh->num_kv_heads > kMapRows) return PA_ERR_UNSUPPORTED;
+  if (sh->num_q_heads / sh->num_kv_heads > kMaxGroup) return PA_ERR_UNSUPPORTED;
   if (num_q_tokens < 0 || max_q_len < 0 || num_q_tokens > 0x3fffffff) return PA_ERR_ARG;
   if (sh->num_blocks * sh->num_kv_heads * kBlock > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   return PA_OK;
@@ -693,8 +749,8 @@ extern "C" size_t pa_decode_diff_workspace_size(const pa_shape* shape, int64_t n
                                                 int max_q_len) {
   if (check_diff_args(shape, num_q_tokens, max_q_len) != PA_OK) return 0;
   if (shape->num_seqs == 0 || num_q_tokens == 0 || max_q_len == 0) return 0;
-  DiffGeometry g;
-  return diff_geometry(shape, num_q_tokens, max_q_len, &g) == PA_OK ? g.ws_bytes : 0;
+  DiffPlan p;
+  return diff_plan(shape, num_q_tokens, max_q_len, &p) == PA_OK ? p.ws_bytes : 0;
 }
 
 extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
@@ -717,11 +773,28 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
       !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(cu_seqlens_q, 4) ||
       !aligned(lambdas, 4) || !aligned(norm_weight, 16) || !aligned(lse, 4))
     return PA_ERR_ARG;
-  DiffGeometry g;
-  rc = diff_geometry(shape, num_q_tokens, max_q_len, &g);
+  DiffPlan p;
+  rc = diff_plan(shape, num_q_tokens, max_q_len, &p);
   if (rc != PA_OK) return rc;
-  if (!workspace || workspace_bytes < g.ws_bytes || !aligned(workspace, 256))
+  if (!workspace || workspace_bytes < p.ws_bytes || !aligned(workspace, 256))
     return PA_ERR_WORKSPACE;
+  DiffOut o;
+  o.out = out;
+  o.lse = lse;
+  o.lambdas = lambdas;
+  o.weight = norm_weight;
+  o.eps = norm_eps;
+  o.gain = out_scale;
+  causal = causal && cu_seqlens_q ? 1 : 0;
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (p.tc.enabled) {
+    rc = launch_diff_tc(p.tc, q, k_cache, v_cache, block_tables, context_lens, cu_seqlens_q,
+                        num_q_tokens, causal, scale, o, shape, ws, st);
+    if (rc != PA_OK) return rc;
+  }
+  if (!p.warp) return PA_OK;
+  const DiffGeometry& g = p.g;
   const int64_t rows = shape->num_blocks * shape->num_kv_heads * kBlock;
   CUtensorMap tmk, tmv;
   if (!make_pair_map(&tmk, k_cache, rows) || !make_pair_map(&tmv, v_cache, rows))
@@ -731,12 +804,7 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
   a.block_tables = block_tables;
   a.context_lens = context_lens;
   a.cu_seqlens_q = cu_seqlens_q;
-  a.o.out = out;
-  a.o.lse = lse;
-  a.o.lambdas = lambdas;
-  a.o.weight = norm_weight;
-  a.o.eps = norm_eps;
-  a.o.gain = out_scale;
+  a.o = o;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.S = shape->num_seqs;
   a.Hq = shape->num_q_heads;
@@ -746,16 +814,16 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
   a.max_blocks = shape->max_blocks_per_seq;
   a.num_blocks = shape->num_blocks;
   a.num_q_tokens = num_q_tokens;
-  a.causal = causal && cu_seqlens_q ? 1 : 0;
+  a.causal = causal;
   a.npairs_cap = g.npairs_cap;
   a.num_workers = g.workers;
   a.nstage = g.nstage;
-  a.max_lq = 0x7fffffff;
-  char* ws = static_cast<char*>(workspace);
-  a.desc = reinterpret_cast<int*>(ws);
-  a.part_lse = reinterpret_cast<float*>(ws + g.ws_desc);
-  a.part_o = reinterpret_cast<float*>(ws + g.ws_desc + g.ws_lse);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  a.cost4 = getenv("PA_COST") ? atoi(getenv("PA_COST")) : 4;
+  a.max_lq = p.tc.enabled ? p.tc.min_lq - 1 : 0x7fffffff;
+  char* wws = ws + p.tc.ws_bytes;
+  a.desc = reinterpret_cast<int*>(wws);
+  a.part_lse = reinterpret_cast<float*>(wws + g.ws_desc);
+  a.part_o = reinterpret_cast<float*>(wws + g.ws_desc + g.ws_lse);
   if (launch_dependent(paged_diff_kernel, dim3(g.grid), dim3(kDWarps * 32), g.smem, st, tmk, tmv,
                        a) != cudaSuccess)
     return PA_ERR_CUDA;

@@ -34,7 +34,20 @@ __device__ __forceinline__ float diff_factor(const DiffOut& o, float squares) {
 }
 
 // ---------------------------------------------------------------------------
-// tcgen05 path (pa_diff_tc.cu)
+// tcgen05 path (pa_diff_tc.cu): windows of min_q_len tokens and more
 // ---------------------------------------------------------------------------
+struct DiffTcGeometry {
+  bool enabled = false;
+  int workers = 0, npairs_cap = 0, nstage = 0, min_lq = 0;
+  size_t smem = 0, ws_lse = 0, ws_o = 0, ws_bytes = 0;
+};
+
+int diff_tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, int min_q_len,
+                     DiffTcGeometry* g);
+int launch_diff_tc(const DiffTcGeometry& g, const pa_bf16* q, const pa_bf16* k_cache,
+                   const pa_bf16* v_cache, const int32_t* block_tables,
+                   const int32_t* context_lens, const int32_t* cu_seqlens_q, int64_t num_q_tokens,
+                   int causal, float scale, const DiffOut& out, const pa_shape* sh, void* workspace,
+                   cudaStream_t st);
 
 }  // namespace pa

@@ -90,6 +90,41 @@ inline bool kernel_occupancy(const void* fn, int threads, size_t smem, int* per_
   return true;
 }
 
+// Clusters of `cluster` CTAs that the current device holds at once (cached as above).
+inline bool cluster_occupancy(const void* fn, int threads, size_t smem, int cluster, int* count) {
+  if (!raise_smem_limit(fn)) return false;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int, size_t, int>, int> cache;
+  const auto key = std::make_tuple(fn, dev, threads, smem, cluster);
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = cache.find(key);
+    if (it != cache.end()) {
+      *count = it->second;
+      return true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cluster);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  cache[key] = n;
+  *count = n;
+  return true;
+}
+
 inline bool aligned(const void* p, size_t a) {
   return (reinterpret_cast<uintptr_t>(p) % a) == 0;
 }
@@ -256,5 +291,6 @@ unsigned take_error_word_weights_tc(cudaStream_t stream, int* rc);
 unsigned take_error_word_evict(cudaStream_t stream, int* rc);
 unsigned take_error_word_rotate(cudaStream_t stream, int* rc);
 unsigned take_error_word_diff(cudaStream_t stream, int* rc);
+unsigned take_error_word_diff_tc(cudaStream_t stream, int* rc);
 
 }  // namespace pa

@@ -53,8 +53,7 @@ def attend(q, kc, vc, tables, lens, cu, scale, lambdas, weight=None, eps=0.0, ga
                     dz = (128 + 4) * U32 * size + 2.0 ** -21
                     m = torch.logsumexp(z, -1)
                     w = torch.exp(z - m[:, None])
-                    got = torch.where(see[..., None], w[..., None] * v, 0.0).sum(1)
-                    mass = torch.where(see[..., None], w[..., None] * v.abs(), 0.0).sum(1)
+                    got, mass = w @ v, w @ v.abs()
                     a_i.append(got)
                     # (the sum over c weights in fp32: c 2^-24 at most)
                     e_i.append((torch.expm1(2 * dz) + UBF + (c + 64) * U32)[:, None] * mass)

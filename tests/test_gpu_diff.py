@@ -160,6 +160,88 @@ def test_windows(lens, qs, hkv, G, causal):
     b.check(again, None, causal=causal)
 
 
+LONG = [
+    # windows of several tiles of 256 rows, and rows that fill none
+    ([128], [128], 2, 1), ([300, 129], [257, 64], 2, 2), ([1000, 70, 515], [130, 70, 1], 4, 2),
+    ([640], [512], 2, 4), ([200, 90], [90, 33], 2, 3), ([333], [200], 2, 8), ([140, 3], [20, 3], 2, 7),
+    # more heads to a KV head than a warp tile holds
+    ([40, 0, 200], [5, 0, 1], 2, 16), ([77], [30], 2, 24), ([100, 260], [2, 3], 2, 128),
+    # few segments in many pieces
+    ([4000], [64], 2, 1), ([3000, 200], [70, 100], 2, 2),
+]
+
+
+@pytest.mark.parametrize("lens,qs,hkv,G", LONG)
+@pytest.mark.parametrize("causal,norm", [(True, True), (False, False)])
+def test_long_windows(lens, qs, hkv, G, causal, norm):
+    b = Batch(sum(lens) + G, lens, qs, hkv, G, heavy=4.0).cuda()
+    out, lse = b.call(causal=causal, norm=norm, spare=3, ws_fill=0xFF)
+    ok()
+    b.check(out, lse, causal=causal, norm=norm)
+    assert (out[b.T:] == 3).all() and (lse[b.T:] == 5).all()
+    again, _ = b.call(causal=causal, norm=norm, with_lse=False, ws_fill=0x11)
+    ok()
+    assert torch.equal(again[:b.T].view(torch.int16), out[:b.T].view(torch.int16))
+
+
+@pytest.mark.parametrize("lens,G", [([33, 0, 1], 9), ([300], 32), ([2000, 17], 16)])
+def test_single_queries_of_many_heads(lens, G):
+    b = Batch(sum(lens) + G, lens, None, 2, G).cuda()
+    out, lse = b.call()
+    ok()
+    b.check(out, lse)
+    for s, c in enumerate(lens):
+        if c == 0:
+            assert (out[s] == 0).all() and (lse[s] == -math.inf).all()
+
+
+def test_a_hidden_key_of_a_long_window_never_reaches_a_query():
+    lens, qs = [700, 200], [300, 150]
+    b = Batch(3, lens, qs, 2, 2)
+    clean = b.kc.clone(), b.vc.clone()
+    # (one head's values alone, in either sequence: the tile's halves hold one each)
+    for s, at, h, what in ((0, 600, 0, float("nan")), (0, 650, 1, float("inf")),
+                           (1, 120, 1, float("-inf"))):
+        blk = int(b.tables[s, at // BLOCK])
+        b.kc[blk, :, at % BLOCK, 3::7] = what
+        b.vc[blk, h, at % BLOCK, 1::5] = what
+    b.cuda()
+    out, lse = b.call()
+    ok()
+    ref, rl, tol, ltol = R.attend(b.q, *clean, b.tables, lens, b.cu, SCALE, b.lambdas, b.weight,
+                                  1e-5, 0.8)
+    got, gl = out.cpu().double(), lse.cpu().double()
+    fine = torch.zeros(b.T, dtype=torch.bool)
+    fine[0:200] = True               # positions 400 .. 599
+    fine[300:370] = True             # positions 50 .. 119
+    assert ((got - ref).abs() <= tol)[fine].all()
+    assert ((gl - rl).abs() <= ltol)[fine].all()
+    assert not torch.isfinite(got[~fine]).all(-1).any()
+
+
+def test_values_that_are_infinite_where_they_are_seen():
+    # finite scores: the queries from the key on get the infinity, the others none
+    for lens, qs in (([700], [300]), ([60], [20])):
+        b = Batch(4, lens, qs, 2, 1)
+        at = lens[0] - 10
+        b.vc[int(b.tables[0, at // BLOCK]), 1, at % BLOCK, 7] = float("inf")
+        b.cuda()
+        out, _ = b.call(norm=False)
+        ok()
+        bad = ~torch.isfinite(out[:b.T, 0].cpu())
+        want = torch.zeros_like(bad)
+        want[qs[0] - 10:, DIM + 7] = True
+        assert torch.equal(bad, want)
+
+
+def test_short_and_long_windows_in_one_call():
+    lens, qs = [900, 40, 333, 64], [200, 5, 100, 1]
+    b = Batch(8, lens, qs, 4, 2).cuda()
+    out, lse = b.call()
+    ok()
+    b.check(out, lse)
+
+
 def test_windows_of_one_are_single_queries():
     lens = [37, 1, 200, 16]
     one = Batch(5, lens, None, 4, 2).cuda()
