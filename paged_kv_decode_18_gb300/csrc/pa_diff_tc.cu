@@ -26,7 +26,7 @@
 // threads to a query row, one per 64-key half. O has the whole 256 columns that
 // S/P leave of tensor memory, one accumulator for both halves, so the halves
 // agree on the row's reference: they exchange their maxima every tile. The
-// reference moves only when a maximum grows by more than 2^8 (exact either way).
+// reference moves only when a maximum grows by more than 2^32 (exact either way).
 #include <cudaTypedefs.h>
 
 #include "pa_diff.cuh"
@@ -52,7 +52,12 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;               // S/P buffers at columns 0 and 128, O at 256 .. 511
 constexpr int kSegCost4 = 6;                  // a segment start in quarters of a key tile
 constexpr int kTDesc = 8;
-constexpr float kRescaleLog2 = 8.f;
+// The reference of a row's exponentials moves only when its maximum has grown by more
+// than this power of two: weights up to 2^32 are as exact in bf16 and fp32 as those below
+// 1, and leave 95 powers of two for V and the sums. (At 2^8, with one key in a hundred
+// eight times as long as the others, nearly every warp rescaled its 256 columns of O in
+// every tile, at 700 clocks each.)
+constexpr float kRescaleLog2 = 32.f;
 
 enum : int {
   B_QFULL = 0,                        // [2], leader: both CTAs' query rows
@@ -117,20 +122,15 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
   return at;
 }
+// Arrives on a barrier of either CTA. What it tells of is in tensor memory (ordered by
+// the tcgen05 fences); a thread that has written shared memory for the peer's products
+// to read makes a fence of the cluster's scope first. (An arrive that releases at that
+// scope costs every softmax warp 600 clocks a tile.)
 __device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-               : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
+__device__ __forceinline__ void fence_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 // tiled copies whose completion counts on a barrier of either CTA of the pair
 __device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
@@ -277,12 +277,11 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Bounded wait; acquires what the peer has released as well.
   auto wait = [&](int b, uint32_t parity) -> bool {
-    if (try_wait_cluster(bar(b), parity)) return true;
+    if (mbar_try_wait(bar(b), parity)) return true;
     const unsigned long long t0 = global_timer_ns();
     while (!*abort_flag) {
-      if (try_wait_cluster(bar(b), parity)) return true;
+      if (mbar_try_wait(bar(b), parity)) return true;
       if (global_timer_ns() - t0 > kWaitLimitNs) {
         flag_error(PA_DEVERR_PIPE_TIMEOUT);
         *abort_flag = 1;
@@ -717,8 +716,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       // keys past the context may hold anything (even NaN): zero their V rows so that P
       // = 0 never meets them; of the window's rows, which only some queries see, the
       // infinities and NaNs (thread (r, hf) has half hf of key row r of this CTA's head)
-      if (!wait_all(B_VFULL + st, use & 1u)) break;
+      // (Only one warp of a CTA sees to it that V is there before the product begins; a
+      // wait costs 130 clocks even when it is over.)
       const int vsafe = a.causal ? c - lq + 1 : c;  // rows before it enter as they are
+      if ((warp == 2 || key0 + kKeysT > vsafe) && !wait_all(B_VFULL + st, use & 1u)) break;
       if (key0 + kKeysT > vsafe && key0 + r >= vsafe) {
         unsigned char* vrow = stages + st * kStageT + kKBytes + (r >> 3) * 2048 + hf * 1024 +
                               (r & 7) * 128;
@@ -727,6 +728,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           for (int ch = 0; ch < 8; ++ch)
             *reinterpret_cast<uint4*>(vrow + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
+          fence_cluster();
         } else {
           bool bad = false;
 #pragma unroll
@@ -752,7 +754,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                                in_cta(flag, to)),
                            "r"(1u)
                            : "memory");
-            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            fence_cluster();
           }
         }
       }
