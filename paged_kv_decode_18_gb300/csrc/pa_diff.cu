@@ -37,12 +37,10 @@ namespace {
 constexpr int kMapRows = 8;                 // rows of one map in a tile
 constexpr int kDRows = 2 * kMapRows;
 constexpr int kDStage = 4 * kTileBytes;     // K[2p] K[2p+1] V[2p] V[2p+1] = 16 KB
-#ifndef DW
-#define DW 4
-#define DS 3
-#endif
-constexpr int kDWarps = DW;
-constexpr int kDMaxStages = DS;
+constexpr int kDWarps = 5;
+constexpr int kDStages = 2;
+// what a segment start weighs in the cut, in quarters of a tile
+constexpr int kSegCost4 = 6;
 constexpr int kDDesc = 8;
 
 struct DiffArgs {
@@ -58,8 +56,6 @@ struct DiffArgs {
   int causal;
   int npairs_cap;
   int num_workers;
-  int nstage;
-  int cost4;        // what a segment start weighs in the cut, in quarters of a tile
   int max_lq;       // longer windows belong to the tcgen05 kernel
   float* part_o;    // [NW*2][16][256]
   float* part_lse;  // [NW*2][16]
@@ -73,6 +69,48 @@ __device__ __forceinline__ uint32_t atom_at(int row, int chunk) {
                     (((chunk & 7) ^ (row & 7)) << 4));
 }
 
+// PieceCut without its array: the cost of tiles 0 .. x-1 is 4x + kSegCost4 * (segment
+// starts below x), and worker w begins at the first tile whose cost reaches
+// floor(w C / nw). A warp wants three starts and one owner only, in closed form behind
+// one bisection; the array of all 608 took 2 us at the head of every call.
+struct CostCut {
+  const PlanSmem* P;
+  int Hp, nw;
+  long long C;
+  __device__ __forceinline__ CostCut(const PlanSmem& plan, int heads, int max_workers)
+      : P(&plan), Hp(heads) {
+    C = 4LL * plan.total + (long long)kSegCost4 * plan.npairs * heads;
+    const long long n = C / (4 + kSegCost4);
+    nw = (int)(n > max_workers ? max_workers : n);
+  }
+  __device__ __forceinline__ long long base(int p) const {
+    return 4LL * P->pair_off[p] + (long long)kSegCost4 * p * Hp;
+  }
+  __device__ __forceinline__ int start(int w) const {  // 0 <= w <= nw
+    if (w <= 0) return 0;
+    if (w >= nw) return P->total;
+    const long long T = ((long long)w * C) / nw;
+    int lo = 0, hi = P->npairs - 1;  // the pair with base(lo) < T <= base(lo + 1)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (base(mid) < T)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int o0 = P->pair_off[lo], nt = (P->pair_off[lo + 1] - o0) / Hp;
+    const int D = (int)(T - base(lo));  // 1 .. Hp (4 nt + kSegCost4)
+    const int seg = 4 * nt + kSegCost4, h = (D - 1) / seg, rem = D - h * seg;
+    return o0 + h * nt + max(1, (rem - kSegCost4 + 3) / 4);
+  }
+  // the worker that holds the last tile of a segment of two tiles or more
+  __device__ __forceinline__ int owner_of_last(const TilePos& t) const {
+    const long long x = P->pair_off[t.p] + (long long)t.h * t.nt + t.nt - 1;
+    const long long cost = 4 * x + (long long)kSegCost4 * (t.p * Hp + t.h + 1);
+    return (int)(((cost + 1) * nw - 1) / C);
+  }
+};
+
 __global__ void __launch_bounds__(kDWarps * 32, 1)
     paged_diff_kernel(const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const DiffArgs a) {
@@ -80,24 +118,24 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   const uint32_t raw = smem_addr(smem_raw);
   unsigned char* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int nstage = a.nstage;
-  unsigned char* wbuf = smem + warp * nstage * kDStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kDWarps * nstage * kDStage) +
-                   warp * kDMaxStages;
+  unsigned char* wbuf = smem + warp * kDStages * kDStage;
+  uint64_t* bars =
+      reinterpret_cast<uint64_t*>(smem + kDWarps * kDStages * kDStage) + warp * kDStages;
   const int S = a.S, Hq = a.Hq, G = a.G, QT = a.QT, Hp = a.Hkv >> 1;
 
   PlanSmem P;
-  P.pair_off = reinterpret_cast<int*>(smem + kDWarps * nstage * kDStage +
-                                      kDWarps * kDMaxStages * 8);
+  P.pair_off = reinterpret_cast<int*>(smem + kDWarps * kDStages * kDStage +
+                                      kDWarps * kDStages * 8);
   P.seq_pair = P.pair_off + (a.npairs_cap + 1);
   P.ctx = P.seq_pair + (S + 1);
   P.qstart = P.ctx + S;
-  int* cut_at = P.qstart + (S + 1);  // [num_workers + 1]
-  // the epilogue's factors: lambdas [Hq / 2], then the norm's weight times the scale [256]
-  float* factors = reinterpret_cast<float*>(cut_at + a.num_workers + 1);
+  // the norm's weights, in shared memory for the epilogue: from global memory its 32
+  // loads a lane, few of them in flight beside 128 accumulators, cost a ragged batch of
+  // short contexts a third of its time
+  __shared__ float2 weights[kDiffDim / 2];
 
   if (lane == 0) {
-    for (int i = 0; i < nstage; ++i) mbar_init(smem_addr(&bars[i]), 1);
+    for (int i = 0; i < kDStages; ++i) mbar_init(smem_addr(&bars[i]), 1);
     mbar_fence_init();
   }
   if (threadIdx.x == 0) {
@@ -105,8 +143,10 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     prefetch_tensormap(&tmv);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int i = threadIdx.x; i < Hq / 2 + kDiffDim; i += blockDim.x)
-    factors[i] = i < Hq / 2 ? a.o.lambdas[i] : (a.o.weight ? a.o.weight[i - Hq / 2] : 1.f);
+  static_assert(kDWarps * 32 >= kDiffDim / 2, "a pair of weights a thread");
+  float2 mine = make_float2(1.f, 1.f);
+  if (a.o.weight && threadIdx.x < kDiffDim / 2)
+    mine = reinterpret_cast<const float2*>(a.o.weight)[threadIdx.x];
   PlanInputs in;
   in.context_lens = a.context_lens;
   in.cu_seqlens_q = a.cu_seqlens_q;
@@ -120,12 +160,12 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   in.max_lq = a.max_lq;
   in.skip_empty = a.cu_seqlens_q == nullptr;
   build_plan(in, P, nullptr);
+  if (threadIdx.x < kDiffDim / 2) weights[threadIdx.x] = mine;
+  __syncthreads();
   const int W = P.total;
   // two tiles a warp at least: cutting a short batch further costs more in the merge
   // than it saves
-  const PieceCut cut = build_piece_cut(P, Hp, min((int)gridDim.x * kDWarps, max(1, W / 2)),
-                                       a.cost4, cut_at);
-  const int nw = W > 0 ? cut.nw : 0;
+  const CostCut cut(P, Hp, min((int)gridDim.x * kDWarps, max(1, W / 2)));
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // a sequence of the single-query form with an empty context has no tiles
@@ -141,28 +181,33 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   }
 
   const int w = warp * (int)gridDim.x + (int)blockIdx.x;
-  int R0 = 0, R1 = 0;
-  if (w < nw) {
-    R0 = cut.start(w);
-    R1 = cut.start(w + 1);
+  int R0 = 0, R1 = 0, R0prev = 0;  // this worker's range, and where the one before begins
+  if (w < cut.nw) {
+    const int at = cut.start(w - 1 + (lane < 3 ? lane : 1));
+    R0prev = __shfl_sync(kFull, at, 0);
+    R0 = __shfl_sync(kFull, at, 1);
+    R1 = __shfl_sync(kFull, at, 2);
   }
+  TilePos cp;
+  if (R0 < R1) cp = locate(P, S, Hp, R0);
   if (lane == 0) {
-    const MergeJob j = merge_job_of(P, S, Hp, w, nw, cut);
-    int* d = a.desc + (size_t)w * kDDesc;
-    d[0] = j.valid ? j.s : -1;
-    if (j.valid) {
-      d[1] = j.qt;
-      d[2] = j.h;
-      d[3] = j.last;
-      d[4] = j.slot_prev;
-      d[5] = P.qstart[j.s];
-      d[6] = P.qstart[j.s + 1] - P.qstart[j.s];
+    // the segment that this boundary cuts, if it is the first to do so
+    int4 d0 = make_int4(-1, 0, 0, 0), d1 = d0;
+    if (R0 < R1 && w > 0 && cp.b > 0) {
+      const int A = R0 - cp.b;  // its first tile
+      if (A >= R0prev) {
+        d0 = make_int4(cp.s, cp.qt, cp.h, cut.owner_of_last(cp));
+        d1 = make_int4(A == R0prev ? 0 : 1, P.qstart[cp.s], P.qstart[cp.s + 1] - P.qstart[cp.s], 0);
+      }
     }
+    int4* d = reinterpret_cast<int4*>(a.desc + (size_t)w * kDDesc);
+    d[0] = d0;
+    d[1] = d1;
   }
   if (R0 >= R1) return;
 
   // ---- producer --------------------------------------------------------------
-  TilePos pp = locate(P, S, Hp, R0);
+  TilePos pp = cp;
   int pidx = R0, wbase = R0;
   // block id of flat tile idx; tiles of a window lie a few pairs past pp
   auto load_phys = [&](int idx) -> int {
@@ -208,16 +253,16 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
       phys_next = load_phys(wbase + 32 + lane);
     }
   };
-  for (int i = 0; i < nstage && pidx < R1; ++i) issue(i);
+  for (int i = 0; i < kDStages && pidx < R1; ++i) issue(i);
 
   // ---- consumer --------------------------------------------------------------
-  TilePos cp = locate(P, S, Hp, R0);
   const int r = lane >> 2, quad = lane & 3;  // this lane's row of either map
   const int mi = lane >> 3, rr = lane & 7;   // ldmatrix: matrix and row of this lane's address
   uint32_t qa[8][4];
   float o[32][4];
   float m_r[2], l_r[2];
   int lim = 0, lim_min = 0, lq = 0, ctx = 0, tok = 0;
+  float lam = 0.f;
   bool valid = false;
   int piece_b0 = 0;
   bool piece_first = true;
@@ -240,6 +285,7 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
             a.q + (((int64_t)P.qstart[cp.s] + tok) * Hq + (int64_t)(2 * cp.h) * G + r % G) *
                       kHeadDim);
       const uint32_t* q1 = q0 + (int64_t)G * (kHeadDim / 2);
+      lam = valid ? a.o.lambdas[cp.h * G + r % G] : 0.f;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         const int c = kk * 8 + quad;  // 32-bit word of dims kk*16 + 2*quad
@@ -263,7 +309,7 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     if (!mbar_wait_bounded(smem_addr(&bars[stage]), parity)) {
       // the copies in flight land before the warp leaves
       for (int j = idx + 1; j < pidx; ++j) {
-        if (++stage == nstage) {
+        if (++stage == kDStages) {
           stage = 0;
           parity ^= 1u;
         }
@@ -412,7 +458,7 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     }
     __syncwarp();
     if (pidx < R1) issue(stage);
-    if (++stage == nstage) {
+    if (++stage == kDStages) {
       stage = 0;
       parity ^= 1u;
     }
@@ -430,7 +476,6 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
       }
       if (piece_b0 == 0 && cp.b == cp.nt - 1) {
         const int head = cp.h * G + r % G;
-        const float lam = valid ? factors[head] : 0.f;
         float squares = 0.f;
 #pragma unroll
         for (int n = 0; n < 32; ++n) {
@@ -446,9 +491,9 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
           uint16_t* dst = a.o.out + (qtok * (Hq / 2) + head) * kDiffDim + quad * 2;
 #pragma unroll
           for (int n = 0; n < 32; ++n) {
-            const float* x = factors + Hq / 2 + n * 8 + quad * 2;
+            const float2 x = weights[n * 4 + quad];
             *reinterpret_cast<uint32_t*>(dst + n * 8) =
-                cvt_bf16x2(o[n][0] * (f * x[0]), o[n][1] * (f * x[1]));
+                cvt_bf16x2(o[n][0] * (f * x.x), o[n][1] * (f * x.y));
           }
           if (a.o.lse && quad == 0) {
             float* l = a.o.lse + qtok * Hq + (int64_t)(2 * cp.h) * G + r % G;
@@ -477,10 +522,11 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
 }
 
 // Merge the pieces of (sequence, query tile, pair) segments cut by the equal
-// ranges, then difference, norm and scale. One CTA per worker boundary; its
-// warps are dealt out to the segment's rows, several to a row where there are
-// few, each taking every n-th round of four pieces with all their loads in
-// flight. A lane holds eight of a row's 256 dims, of both maps. Partials are
+// ranges, then difference, norm and scale. Grid (worker boundary, chunk of
+// chunk_rows rows); a CTA's warps are dealt out to its rows, several to a row where
+// there are few, each taking every n-th round of four pieces with all their loads in
+// flight. (Where segments have many pieces a CTA takes one row: 8 x 32k contexts, 47
+// pieces of 4 rows, 14 us with a CTA to a segment.) A lane holds eight of a row's 256 dims, of both maps. Partials are
 // read through L2 (ld.global.cg): other SMs wrote them.
 constexpr int kDFixWarps = 8;
 
@@ -504,21 +550,24 @@ __device__ __forceinline__ void join(MapSum& x, float mo, float so, const float 
 
 __global__ void __launch_bounds__(kDFixWarps * 32)
     diff_fixup_kernel(const int* desc, const float* part_o, const float* part_lse, const DiffOut out,
-                      int num_workers, int Hq, int G, int QT) {
+                      int num_workers, int chunk_rows, int Hq, int G, int QT) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int w = blockIdx.x;
   if (w >= num_workers) return;
-  const int* d = desc + (size_t)w * kDDesc;
-  if (__ldcg(d) < 0) return;
-  const int qt = __ldcg(d + 1), h = __ldcg(d + 2), last = __ldcg(d + 3),
-            slot_prev = __ldcg(d + 4), q0 = __ldcg(d + 5), lq = __ldcg(d + 6);
+  const int4* d = reinterpret_cast<const int4*>(desc + (size_t)w * kDDesc);
+  const int4 d0 = __ldcg(d), d1 = __ldcg(d + 1);
+  if (d0.x < 0) return;
+  const int qt = d0.y, h = d0.z, last = d0.w, slot_prev = d1.x, q0 = d1.y, lq = d1.z;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int npieces = last - w + 2;                       // workers w-1 .. last
-  const int nrows = min(QT, lq - qt * QT) * G;            // 1 .. 8 of either map
+  const int row0 = (int)blockIdx.y * chunk_rows;
+  const int nrows = min(chunk_rows, min(QT, lq - qt * QT) * G - row0);  // 1 .. 8 of either map
+  if (nrows <= 0) return;
   const int per_row = kDFixWarps / nrows;                 // warps to a row
-  const int r = warp / per_row, group = warp - r * per_row;
-  const bool live = r < nrows;
+  const int rl = warp / per_row, group = warp - rl * per_row;
+  const int r = row0 + rl;
+  const bool live = rl < nrows;
   MapSum x[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -655,7 +704,7 @@ bool make_pair_map(CUtensorMap* map, const void* pool, int64_t rows) {
 }
 
 struct DiffGeometry {
-  int grid = 0, workers = 0, npairs_cap = 0, nstage = 0;
+  int grid = 0, workers = 0, npairs_cap = 0;
   size_t smem = 0, ws_desc = 0, ws_lse = 0, ws_o = 0, ws_bytes = 0;
 };
 
@@ -671,16 +720,11 @@ int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffG
   g->npairs_cap = (int)(cap < S ? S : cap);
   g->grid = dev.num_sms;
   g->workers = g->grid * kDWarps;
-  const size_t plan =
-      sizeof(int) * ((size_t)g->npairs_cap + 1 + 3 * (size_t)S + 2 + (size_t)g->workers + 1) +
-      sizeof(float) * ((size_t)sh->num_q_heads / 2 + kDiffDim);
-  // as many stages as leave room for the plan, two at least
-  for (g->nstage = kDMaxStages; g->nstage >= 2; --g->nstage) {
-    g->smem = 1024 + (size_t)kDWarps * g->nstage * kDStage + kDWarps * kDMaxStages * 8 + plan;
-    if (g->smem <= (size_t)dev.max_smem_optin) break;
-  }
-  if (g->nstage < 2) return PA_ERR_UNSUPPORTED;
-  if (!raise_smem_limit(reinterpret_cast<const void*>(paged_diff_kernel))) return PA_ERR_CUDA;
+  const size_t plan = sizeof(int) * ((size_t)g->npairs_cap + 1 + 3 * (size_t)S + 2);
+  g->smem = 1024 + (size_t)kDWarps * kDStages * kDStage + kDWarps * kDStages * 8 + plan;
+  if (g->smem + kDiffDim * 4 > (size_t)dev.max_smem_optin) return PA_ERR_UNSUPPORTED;
+  if (!raise_smem_limit(reinterpret_cast<const void*>(paged_diff_kernel), kDiffDim * 4))
+    return PA_ERR_CUDA;
   g->ws_desc = round_up(sizeof(int) * kDDesc * (size_t)g->workers, 256);
   g->ws_lse = round_up(sizeof(float) * 2 * kDRows * (size_t)g->workers, 256);
   g->ws_o = round_up(sizeof(float) * 2 * kDRows * kDiffDim * (size_t)g->workers, 256);
@@ -817,8 +861,6 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
   a.causal = causal;
   a.npairs_cap = g.npairs_cap;
   a.num_workers = g.workers;
-  a.nstage = g.nstage;
-  a.cost4 = getenv("PA_COST") ? atoi(getenv("PA_COST")) : 4;
   a.max_lq = p.tc.enabled ? p.tc.min_lq - 1 : 0x7fffffff;
   char* wws = ws + p.tc.ws_bytes;
   a.desc = reinterpret_cast<int*>(wws);
@@ -827,9 +869,17 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
   if (launch_dependent(paged_diff_kernel, dim3(g.grid), dim3(kDWarps * 32), g.smem, st, tmk, tmv,
                        a) != cudaSuccess)
     return PA_ERR_CUDA;
-  if (launch_dependent(diff_fixup_kernel, dim3(g.workers), dim3(kDFixWarps * 32), 0, st,
-                       (const int*)a.desc, (const float*)a.part_o, (const float*)a.part_lse, a.o,
-                       g.workers, a.Hq, a.G, a.QT) != cudaSuccess)
+  // more than eight pieces to a segment on average: a CTA for each of its rows
+  const bool many = (int64_t)g.workers > 8 * (int64_t)a.S * (a.Hkv / 2);
+  const int64_t tile_rows = (int64_t)(max_q_len < a.QT ? max_q_len : a.QT) * a.G;
+  const int chunk = many ? 1 : kMapRows;
+  // (a worker has two tiles at least: of a small call only the first ones work)
+  const int64_t most = (int64_t)g.npairs_cap * (a.Hkv / 2) * a.max_blocks / 2;
+  const unsigned boundaries = (unsigned)(most < 1 ? 1 : most < g.workers ? most : g.workers);
+  if (launch_dependent(diff_fixup_kernel, dim3(boundaries, many ? (unsigned)tile_rows : 1u),
+                       dim3(kDFixWarps * 32), 0, st, (const int*)a.desc, (const float*)a.part_o,
+                       (const float*)a.part_lse, a.o, g.workers, chunk, a.Hq, a.G,
+                       a.QT) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;
 }

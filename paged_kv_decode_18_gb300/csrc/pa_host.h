@@ -47,9 +47,10 @@ inline bool current_device_info(DeviceInfo* out) {
   return true;
 }
 
-// A kernel's dynamic shared-memory limit is raised to the device maximum once
-// per (kernel, device); the launches pass their actual size.
-inline bool raise_smem_limit(const void* fn) {
+// A kernel's dynamic shared-memory limit is raised to the device maximum (less
+// what it declares itself) once per (kernel, device); the launches pass their
+// actual size.
+inline bool raise_smem_limit(const void* fn, int declared = 0) {
   DeviceInfo dev;
   if (!current_device_info(&dev)) return false;
   static std::mutex mu;
@@ -57,7 +58,7 @@ inline bool raise_smem_limit(const void* fn) {
   std::lock_guard<std::mutex> lock(mu);
   if (done.count({fn, dev.device})) return true;
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           dev.max_smem_optin) != cudaSuccess)
+                           dev.max_smem_optin - declared) != cudaSuccess)
     return false;
   done.insert({fn, dev.device});
   return true;

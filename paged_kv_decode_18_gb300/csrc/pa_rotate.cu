@@ -10,9 +10,8 @@
 // position * theta_i. theta_i comes as a fraction of a turn in steps of 2^-64
 // (pa_rotation), so position * theta_i modulo one turn is one 64-bit integer
 // product: exact for any position, where an fp32 product would be off by
-// 2^-24 of an angle of many turns. Its upper 32 bits, as a signed half-open
-// turn, go to the fast sine and cosine, whose error on one period (2^-20.9) is
-// far below the 2^-9 of the bf16 result.
+// 2^-24 of an angle of many turns. Its upper 23 bits go to the fast sine and cosine,
+// which are off by 2^-19.7 then, far below the 2^-9 of the bf16 result.
 //
 // Everything here is bound by HBM, or by the launch where there are few rows:
 // 16 FMA and 8 sines and cosines per 64 bytes moved. Eight lanes hold a row, 16
@@ -94,9 +93,12 @@ struct Spin {
         if (d < h) sg = -sign;
       }
       const unsigned long long phase = rot.turns[pair] * (unsigned long long)(long long)pos;
-      const int hi = (int)(phase >> 32);  // in 2^-32 turns, -half .. half a turn
+      // the phase's upper 23 bits as the fraction of a number in [1, 2), half a turn on, so
+      // that 1.5 stands for 0: an integer conversion would take a third turn on the unit
+      // that sine and cosine share
+      const uint32_t hi = ((uint32_t)(phase >> 32) + 0x80000100u) >> 9;
       float sn, cs;
-      __sincosf((float)hi * (3.14159265358979f / 2147483648.f), &sn, &cs);
+      __sincosf((__uint_as_float(0x3f800000u | hi) - 1.5f) * 6.28318530717959f, &sn, &cs);
       c[j] = cs * magnitude;
       s[j] = sn * (magnitude * sg);
     }
@@ -216,9 +218,14 @@ struct RowsArgs {
   pa_rotation rot;
 };
 
-// A warp turns 4 * ITER rows of one token, four at a time, all loads first.
-template <int MODE, int FMT, int ITER>
-__global__ void __launch_bounds__(kRotWarps * 32)
+// A warp turns 16 rows of one token, four at a time, all loads first, with one set of
+// sines and cosines. (Four rows a warp: 51 us for 12,000 tokens of 16 + 8 + 8 rows; eight:
+// 36; sixteen: 33; 24: 44, too few warps left. At a decode step's 256 tokens all take the
+// 4 us of a launch.)
+constexpr int kIter = 4;
+
+template <int MODE, int FMT>
+__global__ void __launch_bounds__(kRotWarps * 32, 3)
     rotate_rows_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ float exchange[MODE == kAny ? kRotWarps * 4 * kRowPad : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -230,11 +237,11 @@ __global__ void __launch_bounds__(kRotWarps * 32)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (w >= a.num_warps) return;
   const int t = w / a.warps_per_token;
-  const int r0 = (w - t * a.warps_per_token) * 4 * ITER;
+  const int r0 = (w - t * a.warps_per_token) * 4 * kIter;
   const int total = a.Hq + 2 * a.Hkv;
-  uint4 xa[ITER], xb[ITER];
+  uint4 xa[kIter], xb[kIter];
 #pragma unroll
-  for (int i = 0; i < ITER; ++i) {
+  for (int i = 0; i < kIter; ++i) {
     const int r = r0 + i * 4 + sub;
     xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
     if (r < total) {
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(kRotWarps * 32)
     }
   }
   int64_t slot = -1;
-  if (a.Hkv > 0 && r0 + 4 * ITER > a.Hq) {
+  if (a.Hkv > 0 && r0 + 4 * kIter > a.Hq) {
     slot = a.slots[t];
     if (slot >= a.num_slots) {
       // one row of the token tells
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(kRotWarps * 32)
   Spin<MODE> sp;
   if (r0 < a.Hq + a.Hkv) sp.set(a.rot, me, a.positions[t], a.rot.magnitude, a.sign);
 #pragma unroll
-  for (int i = 0; i < ITER; ++i) {
+  for (int i = 0; i < kIter; ++i) {
     if (r0 + i * 4 >= total) break;  // the same for the whole warp
     const int r = r0 + i * 4 + sub;
     const bool turned = r < a.Hq + a.Hkv;
@@ -327,11 +334,16 @@ struct CachedArgs {
   pa_rotation rot;
 };
 
-// One warp turns a (block, KV head) tile of 16 keys, four at a time; the
-// batch's tiles are cut into equal ranges, one per warp (tiles of a sequence
-// and head in order, so that a warp's positions follow one another).
+// One warp turns a (block, KV head) tile of 16 keys, four at a time, the loads of
+// eight ahead; the batch's tiles are cut into equal ranges, one per warp (tiles of a
+// sequence and head in order, so that a warp's positions follow one another).
+// Sines and cosines are made anew only where a row's turn differs from the last.
+// Measured: 8 x 24,000..28,700 keys of 8 heads by a shift 144 us (6.0 TB/s); 32 x 1024
+// behind an eviction 29 us, of which some 7 us is the chain launch, lengths, block
+// ids and turns, first rows. (Loads of the next eight keys held ahead of the present
+// ones: 33 us, for the registers that it takes.)
 template <int MODE, int FMT>
-__global__ void __launch_bounds__(kRotWarps * 32)
+__global__ void __launch_bounds__(kRotWarps * 32, 3)
     rotate_cached_kernel(const __grid_constant__ CachedArgs a) {
   extern __shared__ __align__(16) int area[];  // kAny: the exchange, then the plan
   float* exchange = reinterpret_cast<float*>(area);
@@ -392,30 +404,35 @@ __global__ void __launch_bounds__(kRotWarps * 32)
       const int64_t at = (int64_t)phys * a.Hkv + t.h;
       if constexpr (FMT == kFmtBf16) {
         uint16_t* tile = reinterpret_cast<uint16_t*>(a.kc) + at * (kBlock * kHeadDim);
-        uint4 xa[4], xb[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint16_t* row = tile + (i * 4 + sub) * kHeadDim;
-          if (by[i] != 0 && me.words) {
-            xa[i] = *reinterpret_cast<const uint4*>(row + me.a * 8);
-            xb[i] = *reinterpret_cast<const uint4*>(row + me.b * 8);
-          }
-        }
+        for (int i0 = 0; i0 < 4; i0 += 2) {
+          uint4 xa[2], xb[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (__any_sync(kFull, by[i] != spun && by[i] != 0)) {
-            sp.set(a.rot, me, by[i], 1.f, 1.f);
-            spun = by[i];
+          for (int u = 0; u < 2; ++u) {
+            const uint16_t* row = tile + ((i0 + u) * 4 + sub) * kHeadDim;
+            xa[u] = xb[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (by[i0 + u] != 0 && me.words) {
+              xa[u] = *reinterpret_cast<const uint4*>(row + me.a * 8);
+              xb[u] = *reinterpret_cast<const uint4*>(row + me.b * 8);
+            }
           }
-          float f[16];
-          const bool mine = by[i] != 0 && me.words;
-          if (mine) unpack16(xa[i], xb[i], f);
-          if (MODE == kAny || mine) turn<MODE>(f, sp, me, a.rot.rot_dim, rows, sub);
-          if (mine) {
-            repack16(f, me.words, xa[i], xb[i]);
-            uint16_t* row = tile + (i * 4 + sub) * kHeadDim;
-            *reinterpret_cast<uint4*>(row + me.a * 8) = xa[i];
-            *reinterpret_cast<uint4*>(row + me.b * 8) = xb[i];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int turned = by[i0 + u];
+            if (__any_sync(kFull, turned != spun && turned != 0)) {
+              sp.set(a.rot, me, turned, 1.f, 1.f);
+              spun = turned;
+            }
+            float f[16];
+            const bool mine = turned != 0 && me.words;
+            unpack16(xa[u], xb[u], f);
+            if (MODE == kAny || mine) turn<MODE>(f, sp, me, a.rot.rot_dim, rows, sub);
+            if (mine) {
+              repack16(f, me.words, xa[u], xb[u]);
+              uint16_t* row = tile + ((i0 + u) * 4 + sub) * kHeadDim;
+              *reinterpret_cast<uint4*>(row + me.a * 8) = xa[u];
+              *reinterpret_cast<uint4*>(row + me.b * 8) = xb[u];
+            }
           }
         }
       } else {
@@ -496,19 +513,16 @@ int mode_of(const pa_rotation* r) {
   return r->interleaved ? kSide : (r->rot_dim % 16 == 0 ? kHalf : kAny);
 }
 
-// Rows of a token per warp: 4 while that leaves the GPU short of warps, else 8
-// (both measured; see the table at launch_rows).
-template <int FMT, int ITER>
+template <int FMT>
 cudaError_t launch_rows_of(int mode, unsigned blocks, cudaStream_t st, const RowsArgs& a) {
   const dim3 grid(blocks), block(kRotWarps * 32);
-  if (mode == kHalf) return launch_dependent(rotate_rows_kernel<kHalf, FMT, ITER>, grid, block, 0, st, a);
-  if (mode == kSide) return launch_dependent(rotate_rows_kernel<kSide, FMT, ITER>, grid, block, 0, st, a);
-  return launch_dependent(rotate_rows_kernel<kAny, FMT, ITER>, grid, block, 0, st, a);
+  if (mode == kHalf) return launch_dependent(rotate_rows_kernel<kHalf, FMT>, grid, block, 0, st, a);
+  if (mode == kSide) return launch_dependent(rotate_rows_kernel<kSide, FMT>, grid, block, 0, st, a);
+  return launch_dependent(rotate_rows_kernel<kAny, FMT>, grid, block, 0, st, a);
 }
 
 int launch_rows(RowsArgs a, int64_t tokens, int fmt, const pa_rotation* rot, int transpose,
                 cudaStream_t st) {
-  constexpr int kIter = 2;
   const int64_t total = (int64_t)a.Hq + 2 * (int64_t)a.Hkv;
   if (total > (1 << 24)) return PA_ERR_UNSUPPORTED;
   const int64_t per = (total + 4 * kIter - 1) / (4 * kIter);
@@ -523,11 +537,11 @@ int launch_rows(RowsArgs a, int64_t tokens, int fmt, const pa_rotation* rot, int
   const int mode = mode_of(rot);
   cudaError_t e;
   if (fmt == kFmtBf16)
-    e = launch_rows_of<kFmtBf16, kIter>(mode, blocks, st, a);
+    e = launch_rows_of<kFmtBf16>(mode, blocks, st, a);
   else if (fmt == kFmtInt8)
-    e = launch_rows_of<kFmtInt8, kIter>(mode, blocks, st, a);
+    e = launch_rows_of<kFmtInt8>(mode, blocks, st, a);
   else
-    e = launch_rows_of<kFmtFp8, kIter>(mode, blocks, st, a);
+    e = launch_rows_of<kFmtFp8>(mode, blocks, st, a);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

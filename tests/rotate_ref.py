@@ -7,11 +7,10 @@ import torch
 
 BLOCK, DIM = 16, 128
 UBF = 2.0 ** -8    # half a step of bf16 (finfo.eps / 2)
-# Cosine and sine: the angle's upper 32 bits become an fp32 number of radians
-# below pi in three roundings (the integer's, the constant's, the product's: 3 pi
-# 2^-24 = 2^-20.8), cut off at 2^-32 turns (2^-29.3); the fast functions add
-# 2^-21.1. Together below 2^-19.9.
-UCS = 2.0 ** -19.9
+# Cosine and sine: the phase is rounded to 2^-23 turns (2 pi 2^-24 = 3.7e-7 radians),
+# and turned into radians below pi by an fp32 constant and one product (2 pi 2^-24 =
+# 3.7e-7 together); the fast functions add 2^-21.1 = 4.5e-7. Together 1.2e-6 = 2^-19.7.
+UCS = 2.0 ** -19.7
 
 
 def theta(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len=0.0, low=1.0, high=4.0):
