@@ -21,12 +21,15 @@
 // difference, norm and scale happen when the second map is done; segments that
 // ranges cut leave both maps' partials for diff_tc_fixup_kernel.
 //
-// Roles in each CTA (12 warps): warp 0 loads query tiles and K, warp 10 V; in the
-// leading CTA warp 1 issues S and warp 11 O; warps 2-9 are the softmax, two
-// threads to a query row, one per 64-key half. O has the whole 256 columns that
-// S/P leave of tensor memory, one accumulator for both halves, so the halves
-// agree on the row's reference: they exchange their maxima every tile. The
-// reference moves only when a maximum grows by more than 2^32 (exact either way).
+// Roles in each CTA (20 warps): warp 0 loads query tiles and K, warp 18 V; in the
+// leading CTA warp 1 issues S and warp 19 O; warps 2-17 are the softmax, four
+// threads to a query row, 32 keys each. Tensor memory holds O (256 columns), one S and
+// two P: a tile's scores go to registers at once, so the next S is computed beside
+// the exponentials of this one and the product of the last. (S and P in one buffer,
+// two of those: the next S but one waited for the product, 2400 clocks a tile.) O is
+// one accumulator for all keys, so a row's threads agree on its reference: they
+// exchange their maxima every tile. The reference moves only when a maximum grows by
+// more than 2^32 (exact either way).
 #include <cudaTypedefs.h>
 
 #include "pa_diff.cuh"
@@ -44,13 +47,20 @@ constexpr int kKBytes = kBlocksT / 2 * kTileBytes;  // this CTA's half of the ke
 constexpr int kVBytes = kBlocksT * kTileBytes;      // this CTA's value head: 32 KB
 constexpr int kStageT = kKBytes + kVBytes;
 constexpr int kMaxStagesT = 3;
-constexpr int kSoftmaxWarps = 8;              // warps 2-9
+constexpr int kParts = 4;                     // softmax threads to a query row
+constexpr int kPartKeys = kKeysT / kParts;    // keys of a tile that each has
+constexpr int kPartDims = kDiffDim / kParts;  // output dims
+constexpr int kSoftmaxWarps = 4 * kParts;     // warps 2-17
 constexpr int kVWarp = 2 + kSoftmaxWarps;
 constexpr int kPvWarp = kVWarp + 1;
 constexpr int kThreadsT = 128 + kSoftmaxWarps * 32;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;               // S/P buffers at columns 0 and 128, O at 256 .. 511
-constexpr int kSegCost4 = 6;                  // a segment start in quarters of a key tile
+constexpr uint32_t kColP = 128;               // S at columns 0 .. 127, two P buffers of 64,
+constexpr uint32_t kColO = 256;               // O at 256 .. 511
+// a segment start in quarters of a key tile: what two maps' last tiles and write-outs
+// take on top of the others (6: 139 us for four chunks over 2816 .. 7424 keys, 24: 135,
+// 40: 140)
+constexpr int kSegCost4 = 24;
 constexpr int kTDesc = 8;
 // The reference of a row's exponentials moves only when its maximum has grown by more
 // than this power of two: weights up to 2^32 are as exact in bf16 and fp32 as those below
@@ -66,12 +76,13 @@ enum : int {
   B_KEMPTY = 7,                       // [3], both
   B_VFULL = 10,                       // [3], each CTA its own values
   B_VEMPTY = 13,                      // [3], both
-  B_SFULL = 16,                       // [2], both
-  B_SFREE = 18,                       // [2], both: the product that read this buffer's P is done
+  B_SFULL = 16,                       // both
+  B_SEMPTY = 17,                      // leader: all softmax warps of both hold their scores
+  B_PFREE = 18,                       // [2], both: the product that read this P is done
   // [2], leader: all softmax warps of both. Two, since a warp may be through with the
   // next tile's exponentials before another has arrived for this one
   B_PFULL = 20,
-  B_XCH = 22,                         // [4]: the two warps of 32 rows, every exchange a phase
+  B_XCH = 22,                         // [4]: the four warps of 32 rows, every exchange a phase
   kNumBarsT = 26
 };
 
@@ -80,8 +91,9 @@ constexpr int kOffBars = 0;
 constexpr int kOffSlot = kNumBarsT * 8;
 constexpr int kOffAbort = kOffSlot + 4;
 constexpr int kOffBad = kOffAbort + 4;
-constexpr int kOffXch = 256;                       // [2][2 halves][128] floats
-constexpr int kOffPlanT = kOffXch + 2 * 2 * kRowsT * 4;
+constexpr int kOffXch = 256;                       // [2][kParts][128] floats
+constexpr int kOffPend = kOffXch + 2 * kParts * kRowsT * 4;  // [softmax warps] Pending
+constexpr int kOffPlanT = kOffPend + kSoftmaxWarps * 32;
 static_assert(kOffBad + 4 <= kOffXch, "barrier area");
 
 struct DiffTcArgs {
@@ -99,10 +111,17 @@ struct DiffTcArgs {
   int num_workers;
   int min_lq;
   int nstage;
-  float* part_o;    // [workers * 2 pieces][2 maps][256 rows][256]
+  // [workers * 2 pieces][2 maps][64 groups of 4 dims][256 rows][4]: neighbouring
+  // threads hold neighbouring rows
+  float* part_o;
   float* part_lse;  // [workers * 2 pieces][2 maps][256 rows]
   int* desc;        // [workers][kTDesc]
 };
+
+__device__ __forceinline__ float4* part_rows(const DiffTcArgs& a, int slot, int map) {
+  return reinterpret_cast<float4*>(a.part_o) +
+         ((size_t)slot * 2 + map) * (kDiffDim / 4) * (2 * kRowsT);
+}
 
 // ---------------------------------------------------------------------------
 // pair-of-CTAs wrappers
@@ -131,6 +150,19 @@ __device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
 }
 __device__ __forceinline__ void fence_cluster() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+// mbar_try_wait that may sleep for up to 20 us: a warp that spins takes issue slots from
+// the softmax warps of its sub-partition
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
 }
 // tiled copies whose completion counts on a barrier of either CTA of the pair
 __device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
@@ -202,7 +234,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kNumBarsT; ++i)
-      mbar_init(bar(i), i >= B_XCH ? 2 : i == B_PFULL || i == B_PFULL + 1 ? 2 * kSoftmaxWarps : 1);
+      mbar_init(bar(i), i >= B_XCH ? kParts
+                        : i == B_PFULL || i == B_PFULL + 1 ? 2 * kSoftmaxWarps
+                        : i == B_SEMPTY                  ? 2 * 4
+                                                         : 1);
     *abort_flag = 0;
     *bad_v = 0;
     mbar_fence_init();
@@ -246,19 +281,17 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   const int w = blockIdx.x >> 1;  // the worker: a cluster
   const bool work = P.total > 0 && w < cut.nw;
   if (tid == 32 * kPvWarp && rank == 0) {
-    int* d = a.desc + (size_t)w * kTDesc;
     MergeJob j;
     j.valid = false;
     if (work) j = merge_job_of(P, S, Hp, w, cut.nw, cut);
-    d[0] = j.valid ? j.s : -1;
+    int4 d0 = make_int4(-1, 0, 0, 0), d1 = d0;
     if (j.valid) {
-      d[1] = j.qt;
-      d[2] = j.h;
-      d[3] = j.last;
-      d[4] = j.slot_prev;
-      d[5] = P.qstart[j.s];
-      d[6] = P.qstart[j.s + 1] - P.qstart[j.s];
+      d0 = make_int4(j.s, j.qt, j.h, j.last);
+      d1 = make_int4(j.slot_prev, P.qstart[j.s], P.qstart[j.s + 1] - P.qstart[j.s], 0);
     }
+    int4* d = reinterpret_cast<int4*>(a.desc + (size_t)w * kTDesc);
+    d[0] = d0;
+    d[1] = d1;
   }
   if (!work) return;  // both CTAs of the cluster
   const int R0 = cut.start(w), R1 = cut.start(w + 1);
@@ -278,10 +311,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   const uint32_t tmem = *tmem_slot;
 
   auto wait = [&](int b, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar(b), parity)) return true;
+    if (try_wait_long(bar(b), parity)) return true;
     const unsigned long long t0 = global_timer_ns();
     while (!*abort_flag) {
-      if (mbar_try_wait(bar(b), parity)) return true;
+      if (try_wait_long(bar(b), parity)) return true;
       if (global_timer_ns() - t0 > kWaitLimitNs) {
         flag_error(PA_DEVERR_PIPE_TIMEOUT);
         *abort_flag = 1;
@@ -402,19 +435,19 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           if (!wait(B_QFULL + qs, (uint32_t)(qn >> 1) & 1u)) break;
           ++qn;
         }
-        const int sb = i & 1;
         if (!wait(B_KFULL + st, use & 1u)) break;
-        // the S/P buffer is free once the product that read P of tile i-2 is done
-        if (i >= 2 && !wait(B_SFREE + sb, (uint32_t)((i >> 1) - 1) & 1u)) break;
+        // the softmax holds the scores of the last tile in registers
+        if (i >= 1 && !wait(B_SEMPTY, (uint32_t)(i - 1) & 1u)) break;
+        // and the P buffer that it will fill next is free: S says so to every warp
+        if (i >= 2 && !wait(B_PFREE + (i & 1), (uint32_t)((i >> 1) - 1) & 1u)) break;
         tc_fence_after();
         const uint64_t dq = desc_q + (uint64_t)(qs * (kQBytes >> 4));
         const uint64_t dk = desc_k + (uint64_t)(st * (kStageT >> 4));
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          pair_mma(tmem + (uint32_t)sb * 128u,
-                   dq + (uint64_t)(((k >> 2) * kHalfT + (k & 3) * 32) >> 4),
+          pair_mma(tmem, dq + (uint64_t)(((k >> 2) * kHalfT + (k & 3) * 32) >> 4),
                    dk + (uint64_t)(((k >> 2) * 1024 + (k & 3) * 32) >> 4), idS, k > 0);
-        pair_commit(bar(B_SFULL + sb));
+        pair_commit(bar(B_SFULL));
         pair_commit(bar(B_KEMPTY + st));
         if (++st == nstage) {
           st = 0;
@@ -441,10 +474,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const uint64_t dv = desc_v + (uint64_t)(st * (kStageT >> 4));
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          pair_mma_ts(tmem + kColO, tmem + sb * 128u + (uint32_t)((k >> 2) * 64 + (k & 3) * 8),
-                      dv + (uint64_t)(k * (kTileBytes >> 4)), idPV, (k > 0 || !first) ? 1u : 0u);
+          pair_mma_ts(tmem + kColO, tmem + kColP + sb * 64u + (uint32_t)k * 8u, dv + (uint64_t)(k * (kTileBytes >> 4)), idPV, (k > 0 || !first) ? 1u : 0u);
         pair_commit(bar(B_VEMPTY + st));
-        pair_commit(bar(B_SFREE + (int)sb));
+        pair_commit(bar(B_PFREE + (int)sb));
         if (++st == nstage) st = 0;
         if (idx + 1 < R1) advance(P, S, Hp, t);
       }
@@ -453,155 +485,175 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   } else {
     // ------------------------------------------------------------------ softmax
     const int q4 = warp & 3;
-    const int hf = (warp - 2) >> 2;
+    const int part = (warp - 2) >> 2;  // which keys of a tile and which output dims
     const int r = q4 * 32 + lane;  // this thread's query row (= TMEM lane)
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
-    const uint32_t tO = tmem + lane_base + kColO + (uint32_t)hf * 128u;  // its 128 output dims
-    const uint32_t lead_p = in_cta(bar(B_PFULL), 0);
+    const uint32_t tO = tmem + lane_base + kColO + (uint32_t)(part * kPartDims);  // its output dims
+    // arrives on a barrier of the leading CTA
+    auto arrive = [&](int b) {
+      if (rank == 0)
+        mbar_arrive(bar(b));
+      else
+        arrive_in_cluster(in_cta(bar(b), 0));
+    };
     const float sc = a.scale_log2;
     uint32_t xphase = 0;
-    // Gives `mine` to the thread of the row's other half and takes its value.
-    auto exchange = [&](float mine, float& other) -> bool {
-      float* x = xch + (xphase & 1u) * (2 * kRowsT);
-      x[hf * kRowsT + r] = mine;
+    // Gives `mine` to the other threads of the row; all take the four values.
+    auto exchange = [&](float mine, float (&all)[kParts]) -> bool {
+      float* x = xch + (xphase & 1u) * (kParts * kRowsT) + r;
+      x[part * kRowsT] = mine;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_XCH + q4));
       if (!wait_all(B_XCH + q4, xphase & 1u)) return false;
       ++xphase;
-      other = x[(hf ^ 1) * kRowsT + r];
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) all[k] = x[k * kRowsT];
       return true;
     };
     TilePos t = locate(P, S, Hp, R0);
     float m_ref = neg_inf(), l = 0.f;
-    int lim = 0, c = 0, lq = 0, tok = 0, piece_b0 = 0, st = 0;
-    uint32_t use = 0;
-    bool valid = false, piece_first = true;
+    int lim = 0, c = 0, vsafe = 0, piece_b0 = 0;
+    bool piece_first = true;
     // A finished map's O stays in tensor memory until the next tile's exponentials are
     // done (its last product completes meanwhile); then it is written out.
+    // What it takes is the same for a warp's rows and kept in shared memory: registers
+    // that do not spill are what this loop is short of (beside 218 KB of shared memory a
+    // spilled word comes back from L2).
     struct Pending {
-      bool on, valid, whole, last_of_piece;
-      int s, h, map, b0, b1, n;  // the piece's tiles b0 .. b1 of a segment of 2n
-      int64_t qtok;
-      int k0, k1, vis;           // its keys, and the row's limit
-      size_t slot;
-      float m, l;
-    } pend;
-    pend.on = false;
+      int flags, s, h, k1;   // 1: whole, 2: last tile of the piece; where its keys end
+      int map, b0, n, slot;  // b0: the piece's first tile, of a segment of 2n
+    };
+    static_assert(sizeof(Pending) == 32, "kOffPend");
+    Pending* pending = reinterpret_cast<Pending*>(rest + kOffPend) + (warp - 2);
+    bool pend_on = false;
+    int pend_tok = -1;  // the row's token (-1: padding)
+    float pend_m = 0.f, pend_l = 0.f;
     auto flush = [&]() -> bool {
-      float l_o = 0.f;
-      if (!exchange(pend.l, l_o)) return false;
-      const float lt = hf == 0 ? pend.l + l_o : l_o + pend.l;
+      const Pending pend = *pending;
+      const bool pend_valid = pend_tok >= 0;
+      float ls[kParts];
+      if (!exchange(pend_l, ls)) return false;
+      float lt = ls[0];
+#pragma unroll
+      for (int k = 1; k < kParts; ++k) lt += ls[k];
       // (a NaN score's NaN goes on into the row's results)
       const float inv = lt != 0.f ? 1.f / lt : 0.f;
-      const float lse_v = lt != 0.f ? (pend.m + lg2(lt)) * kLn2 : neg_inf();
+      const float lse_v = lt != 0.f ? (pend_m + lg2(lt)) * kLn2 : neg_inf();
       const int head = pend.h * G + r % G;
-      const bool merge = pend.whole && pend.map == 1;  // both maps are here: the row's output
-      const float lam = merge && pend.valid ? a.o.lambdas[head] : 0.f;
+      const bool merge = (pend.flags & 1) && pend.map == 1;  // both maps are here: the row's output
+      const int64_t qtok = (int64_t)P.qstart[pend.s] + pend_tok;
+      const float lam = merge && pend_valid ? a.o.lambdas[head] : 0.f;
       const int row = rank * kRowsT + r;
-      float* part = a.part_o + ((pend.slot * 2 + pend.map) * (2 * kRowsT) + row) * kDiffDim + hf * 128;
-      const float* first_map = a.part_o + ((pend.slot * 2) * (2 * kRowsT) + row) * kDiffDim + hf * 128;
+      float4* mine = part_rows(a, pend.slot, pend.map) + part * (kPartDims / 4) * (2 * kRowsT) + row;
+      const float4* first_map =
+          part_rows(a, pend.slot, 0) + part * (kPartDims / 4) * (2 * kRowsT) + row;
+      float4 x[4];  // the first map's values
       float squares = 0.f;
-      // twice over a row's dims where it is normed: sum of squares, then the output
-      const int passes = merge && a.o.weight ? 2 : 1;
-      float factor = a.o.gain;
-      for (int pass = 0; pass < passes; ++pass) {
-        const bool out = merge && pass == passes - 1;
-        if (pass == 1) {
-          float sq_o = 0.f;
-          if (!exchange(squares, sq_o)) return false;
-          factor = diff_factor(a.o, hf == 0 ? squares + sq_o : sq_o + squares);
+#pragma unroll 1
+      for (int cc = 0; cc < kPartDims / 16; ++cc) {
+        float z[16];
+        if (merge && pend_valid) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x[q] = first_map[(cc * 4 + q) * (2 * kRowsT)];
+        }
+        __syncwarp();
+        tmem_ld16(tO + (uint32_t)cc * 16u, z);
+        if (*bad_v && pend_valid) {
+          // infinities and NaNs of window rows entered the product as zeros (they must
+          // not reach queries that do not see their row): they join the rows that see
+          // them here
+          const int lqp = P.qstart[pend.s + 1] - P.qstart[pend.s];
+          const int p0 = P.ctx[pend.s] - lqp;
+          const int k0 =
+              pend.b0 < pend.n && pend.map == 1 ? 0 : (pend.b0 - pend.map * pend.n) * kKeysT;
+          const int k1 = min(p0 + pend_tok + 1, pend.k1);  // (a causal window)
+          for (int k = max(p0 + 1, k0); k < k1; ++k) {
+            const int phys = a.block_tables[(size_t)pend.s * a.max_blocks + k / kBlock];
+            if (phys < 0 || (int64_t)phys >= a.num_blocks) continue;
+            const int dim = part * kPartDims + cc * 16;
+            const uint32_t* vr = reinterpret_cast<const uint32_t*>(
+                a.v_cache + ((((int64_t)phys * Hkv + 2 * pend.h + dim / kHeadDim) * kBlock) +
+                             k % kBlock) * kHeadDim + dim % kHeadDim);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t wv = vr[j], fin = bf2_finite_part(wv);
+              if ((wv ^ fin) & 0x7f80u) z[2 * j] += bf_lo(wv);
+              if ((wv ^ fin) & 0x7f800000u) z[2 * j + 1] += bf_hi(wv);
+            }
+          }
+        }
+        if (!merge) {
+          if (pend_valid) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mine[(cc * 4 + q) * (2 * kRowsT)] = make_float4(__fmul_rn(z[4 * q], inv), __fmul_rn(z[4 * q + 1], inv),
+                                   __fmul_rn(z[4 * q + 2], inv), __fmul_rn(z[4 * q + 3], inv));
+          }
+          continue;
+        }
+        uint32_t d[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 f = x[q];
+          const float fs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = diff_value(fs[e], 1.f, z[4 * q + e], inv, lam);
+            squares = fmaf(v, v, squares);
+            d[4 * q + e] = __float_as_uint(v);
+          }
+        }
+        // the difference waits in tensor memory for its norm
+        __syncwarp();
+        tmem_st16(tO + (uint32_t)cc * 16u, d);
+      }
+      if (merge) {
+        tmem_wait_st();
+        float factor = a.o.gain;
+        if (a.o.weight) {
+          float sq[kParts];
+          if (!exchange(squares, sq)) return false;
+          float sum = sq[0];
+#pragma unroll
+          for (int k = 1; k < kParts; ++k) sum += sq[k];
+          factor = diff_factor(a.o, sum);
         }
 #pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t u[32];
+        for (int cc = 0; cc < kPartDims / 16; ++cc) {
+          float v[16];
           __syncwarp();
-          tmem_ld32(tO + (uint32_t)cc * 32u, u);
-          float y[32];
+          tmem_ld16(tO + (uint32_t)cc * 16u, v);
+          if (!pend_valid) continue;
+          const float4* wt = reinterpret_cast<const float4*>(a.o.weight + part * kPartDims + cc * 16);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(u[j]);
-          if (*bad_v && pend.valid) {
-            // infinities and NaNs of window rows entered the product as zeros (they must
-            // not reach queries that do not see their row): they join the rows that see
-            // them here
-            const int lqp = P.qstart[pend.s + 1] - P.qstart[pend.s];
-            const int p0 = P.ctx[pend.s] - lqp;
-            const int k1 = min(pend.vis, pend.k1);
-            for (int k = max(p0 + 1, pend.k0); k < k1; ++k) {
-              const int phys = a.block_tables[(size_t)pend.s * a.max_blocks + k / kBlock];
-              if (phys < 0 || (int64_t)phys >= a.num_blocks) continue;
-              const uint32_t* vr = reinterpret_cast<const uint32_t*>(
-                  a.v_cache + ((((int64_t)phys * Hkv + 2 * pend.h + hf) * kBlock) + k % kBlock) *
-                                  kHeadDim + cc * 32);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const uint32_t wv = vr[j], fin = bf2_finite_part(wv);
-                if ((wv ^ fin) & 0x7f80u) y[2 * j] += bf_lo(wv);
-                if ((wv ^ fin) & 0x7f800000u) y[2 * j + 1] += bf_hi(wv);
-              }
-            }
-          }
-          if (!merge) {
-            if (pend.valid) {
-              float4* dst = reinterpret_cast<float4*>(part + cc * 32);
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                dst[q] = make_float4(__fmul_rn(y[4 * q], inv), __fmul_rn(y[4 * q + 1], inv),
-                                     __fmul_rn(y[4 * q + 2], inv), __fmul_rn(y[4 * q + 3], inv));
-            }
-            continue;
-          }
-          if (!pend.valid) continue;
-          const float4* src = reinterpret_cast<const float4*>(first_map + cc * 32);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 x = src[q];
-            y[4 * q] = diff_value(x.x, 1.f, y[4 * q], inv, lam);
-            y[4 * q + 1] = diff_value(x.y, 1.f, y[4 * q + 1], inv, lam);
-            y[4 * q + 2] = diff_value(x.z, 1.f, y[4 * q + 2], inv, lam);
-            y[4 * q + 3] = diff_value(x.w, 1.f, y[4 * q + 3], inv, lam);
-          }
-          if (!out) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) squares = fmaf(y[j], y[j], squares);
-            continue;
-          }
-          if (a.o.weight) {
-            const float4* wt = reinterpret_cast<const float4*>(a.o.weight + hf * 128 + cc * 32);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 x = wt[q];
-              y[4 * q] *= factor * x.x;
-              y[4 * q + 1] *= factor * x.y;
-              y[4 * q + 2] *= factor * x.z;
-              y[4 * q + 3] *= factor * x.w;
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] *= factor;
+          for (int q = 0; q < 4; ++q) {
+            const float4 w0 = a.o.weight ? wt[q] : make_float4(1.f, 1.f, 1.f, 1.f);
+            v[4 * q] *= factor * w0.x;
+            v[4 * q + 1] *= factor * w0.y;
+            v[4 * q + 2] *= factor * w0.z;
+            v[4 * q + 3] *= factor * w0.w;
           }
           uint4* dst = reinterpret_cast<uint4*>(
-              a.o.out + (pend.qtok * (a.Hq / 2) + head) * kDiffDim + hf * 128 + cc * 32);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            dst[q] = make_uint4(cvt_bf16x2(y[8 * q + 0], y[8 * q + 1]),
-                                cvt_bf16x2(y[8 * q + 2], y[8 * q + 3]),
-                                cvt_bf16x2(y[8 * q + 4], y[8 * q + 5]),
-                                cvt_bf16x2(y[8 * q + 6], y[8 * q + 7]));
+              a.o.out + (qtok * (a.Hq / 2) + head) * kDiffDim + part * kPartDims + cc * 16);
+          dst[0] = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                              cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
+          dst[1] = make_uint4(cvt_bf16x2(v[8], v[9]), cvt_bf16x2(v[10], v[11]),
+                              cvt_bf16x2(v[12], v[13]), cvt_bf16x2(v[14], v[15]));
         }
       }
-      if (hf == 0 && pend.valid) {
-        if (pend.whole) {
+      if (part == 0 && pend_valid) {
+        if (pend.flags & 1) {
           if (a.o.lse)
-            a.o.lse[pend.qtok * a.Hq + (int64_t)(2 * pend.h + pend.map) * G + r % G] = lse_v;
+            a.o.lse[qtok * a.Hq + (int64_t)(2 * pend.h + pend.map) * G + r % G] = lse_v;
         } else {
-          float* pl = a.part_lse + (pend.slot * 2) * (2 * kRowsT) + row;
+          float* pl = a.part_lse + (size_t)pend.slot * 2 * (2 * kRowsT) + row;
           pl[pend.map * (2 * kRowsT)] = lse_v;
           // a map that the piece has no tile of weighs nothing in the merge
-          if (pend.map == 0 && pend.last_of_piece) pl[2 * kRowsT] = neg_inf();
+          if (pend.map == 0 && (pend.flags & 2)) pl[2 * kRowsT] = neg_inf();
           if (pend.map == 1 && pend.b0 >= pend.n) pl[0] = neg_inf();
         }
       }
-      pend.on = false;
+      pend_on = false;
       return true;
     };
     int i = 0;
@@ -612,10 +664,11 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const bool last = piece_last || kt == n - 1;
       if (idx == R0 || t.b == 0) {
         c = P.ctx[t.s];
-        lq = P.qstart[t.s + 1] - P.qstart[t.s];
-        tok = (t.qt * 2 + rank) * QTb + r / G;
-        valid = tok < lq && r < QTb * G;
-        lim = valid ? (a.causal ? c - lq + tok + 1 : c) : 0;
+        const int lq = P.qstart[t.s + 1] - P.qstart[t.s];
+        const int tok = (t.qt * 2 + rank) * QTb + r / G;
+        // keys that the row sees (padding: none; a query sees one at least)
+        lim = tok < lq && r < QTb * G ? (a.causal ? c - lq + tok + 1 : c) : 0;
+        vsafe = a.causal ? c - lq + 1 : c;  // keys before it are seen by every query
         piece_b0 = t.b;
         piece_first = idx == R0;
       }
@@ -623,46 +676,57 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         m_ref = neg_inf();
         l = 0.f;
       }
-      const int sb = i & 1;
-      if (!wait_all(B_SFULL + sb, (uint32_t)(i >> 1) & 1u)) break;
+      const uint32_t sb = (uint32_t)(i & 1);
+      if (!wait_all(B_SFULL, sb)) break;
       tc_fence_after();
-      uint32_t v0[32], v1[32];
-      const uint32_t tS = tmem + lane_base + (uint32_t)sb * 128u + (uint32_t)hf * 64u;
-      tmem_ld32_async(tS, v0);
-      tmem_ld32_async(tS + 32u, v1);
-      tmem_wait_ld(v0);
-      tmem_tie(v1);
-      // scores in log2 units
-      float2 x[32];
+      float2 x[kPartKeys / 2];
+      {
+        uint32_t v[kPartKeys / 32][32];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        x[j] = __fmul2_rn(make_float2(__uint_as_float(v0[2 * j]), __uint_as_float(v0[2 * j + 1])),
-                          make_float2(sc, sc));
-        x[16 + j] =
-            __fmul2_rn(make_float2(__uint_as_float(v1[2 * j]), __uint_as_float(v1[2 * j + 1])),
-                       make_float2(sc, sc));
+        for (int g = 0; g < kPartKeys / 32; ++g)
+          tmem_ld32_async(tmem + lane_base + (uint32_t)(part * kPartKeys + g * 32), v[g]);
+        tmem_wait_ld(v[0]);
+#pragma unroll
+        for (int g = 0; g < kPartKeys / 32; ++g) {
+          if (g > 0) tmem_tie(v[g]);
+          // scores in log2 units
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            x[g * 16 + j] =
+                __fmul2_rn(make_float2(__uint_as_float(v[g][2 * j]), __uint_as_float(v[g][2 * j + 1])),
+                           make_float2(sc, sc));
+        }
       }
-      const int key0 = kt * kKeysT, kb = key0 + hf * 64;  // first key of the tile, of this half
-      if (kb + 64 > lim) {  // the causal diagonal or the end of the context
+      // the scores are in registers: the next tile's may come
+      tc_fence_before();
+      const int key0 = kt * kKeysT, kb = key0 + part * kPartKeys;  // first key of the tile, of this part
+      if (kb + kPartKeys > lim) {  // the causal diagonal or the end of the context
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < kPartKeys / 2; ++j) {
           if (kb + 2 * j >= lim) x[j].x = neg_inf();
           if (kb + 2 * j + 1 >= lim) x[j].y = neg_inf();
         }
       }
-      float mx = fmaxf(x[0].x, x[0].y);
+      float mx;
       {
-        float m4[4] = {mx, neg_inf(), neg_inf(), neg_inf()};
+        float m4[4] = {fmaxf(x[0].x, x[0].y), fmaxf(x[1].x, x[1].y), fmaxf(x[2].x, x[2].y),
+                       fmaxf(x[3].x, x[3].y)};
 #pragma unroll
-        for (int j = 1; j < 32; ++j)
+        for (int j = 4; j < kPartKeys / 2; ++j)
           asm("max.f32 %0, %1, %2, %3;"
               : "=f"(m4[j & 3])
               : "f"(x[j].x), "f"(x[j].y), "f"(m4[j & 3]));
         mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       }
-      float mo;
-      if (!exchange(mx, mo)) break;
-      mx = fmaxf(mx, mo);  // the same in both halves of the row
+      float ms[kParts];
+      if (!exchange(mx, ms)) break;
+      if (part == 0) {
+        tc_fence_after();
+        tc_fence_before();
+        if (lane == 0) arrive(B_SEMPTY);
+      }
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) mx = fmaxf(mx, ms[k]);  // the same in all parts of the row
       float alpha = 1.f;
       bool rescale = false;
       if (m_ref == neg_inf()) {
@@ -672,81 +736,78 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         m_ref = mx;
         rescale = true;
       }
+      const bool scale_o = __any_sync(kFull, rescale) && !first;
       const float ref = m_ref == neg_inf() ? 0.f : m_ref;
       const float2 nref = make_float2(-ref, -ref);
       float2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
       // P enters the product in bf16, the type that V is stored in and that one
       // tcgen05.mma wants of both operands: a weight is off by at most 2^-8 of itself.
       // The sum l, and with it lse, is of the unrounded ones.
-      uint32_t pk[32];
+      uint32_t pk[kPartKeys / 32][16];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
+      for (int j = 0; j < kPartKeys / 2; ++j) {
         const float2 d = __fadd2_rn(x[j], nref);
         const float2 e = make_float2(ex2(d.x), ex2(d.y));
         acc[j & 3] = __fadd2_rn(acc[j & 3], e);
-        pk[j] = cvt_bf16x2(e.x, e.y);
+        pk[j >> 4][j & 15] = cvt_bf16x2(e.x, e.y);
       }
       const float2 s01 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
       l = fmaf(l, alpha, s01.x + s01.y);
+      // P row r, keys of this part
+      __syncwarp();
+#pragma unroll
+      for (int g = 0; g < kPartKeys / 32; ++g)
+        tmem_st16(tmem + lane_base + kColP + sb * 64u + (uint32_t)(part * (kPartKeys / 2) + g * 16),
+                  pk[g]);
       // the previous product must be done before O is rescaled or the previous map's O is
       // read. Its P buffer says so: the product before it on that buffer is done, or this
       // tile's S would not be there, so its phase is not mistaken for an earlier one. (The
       // tensor-memory accesses are warp-wide: the whole warp rescales when one of its
       // rows has to, the others by 1.)
-      const bool scale_o = __any_sync(kFull, rescale) && !first;
-      if (scale_o || pend.on) {
-        if (!wait_all(B_SFREE + (sb ^ 1), (uint32_t)((i - 1) >> 1) & 1u)) break;
+      if (scale_o || pend_on) {
+        if (!wait_all(B_PFREE + (int)(sb ^ 1u), (uint32_t)((i - 1) >> 1) & 1u)) break;
         tc_fence_after();
       }
-      if (pend.on && !flush()) break;
+      if (pend_on && !flush()) break;
       if (scale_o) {
+        __syncwarp();
+#pragma unroll 1
+        for (int cc = 0; cc < kPartDims / 16; ++cc) {
+          float y[16];
+          uint32_t u[16];
+          tmem_ld16(tO + (uint32_t)cc * 16u, y);
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t v[32];
-          tmem_ld32(tO + (uint32_t)cc * 32u, v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
-          tmem_st32(tO + (uint32_t)cc * 32u, v);
+          for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(y[j] * alpha);
+          tmem_st16(tO + (uint32_t)cc * 16u, u);
         }
       }
-      // P row r, keys of half hf, over the S columns this thread has read
-      __syncwarp();
-      tmem_st32(tS, pk);
       tmem_wait_st();
       // keys past the context may hold anything (even NaN): zero their V rows so that P
       // = 0 never meets them; of the window's rows, which only some queries see, the
-      // infinities and NaNs (thread (r, hf) has half hf of key row r of this CTA's head)
-      // (Only one warp of a CTA sees to it that V is there before the product begins; a
-      // wait costs 130 clocks even when it is over.)
-      const int vsafe = a.causal ? c - lq + 1 : c;  // rows before it enter as they are
-      if ((warp == 2 || key0 + kKeysT > vsafe) && !wait_all(B_VFULL + st, use & 1u)) break;
-      if (key0 + kKeysT > vsafe && key0 + r >= vsafe) {
-        unsigned char* vrow = stages + st * kStageT + kKBytes + (r >> 3) * 2048 + hf * 1024 +
-                              (r & 7) * 128;
-        if (key0 + r >= c) {
+      // infinities and NaNs. (Only one warp of a CTA sees to it that V is there before the
+      // product begins; a wait costs 130 clocks even when it is over.)
+      if (warp == 2 || key0 + kKeysT > vsafe) {
+        if (!wait_all(B_VFULL + i % nstage, (uint32_t)(i / nstage) & 1u)) break;
+      }
+      if (key0 + kKeysT > vsafe) {
+        // chunks of 16 bytes in the order in which they lie: (16 keys, 8 of them, 64 dims, key)
+        unsigned char* vt = stages + i % nstage * kStageT + kKBytes;
 #pragma unroll
-          for (int ch = 0; ch < 8; ++ch)
-            *reinterpret_cast<uint4*>(vrow + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          fence_cluster();
-        } else {
-          bool bad = false;
-#pragma unroll
-          for (int ch = 0; ch < 8; ++ch) {
-            const uint4 x4 = *reinterpret_cast<const uint4*>(vrow + ch * 16);
-            bad = bad || bf2_nonfinite(x4.x) || bf2_nonfinite(x4.y) || bf2_nonfinite(x4.z) ||
-                  bf2_nonfinite(x4.w);
-          }
-          if (bad) {
-            for (int ch = 0; ch < 8; ++ch) {
-              uint4 x4 = *reinterpret_cast<const uint4*>(vrow + ch * 16);
-              x4.x = bf2_finite_part(x4.x);
-              x4.y = bf2_finite_part(x4.y);
-              x4.z = bf2_finite_part(x4.z);
-              x4.w = bf2_finite_part(x4.w);
-              *reinterpret_cast<uint4*>(vrow + ch * 16) = x4;
-            }
-            fence_proxy_async_smem();
+        for (int k = 0; k < kVBytes / (kSoftmaxWarps * 32 * 16); ++k) {
+          const int at = (k * kSoftmaxWarps * 32 + tid - 64) * 16;
+          const int key = key0 + (at >> 12) * 16 + ((at >> 11) & 1) * 8 + ((at >> 7) & 7);
+          if (key < vsafe) continue;
+          uint4* chunk = reinterpret_cast<uint4*>(vt + at);
+          uint4 x4 = make_uint4(0u, 0u, 0u, 0u);
+          if (key < c) {
+            x4 = *chunk;
+            // (all exponent bits set: one more in their lowest place carries to the sign's)
+            const uint32_t e = 0x7f807f80u, one = 0x00800080u;
+            if (!((((x4.x & e) + one) | ((x4.y & e) + one) | ((x4.z & e) + one) |
+                   ((x4.w & e) + one)) & 0x80008000u))
+              continue;
+            x4 = make_uint4(bf2_finite_part(x4.x), bf2_finite_part(x4.y), bf2_finite_part(x4.z),
+                            bf2_finite_part(x4.w));
             // both CTAs write dims of both heads out
             const uint32_t flag = smem_addr(rest + kOffBad);
             for (uint32_t to = 0; to < 2; ++to)
@@ -754,40 +815,40 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                                in_cta(flag, to)),
                            "r"(1u)
                            : "memory");
-            fence_cluster();
           }
+          *chunk = x4;
+          fence_proxy_async_smem();
+          fence_cluster();
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_in_cluster(lead_p + sb * 8);
-      if (++st == nstage) {
-        st = 0;
-        ++use;
-      }
+      if (lane == 0) arrive(B_PFULL + (int)sb);
 
       if (last) {
-        pend.on = true;
-        pend.valid = valid;
-        pend.whole = piece_b0 == 0 && (map == 0 ? cut.start(w + 1) - idx > n : t.b == t.nt - 1);
-        pend.last_of_piece = piece_last;
-        pend.s = t.s;
-        pend.h = t.h;
-        pend.map = map;
-        pend.b0 = piece_b0;
-        pend.b1 = t.b;
-        pend.n = n;
-        pend.qtok = (int64_t)P.qstart[t.s] + tok;
-        pend.k0 = (map == 0 || piece_b0 < n ? (map == 0 ? piece_b0 : 0) : piece_b0 - n) * kKeysT;
-        pend.k1 = key0 + kKeysT;
-        pend.vis = lim;
-        pend.slot = (size_t)w * 2 + (piece_first ? 0 : 1);
-        pend.m = m_ref;
-        pend.l = l;
+        pend_on = true;
+        pend_tok = lim > 0 ? (t.qt * 2 + rank) * QTb + r / G : -1;
+        pend_m = m_ref;
+        pend_l = l;
+        __syncwarp();
+        if (lane == 0) {
+          Pending p;
+          p.flags = (piece_b0 == 0 && (map == 0 ? R1 - idx > n : t.b == t.nt - 1) ? 1 : 0) |
+                    (piece_last ? 2 : 0);
+          p.k1 = key0 + kKeysT;
+          p.s = t.s;
+          p.h = t.h;
+          p.map = map;
+          p.b0 = piece_b0;
+          p.n = n;
+          p.slot = w * 2 + (piece_first ? 0 : 1);
+          *pending = p;
+        }
+        __syncwarp();
       }
       if (idx + 1 < R1) advance(P, S, Hp, t);
     }
-    if (pend.on && wait_all(B_SFREE + ((i - 1) & 1), (uint32_t)((i - 1) >> 1) & 1u)) {
+    if (pend_on && wait_all(B_PFREE + ((i - 1) & 1), (uint32_t)((i - 1) >> 1) & 1u)) {
       tc_fence_after();
       flush();
     }
@@ -805,106 +866,128 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 }
 
 // Merge the pieces of the (query tile, pair) segments that the ranges cut, both
-// maps, then difference, norm and scale. Grid (worker boundary, chunk of rows): a
-// warp takes a row at a time, eight of its 256 dims a lane.
-constexpr int kTFixWarps = 8;
-constexpr int kTFixChunks = 16;  // 256 rows: 16 of them a CTA
+// maps, then difference, norm and scale. Grid (worker boundary, chunk of 32 rows): a
+// lane has a row, a warp 32 of its dims; the warps' sums of squares meet in shared
+// memory.
+constexpr int kTFixWarps = 16;
+constexpr int kTFixChunks = 2 * kRowsT / 32;
+constexpr int kTFixDims = kDiffDim / kTFixWarps;
 
-__global__ void __launch_bounds__(kTFixWarps * 32)
+__global__ void __launch_bounds__(kTFixWarps * 32, 2)
     diff_tc_fixup_kernel(const DiffTcArgs a) {
+  __shared__ float squares_of[kTFixWarps][32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int w = blockIdx.x;
-  const int* d = a.desc + (size_t)w * kTDesc;
-  if (__ldcg(d) < 0) return;
-  const int qt = __ldcg(d + 1), h = __ldcg(d + 2), last = __ldcg(d + 3), slot_prev = __ldcg(d + 4),
-            q0 = __ldcg(d + 5), lq = __ldcg(d + 6);
+  const int4* d = reinterpret_cast<const int4*>(a.desc + (size_t)w * kTDesc);
+  const int4 d0 = __ldcg(d), d1 = __ldcg(d + 1);
+  if (d0.x < 0) return;
+  const int qt = d0.y, h = d0.z, last = d0.w, slot_prev = d1.x, q0 = d1.y, lq = d1.z;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int npieces = last - w + 2;  // workers w-1 .. last
-  constexpr int kRowsPerCta = 2 * kRowsT / kTFixChunks;
-  for (int row = blockIdx.y * kRowsPerCta + warp; row < (int)(blockIdx.y + 1) * kRowsPerCta;
-       row += kTFixWarps) {
-    const int r = row & (kRowsT - 1);
-    const int tok = (qt * 2 + row / kRowsT) * a.QTb + r / a.G;
-    if (r >= a.QTb * a.G || tok >= lq) continue;
-    float y[8], lse[2];
-    float a0[8];
+  const int row = blockIdx.y * 32 + lane, r = row & (kRowsT - 1);
+  const int tok = (qt * 2 + row / kRowsT) * a.QTb + r / a.G;
+  const bool live = r < a.QTb * a.G && tok < lq;
+  if (!__syncthreads_or(live)) return;
+  auto slot_of = [&](int i) { return (w - 1 + i) * 2 + (i == 0 ? slot_prev : 0); };
+  const int head = h * a.G + r % a.G;
+  float y[kTFixDims], lse[2] = {neg_inf(), neg_inf()};
+  float squares = 0.f;
+  if (live) {
+    float m[2] = {neg_inf(), neg_inf()}, sum[2] = {0.f, 0.f}, acc[2][kTFixDims];
+    bool nan[2] = {false, false};  // a piece with a NaN score: the row's results are NaNs
+#pragma unroll
+    for (int j = 0; j < kTFixDims; ++j) acc[0][j] = acc[1][j] = 0.f;
+    const float lam = a.o.lambdas[head];
+    for (int i0 = 0; i0 < npieces; i0 += 4) {  // online, four pieces' sums in flight
+      float li[2][4], wt[2][4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int map = 0; map < 2; ++map)
+          li[map][u] = i0 + u < npieces
+                           ? __ldcg(a.part_lse + ((size_t)slot_of(i0 + u) * 2 + map) * (2 * kRowsT) + row)
+                           : neg_inf();
+#pragma unroll
+      for (int map = 0; map < 2; ++map) {
+        float mn = m[map];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          nan[map] = nan[map] || li[map][u] != li[map][u];
+          mn = fmaxf(mn, li[map][u]);
+        }
+        const float shrink = m[map] == neg_inf() ? 0.f : ex2((m[map] - mn) * kLog2e);
+        sum[map] *= shrink;
+#pragma unroll
+        for (int j = 0; j < kTFixDims; ++j) acc[map][j] *= shrink;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          wt[map][u] = li[map][u] == neg_inf() ? 0.f : ex2((li[map][u] - mn) * kLog2e);
+          sum[map] += wt[map][u];
+        }
+        m[map] = mn;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int map = 0; map < 2; ++map) {
+          if (li[map][u] == neg_inf()) continue;  // nothing was written there
+          const float4* src =
+              part_rows(a, slot_of(i0 + u), map) + warp * (kTFixDims / 4) * (2 * kRowsT) + row;
+          float4 v[kTFixDims / 4];
+#pragma unroll
+          for (int q = 0; q < kTFixDims / 4; ++q) v[q] = __ldcg(src + q * (2 * kRowsT));
+#pragma unroll
+          for (int q = 0; q < kTFixDims / 4; ++q) {
+            acc[map][4 * q + 0] = fmaf(wt[map][u], v[q].x, acc[map][4 * q + 0]);
+            acc[map][4 * q + 1] = fmaf(wt[map][u], v[q].y, acc[map][4 * q + 1]);
+            acc[map][4 * q + 2] = fmaf(wt[map][u], v[q].z, acc[map][4 * q + 2]);
+            acc[map][4 * q + 3] = fmaf(wt[map][u], v[q].w, acc[map][4 * q + 3]);
+          }
+        }
+    }
+    float inv[2];
 #pragma unroll
     for (int map = 0; map < 2; ++map) {
-      float m = neg_inf(), sum = 0.f, acc[8];
-      bool nan = false;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-      for (int i0 = 0; i0 < npieces; i0 += 4) {
-        float li[4];
-        float4 v[4][2];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          li[u] = neg_inf();
-          v[u][0] = v[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (i0 + u < npieces) {
-            const size_t sl = (size_t)(w - 1 + i0 + u) * 2 + (i0 + u == 0 ? slot_prev : 0);
-            const size_t at = (sl * 2 + map) * (2 * kRowsT) + row;
-            li[u] = __ldcg(a.part_lse + at);
-            const float4* src = reinterpret_cast<const float4*>(a.part_o + at * kDiffDim + lane * 8);
-            if (li[u] != neg_inf()) {
-              v[u][0] = __ldcg(src);
-              v[u][1] = __ldcg(src + 1);
-            }
-          }
-        }
-        const float mn = fmaxf(fmaxf(m, fmaxf(li[0], li[1])), fmaxf(li[2], li[3]));
-#pragma unroll
-        for (int u = 0; u < 4; ++u) nan = nan || li[u] != li[u];
-        if (mn == neg_inf()) continue;
-        const float shrink = m == neg_inf() ? 0.f : ex2((m - mn) * kLog2e);
-        sum *= shrink;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] *= shrink;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float wt = li[u] == neg_inf() ? 0.f : ex2((li[u] - mn) * kLog2e);
-          sum += wt;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            acc[4 * k + 0] = fmaf(wt, v[u][k].x, acc[4 * k + 0]);
-            acc[4 * k + 1] = fmaf(wt, v[u][k].y, acc[4 * k + 1]);
-            acc[4 * k + 2] = fmaf(wt, v[u][k].z, acc[4 * k + 2]);
-            acc[4 * k + 3] = fmaf(wt, v[u][k].w, acc[4 * k + 3]);
-          }
-        }
-        m = mn;
-      }
-      if (nan) m = sum = __int_as_float(0x7fc00000);
-      const float inv = sum != 0.f ? 1.f / sum : 0.f;
-      lse[map] = sum != 0.f ? m + lg2(sum) * kLn2 : neg_inf();
-      const float lam = a.o.lambdas[h * a.G + r % a.G];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (map == 0)
-          a0[j] = __fmul_rn(acc[j], inv);
-        else
-          y[j] = diff_value(a0[j], 1.f, acc[j], inv, lam);
-      }
+      if (nan[map]) m[map] = sum[map] = __int_as_float(0x7fc00000);
+      inv[map] = sum[map] != 0.f ? 1.f / sum[map] : 0.f;
+      lse[map] = sum[map] != 0.f ? m[map] + lg2(sum[map]) * kLn2 : neg_inf();
     }
-    float squares = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) squares = fmaf(y[j], y[j], squares);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) squares += __shfl_xor_sync(kFull, squares, o);
-    const float f = diff_factor(a.o, squares);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] *= a.o.weight ? f * a.o.weight[lane * 8 + j] : f;
-    const int head = h * a.G + r % a.G;
-    const int64_t qtok = (int64_t)q0 + tok;
-    *reinterpret_cast<uint4*>(a.o.out + (qtok * (a.Hq / 2) + head) * kDiffDim + lane * 8) =
-        make_uint4(cvt_bf16x2(y[0], y[1]), cvt_bf16x2(y[2], y[3]), cvt_bf16x2(y[4], y[5]),
-                   cvt_bf16x2(y[6], y[7]));
-    if (a.o.lse && lane == 0) {
-      float* l = a.o.lse + qtok * a.Hq + (int64_t)(2 * h) * a.G + r % a.G;
-      l[0] = lse[0];
-      l[a.G] = lse[1];
+    for (int j = 0; j < kTFixDims; ++j) {
+      y[j] = diff_value(acc[0][j], inv[0], acc[1][j], inv[1], lam);
+      squares = fmaf(y[j], y[j], squares);
     }
+  }
+  squares_of[warp][lane] = squares;
+  __syncthreads();
+  if (!live) return;
+  squares = 0.f;
+#pragma unroll
+  for (int k = 0; k < kTFixWarps; ++k) squares += squares_of[k][lane];
+  const float f = diff_factor(a.o, squares);
+  const int64_t qtok = (int64_t)q0 + tok;
+  uint4* dst = reinterpret_cast<uint4*>(a.o.out + (qtok * (a.Hq / 2) + head) * kDiffDim +
+                                        warp * kTFixDims);
+#pragma unroll
+  for (int q = 0; q < kTFixDims / 8; ++q) {
+    uint32_t u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = 8 * q + 2 * e;
+      float2 x = make_float2(f, f);
+      if (a.o.weight) {
+        x.x *= a.o.weight[warp * kTFixDims + j];
+        x.y *= a.o.weight[warp * kTFixDims + j + 1];
+      }
+      u[e] = cvt_bf16x2(y[j] * x.x, y[j + 1] * x.y);
+    }
+    dst[q] = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  if (a.o.lse && warp == 0) {
+    float* l = a.o.lse + qtok * a.Hq + (int64_t)(2 * h) * a.G + r % a.G;
+    l[0] = lse[0];
+    l[a.G] = lse[1];
   }
 }
 
