@@ -707,7 +707,7 @@ int pa_rotate_cached(void* k_cache, int kv_format, const int32_t* block_tables,
  *                 per sequence, which sees its whole context
  *   lambdas       [num_q_heads / 2] fp32 (a model's learned vectors make one
  *                 number of them before it is served)
- *   norm_weight   [2 * D] fp32, or NULL; norm_eps >= 0
+ *   norm_weight   [2 * D] fp32, 16-byte aligned, or NULL; norm_eps >= 0
  *   out           [num_q_tokens][num_q_heads / 2][2 * D] bf16
  *   lse           [num_q_tokens][num_q_heads] fp32 of each map, or NULL
  *   workspace     at least pa_decode_diff_workspace_size(...) bytes, 256-byte
@@ -715,7 +715,8 @@ int pa_rotate_cached(void* k_cache, int kv_format, const int32_t* block_tables,
  * bf16 pools with an even num_kv_heads and 1 to 128 query heads per KV head
  * (else PA_ERR_UNSUPPORTED, workspace size 0). Both maps, their difference and
  * the norm are fp32; the softmax weights are rounded to bf16 for the product
- * with V, as in pa_decode_varlen. A sequence of the single-query form with an
+ * with V, as in pa_decode_varlen (so where the two maps' results agree to 2^-8, what
+ * norm_eps does not hold down is their rounding). A sequence of the single-query form with an
  * empty context gives out = 0 and lse = -inf. A key that a query does not see
  * never reaches its result, whatever its K and V hold.
  */

@@ -750,12 +750,17 @@ struct DiffPlan {
 
 int diff_plan(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffPlan* p) {
   const int G = sh->num_q_heads / sh->num_kv_heads;
-  const int min_lq = G > kMapRows ? 1 : (kTcMinRows + G - 1) / G;
+  int min_lq = G > kMapRows ? 1 : (kTcMinRows + G - 1) / G;
+  p->warp = G <= kMapRows;
+  // as many rows as windows of max_q_len hold: every window has that length, as far as
+  // the host can tell. One that is shorter after all (rows behind the last sequence) is
+  // taken by the same kernel then
+  if (max_q_len >= min_lq && num_q_tokens == (int64_t)sh->num_seqs * max_q_len) {
+    min_lq = 1;
+    p->warp = false;
+  }
   int rc = diff_tc_geometry(sh, num_q_tokens, max_q_len, min_lq, &p->tc);
   if (rc != PA_OK) return rc;
-  // as many rows as windows of max_q_len hold: every window has that length
-  p->warp = G <= kMapRows &&
-            !(p->tc.enabled && num_q_tokens == (int64_t)sh->num_seqs * max_q_len);
   if (p->warp) {
     rc = diff_geometry(sh, num_q_tokens, max_q_len, &p->g);
     if (rc != PA_OK) return rc;

@@ -412,6 +412,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
     if (!fine && (rank == 0 || !is_k)) {
       // copies in flight land (within the limit) before the CTA leaves; the leading
       // CTA's barriers count the peer's K and Q as well
+      for (int k = qn < 2 ? 0 : qn - 2; is_k && k < qn; ++k)
+        mbar_wait_bounded(bar(B_QFULL + (k & 1)), (uint32_t)(k >> 1) & 1u);
       for (int k = i < nstage ? i : nstage; k > 0; --k) {
         if (--st < 0) {
           st = nstage - 1;

@@ -242,6 +242,112 @@ def test_short_and_long_windows_in_one_call():
     b.check(out, lse)
 
 
+@pytest.mark.parametrize("lens,qs,T,max_q,G", [
+    ([90, 40], [5, 3], 11, 5, 2),          # short windows
+    ([300, 200], [64, 20], 128, 64, 1),    # as many rows as two windows of 64 would hold
+    ([300, 200, 50], [70, 0, 2], 90, 70, 2),
+])
+def test_rows_behind_the_last_sequence_stay(lens, qs, T, max_q, G):
+    b = Batch(14, lens, qs, 2, G).cuda()
+    g = torch.Generator().manual_seed(1)
+    more = T - b.T
+    d = b.d
+    d["q"] = torch.cat([d["q"], torch.full((more, b.hq, DIM), float("nan"), dtype=torch.bfloat16,
+                                           device="cuda")])
+    out = torch.full((T, b.hq // 2, 2 * DIM), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, b.hq), 5.0, device="cuda")
+    sh = B.shape_of(d["q"], d["kc"], d["tables"])
+    ws = B.workspace(B.pa_decode_diff_workspace_size(sh, T, max_q), "cuda")
+    B.pa_decode_diff(d["q"], d["kc"], d["vc"], d["tables"], d["lens"], SCALE, d["lambdas"], out, lse,
+                     cu_seqlens_q=d["cu"], max_q_len=max_q, norm_weight=d["weight"], out_scale=0.8,
+                     workspace=ws)
+    ok()
+    b.check(out, lse)
+    assert (out[b.T:] == 3).all() and (lse[b.T:] == 5).all()
+
+
+@pytest.mark.parametrize("lens,qs,G", [([5, 40], [9, 3], 2), ([20, 300], [90, 70], 2)])
+def test_more_queries_than_keys_without_a_causal_mask(lens, qs, G):
+    b = Batch(15, lens, qs, 2, G).cuda()
+    out, lse = b.call(causal=False)
+    ok()
+    b.check(out, lse, causal=False)
+
+
+def test_a_small_or_missing_workspace_is_refused():
+    for qs, G in ((None, 2), ([3, 5], 2), ([40, 64], 2)):
+        b = Batch(16, [90, 64], qs, 2, G).cuda()
+        sh = B.shape_of(b.d["q"], b.d["kc"], b.d["tables"])
+        need = B.pa_decode_diff_workspace_size(sh, b.T, b.max_q)
+        assert need > 0
+        for ws in (torch.empty(need - 1, dtype=torch.uint8, device="cuda"),
+                   torch.empty(need + 256, dtype=torch.uint8, device="cuda")[8:]):
+            with pytest.raises(B.PAError) as e:
+                b.call(workspace=ws)
+            assert e.value.status == B.PA_ERR_WORKSPACE
+
+
+def test_two_graphs_that_share_a_workspace():
+    a, c = Batch(51, [600, 40], None, 4, 2).cuda(), Batch(52, [300, 280], [100, 90], 4, 2).cuda()
+    sizes, graphs = [], []
+    for b in (a, c):
+        sh = B.shape_of(b.d["q"], b.d["kc"], b.d["tables"])
+        sizes.append(B.pa_decode_diff_workspace_size(sh, b.T, b.max_q))
+    ws = B.workspace(max(sizes), "cuda")
+    want = [b.call()[0].clone() for b in (a, c)]
+    ok()
+    outs = []
+    for b in (a, c):
+        d = b.d
+        out = torch.zeros((b.T, b.hq // 2, 2 * DIM), dtype=torch.bfloat16, device="cuda")
+        call = B.prepare_decode_diff(d["q"], d["kc"], d["vc"], d["tables"], d["lens"], SCALE,
+                                     d["lambdas"], out,
+                                     cu_seqlens_q=None if b.qs is None else d["cu"],
+                                     max_q_len=b.max_q, norm_weight=d["weight"], out_scale=0.8,
+                                     workspace=ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graphs.append(graph)
+        outs.append(out)
+    for _ in range(3):
+        for out in outs:
+            out.zero_()
+        for graph in graphs:
+            graph.replay()
+        ok()
+        for out, w in zip(outs, want):
+            assert torch.equal(out.view(torch.int16), w.view(torch.int16))
+
+
+def test_a_pool_beyond_32_bit_offsets():
+    # the sequences' blocks lie more than 2^32 bytes into either array
+    far = (1 << 32) // (2 * BLOCK * DIM * 2) + 5
+    for qs in (None, [40, 70]):
+        b = Batch(61, [100, 90], qs, 2, 2)
+        try:
+            big = [torch.empty((far + b.kc.shape[0], 2, BLOCK, DIM), dtype=torch.bfloat16,
+                               device="cuda") for _ in range(2)]
+        except torch.cuda.OutOfMemoryError:
+            pytest.skip("no room")
+        b.cuda()
+        big[0][far:], big[1][far:] = b.d["kc"], b.d["vc"]
+        want, _ = b.call()
+        b.d["kc"], b.d["vc"] = big
+        b.d["tables"] = b.d["tables"] + far
+        out, _ = b.call()
+        ok()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        # the same keys turned there
+        rot, shifts = B.make_rotation(128), torch.tensor([-7, 9], dtype=torch.int32).cuda()
+        B.pa_rotate_cached(big[0], b.d["tables"], b.d["lens"], rot, shifts=shifts)
+        near = b.kc.cuda()
+        B.pa_rotate_cached(near, b.tables.cuda(), b.d["lens"], rot, shifts=shifts)
+        ok()
+        assert torch.equal(big[0][far:].view(torch.int16), near.view(torch.int16))
+        del big, b
+
+
 def test_windows_of_one_are_single_queries():
     lens = [37, 1, 200, 16]
     one = Batch(5, lens, None, 4, 2).cuda()
@@ -323,6 +429,23 @@ def test_a_difference_of_zero():
         out, _ = b.call(eps=eps)
         ok()
         assert (out[:b.T] == 0).all()
+    # windows: of a segment that one worker has, both maps go the same way; of one that
+    # ranges cut, each map at places of its own, so that weights are rounded to bf16
+    # against other references (2^-8 of each at most, in either map): the difference is
+    # then that of two roundings, which is what the bounds say of it
+    for lens, qs in (([130], [70]), ([4000], [100])):
+        b = Batch(2, lens, qs, 2, 1)
+        b.kc[:, 1] = b.kc[:, 0]
+        b.q[:, 1] = b.q[:, 0]
+        b.lambdas.fill_(1.0)
+        b.cuda()
+        for norm in (False, True):
+            out, _ = b.call(norm=norm, eps=0.0 if lens[0] == 130 else 1e-5)
+            ok()
+            if lens[0] == 130:
+                assert (out[:b.T] == 0).all()
+            else:
+                b.check(out, None, norm=norm)
 
 
 def test_many_sequences_and_a_wide_table():
