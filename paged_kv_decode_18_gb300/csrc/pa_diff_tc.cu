@@ -27,9 +27,17 @@
 // two P: a tile's scores go to registers at once, so the next S is computed beside
 // the exponentials of this one and the product of the last. (S and P in one buffer,
 // two of those: the next S but one waited for the product, 2400 clocks a tile.) O is
-// one accumulator for all keys, so a row's threads agree on its reference: they
-// exchange their maxima every tile. The reference moves only when a maximum grows by
-// more than 2^32 (exact either way).
+// one accumulator for all keys, so a row's threads agree on its reference. It moves
+// only when a maximum grows by more than 2^32 (exact either way): the four warps of 32
+// rows vote whether one does, by a hardware barrier, and exchange maxima through
+// shared memory only then. (Exchanging them every tile, with an mbarrier: 365 clocks, 7
+// us of the call below.)
+//
+// Four chunks of 512 queries over 2816 to 7424 keys, 16 heads over 8: 106 us and the
+// merge's 18, 124 in all, of which the products' own operations are 64. A tile takes 1.1
+// us: its products and their hand-offs by themselves (no exponentials) 1.0 to 1.2, the
+// softmax by itself (no products) as much, and leaving the loads out changes neither. A
+// map's end (its diagonal tiles, O read out with nothing beside it) costs 3 to 4 us.
 #include <cudaTypedefs.h>
 
 #include "pa_diff.cuh"
@@ -57,10 +65,10 @@ constexpr int kThreadsT = 128 + kSoftmaxWarps * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColP = 128;               // S at columns 0 .. 127, two P buffers of 64,
 constexpr uint32_t kColO = 256;               // O at 256 .. 511
-// a segment start in quarters of a key tile: what two maps' last tiles and write-outs
-// take on top of the others (6: 139 us for four chunks over 2816 .. 7424 keys, 24: 135,
-// 40: 140)
-constexpr int kSegCost4 = 24;
+// a map's start in quarters of a key tile: what its diagonal tiles and its write-out take
+// on top of the others (four chunks over 2816 .. 7424 keys: 12: 128 us, 16: 125.3, 20:
+// 124.3, 24: 124.5, 28: 127.4; 24 charged where both maps' segment starts: 127.4)
+constexpr int kMapCost4 = 20;
 constexpr int kTDesc = 8;
 // The reference of a row's exponentials moves only when its maximum has grown by more
 // than this power of two: weights up to 2^32 are as exact in bf16 and fp32 as those below
@@ -74,7 +82,7 @@ enum : int {
   B_QEMPTY = 2,                       // [2], both
   B_KFULL = 4,                        // [3], leader: both CTAs' keys
   B_KEMPTY = 7,                       // [3], both
-  B_VFULL = 10,                       // [3], each CTA its own values
+  B_VFULL = 10,                       // [3], leader: both CTAs' values
   B_VEMPTY = 13,                      // [3], both
   B_SFULL = 16,                       // both
   B_SEMPTY = 17,                      // leader: all softmax warps of both hold their scores
@@ -82,8 +90,9 @@ enum : int {
   // [2], leader: all softmax warps of both. Two, since a warp may be through with the
   // next tile's exponentials before another has arrived for this one
   B_PFULL = 20,
-  B_XCH = 22,                         // [4]: the four warps of 32 rows, every exchange a phase
-  kNumBarsT = 26
+  B_VSEEN = 22,                       // both: the values of a tile that has to be cleaned are there
+  B_XCH = 23,                         // [4]: the four warps of 32 rows, every exchange a phase
+  kNumBarsT = 27
 };
 
 // shared memory past the operands
@@ -148,6 +157,22 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same for what the peer is to read by ordinary loads, and the wait for it.
+__device__ __forceinline__ void release_in_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool try_acquire_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void fence_cluster() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
@@ -163,6 +188,19 @@ __device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity), "r"(20000u)
       : "memory");
   return ok != 0;
+}
+// Whether `yes` holds in one of the four warps of 32 rows. Every warp votes once a tile;
+// one that leaves early makes up for the votes that the others wait for.
+__device__ __forceinline__ bool vote(int rows, bool yes) {
+  uint32_t any;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)yes), "r"(1 + rows), "n"(kParts * 32)
+      : "memory");
+  return any != 0;
 }
 // tiled copies whose completion counts on a barrier of either CTA of the pair
 __device__ __forceinline__ void tma_pair_3d(uint32_t dst, const CUtensorMap* map, int x, int y,
@@ -262,8 +300,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   in.min_lq = a.min_lq;
   in.skip_empty = a.cu_seqlens_q == nullptr;
   build_plan(in, P, nullptr);
-  // segments are pairs of KV heads: n tiles of the first map, then n of the second
-  const PieceCut cut = build_piece_cut(P, Hp, a.num_workers, kSegCost4, cut_at);
+  // segments are pairs of KV heads, n tiles of the first map, then n of the second; the
+  // cut charges every map by itself, as if each KV head had a segment of n
+  const PieceCut cut = build_piece_cut(P, Hkv, a.num_workers, kMapCost4, cut_at);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // a sequence of the single-query form with an empty context has no tiles
@@ -329,6 +368,11 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   // map and key tile of a segment's tile b
   auto map_of = [](const TilePos& t) { return 2 * t.b >= t.nt ? 1 : 0; };
   auto key_tile_of = [&](const TilePos& t) { return t.b - map_of(t) * (t.nt >> 1); };
+  // keys before it are seen by every query of the tile
+  auto safe_keys = [&](const TilePos& t) {
+    const int c = P.ctx[t.s];
+    return a.causal ? c - (P.qstart[t.s + 1] - P.qstart[t.s]) + t.qt * 2 * QTb + 1 : c;
+  };
   // whether a tile begins a map of a piece
   auto begins = [&](const TilePos& t, int idx) { return idx == R0 || key_tile_of(t) == 0; };
 
@@ -345,7 +389,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
                  ? a.block_tables[(size_t)tp.s * a.max_blocks + key_tile_of(tp) * kBlocksT + lane]
                  : 0;
     };
-    const uint32_t lead_q = in_cta(bar(B_QFULL), 0), lead_k = in_cta(bar(B_KFULL), 0);
+    const uint32_t lead_q = in_cta(bar(B_QFULL), 0), lead_k = in_cta(bar(B_KFULL), 0),
+                   lead_v = in_cta(bar(B_VFULL), 0);
     int ids = fetch_ids(t);
     int qn = 0, st = 0, i = 0;
     uint32_t use = 0;  // how often the ring has come round
@@ -397,11 +442,12 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           tma_pair_block(smem_addr(base + half * kTileBytes), &tmk,
                          (int)(((int64_t)my_id * Hkv + h0 + map) * (kBlock / 8)), lead_k + st * 8);
       } else {
-        if (lane == 0) mbar_arrive_expect_tx(bar(B_VFULL + st), (uint32_t)nb * (uint32_t)kTileBytes);
+        if (lane == 0 && rank == 0)
+          mbar_arrive_expect_tx(bar(B_VFULL + st), 2u * (uint32_t)nb * (uint32_t)kTileBytes);
         __syncwarp();
         if (lane < nb)
-          tma_load_block(smem_addr(base + kKBytes + lane * kTileBytes), &tmv,
-                         (int)(((int64_t)my_id * Hkv + h0 + rank) * (kBlock / 8)), bar(B_VFULL + st));
+          tma_pair_block(smem_addr(base + kKBytes + lane * kTileBytes), &tmv,
+                         (int)(((int64_t)my_id * Hkv + h0 + rank) * (kBlock / 8)), lead_v + st * 8);
       }
       __syncwarp();
       if (++st == nstage) {
@@ -409,9 +455,9 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         ++use;
       }
     }
-    if (!fine && (rank == 0 || !is_k)) {
+    if (!fine && rank == 0) {
       // copies in flight land (within the limit) before the CTA leaves; the leading
-      // CTA's barriers count the peer's K and Q as well
+      // CTA's barriers count the peer's as well
       for (int k = qn < 2 ? 0 : qn - 2; is_k && k < qn; ++k)
         mbar_wait_bounded(bar(B_QFULL + (k & 1)), (uint32_t)(k >> 1) & 1u);
       for (int k = i < nstage ? i : nstage; k > 0; --k) {
@@ -467,10 +513,14 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       const uint64_t desc_v = sw128_desc(smem_addr(stages + kKBytes), 1024, 2048);
       TilePos t = locate(P, S, Hp, R0);
       int st = 0;
+      uint32_t use = 0;
       for (int idx = R0, i = 0; idx < R1; ++idx, ++i) {
         const bool first = begins(t, idx);
         const uint32_t sb = (uint32_t)(i & 1);
-        // (a softmax warp of either CTA has seen its values land before it arrives)
+        if (!wait(B_VFULL + st, use & 1u)) break;
+        // the softmax warps clean these values before they arrive
+        if ((key_tile_of(t) + 1) * kKeysT > safe_keys(t))
+          for (uint32_t to = 0; to < 2; ++to) release_in_cluster(in_cta(bar(B_VSEEN), to));
         if (!wait(B_PFULL + (int)sb, (uint32_t)(i >> 1) & 1u)) break;
         tc_fence_after();
         const uint64_t dv = desc_v + (uint64_t)(st * (kStageT >> 4));
@@ -479,7 +529,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
           pair_mma_ts(tmem + kColO, tmem + kColP + sb * 64u + (uint32_t)k * 8u, dv + (uint64_t)(k * (kTileBytes >> 4)), idPV, (k > 0 || !first) ? 1u : 0u);
         pair_commit(bar(B_VEMPTY + st));
         pair_commit(bar(B_PFREE + (int)sb));
-        if (++st == nstage) st = 0;
+        if (++st == nstage) {
+          st = 0;
+          ++use;
+        }
         if (idx + 1 < R1) advance(P, S, Hp, t);
       }
     }
@@ -499,7 +552,8 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         arrive_in_cluster(in_cta(bar(b), 0));
     };
     const float sc = a.scale_log2;
-    uint32_t xphase = 0;
+    uint32_t xphase = 0, cleaned = 0;  // exchanges; tiles whose values were cleaned
+    int st = 0, votes = 0;
     // Gives `mine` to the other threads of the row; all take the four values.
     auto exchange = [&](float mine, float (&all)[kParts]) -> bool {
       float* x = xch + (xphase & 1u) * (kParts * kRowsT) + r;
@@ -561,15 +615,16 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         __syncwarp();
         tmem_ld16(tO + (uint32_t)cc * 16u, z);
         if (*bad_v && pend_valid) {
-          // infinities and NaNs of window rows entered the product as zeros (they must
-          // not reach queries that do not see their row): they join the rows that see
-          // them here
+          // infinities and NaNs of rows that not all of the tile's queries see entered the
+          // product as zeros (they must not reach the others): they join the rows that
+          // see them here
           const int lqp = P.qstart[pend.s + 1] - P.qstart[pend.s];
           const int p0 = P.ctx[pend.s] - lqp;
           const int k0 =
               pend.b0 < pend.n && pend.map == 1 ? 0 : (pend.b0 - pend.map * pend.n) * kKeysT;
           const int k1 = min(p0 + pend_tok + 1, pend.k1);  // (a causal window)
-          for (int k = max(p0 + 1, k0); k < k1; ++k) {
+          const int seen = p0 + pend_tok / (2 * QTb) * (2 * QTb) + 1;  // by all of the tile
+          for (int k = max(seen, k0); k < k1; ++k) {
             const int phys = a.block_tables[(size_t)pend.s * a.max_blocks + k / kBlock];
             if (phys < 0 || (int64_t)phys >= a.num_blocks) continue;
             const int dim = part * kPartDims + cc * 16;
@@ -670,7 +725,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
         const int tok = (t.qt * 2 + rank) * QTb + r / G;
         // keys that the row sees (padding: none; a query sees one at least)
         lim = tok < lq && r < QTb * G ? (a.causal ? c - lq + tok + 1 : c) : 0;
-        vsafe = a.causal ? c - lq + 1 : c;  // keys before it are seen by every query
+        vsafe = safe_keys(t);
         piece_b0 = t.b;
         piece_first = idx == R0;
       }
@@ -720,23 +775,28 @@ __global__ void __launch_bounds__(kThreadsT, 1)
               : "f"(x[j].x), "f"(x[j].y), "f"(m4[j & 3]));
         mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       }
-      float ms[kParts];
-      if (!exchange(mx, ms)) break;
-      if (part == 0) {
+      // m_ref moves only where a maximum is 2^kRescaleLog2 above it, in one of the row's
+      // parts: mostly nowhere, and then no maxima have to be exchanged.
+      const bool moves = vote(q4, mx > m_ref + kRescaleLog2);
+      ++votes;
+      if (part == 0) {  // (the other parts' scores are in registers, too)
         tc_fence_after();
         tc_fence_before();
         if (lane == 0) arrive(B_SEMPTY);
       }
-#pragma unroll
-      for (int k = 0; k < kParts; ++k) mx = fmaxf(mx, ms[k]);  // the same in all parts of the row
       float alpha = 1.f;
       bool rescale = false;
-      if (m_ref == neg_inf()) {
-        m_ref = mx;  // nothing accumulated yet (O and l are zero)
-      } else if (mx > m_ref + kRescaleLog2) {
-        alpha = ex2(m_ref - mx);
-        m_ref = mx;
-        rescale = true;
+      if (moves) {
+        float ms[kParts];
+        if (!exchange(mx, ms)) break;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) mx = fmaxf(mx, ms[k]);  // the same in all parts of the row
+        if (mx > m_ref + kRescaleLog2) {
+          // (with m_ref = -inf nothing has accumulated yet: O and l are zero)
+          rescale = m_ref != neg_inf();
+          if (rescale) alpha = ex2(m_ref - mx);
+          m_ref = mx;
+        }
       }
       const bool scale_o = __any_sync(kFull, rescale) && !first;
       const float ref = m_ref == neg_inf() ? 0.f : m_ref;
@@ -785,40 +845,52 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       }
       tmem_wait_st();
       // keys past the context may hold anything (even NaN): zero their V rows so that P
-      // = 0 never meets them; of the window's rows, which only some queries see, the
-      // infinities and NaNs. (Only one warp of a CTA sees to it that V is there before the
-      // product begins; a wait costs 130 clocks even when it is over.)
-      if (warp == 2 || key0 + kKeysT > vsafe) {
-        if (!wait_all(B_VFULL + i % nstage, (uint32_t)(i / nstage) & 1u)) break;
-      }
+      // = 0 never meets them; of the rows that only some of the tile's queries see, the
+      // infinities and NaNs. (Other tiles' values are the issuing thread's to wait for: a wait
+      // costs 130 clocks even when it is over, and the divisions for its stage as much again;
+      // one warp that made it for its CTA held up its rows by 400 clocks a tile.)
       if (key0 + kKeysT > vsafe) {
+        bool there = try_acquire_cluster(bar(B_VSEEN), cleaned & 1u);
+        if (!there)
+          there = wait(B_VSEEN, cleaned & 1u) && try_acquire_cluster(bar(B_VSEEN), cleaned & 1u);
+        if (!__all_sync(kFull, there)) break;
+        ++cleaned;
         // chunks of 16 bytes in the order in which they lie: (16 keys, 8 of them, 64 dims, key)
-        unsigned char* vt = stages + i % nstage * kStageT + kKBytes;
+        constexpr int kChunks = kVBytes / (kSoftmaxWarps * 32 * 16);
+        unsigned char* vt = stages + st * kStageT + kKBytes;
+        uint4 x4[kChunks];
+        uint32_t unfit = 0;  // chunks to be put right
 #pragma unroll
-        for (int k = 0; k < kVBytes / (kSoftmaxWarps * 32 * 16); ++k) {
+        for (int k = 0; k < kChunks; ++k)
+          x4[k] = *reinterpret_cast<uint4*>(vt + (k * kSoftmaxWarps * 32 + tid - 64) * 16);
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
           const int at = (k * kSoftmaxWarps * 32 + tid - 64) * 16;
           const int key = key0 + (at >> 12) * 16 + ((at >> 11) & 1) * 8 + ((at >> 7) & 7);
-          if (key < vsafe) continue;
-          uint4* chunk = reinterpret_cast<uint4*>(vt + at);
-          uint4 x4 = make_uint4(0u, 0u, 0u, 0u);
-          if (key < c) {
-            x4 = *chunk;
-            // (all exponent bits set: one more in their lowest place carries to the sign's)
-            const uint32_t e = 0x7f807f80u, one = 0x00800080u;
-            if (!((((x4.x & e) + one) | ((x4.y & e) + one) | ((x4.z & e) + one) |
-                   ((x4.w & e) + one)) & 0x80008000u))
-              continue;
-            x4 = make_uint4(bf2_finite_part(x4.x), bf2_finite_part(x4.y), bf2_finite_part(x4.z),
-                            bf2_finite_part(x4.w));
+          // (all exponent bits set: one more in their lowest place carries to the sign's)
+          const uint32_t e = 0x7f807f80u, one = 0x00800080u;
+          const bool odd = ((((x4[k].x & e) + one) | ((x4[k].y & e) + one) |
+                             ((x4[k].z & e) + one) | ((x4[k].w & e) + one)) & 0x80008000u) != 0;
+          if (key >= c || (key >= vsafe && odd)) unfit |= 1u << k;
+          if (key >= c) x4[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (unfit) {
+          const uint32_t flag = smem_addr(rest + kOffBad);
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) {
+            if (!((unfit >> k) & 1u)) continue;
+            const int at = (k * kSoftmaxWarps * 32 + tid - 64) * 16;
+            const uint4 y = make_uint4(bf2_finite_part(x4[k].x), bf2_finite_part(x4[k].y),
+                                       bf2_finite_part(x4[k].z), bf2_finite_part(x4[k].w));
             // both CTAs write dims of both heads out
-            const uint32_t flag = smem_addr(rest + kOffBad);
-            for (uint32_t to = 0; to < 2; ++to)
-              asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(
-                               in_cta(flag, to)),
-                           "r"(1u)
-                           : "memory");
+            if ((x4[k].x ^ y.x) | (x4[k].y ^ y.y) | (x4[k].z ^ y.z) | (x4[k].w ^ y.w))
+              for (uint32_t to = 0; to < 2; ++to)
+                asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(
+                                 in_cta(flag, to)),
+                             "r"(1u)
+                             : "memory");
+            *reinterpret_cast<uint4*>(vt + at) = y;
           }
-          *chunk = x4;
           fence_proxy_async_smem();
           fence_cluster();
         }
@@ -826,6 +898,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive(B_PFULL + (int)sb);
+      if (++st == nstage) st = 0;
 
       if (last) {
         pend_on = true;
@@ -850,6 +923,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
       }
       if (idx + 1 < R1) advance(P, S, Hp, t);
     }
+    for (; votes < R1 - R0; ++votes) vote(q4, false);
     if (pend_on && wait_all(B_PFREE + ((i - 1) & 1), (uint32_t)((i - 1) >> 1) & 1u)) {
       tc_fence_after();
       flush();

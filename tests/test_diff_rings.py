@@ -55,12 +55,14 @@ class Model:
         warps = GROUPS * PARTS * 2
         self.qfull = [Bar(3) for _ in range(2)]           # the leader's announcement, two copies
         self.kfull = [Bar(3) for _ in range(ring)]
-        self.vfull, self.vempty = both(ring, 2), both(ring)
+        self.vfull = [Bar(3) for _ in range(ring)]
+        self.vempty, self.vseen = both(ring), both(1)
         self.kempty, self.qempty = both(ring), both(2)
         self.sfull, self.pfree = both(1), both(2)
         self.sempty = Bar(GROUPS * 2)
         self.pfull = [Bar(warps) for _ in range(p_barriers)]
         self.xch = {(c, g): Bar(PARTS) for c in CTAS for g in range(GROUPS)}
+        self.vote = {(c, g): Bar(PARTS) for c in CTAS for g in range(GROUPS)}
         self.k, self.v, self.q = {}, {}, {}
         self.scores, self.held = None, set()              # tile in S; who holds it in registers
         self.p = [{}, {}]
@@ -108,8 +110,9 @@ class Model:
             st, use = i % self.ring, i // self.ring
             if use > 0:
                 yield self.vempty[c][st], (use - 1) & 1
-            self.vfull[c][st].arrive()
-            self.flying.append((self.v, (c, st), i, self.vfull[c][st]))
+            if c == 0:
+                self.vfull[st].arrive()
+            self.flying.append((self.v, (c, st), i, self.vfull[st]))
             yield
 
     def issue_s(self):
@@ -148,6 +151,11 @@ class Model:
     def issue_pv(self):
         for i in range(self.n):
             b = i % self.p_barriers
+            yield self.vfull[i % self.ring], (i // self.ring) & 1
+            if self.cleaned(i):
+                for c in CTAS:
+                    self.vseen[c][0].arrive()
+                    yield
             yield self.pfull[b], (i // self.p_barriers) & 1
             self.pv_queue.append(i)
             yield
@@ -175,22 +183,32 @@ class Model:
                 self.pfree[c][i & 1].arrive()
             yield
 
+    # tiles with values that not every query sees, and tiles that move a reference
+    def cleaned(self, i):
+        return i % 4 == 2 or i + 1 == self.n or i + 1 in self.first
+
+    def moves(self, i):
+        return i in self.first or i % 3 == 1
+
     def softmax(self, c, g, part):
-        me, phase, pending = (c, g, part), 0, None
+        me, phase, seen, pending = (c, g, part), 0, 0, None
         for i in range(self.n):
             yield self.sfull[c][0], i & 1
             assert self.scores == i and self.s_done == i, "another tile's scores"
             self.held.add(me)
-            self.xch[c, g].arrive()
-            yield self.xch[c, g], phase & 1
-            phase += 1
+            self.vote[c, g].arrive()
+            yield self.vote[c, g], i & 1
             if part == 0:
                 self.sempty.arrive()
                 yield
+            if self.moves(i):
+                self.xch[c, g].arrive()
+                yield self.xch[c, g], phase & 1
+                phase += 1
             assert self.pv_done >= i - 2, "weights that a product still reads"
             self.p[i & 1][me] = i
             yield
-            if pending is not None or (i not in self.first and i % 3 == 1):
+            if pending is not None or (i not in self.first and self.moves(i)):
                 yield self.pfree[c][(i - 1) & 1], ((i - 1) >> 1) & 1
                 assert self.pv_done == i - 1, "an accumulator under a product"
             if pending is not None:
@@ -199,8 +217,9 @@ class Model:
                 phase += 1
                 self.flushed[me] = pending
                 pending = None
-            if (g == 0 and part == 0) or i % 4 == 2:   # sees V land, or cleans it
-                yield self.vfull[c][i % self.ring], (i // self.ring) & 1
+            if self.cleaned(i):
+                yield self.vseen[c][0], seen & 1
+                seen += 1
                 assert self.v[c, i % self.ring] == i
             self.pfull[i % self.p_barriers].arrive()
             if i + 1 == self.n or i + 1 in self.first:

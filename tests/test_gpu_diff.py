@@ -234,6 +234,32 @@ def test_values_that_are_infinite_where_they_are_seen():
         assert torch.equal(bad, want)
 
 
+@pytest.mark.parametrize("G", [1, 2, 8])
+@pytest.mark.parametrize("ctx", [600, 1337, 20000])
+def test_infinite_values_in_every_part_of_a_long_window(G, ctx):
+    # one to five query tiles of a window of 600: an infinity in a tile's own rows reaches
+    # the queries from its own on, one in an earlier tile's all of the tile
+    b = Batch(21, [ctx], [600], 2, G)
+    spots = ((ctx - 600 + 40, 0, 7), (ctx - 600 + 300, 1, 9), (ctx - 600 + 555, 0, 100))
+    for at, h, dim in spots:
+        b.vc[int(b.tables[0, at // BLOCK]), h, at % BLOCK, dim] = float("inf")
+    b.cuda()
+    out, lse = b.call(norm=False)
+    ok()
+    bad = ~torch.isfinite(out[:b.T].cpu())
+    want = torch.zeros_like(bad)
+    for at, h, dim in spots:
+        want[at - ctx + 600:, :, h * DIM + dim] = True
+    assert torch.equal(bad, want)
+    for at, h, dim in spots:
+        b.vc[int(b.tables[0, at // BLOCK]), h, at % BLOCK, dim] = 0.0
+    ref, rl, tol, ltol = R.attend(b.q, b.kc, b.vc, b.tables, b.lens, b.cu, SCALE, b.lambdas, None,
+                                  1e-5, 0.8)
+    got = out[:b.T].cpu().double()
+    assert ((got - ref).abs() <= tol)[~want].all()
+    assert ((lse[:b.T].cpu().double() - rl).abs() <= ltol).all()
+
+
 def test_short_and_long_windows_in_one_call():
     lens, qs = [900, 40, 333, 64], [200, 5, 100, 1]
     b = Batch(8, lens, qs, 4, 2).cuda()
