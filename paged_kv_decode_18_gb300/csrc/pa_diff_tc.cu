@@ -34,7 +34,7 @@
 // us of the call below.)
 //
 // Four chunks of 512 queries over 2816 to 7424 keys, 16 heads over 8: 106 us and the
-// merge's 18, 124 in all, of which the products' own operations are 64. A tile takes 1.1
+// merge's 15, 121 in all, of which the products' own operations are 64. A tile takes 1.1
 // us: its products and their hand-offs by themselves (no exponentials) 1.0 to 1.2, the
 // softmax by itself (no products) as much, and leaving the loads out changes neither. A
 // map's end (its diagonal tiles, O read out with nothing beside it) costs 3 to 4 us.
@@ -942,16 +942,23 @@ __global__ void __launch_bounds__(kThreadsT, 1)
 }
 
 // Merge the pieces of the (query tile, pair) segments that the ranges cut, both
-// maps, then difference, norm and scale. Grid (worker boundary, chunk of 32 rows): a
-// lane has a row, a warp 32 of its dims; the warps' sums of squares meet in shared
-// memory.
-constexpr int kTFixWarps = 16;
-constexpr int kTFixChunks = 2 * kRowsT / 32;
-constexpr int kTFixDims = kDiffDim / kTFixWarps;
+// maps, then difference, norm and scale. Grid (worker boundary, chunk of 8 rows): a
+// thread has 16 dims of a row, eight neighbours the same dims of the chunk (128 bytes of
+// partials), whose sums of squares meet in shared memory. 18 us after the call of the
+// head comment with chunks of 32 rows in CTAs of 16 warps, since a quarter of them came
+// in a second round on the SMs; 16 us of 16 rows, 15 of 8, for 52 MB out of L2. Four
+// pieces at a time: two are as fast there (two or three pieces to a segment) and 2 us
+// slower where 19 meet.
+constexpr int kTFixWarps = 4;
+constexpr int kTFixRows = 8;
+constexpr int kTFixChunks = 2 * kRowsT / kTFixRows;
+constexpr int kTFixDims = 16;  // of a thread
+constexpr int kTFixParts = kDiffDim / kTFixDims;
+static_assert(kTFixWarps * 32 == kTFixRows * kTFixParts, "a thread has 16 dims of a row");
 
-__global__ void __launch_bounds__(kTFixWarps * 32, 2)
+__global__ void __launch_bounds__(kTFixWarps * 32, 8)
     diff_tc_fixup_kernel(const DiffTcArgs a) {
-  __shared__ float squares_of[kTFixWarps][32];
+  __shared__ float squares_of[kTFixParts][kTFixRows];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int w = blockIdx.x;
@@ -959,9 +966,9 @@ __global__ void __launch_bounds__(kTFixWarps * 32, 2)
   const int4 d0 = __ldcg(d), d1 = __ldcg(d + 1);
   if (d0.x < 0) return;
   const int qt = d0.y, h = d0.z, last = d0.w, slot_prev = d1.x, q0 = d1.y, lq = d1.z;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int at = threadIdx.x % kTFixRows, part = threadIdx.x / kTFixRows;
   const int npieces = last - w + 2;  // workers w-1 .. last
-  const int row = blockIdx.y * 32 + lane, r = row & (kRowsT - 1);
+  const int row = blockIdx.y * kTFixRows + at, r = row & (kRowsT - 1);
   const int tok = (qt * 2 + row / kRowsT) * a.QTb + r / a.G;
   const bool live = r < a.QTb * a.G && tok < lq;
   if (!__syncthreads_or(live)) return;
@@ -1009,7 +1016,7 @@ __global__ void __launch_bounds__(kTFixWarps * 32, 2)
         for (int map = 0; map < 2; ++map) {
           if (li[map][u] == neg_inf()) continue;  // nothing was written there
           const float4* src =
-              part_rows(a, slot_of(i0 + u), map) + warp * (kTFixDims / 4) * (2 * kRowsT) + row;
+              part_rows(a, slot_of(i0 + u), map) + part * (kTFixDims / 4) * (2 * kRowsT) + row;
           float4 v[kTFixDims / 4];
 #pragma unroll
           for (int q = 0; q < kTFixDims / 4; ++q) v[q] = __ldcg(src + q * (2 * kRowsT));
@@ -1035,32 +1042,38 @@ __global__ void __launch_bounds__(kTFixWarps * 32, 2)
       squares = fmaf(y[j], y[j], squares);
     }
   }
-  squares_of[warp][lane] = squares;
+  squares_of[part][at] = squares;
+  float weight[kTFixDims];
+#pragma unroll
+  for (int q = 0; q < kTFixDims / 4; ++q) {
+    const float4 x = a.o.weight
+                         ? reinterpret_cast<const float4*>(a.o.weight + part * kTFixDims)[q]
+                         : make_float4(1.f, 1.f, 1.f, 1.f);
+    weight[4 * q] = x.x;
+    weight[4 * q + 1] = x.y;
+    weight[4 * q + 2] = x.z;
+    weight[4 * q + 3] = x.w;
+  }
   __syncthreads();
   if (!live) return;
   squares = 0.f;
 #pragma unroll
-  for (int k = 0; k < kTFixWarps; ++k) squares += squares_of[k][lane];
+  for (int k = 0; k < kTFixParts; ++k) squares += squares_of[k][at];
   const float f = diff_factor(a.o, squares);
   const int64_t qtok = (int64_t)q0 + tok;
   uint4* dst = reinterpret_cast<uint4*>(a.o.out + (qtok * (a.Hq / 2) + head) * kDiffDim +
-                                        warp * kTFixDims);
+                                        part * kTFixDims);
 #pragma unroll
   for (int q = 0; q < kTFixDims / 8; ++q) {
     uint32_t u[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int j = 8 * q + 2 * e;
-      float2 x = make_float2(f, f);
-      if (a.o.weight) {
-        x.x *= a.o.weight[warp * kTFixDims + j];
-        x.y *= a.o.weight[warp * kTFixDims + j + 1];
-      }
-      u[e] = cvt_bf16x2(y[j] * x.x, y[j + 1] * x.y);
+      u[e] = cvt_bf16x2(y[j] * (f * weight[j]), y[j + 1] * (f * weight[j + 1]));
     }
     dst[q] = make_uint4(u[0], u[1], u[2], u[3]);
   }
-  if (a.o.lse && warp == 0) {
+  if (a.o.lse && part == 0) {
     float* l = a.o.lse + qtok * a.Hq + (int64_t)(2 * h) * a.G + r % a.G;
     l[0] = lse[0];
     l[a.G] = lse[1];
