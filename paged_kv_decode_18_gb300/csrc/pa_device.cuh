@@ -397,6 +397,9 @@ __device__ inline void build_plan(const PlanInputs& in, PlanSmem& P, int* /*scra
       if (lq < in.min_lq || lq > in.max_lq) lq = 0;  // handled by another kernel
       P.qstart[s] = q0;
       P.seq_pair[s] = (lq + in.qtile - 1) / in.qtile;  // query tiles of s
+      if (in.skip_empty)
+        P.pair_off[s] =
+            lq > 0 ? in.Hkv * pair_tiles(c, lq, 0, in.qtile, in.causal, in.key_tile) : 0;
       if (s == S - 1) P.qstart[S] = in.cu_seqlens_q ? in.cu_seqlens_q[S] : S;
     } else if (in.parts <= 1) {
       P.qstart[s] = s;
@@ -421,6 +424,28 @@ __device__ inline void build_plan(const PlanInputs& in, PlanSmem& P, int* /*scra
   }
   __syncthreads();
   int npairs = varlen || in.parts <= 1 ? S : S * in.parts;
+  if (in.skip_empty) {
+    // one tile's query each: both sums side by side (two warps at least), and the pairs
+    // moved together only where a context is empty
+    if (tid < 64) {
+      int* data = tid < 32 ? P.seq_pair : P.pair_off;
+      const int n = warp0_exclusive_scan(data, S);
+      if ((tid & 31) == 0) data[S] = n;
+    }
+    __syncthreads();
+    P.npairs = P.seq_pair[S];
+    P.total = P.pair_off[S];
+    if (P.npairs == S) return;
+    for (int s0 = 0; s0 < S; s0 += nthreads) {
+      const int s = s0 + tid, at = s < S ? P.pair_off[s] : 0;
+      __syncthreads();  // pair <= s: what is written here has been read
+      if (s < S && P.seq_pair[s + 1] > P.seq_pair[s]) P.pair_off[P.seq_pair[s]] = at;
+      __syncthreads();
+    }
+    if (tid == 0) P.pair_off[P.npairs] = P.total;
+    __syncthreads();
+    return;
+  }
   if (varlen) {
     if (tid < 32) {
       const int n = warp0_exclusive_scan(P.seq_pair, S);

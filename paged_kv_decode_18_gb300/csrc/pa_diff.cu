@@ -75,12 +75,14 @@ __device__ __forceinline__ uint32_t atom_at(int row, int chunk) {
 struct CostCut {
   const PlanSmem* P;
   int Hp, nw;
+  bool narrow;  // 32-bit divisions do (a 64-bit one is 100 instructions)
   long long C;
   __device__ __forceinline__ CostCut(const PlanSmem& plan, int heads, int max_workers)
       : P(&plan), Hp(heads) {
     C = 4LL * plan.total + (long long)kSegCost4 * plan.npairs * heads;
     const long long n = C / (4 + kSegCost4);
     nw = (int)(n > max_workers ? max_workers : n);
+    narrow = C * nw < (1LL << 32);
   }
   __device__ __forceinline__ long long base(int p) const {
     return 4LL * P->pair_off[p] + (long long)kSegCost4 * p * Hp;
@@ -88,7 +90,8 @@ struct CostCut {
   __device__ __forceinline__ int start(int w) const {  // 0 <= w <= nw
     if (w <= 0) return 0;
     if (w >= nw) return P->total;
-    const long long T = ((long long)w * C) / nw;
+    const long long T = narrow ? (long long)((uint32_t)w * (uint32_t)C / (uint32_t)nw)
+                               : ((long long)w * C) / nw;
     int lo = 0, hi = P->npairs - 1;  // the pair with base(lo) < T <= base(lo + 1)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -106,7 +109,8 @@ struct CostCut {
   __device__ __forceinline__ int owner_of_last(const TilePos& t) const {
     const long long x = P->pair_off[t.p] + (long long)t.h * t.nt + t.nt - 1;
     const long long cost = 4 * x + (long long)kSegCost4 * (t.p * Hp + t.h + 1);
-    return (int)(((cost + 1) * nw - 1) / C);
+    return narrow ? (int)(((uint32_t)(cost + 1) * (uint32_t)nw - 1u) / (uint32_t)C)
+                  : (int)(((cost + 1) * nw - 1) / C);
   }
 };
 
@@ -189,8 +193,8 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   }
   TilePos cp;
   if (R0 < R1) cp = locate(P, S, Hp, R0);
-  if (lane == 0) {
-    // the segment that this boundary cuts, if it is the first to do so
+  // the segment that this boundary cuts, if it is the first to do so
+  auto describe = [&]() {
     int4 d0 = make_int4(-1, 0, 0, 0), d1 = d0;
     if (R0 < R1 && w > 0 && cp.b > 0) {
       const int A = R0 - cp.b;  // its first tile
@@ -202,8 +206,11 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     int4* d = reinterpret_cast<int4*>(a.desc + (size_t)w * kDDesc);
     d[0] = d0;
     d[1] = d1;
+  };
+  if (R0 >= R1) {
+    if (lane == 0) describe();
+    return;
   }
-  if (R0 >= R1) return;
 
   // ---- producer --------------------------------------------------------------
   TilePos pp = cp;
@@ -253,6 +260,7 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     }
   };
   for (int i = 0; i < kDStages && pidx < R1; ++i) issue(i);
+  if (lane == 0) describe();  // (while the first copies are on their way)
 
   // ---- consumer --------------------------------------------------------------
   const int r = lane >> 2, quad = lane & 3;  // this lane's row of either map
