@@ -22,6 +22,10 @@
 // The two results of a row end in the same lane, so difference, norm and scale
 // cost no exchange but the sum of squares: a segment that one warp has worked
 // through alone writes its bf16 output at once.
+// Bound by HBM: 518 MB of 256 ragged contexts in 92 us, 514 MB of 8 x 30k .. 32k in 90.5,
+// 5.6 and 5.7 TB/s, of which 5 us are launch, plan and first copy and 4 to 6 the merge;
+// between them equal ranges end up to 15 us apart, some SMs getting a tenth more than
+// others. Four short contexts: 12.3 us, all latency.
 // A warp is a worker with its own ring of 16 KB stages and an equal range of
 // the batch's (sequence, query tile, pair, block) tiles; segments that ranges
 // cut leave fp32 partials, which diff_fixup_kernel merges.
@@ -58,7 +62,9 @@ struct DiffArgs {
   int max_lq;       // longer windows belong to the tcgen05 kernel
   float* part_o;    // [NW*2][16][256]
   float* part_lse;  // [NW*2][16]
-  int* desc;        // [NW][kDDesc]
+  int* desc;        // [NW][kDDesc]: of the segment that worker w's start cuts first, or
+  int by_segment;   // of each of `segments`, where there are far fewer of those
+  int segments;
 };
 
 // byte offset of a row's 16-byte chunk (0 .. 15) in a 16 x 128 tile that came in as
@@ -183,6 +189,10 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     }
   }
 
+  if (a.by_segment && blockIdx.x == 0)  // (nor have those that the batch does not have)
+    for (int i = P.npairs * Hp + (int)threadIdx.x; i < a.segments; i += blockDim.x)
+      reinterpret_cast<int4*>(a.desc)[2 * i] = make_int4(-1, 0, 0, 0);
+
   const int w = warp * (int)gridDim.x + (int)blockIdx.x;
   int R0 = 0, R1 = 0, R0prev = 0;  // this worker's range, and where the one before begins
   if (w < cut.nw) {
@@ -200,12 +210,29 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
       const int A = R0 - cp.b;  // its first tile
       if (A >= R0prev) {
         d0 = make_int4(cp.s, cp.qt, cp.h, cut.owner_of_last(cp));
-        d1 = make_int4(A == R0prev ? 0 : 1, P.qstart[cp.s], P.qstart[cp.s + 1] - P.qstart[cp.s], 0);
+        d1 = make_int4(A == R0prev ? 0 : 1, P.qstart[cp.s], P.qstart[cp.s + 1] - P.qstart[cp.s], w);
       }
     }
-    int4* d = reinterpret_cast<int4*>(a.desc + (size_t)w * kDDesc);
-    d[0] = d0;
-    d[1] = d1;
+    int4* d = reinterpret_cast<int4*>(a.desc);
+    if (!a.by_segment) {
+      d[2 * w] = d0;
+      d[2 * w + 1] = d1;
+      return;
+    }
+    if (R0 >= R1) return;
+    if (d0.x >= 0) {
+      d[2 * (cp.p * Hp + cp.h)] = d0;
+      d[2 * (cp.p * Hp + cp.h) + 1] = d1;
+    }
+    // segments that lie in this range as a whole have no pieces
+    TilePos t = cp;
+    for (int at = R0 - cp.b;;) {
+      if (at >= R0 && at + t.nt <= R1) d[2 * (t.p * Hp + t.h)] = make_int4(-1, 0, 0, 0);
+      at += t.nt;
+      if (at >= R1) break;
+      t.b = t.nt - 1;
+      advance(P, S, Hp, t);
+    }
   };
   if (R0 >= R1) {
     if (lane == 0) describe();
@@ -528,14 +555,18 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   }
 }
 
-// Merge the pieces of (sequence, query tile, pair) segments cut by the equal
-// ranges, then difference, norm and scale. Grid (worker boundary, chunk of
-// chunk_rows rows); a CTA's warps are dealt out to its rows, several to a row where
-// there are few, each taking every n-th round of four pieces with all their loads in
-// flight. (Where segments have many pieces a CTA takes one row: 8 x 32k contexts, 47
-// pieces of 4 rows, 14 us with a CTA to a segment.) A lane holds eight of a row's 256 dims, of both maps. Partials are
-// read through L2 (ld.global.cg): other SMs wrote them.
-constexpr int kDFixWarps = 8;
+// Merge the pieces of (sequence, query tile, pair) segments cut by the workers'
+// ranges, then difference, norm and scale. Grid (worker boundary, or segment where
+// there are far fewer of those; chunk of chunk_rows rows); a CTA's warps are dealt out
+// to its rows, several to a row where there are few, each taking every n-th round of
+// four pieces with all their loads in flight. A lane holds eight of a row's 256 dims, of
+// both maps. Partials are read through L2 (ld.global.cg): other SMs wrote them. Bound by
+// launching and latency: 4 to 6 us of a call.
+// Where segments have many pieces a CTA takes one row (8 x 32k contexts, 47 pieces of 4
+// rows, 14 us with a CTA to a segment), and the grid has the segments: 32 x 4 CTAs come
+// and go 3 us sooner than 760 x 4. Elsewhere four rows or fewer get four warps: 346
+// live CTAs of eight (256 contexts of up to 4096) take a second round on the SMs, 2 us.
+constexpr int kDFixWarps = 8;  // at most
 
 struct MapSum {
   float m, sum;
@@ -557,21 +588,19 @@ __device__ __forceinline__ void join(MapSum& x, float mo, float so, const float 
 
 __global__ void __launch_bounds__(kDFixWarps * 32)
     diff_fixup_kernel(const int* desc, const float* part_o, const float* part_lse, const DiffOut out,
-                      int num_workers, int chunk_rows, int Hq, int G, int QT) {
+                      int chunk_rows, int Hq, int G, int QT) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int w = blockIdx.x;
-  if (w >= num_workers) return;
-  const int4* d = reinterpret_cast<const int4*>(desc + (size_t)w * kDDesc);
+  const int4* d = reinterpret_cast<const int4*>(desc + (size_t)blockIdx.x * kDDesc);
   const int4 d0 = __ldcg(d), d1 = __ldcg(d + 1);
   if (d0.x < 0) return;
-  const int qt = d0.y, h = d0.z, last = d0.w, slot_prev = d1.x, q0 = d1.y, lq = d1.z;
+  const int qt = d0.y, h = d0.z, last = d0.w, slot_prev = d1.x, q0 = d1.y, lq = d1.z, w = d1.w;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int npieces = last - w + 2;                       // workers w-1 .. last
   const int row0 = (int)blockIdx.y * chunk_rows;
   const int nrows = min(chunk_rows, min(QT, lq - qt * QT) * G - row0);  // 1 .. 8 of either map
   if (nrows <= 0) return;
-  const int per_row = kDFixWarps / nrows;                 // warps to a row
+  const int per_row = ((int)blockDim.x >> 5) / nrows;     // warps to a row
   const int rl = warp / per_row, group = warp - rl * per_row;
   const int r = row0 + rl;
   const bool live = rl < nrows;
@@ -881,19 +910,23 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
   a.desc = reinterpret_cast<int*>(wws);
   a.part_lse = reinterpret_cast<float*>(wws + g.ws_desc);
   a.part_o = reinterpret_cast<float*>(wws + g.ws_desc + g.ws_lse);
+  // more than eight pieces to a segment on average (if the batch fills its contexts)
+  const int64_t segments = (int64_t)g.npairs_cap * (a.Hkv / 2);
+  const bool many = (int64_t)g.workers > 8 * segments;
+  a.by_segment = many;
+  a.segments = many ? (int)segments : 0;
   if (launch_dependent(paged_diff_kernel, dim3(g.grid), dim3(kDWarps * 32), g.smem, st, tmk, tmv,
                        a) != cudaSuccess)
     return PA_ERR_CUDA;
-  // more than eight pieces to a segment on average: a CTA for each of its rows
-  const bool many = (int64_t)g.workers > 8 * (int64_t)a.S * (a.Hkv / 2);
   const int64_t tile_rows = (int64_t)(max_q_len < a.QT ? max_q_len : a.QT) * a.G;
   const int chunk = many ? 1 : kMapRows;
   // (a worker has two tiles at least: of a small call only the first ones work)
   const int64_t most = (int64_t)g.npairs_cap * (a.Hkv / 2) * a.max_blocks / 2;
-  const unsigned boundaries = (unsigned)(most < 1 ? 1 : most < g.workers ? most : g.workers);
-  if (launch_dependent(diff_fixup_kernel, dim3(boundaries, many ? (unsigned)tile_rows : 1u),
-                       dim3(kDFixWarps * 32), 0, st, (const int*)a.desc, (const float*)a.part_o,
-                       (const float*)a.part_lse, a.o, g.workers, chunk, a.Hq, a.G,
+  const int64_t boundaries = most < 1 ? 1 : most < g.workers ? most : g.workers;
+  const dim3 grid((unsigned)(many ? segments : boundaries), many ? (unsigned)tile_rows : 1u);
+  const unsigned warps = many || tile_rows > 4 ? kDFixWarps : 4;
+  if (launch_dependent(diff_fixup_kernel, grid, dim3(warps * 32), 0, st, (const int*)a.desc,
+                       (const float*)a.part_o, (const float*)a.part_lse, a.o, chunk, a.Hq, a.G,
                        a.QT) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;

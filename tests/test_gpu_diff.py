@@ -260,6 +260,45 @@ def test_infinite_values_in_every_part_of_a_long_window(G, ctx):
     assert ((lse[:b.T].cpu().double() - rl).abs() <= ltol).all()
 
 
+@pytest.mark.parametrize("lens,hkv,G", [
+    ([5000, 0, 17, 0, 500], 2, 2),                                   # many pieces, by segment
+    ([0, 0, 0, 4000], 4, 1),
+    ([16, 16, 3000], 2, 8),                                          # whole segments among them
+    ([0] + [7 + 13 * i % 90 if i % 3 else 0 for i in range(330)], 2, 1),   # mostly by boundary
+    ([9000] + [5] * 300, 2, 2),                                      # one of many pieces
+    ([40 * i for i in range(60)] + [0], 2, 5),
+])
+@pytest.mark.parametrize("fill", [0, 0x7f, 0xff])
+def test_whatever_the_workspace_held(lens, hkv, G, fill):
+    # descriptors and partials of an earlier call mean nothing; empty contexts between others
+    b = Batch(31, lens, None, hkv, G).cuda()
+    out, lse = b.call(ws_fill=fill)
+    ok()
+    b.check(out, lse)
+
+
+@pytest.mark.parametrize("lens,qs,T,max_q", [
+    ([5000, 64], [3, 1], 20, 16),     # room for more windows than there are
+    ([5000, 700], [16, 0], 16, 16),
+])
+def test_a_padded_batch_of_few_windows(lens, qs, T, max_q):
+    b = Batch(32, lens, qs, 2, 1).cuda()
+    d = b.d
+    d["q"] = torch.cat([d["q"], torch.full((T - b.T, b.hq, DIM), float("nan"), dtype=torch.bfloat16,
+                                           device="cuda")])
+    out = torch.full((T, b.hq // 2, 2 * DIM), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, b.hq), 5.0, device="cuda")
+    sh = B.shape_of(d["q"], d["kc"], d["tables"])
+    ws = B.workspace(B.pa_decode_diff_workspace_size(sh, T, max_q), "cuda")
+    ws.fill_(0x11)
+    B.pa_decode_diff(d["q"], d["kc"], d["vc"], d["tables"], d["lens"], SCALE, d["lambdas"], out, lse,
+                     cu_seqlens_q=d["cu"], max_q_len=max_q, norm_weight=d["weight"], out_scale=0.8,
+                     workspace=ws)
+    ok()
+    b.check(out, lse)
+    assert (out[b.T:] == 3.0).all() and (lse[b.T:] == 5.0).all()
+
+
 def test_short_and_long_windows_in_one_call():
     lens, qs = [900, 40, 333, 64], [200, 5, 100, 1]
     b = Batch(8, lens, qs, 4, 2).cuda()
