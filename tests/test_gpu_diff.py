@@ -277,6 +277,26 @@ def test_whatever_the_workspace_held(lens, hkv, G, fill):
     b.check(out, lse)
 
 
+@pytest.mark.parametrize("lens,qs,hkv,G", [
+    ([12900 + 77 * i for i in range(8)], None, 8, 1),          # few segments, many pieces
+    ([0, 30000, 5, 51000, 16, 0, 25000], None, 8, 2),          # empty and whole ones among them
+    ([(997 * i) % 4100 for i in range(100)], None, 8, 1),      # ragged
+    ([(997 * i) % 4100 + 4 for i in range(64)], [i % 4 for i in range(64)], 8, 2),
+    ([98000, 100], [2, 1], 8, 3),
+])
+def test_large_batches(lens, qs, hkv, G):
+    # thirty tiles of 16 keys of a pair and more for each of the workers
+    b = Batch(41 + G, lens, qs, hkv, G, heavy=2.0).cuda()
+    out, lse = b.call(ws_fill=0x7f)
+    ok()
+    b.check(out, lse)
+    for fill in (0, 0xff):
+        again, la = b.call(ws_fill=fill)
+        ok()
+        assert torch.equal(again[:b.T].view(torch.int16), out[:b.T].view(torch.int16))
+        assert torch.equal(la[:b.T].view(torch.int32), lse[:b.T].view(torch.int32))
+
+
 @pytest.mark.parametrize("lens,qs,T,max_q", [
     ([5000, 64], [3, 1], 20, 16),     # room for more windows than there are
     ([5000, 700], [16, 0], 16, 16),
