@@ -222,10 +222,12 @@ struct RowsArgs {
 // sines and cosines. (Four rows a warp: 51 us for 12,000 tokens of 16 + 8 + 8 rows; eight:
 // 36; sixteen: 33; 24: 44, too few warps left. At a decode step's 256 tokens all take the
 // 4 us of a launch.)
+// kAny's sines and cosines of 16 values want 128 registers: 46.6 us for 16,200 x 16 rows of
+// r = 72 with two CTAs to an SM, 49.3 with three, where the other layouts take 23.
 constexpr int kIter = 4;
 
 template <int MODE, int FMT>
-__global__ void __launch_bounds__(kRotWarps * 32, 3)
+__global__ void __launch_bounds__(kRotWarps * 32, MODE == kAny ? 2 : 3)
     rotate_rows_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ float exchange[MODE == kAny ? kRotWarps * 4 * kRowPad : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -338,12 +340,12 @@ struct CachedArgs {
 // eight ahead; the batch's tiles are cut into equal ranges, one per warp (tiles of a
 // sequence and head in order, so that a warp's positions follow one another).
 // Sines and cosines are made anew only where a row's turn differs from the last.
-// Measured: 8 x 24,000..28,700 keys of 8 heads by a shift 144 us (6.0 TB/s); 32 x 1024
+// Measured: 8 x 24,000..28,700 keys of 8 heads by a shift 142 us (6.1 TB/s); 32 x 1024
 // behind an eviction 29 us, of which some 7 us is the chain launch, lengths, block
 // ids and turns, first rows. (Loads of the next eight keys held ahead of the present
 // ones: 33 us, for the registers that it takes.)
 template <int MODE, int FMT>
-__global__ void __launch_bounds__(kRotWarps * 32, 3)
+__global__ void __launch_bounds__(kRotWarps * 32, MODE == kAny && FMT == kFmtBf16 ? 2 : 3)
     rotate_cached_kernel(const __grid_constant__ CachedArgs a) {
   extern __shared__ __align__(16) int area[];  // kAny: the exchange, then the plan
   float* exchange = reinterpret_cast<float*>(area);
@@ -377,11 +379,10 @@ __global__ void __launch_bounds__(kRotWarps * 32, 3)
   TilePos t = locate(P, a.S, a.Hkv, R0);
   Spin<MODE> sp;
   int spun = 0;  // the turn that sp holds (0: none yet)
-  for (int idx = R0; idx < R1; ++idx) {
-    const int phys = a.block_tables[(int64_t)t.s * a.max_blocks + t.b];
+  // a tile's block, and the turns of this lane's rows in it
+  auto fetch = [&](int& phys, int (&by)[4]) {
+    phys = a.block_tables[(int64_t)t.s * a.max_blocks + t.b];
     const int c = P.ctx[t.s];
-    int by[4];
-    bool any = false;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int pos = t.b * kBlock + i * 4 + sub;
@@ -396,12 +397,31 @@ __global__ void __launch_bounds__(kRotWarps * 32, 3)
           by[i] = a.shifts[t.s];
         }
       }
+    }
+  };
+  // (a tile ahead with bf16 keys; 8-bit ones have no registers left for it: 36 us against
+  // 33.5 for 16 x 4096 FP8 keys of 8 heads, bf16 46.9 against 47.7)
+  constexpr bool kAhead = FMT == kFmtBf16;
+  int phys_next = 0, by_next[4] = {0, 0, 0, 0};
+  if (kAhead) fetch(phys_next, by_next);
+  for (int idx = R0; idx < R1; ++idx) {
+    if (!kAhead) fetch(phys_next, by_next);
+    const int phys = phys_next, h = t.h;
+    int by[4];
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      by[i] = by_next[i];
       any = any || by[i] != 0;
+    }
+    if (idx + 1 < R1) {
+      advance(P, a.S, a.Hkv, t);
+      if (kAhead) fetch(phys_next, by_next);
     }
     const bool inside = phys >= 0 && (int64_t)phys < a.num_blocks;
     if (!inside && lane == 0) flag_error(PA_DEVERR_BLOCK_RANGE);
     if (inside && __any_sync(kFull, any)) {
-      const int64_t at = (int64_t)phys * a.Hkv + t.h;
+      const int64_t at = (int64_t)phys * a.Hkv + h;
       if constexpr (FMT == kFmtBf16) {
         uint16_t* tile = reinterpret_cast<uint16_t*>(a.kc) + at * (kBlock * kHeadDim);
 #pragma unroll
@@ -465,7 +485,6 @@ __global__ void __launch_bounds__(kRotWarps * 32, 3)
         }
       }
     }
-    if (idx + 1 < R1) advance(P, a.S, a.Hkv, t);
   }
 }
 
