@@ -65,9 +65,8 @@ __device__ __forceinline__ void quantize_row_to(const uint2 x, int lane, int8_t*
   uint32_t packed = 0u;
   if (amax > 0.f) {
     const float inv = __fdiv_rn(127.f, amax);
-    const float fs[4] = {f0, f1, f2, f3};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) packed |= int8_code(fs[j], inv) << (8 * j);
+    packed = low_bytes(int8_code(f0, inv), int8_code(f1, inv), int8_code(f2, inv),
+                       int8_code(f3, inv));
   }
   reinterpret_cast<uint32_t*>(dst)[lane] = packed;
   if (lane == 0) *scale_dst = amax > 0.f ? __fdiv_rn(amax, 127.f) : 0.f;

@@ -6,10 +6,18 @@
 
 namespace pa {
 
-// The int8 code of one value (as its low byte), inv = 127 / amax of its row.
+// The int8 code of one value as the low byte of its result, inv = 127 / amax of its row.
+// 1.5 * 2^23 added to a float of that size leaves its nearest integer, ties to even, in the
+// lowest bits. (The conversion instructions, an eighth of the addition's rate, bound the
+// int8 kernels: 53 us in the place of 43 for 16 x 4096 cached keys of 8 heads turned.)
 __device__ __forceinline__ uint32_t int8_code(float x, float inv) {
-  const float t = fminf(fmaxf(rintf(__fmul_rn(x, inv)), -127.f), 127.f);
-  return (uint32_t)(int)t & 0xffu;
+  const float t = fminf(fmaxf(__fmul_rn(x, inv), -127.f), 127.f);
+  return __float_as_uint(__fadd_rn(t, 12582912.f));
+}
+
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 // The E4M3 codes of two scaled values, the first in the low byte.
@@ -47,8 +55,8 @@ __device__ __forceinline__ uint2 codes_of8(const float* x, float inv) {
       w[i] = e4m3x2_of(__fmul_rn(f[0], inv), __fmul_rn(f[1], inv)) |
              (e4m3x2_of(__fmul_rn(f[2], inv), __fmul_rn(f[3], inv)) << 16);
     else
-      w[i] = int8_code(f[0], inv) | (int8_code(f[1], inv) << 8) | (int8_code(f[2], inv) << 16) |
-             (int8_code(f[3], inv) << 24);
+      w[i] = low_bytes(int8_code(f[0], inv), int8_code(f[1], inv), int8_code(f[2], inv),
+                       int8_code(f[3], inv));
   }
   return make_uint2(w[0], w[1]);
 }
@@ -67,8 +75,11 @@ __device__ __forceinline__ void values_of8(uint2 c, float scale, float* x) {
       x[4 * i + 3] = hi.y * scale;
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[4 * i + j] = (float)(int)(int8_t)((w[i] >> (8 * j)) & 0xffu) * scale;
+      for (int j = 0; j < 4; ++j) {
+        // code + 128 as the lowest byte of 2^23's mantissa: exact
+        const uint32_t bits = __byte_perm(w[i] ^ 0x80808080u, 0x4b000000u, 0x7440 | j);
+        x[4 * i + j] = __fadd_rn(__uint_as_float(bits), -8388736.f) * scale;
+      }
     }
   }
 }

@@ -436,6 +436,48 @@ def test_cached_keys_by_what_was_kept(lens, hkv, r, side, fmt):
     check_moved(before, pool, tables, lens, by, th, side, fmt)
 
 
+def test_int8_codes_of_ties_extremes_and_nans():
+    # amax 127, so that a value is its own code: integers, halves between (to even), tiny ones
+    x = torch.zeros(3, 1, 128)
+    x[0, 0, :127] = torch.arange(127).float() - 63.5
+    x[1, 0, :127] = torch.arange(-127, 0).float()
+    x[2, 0, :12] = torch.tensor([0.5, 1.5, -0.5, -2.5, 1e-30, -1e-38, 126.5, -126.5, 3.25, -0.0,
+                                 float("nan"), 7.0])
+    x[:, 0, 127] = 127.0
+    x = x.to(torch.bfloat16).cuda()
+    kc, vc = empty_pool(1, 1, "int8"), empty_pool(1, 1, "int8")
+    slots = torch.arange(3, dtype=torch.int64, device="cuda")
+    plain_write(x, x, slots, kc, vc, "int8")
+    ok()
+    got = kc[0, 0, :384].view(torch.int8).view(3, 128).cpu()
+    want = x[:, 0].float().cpu().round()
+    want = torch.where(want.isnan(), torch.tensor(-127.0), want).to(torch.int8)
+    assert torch.equal(got, want)
+    assert torch.equal(vc, kc)
+    assert (kc[0, 0, 2048:2060].view(torch.float32).cpu() == 1.0).all()
+
+
+def test_every_int8_code_passes_a_turn_by_nothing():
+    # an angle of zero: read as values, turned, written as codes again
+    codes = torch.empty(16, 128, dtype=torch.int8)
+    codes[0::2] = torch.arange(-127, 1).to(torch.int8)
+    codes[1::2] = torch.arange(0, 128).to(torch.int8)
+    pool = torch.zeros(1, 1, TILE, dtype=torch.uint8)
+    pool[0, 0, :2048] = codes.view(torch.uint8).flatten()
+    scales = 2.0 ** (torch.arange(16) * 5.0 - 40) * (1 + torch.arange(16) / 37)
+    pool[0, 0, 2048:] = scales.float().view(torch.uint8)
+    pool = pool.cuda()
+    before = pool.clone()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    B.pa_rotate_cached(pool, torch.zeros(1, 1, **i32), torch.tensor([16], **i32),
+                       B.make_rotation_from([0.0] * 64), shifts=torch.tensor([3], **i32),
+                       kv_format=B.PA_KV_INT8)
+    ok()
+    assert torch.equal(pool[0, 0, :2048], before[0, 0, :2048])
+    a, b = (x[0, 0, 2048:].view(torch.float32).cpu() for x in (pool, before))
+    assert ((a - b).abs() <= 2.0 ** -22 * b).all()   # code times scale, amax over 127: two roundings
+
+
 def test_moved_keys_leave_out_the_magnitude():
     g = torch.Generator().manual_seed(3)
     tables, blocks = tables_of(g, [40])
