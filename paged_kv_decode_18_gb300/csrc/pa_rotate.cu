@@ -70,6 +70,16 @@ struct Lane {
   __device__ __forceinline__ int dim(int e) const { return (e < 8 ? a : b) * 8 + (e & 7); }
 };
 
+// The rotation's turns in shared memory, a word of padding after every eight: a warp's
+// lanes want eight of them at a time, which the constant bank gives one by one (32 x 1024
+// cached keys behind an eviction 29.0 us, with sines made anew in every row; 26.2 so).
+constexpr int kTurns = 64 + 8;
+__device__ __forceinline__ int turn_at(int pair) { return pair + (pair >> 3); }
+__device__ __forceinline__ void load_turns(unsigned long long* turns, const pa_rotation& rot) {
+  if (threadIdx.x < 64) turns[turn_at(threadIdx.x)] = rot.turns[threadIdx.x];
+  __syncthreads();
+}
+
 // Cosines and sines for a lane's values at one position. kHalf: of the pairs
 // (value j, value 8 + j); kSide: of the pairs (value 2j, value 2j + 1); kAny: of
 // each value on its own, the sine with the sign that its side takes.
@@ -77,22 +87,25 @@ template <int MODE>
 struct Spin {
   static constexpr int N = MODE == kAny ? 16 : 8;
   float c[N], s[N];
-  __device__ __forceinline__ void set(const pa_rotation& rot, const Lane<MODE>& me, int pos,
-                                      float magnitude, float sign) {
+  __device__ __forceinline__ void set(const unsigned long long* turns, int r,
+                                      const Lane<MODE>& me, int pos, float magnitude, float sign) {
+    // (volatile: read where they are wanted, or a loop around this would hold them all)
+    const volatile unsigned long long* mine =
+        turns + (MODE == kHalf ? turn_at(me.c * 8) : MODE == kSide ? turn_at(me.c * 4) : 0);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      int pair;
+      int at;
       float sg = sign;
       if constexpr (MODE == kHalf) {
-        pair = me.c * 8 + j;
+        at = j;  // pair c * 8 + j
       } else if constexpr (MODE == kSide) {
-        pair = me.dim(2 * j) >> 1;
+        at = j < 4 ? j : turn_at(32) + j - 4;  // pairs c * 4 + j, 32 + c * 4 + j - 4
       } else {
-        const int d = me.dim(j), h = rot.rot_dim >> 1;
-        pair = d < h ? d : (d < 2 * h ? d - h : 0);
+        const int d = me.dim(j), h = r >> 1;
+        at = turn_at(d < h ? d : (d < 2 * h ? d - h : 0));
         if (d < h) sg = -sign;
       }
-      const unsigned long long phase = rot.turns[pair] * (unsigned long long)(long long)pos;
+      const unsigned long long phase = mine[at] * (unsigned long long)(long long)pos;
       // the phase's upper 23 bits as the fraction of a number in [1, 2), half a turn on, so
       // that 1.5 stands for 0: an integer conversion would take a third turn on the unit
       // that sine and cosine share
@@ -107,7 +120,10 @@ struct Spin {
 
 // Turns a lane's values. kAny: rows holds this warp's four rows of shared
 // memory; the whole warp calls it.
-constexpr int kRowPad = kHeadDim + 4;
+// (a word more every 32, and rows 134 apart: a warp's accesses, eight words apart in four
+// rows, then fall into 32 banks; 4-way conflicts made these layouts twice as slow)
+constexpr int kRowPad = kHeadDim + 6;
+__device__ __forceinline__ int skewed(int d) { return d + (d >> 5); }
 
 template <int MODE>
 __device__ __forceinline__ void turn(float (&f)[16], const Spin<MODE>& sp, const Lane<MODE>& me,
@@ -133,13 +149,13 @@ __device__ __forceinline__ void turn(float (&f)[16], const Spin<MODE>& sp, const
     float* row = rows + sub * kRowPad;
     __syncwarp();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) row[me.dim(e)] = f[e];
+    for (int e = 0; e < 16; ++e) row[skewed(me.dim(e))] = f[e];
     __syncwarp();
     const int h = r >> 1;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int d = me.dim(e);
-      if (d < r) f[e] = f[e] * sp.c[e] + row[d < h ? d + h : d - h] * sp.s[e];
+      if (d < r) f[e] = f[e] * sp.c[e] + row[skewed(d < h ? d + h : d - h)] * sp.s[e];
     }
   }
 }
@@ -220,8 +236,9 @@ struct RowsArgs {
 
 // A warp turns 16 rows of one token, four at a time, all loads first, with one set of
 // sines and cosines. (Four rows a warp: 51 us for 12,000 tokens of 16 + 8 + 8 rows; eight:
-// 36; sixteen: 33; 24: 44, too few warps left. At a decode step's 256 tokens all take the
-// 4 us of a launch.)
+// 36; sixteen: 33; 24: 44, too few warps left; all before turns lay in shared memory. At a decode step's 256 tokens all take the
+// 4 us of a launch.) Measured: 16,200 x 16 rows 22.6 us, 5.9 TB/s; 12,000 tokens into the
+// cache 32.2 us, 6.2 TB/s.
 // kAny's sines and cosines of 16 values want 128 registers: 46.6 us for 16,200 x 16 rows of
 // r = 72 with two CTAs to an SM, 49.3 with three, where the other layouts take 23.
 constexpr int kIter = 4;
@@ -230,6 +247,8 @@ template <int MODE, int FMT>
 __global__ void __launch_bounds__(kRotWarps * 32, MODE == kAny ? 2 : 3)
     rotate_rows_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ float exchange[MODE == kAny ? kRotWarps * 4 * kRowPad : 1];
+  __shared__ unsigned long long turns[kTurns];
+  load_turns(turns, a.rot);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int w = (int)blockIdx.x * kRotWarps + warp;
   const Lane<MODE> me(lane, a.rot.rot_dim);
@@ -268,7 +287,7 @@ __global__ void __launch_bounds__(kRotWarps * 32, MODE == kAny ? 2 : 3)
     }
   }
   Spin<MODE> sp;
-  if (r0 < a.Hq + a.Hkv) sp.set(a.rot, me, a.positions[t], a.rot.magnitude, a.sign);
+  if (r0 < a.Hq + a.Hkv) sp.set(turns, a.rot.rot_dim, me, a.positions[t], a.rot.magnitude, a.sign);
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     if (r0 + i * 4 >= total) break;  // the same for the whole warp
@@ -340,16 +359,18 @@ struct CachedArgs {
 // eight ahead; the batch's tiles are cut into equal ranges, one per warp (tiles of a
 // sequence and head in order, so that a warp's positions follow one another).
 // Sines and cosines are made anew only where a row's turn differs from the last.
-// Measured: 8 x 24,000..28,700 keys of 8 heads by a shift 142 us (6.1 TB/s); 32 x 1024
-// behind an eviction 29 us, of which some 7 us is the chain launch, lengths, block
+// Measured: 8 x 24,000..28,700 keys of 8 heads by a shift 143 us (6.0 TB/s); 32 x 1024
+// behind an eviction 26 us, of which some 7 us is the chain launch, lengths, block
 // ids and turns, first rows. (Loads of the next eight keys held ahead of the present
 // ones: 33 us, for the registers that it takes.)
 template <int MODE, int FMT>
 __global__ void __launch_bounds__(kRotWarps * 32, MODE == kAny && FMT == kFmtBf16 ? 2 : 3)
     rotate_cached_kernel(const __grid_constant__ CachedArgs a) {
-  extern __shared__ __align__(16) int area[];  // kAny: the exchange, then the plan
-  float* exchange = reinterpret_cast<float*>(area);
-  int* plan = area + (MODE == kAny ? kRotWarps * 4 * kRowPad : 0);
+  extern __shared__ __align__(16) int area[];  // turns, kAny: the exchange, the plan
+  unsigned long long* turns = reinterpret_cast<unsigned long long*>(area);
+  float* exchange = reinterpret_cast<float*>(turns + kTurns);
+  int* plan = area + 2 * kTurns + (MODE == kAny ? kRotWarps * 4 * kRowPad : 0);
+  load_turns(turns, a.rot);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Lane<MODE> me(lane, a.rot.rot_dim);
   const int sub = lane >> 3;
@@ -400,7 +421,7 @@ __global__ void __launch_bounds__(kRotWarps * 32, MODE == kAny && FMT == kFmtBf1
     }
   };
   // (a tile ahead with bf16 keys; 8-bit ones have no registers left for it: 36 us against
-  // 33.5 for 16 x 4096 FP8 keys of 8 heads, bf16 46.9 against 47.7)
+  // 33.5 for 16 x 4096 FP8 keys of 8 heads, bf16 46.4 against 47.7)
   constexpr bool kAhead = FMT == kFmtBf16;
   int phys_next = 0, by_next[4] = {0, 0, 0, 0};
   if (kAhead) fetch(phys_next, by_next);
@@ -440,7 +461,7 @@ __global__ void __launch_bounds__(kRotWarps * 32, MODE == kAny && FMT == kFmtBf1
           for (int u = 0; u < 2; ++u) {
             const int turned = by[i0 + u];
             if (__any_sync(kFull, turned != spun && turned != 0)) {
-              sp.set(a.rot, me, turned, 1.f, 1.f);
+              sp.set(turns, a.rot.rot_dim, me, turned, 1.f, 1.f);
               spun = turned;
             }
             float f[16];
@@ -474,7 +495,7 @@ __global__ void __launch_bounds__(kRotWarps * 32, MODE == kAny && FMT == kFmtBf1
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (__any_sync(kFull, by[i] != spun && by[i] != 0)) {
-            sp.set(a.rot, me, by[i], 1.f, 1.f);
+            sp.set(turns, a.rot.rot_dim, me, by[i], 1.f, 1.f);
             spun = by[i];
           }
           float f[16];
@@ -741,7 +762,7 @@ extern "C" int pa_rotate_cached(void* k_cache, int kv_format, const int32_t* blo
   DeviceInfo dev;
   if (!current_device_info(&dev)) return PA_ERR_CUDA;
   const int mode = mode_of(rot);
-  const size_t smem = sizeof(int) * (4 * (size_t)shape->num_seqs + 3) +
+  const size_t smem = sizeof(int) * (4 * (size_t)shape->num_seqs + 3 + 2 * kTurns) +
                       (mode == kAny ? sizeof(float) * kRotWarps * 4 * kRowPad : 0);
   if (smem > (size_t)dev.max_smem_optin) return PA_ERR_UNSUPPORTED;
   // flat tile indices are 32-bit
