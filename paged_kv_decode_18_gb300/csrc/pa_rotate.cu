@@ -235,10 +235,10 @@ struct RowsArgs {
 };
 
 // A warp turns 16 rows of one token, four at a time, all loads first, with one set of
-// sines and cosines. (Four rows a warp: 51 us for 12,000 tokens of 16 + 8 + 8 rows; eight:
-// 36; sixteen: 33; 24: 44, too few warps left; all before turns lay in shared memory. At a decode step's 256 tokens all take the
-// 4 us of a launch.) Measured: 16,200 x 16 rows 22.6 us, 5.9 TB/s; 12,000 tokens into the
-// cache 32.2 us, 6.2 TB/s.
+// sines and cosines. Measured: 16,200 x 16 rows 22.5 us, 5.9 TB/s; 12,000 tokens of 16 + 8
+// + 8 rows into the cache 32.1 us, 6.2 TB/s. (Eight rows a warp: 23.5 and 37.8; twelve: 26.9
+// and 34.9; twenty: 23.1 and 37.8. At a decode step's 256 tokens all take the 4 us of a
+// launch.)
 // kAny's sines and cosines of 16 values want 128 registers: 46.6 us for 16,200 x 16 rows of
 // r = 72 with two CTAs to an SM, 49.3 with three, where the other layouts take 23.
 constexpr int kIter = 4;
