@@ -771,10 +771,10 @@ int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffG
 // The kernels of a call. A window whose rows of a KV head (query tokens x group) are
 // fewer than kTcMinRows goes through warp tiles of eight rows, the others through
 // tcgen05 tiles of 256; more than eight query heads to a KV head always do. Measured,
-// warp tiles against tcgen05, two heads to a KV head: 32 x 4096 keys 16 rows 165 against
-// 203 us, 24 rows 217 against 204, 32 rows 265 against 194; 4 x 2048 keys 31 against 35,
-// 35 against 35, 38 against 34; 64 x 512 keys 47 against 90, 61 against 92, 77 against
-// 89, and 48 rows 99 against 93.
+// warp tiles against tcgen05, two heads to a KV head: 32 x 4096 keys 16 rows 163 against
+// 184 us, 24 rows 214 against 185, 32 rows 263 against 182; 4 x 2048 keys 22 against 33,
+// 29 against 33, 31 against 33, 48 rows 38 against 33; 64 x 512 keys 47 against 90, 62
+// against 91, 77 against 90, 48 rows 100 against 92.
 constexpr int kMaxGroup = 128;
 constexpr int kTcMinRows = 32;
 
