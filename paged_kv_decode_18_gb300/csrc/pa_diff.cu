@@ -25,7 +25,7 @@
 // Bound by HBM: 518 MB of 256 ragged contexts in 92 us, 514 MB of 8 x 30k .. 32k in 90.5,
 // 5.6 and 5.7 TB/s, of which 5 us are launch, plan and first copy and 4 to 6 the merge;
 // between them equal ranges end up to 15 us apart, some SMs getting a tenth more than
-// others. Four short contexts: 12.3 us, all latency.
+// others. Four short contexts, a CTA to a segment: 10.4 us, all latency.
 // A warp is a worker with its own ring of 16 KB stages and an equal range of
 // the batch's (sequence, query tile, pair, block) tiles; segments that ranges
 // cut leave fp32 partials, which diff_fixup_kernel merges.
@@ -45,6 +45,9 @@ constexpr int kDStages = 2;
 // what a segment start weighs in the cut, in quarters of a tile
 constexpr int kSegCost4 = 6;
 constexpr int kDDesc = 8;
+// a row of a part in shared memory: eight words apart, so that a warp's stores spread
+constexpr int kPartStride = kDiffDim + 8;
+static_assert(kDRows * kPartStride * 4 <= kDStages * kDStage, "a warp's parts in its ring");
 
 struct DiffArgs {
   const uint16_t* q;
@@ -120,6 +123,64 @@ struct CostCut {
   }
 };
 
+struct MapSum {
+  float m, sum;
+  float acc[8];
+};
+
+// Adds (m, sum, acc) of another group.
+__device__ __forceinline__ void join(MapSum& x, float mo, float so, const float (&ao)[8]) {
+  if (mo == neg_inf()) return;
+  const float mn = fmaxf(x.m, mo);
+  const float mine = x.m == neg_inf() ? 0.f : ex2((x.m - mn) * kLog2e);
+  const float other = ex2((mo - mn) * kLog2e);
+  x.sum = x.sum * mine + so * other;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x.acc[j] = x.acc[j] * mine + ao[j] * other;
+  x.m = mn;
+  if (mo != mo) x.m = x.sum = mo;  // a NaN stays one
+}
+
+// Difference, norm and scale of a query row whose maps are merged: row r of a query
+// tile, eight dims a lane.
+__device__ __forceinline__ void finish_row(const MapSum (&x)[2], const DiffOut& out, int h, int r,
+                                           int64_t qtok, int Hq, int G, int lane) {
+  const int head = h * G + r % G;
+  const float lam = out.lambdas[head];
+  const float inv0 = x[0].sum != 0.f ? 1.f / x[0].sum : 0.f;
+  const float inv1 = x[1].sum != 0.f ? 1.f / x[1].sum : 0.f;
+  float y[8], squares = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    y[j] = diff_value(x[0].acc[j], inv0, x[1].acc[j], inv1, lam);
+    squares = fmaf(y[j], y[j], squares);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) squares += __shfl_xor_sync(kFull, squares, o);
+  const float f = diff_factor(out, squares);
+  if (out.weight) {
+    const float4* wt = reinterpret_cast<const float4*>(out.weight + lane * 8);
+    const float4 w0 = wt[0], w1 = wt[1];
+    const float ws[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] *= f * ws[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] *= f;
+  }
+  *reinterpret_cast<uint4*>(out.out + (qtok * (Hq / 2) + head) * kDiffDim + lane * 8) =
+      make_uint4(cvt_bf16x2(y[0], y[1]), cvt_bf16x2(y[2], y[3]), cvt_bf16x2(y[4], y[5]),
+                 cvt_bf16x2(y[6], y[7]));
+  if (out.lse && lane == 0) {
+    float* l = out.lse + qtok * Hq + (int64_t)(2 * h) * G + r % G;
+    l[0] = x[0].sum != 0.f ? x[0].m + lg2(x[0].sum) * kLn2 : neg_inf();
+    l[G] = x[1].sum != 0.f ? x[1].m + lg2(x[1].sum) * kLn2 : neg_inf();
+  }
+}
+
+// kWhole: a CTA has a segment for itself, an equal part of its tiles a warp, and merges
+// in shared memory: no second grid.
+template <bool kWhole>
 __global__ void __launch_bounds__(kDWarps * 32, 1)
     paged_diff_kernel(const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const DiffArgs a) {
@@ -142,6 +203,8 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   // loads a lane, few of them in flight beside 128 accumulators, cost a ragged batch of
   // short contexts a third of its time
   __shared__ float2 weights[kDiffDim / 2];
+  __shared__ float part_lse[kWhole ? kDWarps : 1][kDRows];
+  if (kWhole && lane < kDRows) part_lse[warp][lane] = neg_inf();  // a warp without tiles
 
   if (lane == 0) {
     for (int i = 0; i < kDStages; ++i) mbar_init(smem_addr(&bars[i]), 1);
@@ -195,7 +258,13 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
 
   const int w = warp * (int)gridDim.x + (int)blockIdx.x;
   int R0 = 0, R1 = 0, R0prev = 0;  // this worker's range, and where the one before begins
-  if (w < cut.nw) {
+  if constexpr (kWhole) {
+    const int p = (int)blockIdx.x / Hp, h = (int)blockIdx.x - p * Hp;
+    if (p >= P.npairs) return;
+    const int o0 = P.pair_off[p], nt = (P.pair_off[p + 1] - o0) / Hp;
+    R0 = o0 + h * nt + nt * warp / kDWarps;
+    R1 = o0 + h * nt + nt * (warp + 1) / kDWarps;
+  } else if (w < cut.nw) {
     const int at = cut.start(w - 1 + (lane < 3 ? lane : 1));
     R0prev = __shfl_sync(kFull, at, 0);
     R0 = __shfl_sync(kFull, at, 1);
@@ -234,7 +303,7 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
       advance(P, S, Hp, t);
     }
   };
-  if (R0 >= R1) {
+  if (!kWhole && R0 >= R1) {
     if (lane == 0) describe();
     return;
   }
@@ -287,7 +356,7 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     }
   };
   for (int i = 0; i < kDStages && pidx < R1; ++i) issue(i);
-  if (lane == 0) describe();  // (while the first copies are on their way)
+  if (!kWhole && lane == 0) describe();  // (while the first copies are on their way)
 
   // ---- consumer --------------------------------------------------------------
   const int r = lane >> 2, quad = lane & 3;  // this lane's row of either map
@@ -349,7 +418,8 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
         }
         mbar_wait_bounded(smem_addr(&bars[stage]), parity);
       }
-      return;
+      if (!kWhole) return;
+      break;  // (its results are of no use; the others wait for it below)
     }
     const int key0 = cp.b * kBlock;
     // keys past the context may hold anything: zero those V rows so that
@@ -508,7 +578,19 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
         inv[i] = x != 0.f ? 1.f / x : 0.f;
         lse[i] = x != 0.f ? (m_r[i] + lg2(x)) * kLn2 : neg_inf();
       }
-      if (piece_b0 == 0 && cp.b == cp.nt - 1) {
+      if constexpr (kWhole) {
+        // the warp's ring is done with: its rows' parts go there
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float* dst = reinterpret_cast<float*>(wbuf) + (i * kMapRows + r) * kPartStride + quad * 2;
+#pragma unroll
+          for (int n = 0; n < 32; ++n)
+            *reinterpret_cast<float2*>(dst + n * 8) =
+                make_float2(o[n][2 * i] * inv[i], o[n][2 * i + 1] * inv[i]);
+          if (quad == 0) part_lse[warp][i * kMapRows + r] = lse[i];
+        }
+      } else if (piece_b0 == 0 && cp.b == cp.nt - 1) {
         const int head = cp.h * G + r % G;
         float squares = 0.f;
 #pragma unroll
@@ -553,6 +635,31 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     }
     if (idx + 1 < R1) advance(P, S, Hp, cp);
   }
+  if constexpr (kWhole) {
+    __syncthreads();
+    const int p = (int)blockIdx.x / Hp, h = (int)blockIdx.x - p * Hp;
+    const int s = upper_index(P.seq_pair, 0, S, p), qt = p - P.seq_pair[s];
+    const int nrows = min(QT, P.qstart[s + 1] - P.qstart[s] - qt * QT) * G;
+    for (int row = warp; row < nrows; row += kDWarps) {
+      MapSum x[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[i].m = neg_inf();
+        x[i].sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i].acc[j] = 0.f;
+        for (int k = 0; k < kDWarps; ++k) {
+          const float4* src = reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(smem + k * kDStages * kDStage) +
+              (i * kMapRows + row) * kPartStride + lane * 8);
+          const float4 a0 = src[0], a1 = src[1];
+          const float ao[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+          join(x[i], part_lse[k][i * kMapRows + row], 1.f, ao);
+        }
+      }
+      finish_row(x, a.o, h, row, (int64_t)P.qstart[s] + qt * QT + row / G, Hq, G, lane);
+    }
+  }
 }
 
 // Merge the pieces of (sequence, query tile, pair) segments cut by the workers'
@@ -567,24 +674,6 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
 // and go 3 us sooner than 760 x 4. Elsewhere four rows or fewer get four warps: 346
 // live CTAs of eight (256 contexts of up to 4096) take a second round on the SMs, 2 us.
 constexpr int kDFixWarps = 8;  // at most
-
-struct MapSum {
-  float m, sum;
-  float acc[8];
-};
-
-// Adds (m, sum, acc) of another group.
-__device__ __forceinline__ void join(MapSum& x, float mo, float so, const float (&ao)[8]) {
-  if (mo == neg_inf()) return;
-  const float mn = fmaxf(x.m, mo);
-  const float mine = x.m == neg_inf() ? 0.f : ex2((x.m - mn) * kLog2e);
-  const float other = ex2((mo - mn) * kLog2e);
-  x.sum = x.sum * mine + so * other;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x.acc[j] = x.acc[j] * mine + ao[j] * other;
-  x.m = mn;
-  if (mo != mo) x.m = x.sum = mo;  // a NaN stays one
-}
 
 __global__ void __launch_bounds__(kDFixWarps * 32)
     diff_fixup_kernel(const int* desc, const float* part_o, const float* part_lse, const DiffOut out,
@@ -688,38 +777,7 @@ __global__ void __launch_bounds__(kDFixWarps * 32)
     }
   }
   if (!live || group > 0) return;
-  const int head = h * G + r % G;
-  const float lam = out.lambdas[head];
-  const float inv0 = x[0].sum != 0.f ? 1.f / x[0].sum : 0.f;
-  const float inv1 = x[1].sum != 0.f ? 1.f / x[1].sum : 0.f;
-  float y[8], squares = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    y[j] = diff_value(x[0].acc[j], inv0, x[1].acc[j], inv1, lam);
-    squares = fmaf(y[j], y[j], squares);
-  }
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) squares += __shfl_xor_sync(kFull, squares, o);
-  const float f = diff_factor(out, squares);
-  if (out.weight) {
-    const float4* wt = reinterpret_cast<const float4*>(out.weight + lane * 8);
-    const float4 w0 = wt[0], w1 = wt[1];
-    const float ws[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] *= f * ws[j];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] *= f;
-  }
-  const int64_t qtok = (int64_t)q0 + qt * QT + r / G;
-  *reinterpret_cast<uint4*>(out.out + (qtok * (Hq / 2) + head) * kDiffDim + lane * 8) =
-      make_uint4(cvt_bf16x2(y[0], y[1]), cvt_bf16x2(y[2], y[3]), cvt_bf16x2(y[4], y[5]),
-                 cvt_bf16x2(y[6], y[7]));
-  if (out.lse && lane == 0) {
-    float* l = out.lse + qtok * Hq + (int64_t)(2 * h) * G + r % G;
-    l[0] = x[0].sum != 0.f ? x[0].m + lg2(x[0].sum) * kLn2 : neg_inf();
-    l[G] = x[1].sum != 0.f ? x[1].m + lg2(x[1].sum) * kLn2 : neg_inf();
-  }
+  finish_row(x, out, h, r, (int64_t)q0 + qt * QT + r / G, Hq, G, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -759,7 +817,9 @@ int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffG
   const size_t plan = sizeof(int) * ((size_t)g->npairs_cap + 1 + 3 * (size_t)S + 2);
   g->smem = 1024 + (size_t)kDWarps * kDStages * kDStage + kDWarps * kDStages * 8 + plan;
   if (g->smem + kDiffDim * 4 > (size_t)dev.max_smem_optin) return PA_ERR_UNSUPPORTED;
-  if (!raise_smem_limit(reinterpret_cast<const void*>(paged_diff_kernel), kDiffDim * 4))
+  if (!raise_smem_limit(reinterpret_cast<const void*>(paged_diff_kernel<false>), kDiffDim * 4) ||
+      !raise_smem_limit(reinterpret_cast<const void*>(paged_diff_kernel<true>),
+                        2 * 1024))  // (the ring's alignment rounds 1.3 KB up)
     return PA_ERR_CUDA;
   g->ws_desc = round_up(sizeof(int) * kDDesc * (size_t)g->workers, 256);
   g->ws_lse = round_up(sizeof(float) * 2 * kDRows * (size_t)g->workers, 256);
@@ -776,6 +836,15 @@ int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffG
 // 29 against 33, 31 against 33, 48 rows 38 against 33; 64 x 512 keys 47 against 90, 62
 // against 91, 77 against 90, 48 rows 100 against 92.
 constexpr int kMaxGroup = 128;
+
+// Whether every segment gets a CTA, which ends in one grid, in the place of a cut over all
+// warps and a second grid. Without: 12.4 us for 16 segments of 24 blocks, 13.1 for 32
+// blocks, 13.7 for 64, 22.6 and 32.2 for 128 segments of 32 and 64; with: 10.4, 13.6, 20.3,
+// 18.0 and 27.4. The bound on the table keeps a batch whose contexts differ from waiting
+// long for one of them.
+bool whole_segments(int64_t segments, int max_blocks, int sms) {
+  return segments <= sms && max_blocks <= (3 * segments >= 2 * sms ? 64 : 28);
+}
 constexpr int kTcMinRows = 32;
 
 struct DiffPlan {
@@ -912,10 +981,15 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
   a.part_o = reinterpret_cast<float*>(wws + g.ws_desc + g.ws_lse);
   // more than eight pieces to a segment on average (if the batch fills its contexts)
   const int64_t segments = (int64_t)g.npairs_cap * (a.Hkv / 2);
+  if (whole_segments(segments, a.max_blocks, g.grid))
+    return launch_dependent(paged_diff_kernel<true>, dim3((unsigned)segments), dim3(kDWarps * 32),
+                            g.smem, st, tmk, tmv, a) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
   const bool many = (int64_t)g.workers > 8 * segments;
   a.by_segment = many;
   a.segments = many ? (int)segments : 0;
-  if (launch_dependent(paged_diff_kernel, dim3(g.grid), dim3(kDWarps * 32), g.smem, st, tmk, tmv,
+  if (launch_dependent(paged_diff_kernel<false>, dim3(g.grid), dim3(kDWarps * 32), g.smem, st, tmk, tmv,
                        a) != cudaSuccess)
     return PA_ERR_CUDA;
   const int64_t tile_rows = (int64_t)(max_q_len < a.QT ? max_q_len : a.QT) * a.G;

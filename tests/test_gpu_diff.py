@@ -146,6 +146,37 @@ WINDOWS = [
 ]
 
 
+@pytest.mark.parametrize("lens,hkv,G", DECODE)
+def test_one_query_per_sequence_under_a_wide_table(lens, hkv, G):
+    # the table's width chooses how the batch is cut
+    b = Batch(len(lens) * 100 + lens[0] + G, lens, None, hkv, G, width=400, heavy=4.0).cuda()
+    out, lse = b.call(ws_fill=0xFF)
+    ok()
+    b.check(out, lse)
+
+
+@pytest.mark.parametrize("lens,qs,hkv,G", WINDOWS)
+def test_windows_under_a_wide_table(lens, qs, hkv, G):
+    b = Batch(sum(lens) + hkv, lens, qs, hkv, G, width=400).cuda()
+    out, lse = b.call(ws_fill=0xFF)
+    ok()
+    b.check(out, lse)
+
+
+@pytest.mark.parametrize("lens,hkv,G", [
+    ([1000, 3, 1024, 0, 700] + [16 * i + 5 for i in range(45)], 4, 2),   # a CTA to 100 segments
+    ([500] * 38, 8, 1), ([448, 1, 0, 2], 2, 8), ([449], 2, 3), ([5, 80, 79, 81], 4, 1),
+])
+def test_segments_of_one_cta(lens, hkv, G):
+    b = Batch(51 + G, lens, None, hkv, G, heavy=3.0).cuda()
+    out, lse = b.call(ws_fill=0x7f)
+    ok()
+    b.check(out, lse)
+    again, _ = b.call(norm=True, with_lse=False)
+    ok()
+    assert torch.equal(again[:b.T].view(torch.int16), out[:b.T].view(torch.int16))
+
+
 @pytest.mark.parametrize("lens,qs,hkv,G", WINDOWS)
 @pytest.mark.parametrize("causal", [True, False])
 def test_windows(lens, qs, hkv, G, causal):
