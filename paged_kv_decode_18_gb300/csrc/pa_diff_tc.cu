@@ -33,8 +33,8 @@
 // shared memory only then. (Exchanging them every tile, with an mbarrier: 365 clocks, 7
 // us of the call below.)
 //
-// Four chunks of 512 queries over 2816 to 7424 keys, 16 heads over 8: 106 us and the
-// merge's 15, 121 in all, of which the products' own operations are 64. A tile takes 1.1
+// Four chunks of 512 queries over 2816 to 7424 keys, 16 heads over 8: 104 us and the
+// merge's 15, 119 in all, of which the products' own operations are 64. A tile takes 1.1
 // us: its products and their hand-offs by themselves (no exponentials) 1.0 to 1.2, the
 // softmax by itself (no products) as much, and leaving the loads out changes neither. A
 // map's end (its diagonal tiles, O read out with nothing beside it) costs 3 to 4 us.
@@ -336,6 +336,26 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   const int R0 = cut.start(w), R1 = cut.start(w + 1);
   if (R0 >= R1) return;
 
+  // map and key tile of a segment's tile b
+  auto map_of = [](const TilePos& t) { return 2 * t.b >= t.nt ? 1 : 0; };
+  auto key_tile_of = [&](const TilePos& t) { return t.b - map_of(t) * (t.nt >> 1); };
+  auto nblocks_of = [&](const TilePos& tp) {
+    const int nb_seq = (P.ctx[tp.s] + kBlock - 1) / kBlock;
+    return min(kBlocksT, nb_seq - key_tile_of(tp) * kBlocksT);
+  };
+  auto fetch_ids = [&](const TilePos& tp) -> int {
+    return lane < nblocks_of(tp)
+               ? a.block_tables[(size_t)tp.s * a.max_blocks + key_tile_of(tp) * kBlocksT + lane]
+               : 0;
+  };
+  // the producers' first tile, its block ids on their way while the pair meets (2 us of
+  // the call of the head comment)
+  TilePos t0;
+  int ids0 = 0;
+  if (warp == 0 || warp == kVWarp) {
+    t0 = locate(P, S, Hp, R0);
+    ids0 = fetch_ids(t0);
+  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(tmem_slot)),
@@ -365,9 +385,6 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   auto wait_all = [&](int b, uint32_t parity) -> bool {
     return __all_sync(kFull, wait(b, parity));
   };
-  // map and key tile of a segment's tile b
-  auto map_of = [](const TilePos& t) { return 2 * t.b >= t.nt ? 1 : 0; };
-  auto key_tile_of = [&](const TilePos& t) { return t.b - map_of(t) * (t.nt >> 1); };
   // keys before it are seen by every query of the tile
   auto safe_keys = [&](const TilePos& t) {
     const int c = P.ctx[t.s];
@@ -379,19 +396,10 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   if (warp == 0 || warp == kVWarp) {
     // ------------------------------------------------------------------ producers
     const bool is_k = warp == 0;
-    TilePos t = locate(P, S, Hp, R0);
-    auto nblocks_of = [&](const TilePos& tp) {
-      const int nb_seq = (P.ctx[tp.s] + kBlock - 1) / kBlock;
-      return min(kBlocksT, nb_seq - key_tile_of(tp) * kBlocksT);
-    };
-    auto fetch_ids = [&](const TilePos& tp) -> int {
-      return lane < nblocks_of(tp)
-                 ? a.block_tables[(size_t)tp.s * a.max_blocks + key_tile_of(tp) * kBlocksT + lane]
-                 : 0;
-    };
+    TilePos t = t0;
     const uint32_t lead_q = in_cta(bar(B_QFULL), 0), lead_k = in_cta(bar(B_KFULL), 0),
                    lead_v = in_cta(bar(B_VFULL), 0);
-    int ids = fetch_ids(t);
+    int ids = ids0;
     int qn = 0, st = 0, i = 0;
     uint32_t use = 0;  // how often the ring has come round
     bool fine = true;
