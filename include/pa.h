@@ -702,9 +702,10 @@ int pa_rotate_cached(void* k_cache, int kv_format, const int32_t* block_tables,
  *       = out_scale * norm_weight * d / sqrt(mean(d^2) + norm_eps)   with it.
  *
  *   q             [num_q_tokens][num_q_heads][D] bf16
- *   cu_seqlens_q, num_q_tokens, max_q_len, causal   as in pa_decode_varlen; or
- *                 cu_seqlens_q NULL, num_q_tokens == S and max_q_len 1: one query
- *                 per sequence, which sees its whole context
+ *   cu_seqlens_q, num_q_tokens, max_q_len, causal   as in pa_decode_varlen, and a
+ *                 window longer than max_q_len sets PA_DEVERR_QLEN_RANGE and leaves
+ *                 its rows as they were; or cu_seqlens_q NULL, num_q_tokens == S and
+ *                 max_q_len 1: one query per sequence, which sees its whole context
  *   lambdas       [num_q_heads / 2] fp32 (a model's learned vectors make one
  *                 number of them before it is served)
  *   norm_weight   [2 * D] fp32, 16-byte aligned, or NULL; norm_eps >= 0

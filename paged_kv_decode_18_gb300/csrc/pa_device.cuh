@@ -310,6 +310,8 @@ struct PlanInputs {
   // > 0 (non-causal): a query window is the last lq positions of its context
   // and holds at most this many (the bits of a tree mask row)
   int max_window = 0;
+  // the longest window that the host was told of: a longer one is refused
+  int announced = 0x7fffffff;
   // without cu_seqlens_q: sequences with an empty context are no pairs at all
   // (for a cut that needs every pair to hold tiles)
   bool skip_empty = false;
@@ -359,9 +361,10 @@ __device__ __forceinline__ int pair_tiles(int c, int lq, int qt, int qtile, int 
 
 // Whether a window of lq queries starting at row q0, over a context of c keys,
 // is one the plan refuses: a causal (or tree) window lies inside its context;
-// other queries see the whole (non-empty) context whatever their number.
+// other queries see the whole (non-empty) context whatever their number. What
+// the host sized a launch by bounds it too.
 __device__ __forceinline__ bool bad_window(const PlanInputs& in, int lq, int q0, int c) {
-  return lq < 0 || (lq > c && (in.causal || in.max_window > 0 || c == 0)) || q0 < 0 ||
+  return lq < 0 || lq > in.announced || (lq > c && (in.causal || in.max_window > 0 || c == 0)) || q0 < 0 ||
          (in.max_window > 0 && lq > in.max_window) || (int64_t)q0 + lq > in.num_q_rows;
 }
 

@@ -32,12 +32,12 @@
 #include <cudaTypedefs.h>
 
 #include "pa_diff.cuh"
+#include "pa_diff_plan.h"
 #include "pa_tcgen05.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kMapRows = 8;                 // rows of one map in a tile
 constexpr int kDRows = 2 * kMapRows;
 constexpr int kDStage = 4 * kTileBytes;     // K[2p] K[2p+1] V[2p] V[2p+1] = 16 KB
 constexpr int kDWarps = 5;
@@ -63,6 +63,7 @@ struct DiffArgs {
   int npairs_cap;
   int num_workers;
   int max_lq;       // longer windows belong to the tcgen05 kernel
+  int max_q_len;    // no window is longer than this
   float* part_o;    // [NW*2][16][256]
   float* part_lse;  // [NW*2][16]
   int* desc;        // [NW][kDDesc]: of the segment that worker w's start cuts first, or
@@ -230,6 +231,7 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   in.npairs_cap = a.npairs_cap;
   in.num_q_rows = a.num_q_tokens;
   in.max_lq = a.max_lq;
+  in.announced = a.max_q_len;
   in.skip_empty = a.cu_seqlens_q == nullptr;
   build_plan(in, P, nullptr);
   if (threadIdx.x < kDiffDim / 2) weights[threadIdx.x] = mine;
@@ -673,8 +675,6 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
 // rows, 14 us with a CTA to a segment), and the grid has the segments: 32 x 4 CTAs come
 // and go 3 us sooner than 760 x 4. Elsewhere four rows or fewer get four warps: 346
 // live CTAs of eight (256 contexts of up to 4096) take a second round on the SMs, 2 us.
-constexpr int kDFixWarps = 8;  // at most
-
 __global__ void __launch_bounds__(kDFixWarps * 32)
     diff_fixup_kernel(const int* desc, const float* part_o, const float* part_lse, const DiffOut out,
                       int chunk_rows, int Hq, int G, int QT) {
@@ -687,10 +687,10 @@ __global__ void __launch_bounds__(kDFixWarps * 32)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int npieces = last - w + 2;                       // workers w-1 .. last
   const int row0 = (int)blockIdx.y * chunk_rows;
-  const int nrows = min(chunk_rows, min(QT, lq - qt * QT) * G - row0);  // 1 .. 8 of either map
+  const int nrows = min(chunk_rows, min(QT, lq - qt * QT) * G - row0);  // 1 .. chunk_rows of either map
   if (nrows <= 0) return;
-  const int per_row = ((int)blockDim.x >> 5) / nrows;     // warps to a row
-  const int rl = warp / per_row, group = warp - rl * per_row;
+  const DiffDeal deal = diff_deal((int)blockDim.x >> 5, nrows, warp);
+  const int per_row = deal.per_row, rl = deal.row, group = deal.group;
   const int r = row0 + rl;
   const bool live = rl < nrows;
   MapSum x[2];
@@ -947,7 +947,7 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (p.tc.enabled) {
     rc = launch_diff_tc(p.tc, q, k_cache, v_cache, block_tables, context_lens, cu_seqlens_q,
-                        num_q_tokens, causal, scale, o, shape, ws, st);
+                        num_q_tokens, max_q_len, causal, scale, o, shape, ws, st);
     if (rc != PA_OK) return rc;
   }
   if (!p.warp) return PA_OK;
@@ -975,6 +975,7 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
   a.npairs_cap = g.npairs_cap;
   a.num_workers = g.workers;
   a.max_lq = p.tc.enabled ? p.tc.min_lq - 1 : 0x7fffffff;
+  a.max_q_len = max_q_len;
   char* wws = ws + p.tc.ws_bytes;
   a.desc = reinterpret_cast<int*>(wws);
   a.part_lse = reinterpret_cast<float*>(wws + g.ws_desc);
@@ -992,15 +993,13 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
   if (launch_dependent(paged_diff_kernel<false>, dim3(g.grid), dim3(kDWarps * 32), g.smem, st, tmk, tmv,
                        a) != cudaSuccess)
     return PA_ERR_CUDA;
-  const int64_t tile_rows = (int64_t)(max_q_len < a.QT ? max_q_len : a.QT) * a.G;
-  const int chunk = many ? 1 : kMapRows;
+  const DiffMerge m = diff_merge(many, max_q_len, a.QT, a.G);
   // (a worker has two tiles at least: of a small call only the first ones work)
   const int64_t most = (int64_t)g.npairs_cap * (a.Hkv / 2) * a.max_blocks / 2;
   const int64_t boundaries = most < 1 ? 1 : most < g.workers ? most : g.workers;
-  const dim3 grid((unsigned)(many ? segments : boundaries), many ? (unsigned)tile_rows : 1u);
-  const unsigned warps = many || tile_rows > 4 ? kDFixWarps : 4;
-  if (launch_dependent(diff_fixup_kernel, grid, dim3(warps * 32), 0, st, (const int*)a.desc,
-                       (const float*)a.part_o, (const float*)a.part_lse, a.o, chunk, a.Hq, a.G,
+  const dim3 grid((unsigned)(many ? segments : boundaries), (unsigned)m.chunks);
+  if (launch_dependent(diff_fixup_kernel, grid, dim3(m.warps * 32), 0, st, (const int*)a.desc,
+                       (const float*)a.part_o, (const float*)a.part_lse, a.o, m.chunk, a.Hq, a.G,
                        a.QT) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;

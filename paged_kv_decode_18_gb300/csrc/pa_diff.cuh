@@ -47,7 +47,7 @@ int diff_tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, in
 int launch_diff_tc(const DiffTcGeometry& g, const pa_bf16* q, const pa_bf16* k_cache,
                    const pa_bf16* v_cache, const int32_t* block_tables,
                    const int32_t* context_lens, const int32_t* cu_seqlens_q, int64_t num_q_tokens,
-                   int causal, float scale, const DiffOut& out, const pa_shape* sh, void* workspace,
-                   cudaStream_t st);
+                   int max_q_len, int causal, float scale, const DiffOut& out, const pa_shape* sh,
+                   void* workspace, cudaStream_t st);
 
 }  // namespace pa

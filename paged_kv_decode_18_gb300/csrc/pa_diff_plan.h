@@ -1,0 +1,49 @@
+// pa_diff_plan.h -- sizes of differential attention's launches; plain
+// arithmetic, for the library and for a test on the host.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define PA_HD __host__ __device__ __forceinline__
+#else
+#define PA_HD inline
+#endif
+
+namespace pa {
+
+constexpr int kMapRows = 8;    // rows of one map in a warp tile
+constexpr int kDFixWarps = 8;  // of a CTA of the warp tiles' merge, at most
+
+// The merge of warp tiles: a CTA has `warps` warps for `chunk` rows of a segment, and
+// `chunks` CTAs a segment's rows. A row has a warp at least, whatever number of rows the
+// device finds in a window: chunk <= warps.
+struct DiffMerge {
+  int warps, chunk, chunks;
+};
+
+// by_row: few segments in many pieces. longest: the longest window that the call
+// announces; QT query tokens and G heads make a tile.
+inline DiffMerge diff_merge(bool by_row, int64_t longest, int QT, int G) {
+  const int rows = (int)(longest < QT ? longest : QT) * G;
+  DiffMerge m;
+  m.warps = by_row || rows > kDFixWarps / 2 ? kDFixWarps : kDFixWarps / 2;
+  m.chunk = by_row ? 1 : m.warps;
+  m.chunks = by_row ? rows : 1;
+  return m;
+}
+
+// Which row of its CTA's a warp merges, and which of the row's `per_row` warps it is
+// (a row is `nrows` or more: none).
+struct DiffDeal {
+  int row, group, per_row;
+};
+PA_HD DiffDeal diff_deal(int warps, int nrows, int warp) {
+  DiffDeal d;
+  d.per_row = warps / nrows;
+  d.row = warp / d.per_row;
+  d.group = warp - d.row * d.per_row;
+  return d;
+}
+
+}  // namespace pa

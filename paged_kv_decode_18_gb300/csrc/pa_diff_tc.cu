@@ -119,6 +119,7 @@ struct DiffTcArgs {
   int npairs_cap;
   int num_workers;
   int min_lq;
+  int max_q_len;
   int nstage;
   // [workers * 2 pieces][2 maps][64 groups of 4 dims][256 rows][4]: neighbouring
   // threads hold neighbouring rows
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(kThreadsT, 1)
   in.num_q_rows = a.num_q_tokens;
   in.key_tile = kKeysT;
   in.min_lq = a.min_lq;
+  in.announced = a.max_q_len;
   in.skip_empty = a.cu_seqlens_q == nullptr;
   build_plan(in, P, nullptr);
   // segments are pairs of KV heads, n tiles of the first map, then n of the second; the
@@ -1129,8 +1131,8 @@ int diff_tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, in
 int launch_diff_tc(const DiffTcGeometry& g, const pa_bf16* q, const pa_bf16* k_cache,
                    const pa_bf16* v_cache, const int32_t* block_tables,
                    const int32_t* context_lens, const int32_t* cu_seqlens_q, int64_t num_q_tokens,
-                   int causal, float scale, const DiffOut& out, const pa_shape* sh, void* workspace,
-                   cudaStream_t st) {
+                   int max_q_len, int causal, float scale, const DiffOut& out, const pa_shape* sh,
+                   void* workspace, cudaStream_t st) {
   const int G = sh->num_q_heads / sh->num_kv_heads, QTb = kRowsT / G;
   CUtensorMap tmq, tmk, tmv;
   const int64_t pool_rows = sh->num_blocks * sh->num_kv_heads * kBlock;
@@ -1156,6 +1158,7 @@ int launch_diff_tc(const DiffTcGeometry& g, const pa_bf16* q, const pa_bf16* k_c
   a.npairs_cap = g.npairs_cap;
   a.num_workers = g.workers;
   a.min_lq = g.min_lq;
+  a.max_q_len = max_q_len;
   a.nstage = g.nstage;
   char* ws = static_cast<char*>(workspace);
   a.part_lse = reinterpret_cast<float*>(ws);

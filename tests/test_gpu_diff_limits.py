@@ -1,0 +1,45 @@
+"""Differential attention at the limits of what a call announces, on the GPU."""
+import pytest
+import torch
+
+from paged_kv_decode_18_gb300 import binding as B
+from tests import diff_ref as R
+from tests.test_gpu_diff import SCALE, Batch, _errors, _lib, ok  # noqa: F401 (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+
+def check_rows(b, out, lse, rows, norm=True, gain=0.8):
+    """The rows of a boolean mask, against 64 bits."""
+    ref, rl, tol, ltol = R.attend(b.q, b.kc, b.vc, b.tables, b.lens, b.cu, SCALE, b.lambdas,
+                                  b.weight if norm else None, 1e-5, gain)
+    got, gl = out[:b.T].cpu().double(), lse[:b.T].cpu().double()
+    assert ((got - ref).abs() <= tol)[rows].all()
+    assert ((gl - rl).abs() <= ltol)[rows].all()
+
+
+@pytest.mark.parametrize("lens,qs,G,max_q,width", [
+    ([600, 300], [4, 2], 2, 2, 0),                     # a CTA to a segment
+    ([5000, 300], [4, 2], 2, 2, 400),                  # cut over all warps, merged by segment
+    ([3000] + [90] * 120, [4] + [2] * 120, 2, 2, 0),   # merged by boundary, four warps to a CTA
+    ([3000] + [90] * 120, [8] + [1] * 120, 1, 1, 0),
+    ([3000] + [90] * 120, [2] + [1] * 120, 4, 1, 0),
+    ([400, 200, 90], [300, 70, 3], 2, 70, 0),          # tcgen05 tiles and warp tiles
+    ([400, 200], [90, 50], 2, 70, 0),                  # as many rows as two windows of 70
+    ([400, 200], [9, 3], 16, 5, 0),
+])
+def test_a_window_longer_than_announced_is_flagged(lens, qs, G, max_q, width):
+    b = Batch(71 + G, lens, qs, 2, G, width=width).cuda()
+    out, lse = b.call(max_q=max_q, ws_fill=0)
+    torch.cuda.synchronize()
+    assert B.pa_debug_read_error() == B.PA_DEVERR_QLEN_RANGE
+    # its rows are left as they were, the others get their results
+    n = qs[0]
+    assert (out[:n] == 3).all() and (lse[:n] == 5).all()
+    rest = torch.ones(b.T, dtype=torch.bool)
+    rest[:n] = False
+    check_rows(b, out, lse, rest)
+    # announced, it is served
+    out, lse = b.call()
+    ok()
+    b.check(out, lse)
