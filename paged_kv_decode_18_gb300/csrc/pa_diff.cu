@@ -802,14 +802,13 @@ struct DiffGeometry {
   size_t smem = 0, ws_desc = 0, ws_lse = 0, ws_o = 0, ws_bytes = 0;
 };
 
-int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffGeometry* g) {
+// longest: the longest window that comes here
+int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int64_t longest, DiffGeometry* g) {
   DeviceInfo dev;
   if (!current_device_info(&dev)) return PA_ERR_CUDA;
   const int S = sh->num_seqs;
   const int G = sh->num_q_heads / sh->num_kv_heads, QT = kMapRows / G;
-  const int64_t cap1 = (int64_t)S * (((int64_t)max_q_len + QT - 1) / QT);
-  const int64_t cap2 = (num_q_tokens + QT - 1) / QT + S;
-  const int64_t cap = cap1 < cap2 ? cap1 : cap2;
+  const int64_t cap = diff_pairs(S, num_q_tokens, longest, QT);
   if (cap > (1 << 22)) return PA_ERR_UNSUPPORTED;
   g->npairs_cap = (int)(cap < S ? S : cap);
   g->grid = dev.num_sms;
@@ -868,7 +867,7 @@ int diff_plan(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, DiffPlan*
   int rc = diff_tc_geometry(sh, num_q_tokens, max_q_len, min_lq, &p->tc);
   if (rc != PA_OK) return rc;
   if (p->warp) {
-    rc = diff_geometry(sh, num_q_tokens, max_q_len, &p->g);
+    rc = diff_geometry(sh, num_q_tokens, diff_warp_longest(max_q_len, min_lq), &p->g);
     if (rc != PA_OK) return rc;
   }
   p->ws_bytes = (p->warp ? p->g.ws_bytes : 0) + p->tc.ws_bytes;

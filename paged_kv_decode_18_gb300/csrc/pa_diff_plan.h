@@ -15,6 +15,18 @@ namespace pa {
 constexpr int kMapRows = 8;    // rows of one map in a warp tile
 constexpr int kDFixWarps = 8;  // of a CTA of the warp tiles' merge, at most
 
+// Most (sequence, query tile) pairs of S windows of at most `longest` tokens, T tokens in
+// all, in tiles of `unit` tokens.
+inline int64_t diff_pairs(int64_t S, int64_t T, int64_t longest, int unit) {
+  const int64_t by_window = S * ((longest + unit - 1) / unit), by_token = (T + unit - 1) / unit + S;
+  return by_window < by_token ? by_window : by_token;
+}
+
+// The longest window that the warp tiles take beside tcgen05 tiles of min_lq tokens and more.
+inline int64_t diff_warp_longest(int64_t max_q_len, int min_lq) {
+  return max_q_len < min_lq ? max_q_len : min_lq - 1;
+}
+
 // The merge of warp tiles: a CTA has `warps` warps for `chunk` rows of a segment, and
 // `chunks` CTAs a segment's rows. A row has a warp at least, whatever number of rows the
 // device finds in a window: chunk <= warps.

@@ -41,6 +41,7 @@
 #include <cudaTypedefs.h>
 
 #include "pa_diff.cuh"
+#include "pa_diff_plan.h"
 #include "pa_tcgen05.cuh"
 
 namespace pa {
@@ -1101,9 +1102,7 @@ int diff_tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, in
   g->ws_bytes = 0;
   if (!g->enabled) return PA_OK;
   const int S = sh->num_seqs, unit = 2 * (kRowsT / G);
-  const int64_t cap1 = (int64_t)S * (((int64_t)max_q_len + unit - 1) / unit);
-  const int64_t cap2 = (num_q_tokens + unit - 1) / unit + S;
-  const int64_t cap = cap1 < cap2 ? cap1 : cap2;
+  const int64_t cap = diff_pairs(S, num_q_tokens, max_q_len, unit);
   if (cap > (1 << 20)) return PA_ERR_UNSUPPORTED;
   g->npairs_cap = (int)(cap < 1 ? 1 : cap);
   g->min_lq = min_q_len;

@@ -1,6 +1,7 @@
 """Sizes of differential attention's launches, compiled for the host."""
 import ctypes
 import os
+import random
 import subprocess
 
 import pytest
@@ -12,6 +13,12 @@ HOST = r"""
 extern "C" void merge(int by_row, long long longest, int qt, int g, int* out) {
   const pa::DiffMerge m = pa::diff_merge(by_row != 0, longest, qt, g);
   out[0] = m.warps, out[1] = m.chunk, out[2] = m.chunks;
+}
+extern "C" long long pairs(long long s, long long t, long long longest, int unit) {
+  return pa::diff_pairs(s, t, longest, unit);
+}
+extern "C" long long warp_longest(long long max_q_len, int min_lq) {
+  return pa::diff_warp_longest(max_q_len, min_lq);
 }
 extern "C" void deal(int warps, int nrows, int warp, int* out) {
   const pa::DiffDeal d = pa::diff_deal(warps, nrows, warp);
@@ -27,7 +34,11 @@ def plan(tmp_path_factory):
     src.write_text(HOST)
     subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-ftrapv", "-I", CSRC,
                     "-o", str(lib), str(src)], check=True)
-    return ctypes.CDLL(str(lib))
+    lib = ctypes.CDLL(str(lib))
+    i64 = ctypes.c_longlong
+    lib.pairs.restype = lib.warp_longest.restype = i64
+    lib.pairs.argtypes, lib.warp_longest.argtypes = [i64, i64, i64, ctypes.c_int], [i64, ctypes.c_int]
+    return lib
 
 
 def three(fn, *args):
@@ -54,3 +65,27 @@ def test_a_merge_has_a_warp_for_every_row(plan, by_row, G):
                 assert per_row >= 1 and 0 <= group < per_row
             for row in range(nrows):
                 assert sorted(g for r, g, _ in got if r == row) == list(range(got[0][2]))
+
+
+def test_a_plan_holds_the_windows_that_come_to_it(plan):
+    # the warp tiles' plan: of a batch with longer windows, which the tcgen05 tiles take, the
+    # short ones alone
+    rng = random.Random(3)
+    for _ in range(300):
+        G = rng.randint(1, 8)
+        QT, min_lq = 8 // G, -(-32 // G)
+        qs = [rng.randint(0, rng.choice([3, 40, 400])) for _ in range(rng.randint(1, 60))]
+        longest, T = max(qs), sum(qs) + rng.choice([0, 0, 50])
+        cap = plan.pairs(len(qs), T, plan.warp_longest(longest, min_lq), QT)
+        assert sum(-(-n // QT) for n in qs if n < min_lq) <= cap <= len(qs) * -(-(min_lq - 1) // QT)
+        unit = 2 * (128 // G)
+        assert sum(-(-n // unit) for n in qs) <= plan.pairs(len(qs), T, longest, unit)
+
+
+@pytest.mark.parametrize("G,seqs,total,longest", [(8, 81, 20250, 330), (8, 8, 16700, 4000),
+                                                  (4, 8, 33400, 8000), (2, 8, 66800, 16000),
+                                                  (1, 8, 1 << 20, 1 << 18)])
+def test_long_windows_take_no_room_in_the_plan_of_short_ones(plan, G, seqs, total, longest):
+    # beside the ring of 160 KB a plan has some 16,600 words: a word a pair, three a sequence
+    cap = plan.pairs(seqs, total, plan.warp_longest(longest, -(-32 // G)), 8 // G)
+    assert cap + 3 * seqs + 3 < 1000

@@ -43,3 +43,35 @@ def test_a_window_longer_than_announced_is_flagged(lens, qs, G, max_q, width):
     out, lse = b.call()
     ok()
     b.check(out, lse)
+
+
+@pytest.mark.parametrize("G,qs", [
+    (8, [169 + 2 * i for i in range(81)]),               # 20,169 tokens
+    (4, [8000, 7000, 6500, 5000, 4000, 2200, 900, 3]),   # 33,603
+])
+def test_unequal_long_windows(G, qs):
+    lens = [n + 40 for n in qs]
+    b = Batch(81, lens, qs, 2, G).cuda()
+    sh = B.shape_of(b.d["q"], b.d["kc"], b.d["tables"])
+    assert B.pa_decode_diff_workspace_size(sh, b.T, b.max_q) > 0
+    out, lse = b.call(ws_fill=0x7f)
+    ok()
+    if G == 8:
+        b.check(out, lse)
+        return
+    # the same windows one by one (of the longest the 64-bit form would take minutes)
+    for s in (0, 3, 6, 7):
+        a, e = int(b.cu[s]), int(b.cu[s + 1])
+        one = Batch.__new__(Batch)
+        one.__dict__.update(b.__dict__)
+        one.lens, one.qs, one.T, one.max_q = [lens[s]], [qs[s]], e - a, e - a
+        one.cu = torch.tensor([0, e - a], dtype=torch.int32)
+        one.d = dict(b.d, q=b.d["q"][a:e].contiguous(), cu=one.cu.cuda(),
+                     tables=b.d["tables"][s:s + 1].contiguous(),
+                     lens=torch.tensor([lens[s]], dtype=torch.int32).cuda())
+        alone, la = one.call()
+        ok()
+        # weights rounded to bf16 against other references, then the output's own rounding
+        far = (alone[:one.T].double() - out[a:e].double()).norm() / out[a:e].double().norm()
+        assert float(far) < 1e-2
+        assert (la - lse[a:e]).abs().max() < 1e-3
