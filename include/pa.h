@@ -714,7 +714,8 @@ int pa_rotate_cached(void* k_cache, int kv_format, const int32_t* block_tables,
  *   workspace     at least pa_decode_diff_workspace_size(...) bytes, 256-byte
  *                 aligned; clobbered
  * bf16 pools with an even num_kv_heads and 1 to 128 query heads per KV head
- * (else PA_ERR_UNSUPPORTED, workspace size 0). Both maps, their difference and
+ * (else PA_ERR_UNSUPPORTED, workspace size 0, as for a batch whose windows times KV
+ * heads times the table's width pass 2^31 tiles of 16 keys). Both maps, their difference and
  * the norm are fp32; the softmax weights are rounded to bf16 for the product
  * with V, as in pa_decode_varlen (so where the two maps' results agree to 2^-8, what
  * norm_eps does not hold down is their rounding). A sequence of the single-query form with an

@@ -811,6 +811,8 @@ int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int64_t longest, Dif
   const int64_t cap = diff_pairs(S, num_q_tokens, longest, QT);
   if (cap > (1 << 22)) return PA_ERR_UNSUPPORTED;
   g->npairs_cap = (int)(cap < S ? S : cap);
+  if (!diff_tiles_fit(g->npairs_cap, sh->num_kv_heads / 2, sh->max_blocks_per_seq, kSegCost4))
+    return PA_ERR_UNSUPPORTED;
   g->grid = dev.num_sms;
   g->workers = g->grid * kDWarps;
   const size_t plan = sizeof(int) * ((size_t)g->npairs_cap + 1 + 3 * (size_t)S + 2);

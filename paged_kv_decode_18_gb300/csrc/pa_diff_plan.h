@@ -27,6 +27,15 @@ inline int64_t diff_warp_longest(int64_t max_q_len, int min_lq) {
   return max_q_len < min_lq ? max_q_len : min_lq - 1;
 }
 
+// Whether a plan's flat tiles, `heads` segments of up to `tiles` each to a pair, are counted in
+// 32 bits, and (the cuts' arithmetic inside a pair) their costs in quarters of a tile too.
+inline bool diff_tiles_fit(int64_t pairs, int64_t heads, int64_t tiles, int start_cost4) {
+  const int64_t most = 0x7fffffff;
+  if (heads <= 0 || tiles <= 0) return true;
+  return tiles <= most / heads && pairs <= most / (heads * tiles) &&
+         4 * tiles + start_cost4 <= most / heads;
+}
+
 // The merge of warp tiles: a CTA has `warps` warps for `chunk` rows of a segment, and
 // `chunks` CTAs a segment's rows. A row has a warp at least, whatever number of rows the
 // device finds in a window: chunk <= warps.

@@ -1105,6 +1105,10 @@ int diff_tc_geometry(const pa_shape* sh, int64_t num_q_tokens, int max_q_len, in
   const int64_t cap = diff_pairs(S, num_q_tokens, max_q_len, unit);
   if (cap > (1 << 20)) return PA_ERR_UNSUPPORTED;
   g->npairs_cap = (int)(cap < 1 ? 1 : cap);
+  // (a KV head is a segment of its own in the cut)
+  if (!diff_tiles_fit(g->npairs_cap, sh->num_kv_heads,
+                      ((int64_t)sh->max_blocks_per_seq + kBlocksT - 1) / kBlocksT, kMapCost4))
+    return PA_ERR_UNSUPPORTED;
   g->min_lq = min_q_len;
   g->workers = dev.num_sms / 2;
   const size_t plan =

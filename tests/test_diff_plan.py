@@ -20,6 +20,9 @@ extern "C" long long pairs(long long s, long long t, long long longest, int unit
 extern "C" long long warp_longest(long long max_q_len, int min_lq) {
   return pa::diff_warp_longest(max_q_len, min_lq);
 }
+extern "C" int fit(long long pairs, long long heads, long long tiles, int start_cost4) {
+  return pa::diff_tiles_fit(pairs, heads, tiles, start_cost4);
+}
 extern "C" void deal(int warps, int nrows, int warp, int* out) {
   const pa::DiffDeal d = pa::diff_deal(warps, nrows, warp);
   out[0] = d.row, out[1] = d.group, out[2] = d.per_row;
@@ -37,6 +40,7 @@ def plan(tmp_path_factory):
     lib = ctypes.CDLL(str(lib))
     i64 = ctypes.c_longlong
     lib.pairs.restype = lib.warp_longest.restype = i64
+    lib.fit.argtypes = [i64, i64, i64, ctypes.c_int]
     lib.pairs.argtypes, lib.warp_longest.argtypes = [i64, i64, i64, ctypes.c_int], [i64, ctypes.c_int]
     return lib
 
@@ -89,3 +93,18 @@ def test_long_windows_take_no_room_in_the_plan_of_short_ones(plan, G, seqs, tota
     # beside the ring of 160 KB a plan has some 16,600 words: a word a pair, three a sequence
     cap = plan.pairs(seqs, total, plan.warp_longest(longest, -(-32 // G)), 8 // G)
     assert cap + 3 * seqs + 3 < 1000
+
+
+def test_flat_tiles_stay_in_32_bits(plan):
+    # (-ftrapv: the check itself must not wrap)
+    rng = random.Random(4)
+    for _ in range(4000):
+        pairs, heads = rng.randint(1, 1 << 22), rng.randint(1, 1 << 24)
+        tiles, cost = rng.randint(0, 1 << 26) >> rng.randint(0, 20), rng.choice([6, 20])
+        want = pairs * heads * tiles < 1 << 31 and heads * (4 * tiles + cost) < 1 << 31
+        assert bool(plan.fit(pairs, heads, tiles, cost)) == (want or tiles == 0)
+    # thousands of sequences over one long prefix, many heads; the batches of the tests
+    assert not plan.fit(4096, 16, 1 << 16, 6)
+    assert not plan.fit(1, 8, 1 << 26, 6)
+    assert plan.fit(4096, 4, 1 << 16, 6) and plan.fit(4096, 16, 8192, 6)
+    assert plan.fit(1 << 20, 8, 0, 20)

@@ -75,3 +75,18 @@ def test_unequal_long_windows(G, qs):
         far = (alone[:one.T].double() - out[a:e].double()).norm() / out[a:e].double().norm()
         assert float(far) < 1e-2
         assert (la - lse[a:e]).abs().max() < 1e-3
+
+
+def test_tiles_that_32_bits_do_not_count_are_refused():
+    # many heads under wide tables: only sizes are asked for
+    def size(S, hq, hkv, width, T, max_q):
+        sh = B.make_shape(num_seqs=S, num_q_heads=hq, num_kv_heads=hkv, head_dim=128,
+                          block_size=16, max_blocks_per_seq=width, num_blocks=1024)
+        return B.pa_decode_diff_workspace_size(sh, T, max_q)
+    assert size(4096, 32, 32, (1 << 15) - 1, 4096, 1) > 0
+    assert size(4096, 32, 32, 1 << 15, 4096, 1) == 0           # 4096 x 16 pairs x 2^15 tiles
+    assert size(4000, 32, 32, 1 << 16, 4000, 1) == 0
+    assert size(256, 64, 64, 1 << 20, 256, 1) == 0
+    assert size(1, 16, 16, 1 << 26, 1, 1) == 0
+    assert size(1000, 32, 32, 1 << 16, 64001, 64) == 0          # four query tiles to a window
+    assert size(100, 32, 32, 1 << 16, 6401, 64) > 0
