@@ -678,8 +678,9 @@ int pa_rotate_and_cache(const pa_row_view* q, const pa_row_view* k, const pa_row
  *   context_lens  [S] int32 of the cache as it is now (new_lens of pa_evict)
  *   rot      the rotation that the keys were cached with; its magnitude is not
  *            applied again
- * A key turned by 0 keeps its bytes; another is rounded again (an 8-bit one is
- * dequantised, turned and quantised anew). Blocks that hold turned keys must
+ * A key turned by 0 keeps its bytes; another is rounded again (of an 8-bit one the
+ * codes' values are turned and quantised anew, and its scale is multiplied: one
+ * that is infinite or NaN stays so). Blocks that hold turned keys must
  * belong to one sequence alone. A context longer than the table sets
  * PA_DEVERR_CONTEXT_RANGE, a block outside the pool PA_DEVERR_BLOCK_RANGE (its
  * keys are skipped). Plan limits as above.

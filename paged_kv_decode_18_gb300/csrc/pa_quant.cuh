@@ -61,24 +61,24 @@ __device__ __forceinline__ uint2 codes_of8(const float* x, float inv) {
   return make_uint2(w[0], w[1]);
 }
 
-// Values of eight codes times their row's scale.
+// Values of eight codes, without their row's scale.
 template <bool FP8>
-__device__ __forceinline__ void values_of8(uint2 c, float scale, float* x) {
+__device__ __forceinline__ void values_of8(uint2 c, float* x) {
   const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if constexpr (FP8) {
       const float2 lo = e4m3x2_values(w[i] & 0xffffu), hi = e4m3x2_values(w[i] >> 16);
-      x[4 * i] = lo.x * scale;
-      x[4 * i + 1] = lo.y * scale;
-      x[4 * i + 2] = hi.x * scale;
-      x[4 * i + 3] = hi.y * scale;
+      x[4 * i] = lo.x;
+      x[4 * i + 1] = lo.y;
+      x[4 * i + 2] = hi.x;
+      x[4 * i + 3] = hi.y;
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         // code + 128 as the lowest byte of 2^23's mantissa: exact
         const uint32_t bits = __byte_perm(w[i] ^ 0x80808080u, 0x4b000000u, 0x7440 | j);
-        x[4 * i + j] = __fadd_rn(__uint_as_float(bits), -8388736.f) * scale;
+        x[4 * i + j] = __fadd_rn(__uint_as_float(bits), -8388736.f);
       }
     }
   }

@@ -190,6 +190,14 @@ __device__ __forceinline__ float row_amax(const float (&f)[16]) {
   return m;
 }
 
+__device__ __forceinline__ void store_row(uint2 ca, uint2 cb, float scale, int a, int b, int c,
+                                          uint8_t* tile, int off) {
+  uint8_t* row = tile + off * kHeadDim;
+  *reinterpret_cast<uint2*>(row + a * 8) = ca;
+  *reinterpret_cast<uint2*>(row + b * 8) = cb;
+  if (c == 0) *(reinterpret_cast<float*>(tile + kBlock * kHeadDim) + off) = scale;
+}
+
 // Quantises a row held by eight lanes into the tile's row `off`. The whole warp
 // calls it; write: this lane's row goes to memory.
 template <bool FP8>
@@ -203,12 +211,20 @@ __device__ __forceinline__ void store_codes(const float (&f)[16], int a, int b, 
     ca = codes_of8<FP8>(f, inv);
     cb = codes_of8<FP8>(f + 8, inv);
   }
-  uint8_t* row = tile + off * kHeadDim;
-  *reinterpret_cast<uint2*>(row + a * 8) = ca;
-  *reinterpret_cast<uint2*>(row + b * 8) = cb;
-  if (c == 0)
-    *(reinterpret_cast<float*>(tile + kBlock * kHeadDim) + off) =
-        amax > 0.f ? __fdiv_rn(amax, code_range<FP8>()) : 0.f;
+  store_row(ca, cb, amax > 0.f ? __fdiv_rn(amax, code_range<FP8>()) : 0.f, a, b, c, tile, off);
+}
+
+// The same for a row that the tile held with `scale` and whose codes' own values were
+// turned: a turn is linear, so the scale passes by it. One that is infinite or NaN (keys
+// that had overflowed) stays one, and so does an FP8 code that is a NaN.
+template <bool FP8>
+__device__ __forceinline__ void store_turned(const float (&f)[16], float scale, int a, int b,
+                                             int c, uint8_t* tile, int off, bool write) {
+  const float amax = row_amax(f);
+  if (!write) return;
+  const float inv = amax > 0.f ? __fdiv_rn(code_range<FP8>(), amax) : 1.f;
+  store_row(codes_of8<FP8>(f, inv), codes_of8<FP8>(f + 8, inv),
+            __fmul_rn(scale, __fdiv_rn(amax, code_range<FP8>())), a, b, c, tile, off);
 }
 
 // ---------------------------------------------------------------------------
@@ -499,10 +515,11 @@ __global__ void __launch_bounds__(kRotWarps * 32, MODE == kAny && FMT == kFmtBf1
             spun = by[i];
           }
           float f[16];
-          values_of8<FMT == kFmtFp8>(ca[i], scale[i], f);
-          values_of8<FMT == kFmtFp8>(cb[i], scale[i], f + 8);
+          values_of8<FMT == kFmtFp8>(ca[i], f);
+          values_of8<FMT == kFmtFp8>(cb[i], f + 8);
           turn<MODE>(f, sp, me, a.rot.rot_dim, rows, sub);
-          store_codes<FMT == kFmtFp8>(f, me.a, me.b, me.c, tile, i * 4 + sub, by[i] != 0);
+          store_turned<FMT == kFmtFp8>(f, scale[i], me.a, me.b, me.c, tile, i * 4 + sub,
+                                       by[i] != 0);
         }
       }
     }
