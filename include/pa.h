@@ -258,8 +258,10 @@ size_t pa_decode_varlen_workspace_size(const pa_shape* shape, int64_t num_q_toke
  * if amax == 0 every code is 0 and the scale 0; otherwise
  * inv = fl(127 / amax), code_d = clamp(rint(fl(x_d * inv)), -127, 127) with
  * rint rounding half to even, scale = fl(amax / 127), where fl() is one
- * IEEE fp32 operation rounded to nearest even. A row dequantises to
- * code_d * scale. Rows are written once, so a block's earlier rows never
+ * IEEE fp32 operation rounded to nearest even (inv the largest finite number
+ * where the quotient is infinite). A row dequantises to code_d * scale. amax
+ * leaves NaNs out: one among numbers gets the code -127, a row of nothing else
+ * is stored as zeros. Rows are written once, so a block's earlier rows never
  * change when later tokens arrive.
  */
 #define PA_INT8_TILE_BYTES 2112
@@ -307,11 +309,12 @@ size_t pa_decode_int8_workspace_size(const pa_shape* shape, int num_splits);
  * infinities, 0x7F / 0xFF = NaN, largest finite value 448.
  *
  * Row quantisation (group = one head row): amax = max_d |x_d|; if amax == 0
- * every code is 0 and the scale 0; otherwise inv = fl(448 / amax),
+ * every code is 0 and the scale 0; otherwise inv = fl(448 / amax), finite as above,
  * code_d = the E4M3 value nearest to fl(x_d * inv) (ties to the code with
  * an even last mantissa bit; beyond +-448 it saturates to +-448),
- * scale = fl(amax / 448). The writer never stores a NaN code. A row
- * dequantises to value(code_d) * scale.
+ * scale = fl(amax / 448). Of a row of finite values the writer never stores a NaN
+ * code; a NaN among numbers keeps one, a row of nothing else is stored as zeros.
+ * A row dequantises to value(code_d) * scale.
  */
 
 /*

@@ -45,7 +45,8 @@
  *   head) row of head_dim values, every step one IEEE fp32 operation:
  *     amax = max_d |x_d|;  amax == 0 -> all codes 0 and scale 0; else
  *     inv = 127 / amax,  code_d = clamp(rint(x_d * inv), -127, 127),
- *     scale = amax / 127   (rint: nearest, ties to even).
+ *     scale = amax / 127   (rint: nearest, ties to even; inv at most the
+ *     largest finite number, as below).
  *   A row dequantises to code_d * scale (exact in fp64). Attention over an
  *   int8 pool is the attention above over the dequantised rows.
  *
@@ -63,6 +64,7 @@
  * Numbers: bf16 inputs are bit patterns (uint16). They are widened to fp64
  * exactly (bf16 -> fp32 is a 16-bit shift; fp32 -> fp64 is exact).
  */
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
@@ -145,7 +147,7 @@ static void quantize_row_i8(const uint16_t *x, int D, int8_t *codes, float *scal
         *scale = 0.0f;
         return;
     }
-    float inv = 127.0f / amax;
+    float inv = fminf(127.0f / amax, FLT_MAX);
     for (int d = 0; d < D; ++d) {
         float t = rintf(bf16_bits_to_float(x[d]) * inv);
         if (t > 127.0f) t = 127.0f;
@@ -206,7 +208,7 @@ static void quantize_row_f8(const uint16_t *x, int D, uint8_t *codes, float *sca
         *scale = 0.0f;
         return;
     }
-    const float inv = 448.0f / amax;
+    const float inv = fminf(448.0f / amax, FLT_MAX);
     for (int d = 0; d < D; ++d) {
         const float y = bf16_bits_to_float(x[d]) * inv;
         codes[d] = e4m3_code(y);

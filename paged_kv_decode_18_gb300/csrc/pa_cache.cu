@@ -64,7 +64,7 @@ __device__ __forceinline__ void quantize_row_to(const uint2 x, int lane, int8_t*
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
   uint32_t packed = 0u;
   if (amax > 0.f) {
-    const float inv = __fdiv_rn(127.f, amax);
+    const float inv = code_factor<false>(amax);
     packed = low_bytes(int8_code(f0, inv), int8_code(f1, inv), int8_code(f2, inv),
                        int8_code(f3, inv));
   }
@@ -76,7 +76,7 @@ __device__ __forceinline__ void quantize_row_to(const uint2 x, int lane, int8_t*
 // mapped to the largest finite E4M3 value 448: y = x * (448 / amax) in IEEE
 // fp32, code = the nearest E4M3 value of y (ties to the even code), saturated
 // to +-448 (the hardware conversion with .satfinite), scale = amax / 448. A
-// zero row stores code 0 and scale 0. The codes never hold the NaN patterns.
+// zero row stores code 0 and scale 0. Codes of finite values are never the NaN patterns.
 __device__ __forceinline__ void quantize_row_f8_to(const uint2 x, int lane,
                                                    uint8_t* __restrict__ dst,
                                                    float* __restrict__ scale_dst) {
@@ -86,7 +86,7 @@ __device__ __forceinline__ void quantize_row_f8_to(const uint2 x, int lane,
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
   uint32_t packed = 0u;
   if (amax > 0.f) {
-    const float inv = __fdiv_rn(448.f, amax);
+    const float inv = code_factor<true>(amax);
     packed = e4m3x2_of(__fmul_rn(f0, inv), __fmul_rn(f1, inv)) |
              (e4m3x2_of(__fmul_rn(f2, inv), __fmul_rn(f3, inv)) << 16);
   }

@@ -44,6 +44,13 @@ __device__ __forceinline__ float code_range() {
   return FP8 ? 448.f : 127.f;
 }
 
+// The factor from a row's values to its codes. Of rows below 1.3e-36 (FP8) the quotient
+// is infinite, and an infinity times a zero beside the largest value a NaN.
+template <bool FP8>
+__device__ __forceinline__ float code_factor(float amax) {
+  return fminf(__fdiv_rn(code_range<FP8>(), amax), 3.402823466e38f);
+}
+
 // Codes of eight consecutive values of a row as eight bytes.
 template <bool FP8>
 __device__ __forceinline__ uint2 codes_of8(const float* x, float inv) {

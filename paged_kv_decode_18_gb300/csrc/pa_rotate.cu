@@ -207,7 +207,7 @@ __device__ __forceinline__ void store_codes(const float (&f)[16], int a, int b, 
   if (!write) return;
   uint2 ca = make_uint2(0u, 0u), cb = ca;
   if (amax > 0.f) {
-    const float inv = __fdiv_rn(code_range<FP8>(), amax);
+    const float inv = code_factor<FP8>(amax);
     ca = codes_of8<FP8>(f, inv);
     cb = codes_of8<FP8>(f + 8, inv);
   }
