@@ -719,12 +719,14 @@ int pa_rotate_cached(void* k_cache, int kv_format, const int32_t* block_tables,
  *                 aligned; clobbered
  * bf16 pools with an even num_kv_heads and 1 to 128 query heads per KV head
  * (else PA_ERR_UNSUPPORTED, workspace size 0, as for a batch whose windows times KV
- * heads times the table's width pass 2^31 tiles of 16 keys). Both maps, their difference and
- * the norm are fp32; the softmax weights are rounded to bf16 for the product
- * with V, as in pa_decode_varlen (so where the two maps' results agree to 2^-8, what
- * norm_eps does not hold down is their rounding). A sequence of the single-query form with an
- * empty context gives out = 0 and lse = -inf. A key that a query does not see
- * never reaches its result, whatever its K and V hold.
+ * heads times the table's width pass 2^31 tiles of 16 keys). Both maps, their
+ * difference and the norm are fp32. With max_q_len 1 and up to 8 query heads per
+ * KV head the softmax weights enter the product with V to 2^-15; of windows and of
+ * more heads they are rounded to bf16, as in pa_decode_varlen (so where the two
+ * maps' results agree to 2^-8, what norm_eps does not hold down is their rounding).
+ * A sequence of the single-query form with an empty context gives out = 0 and
+ * lse = -inf. A key that a query does not see never reaches its result, whatever
+ * its K and V hold.
  */
 int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa_bf16* v_cache,
                    const int32_t* block_tables, const int32_t* context_lens,

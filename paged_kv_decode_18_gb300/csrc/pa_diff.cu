@@ -22,10 +22,10 @@
 // The two results of a row end in the same lane, so difference, norm and scale
 // cost no exchange but the sum of squares: a segment that one warp has worked
 // through alone writes its bf16 output at once.
-// Bound by HBM: 518 MB of 256 ragged contexts in 92 us, 514 MB of 8 x 30k .. 32k in 90.5,
-// 5.6 and 5.7 TB/s, of which 5 us are launch, plan and first copy and 4 to 6 the merge;
+// Bound by HBM: 518 MB of 256 ragged contexts in 93.5 us, 514 MB of 8 x 30k .. 32k in 91.7,
+// 5.5 and 5.6 TB/s, of which 5 us are launch, plan and first copy and 4 to 6 the merge;
 // between them equal ranges end up to 15 us apart, some SMs getting a tenth more than
-// others. Four short contexts, a CTA to a segment: 10.4 us, all latency.
+// others. Four short contexts, a CTA to a segment: 10.7 us, all latency.
 // A warp is a worker with its own ring of 16 KB stages and an equal range of
 // the batch's (sequence, query tile, pair, block) tiles; segments that ranges
 // cut leave fp32 partials, which diff_fixup_kernel merges.
@@ -124,6 +124,16 @@ struct CostCut {
   }
 };
 
+// Two weights (not negative) as the pair of their upper halves and a pair of what those leave.
+// Neither half of a weight of 2^-96 or more is 0, so that an infinite value times it is not a NaN.
+__device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t& high, uint32_t& low) {
+  const uint32_t bx = __float_as_uint(x), by = __float_as_uint(y);
+  high = __byte_perm(bx, by, 0x7632);
+  const float lx = fmaxf(x - __uint_as_float(bx & 0xffff0000u), x * 0x1p-30f);
+  const float ly = fmaxf(y - __uint_as_float(by & 0xffff0000u), y * 0x1p-30f);
+  low = cvt_bf16x2(lx, ly);
+}
+
 struct MapSum {
   float m, sum;
   float acc[8];
@@ -181,7 +191,9 @@ __device__ __forceinline__ void finish_row(const MapSum (&x)[2], const DiffOut& 
 
 // kWhole: a CTA has a segment for itself, an equal part of its tiles a warp, and merges
 // in shared memory: no second grid.
-template <bool kWhole>
+// kWeights: how the softmax weights enter the product with V (kTwin: of whole segments).
+enum : int { kRounded, kSplit, kTwin };
+template <bool kWhole, int kWeights>
 __global__ void __launch_bounds__(kDWarps * 32, 1)
     paged_diff_kernel(const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const DiffArgs a) {
@@ -361,7 +373,11 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   if (!kWhole && lane == 0) describe();  // (while the first copies are on their way)
 
   // ---- consumer --------------------------------------------------------------
-  const int r = lane >> 2, quad = lane & 3;  // this lane's row of either map
+  // this lane's row of either map's tile, and the query row that it holds. A CTA's segment of
+  // four rows or fewer holds them twice, for the weights' halves (four short contexts 10.7
+  // us; a second product for the lower ones 11.7, rounded weights 10.4)
+  const int rt = lane >> 2, quad = lane & 3;
+  const int r = kWeights == kTwin ? rt & 3 : rt;
   const int mi = lane >> 3, rr = lane & 7;   // ldmatrix: matrix and row of this lane's address
   uint32_t qa[8][4];
   float o[32][4];
@@ -543,13 +559,20 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     }
     // ---- O += P V --------------------------------------------------------------------
     // P enters the product in bf16, the type that V is stored in and the MMA takes
-    // beside it: a weight is off by at most 2^-8 of itself, each its own way. The sums
-    // of the weights, and with them lse, are of the unrounded ones.
-    uint32_t p4[4];
-    p4[0] = cvt_bf16x2(s[0][0], s[0][1]);
-    p4[1] = cvt_bf16x2(s[0][2], s[0][3]);
-    p4[2] = cvt_bf16x2(s[1][0], s[1][1]);
-    p4[3] = cvt_bf16x2(s[1][2], s[1][3]);
+    // beside it. Of single queries a weight is two such numbers, its upper half and what
+    // that leaves, off by 2^-15 of it together (1.5 us of the calls above); of windows, as
+    // elsewhere, it is one, off by 2^-8 at most: their tiles are full, and a second product
+    // takes 46.7 to 53.1 us for 64 windows of 16 rows over 512 keys. The sums of the weights, and with them lse, are of the unrounded ones.
+    uint32_t p4[4], p4_low[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = s[i >> 1][2 * (i & 1)], y = s[i >> 1][2 * (i & 1) + 1];
+      if constexpr (kWeights == kRounded)
+        p4[i] = cvt_bf16x2(x, y);
+      else
+        split_bf16x2(x, y, p4[i], p4_low[i]);
+      if (kWeights == kTwin && rt != r) p4[i] = p4_low[i];
+    }
     {
       const int key = (mi & 1) * 8 + rr;
 #pragma unroll
@@ -560,6 +583,10 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
           ldsm_x4_trans(sV + t * kTileBytes + atom_at(key, 2 * c + (mi >> 1)), b0, b1, b2, b3);
           mma_bf16_16816(o[t * 16 + 2 * c], p4, b0, b1);
           mma_bf16_16816(o[t * 16 + 2 * c + 1], p4, b2, b3);
+          if constexpr (kWeights == kSplit) {
+            mma_bf16_16816(o[t * 16 + 2 * c], p4_low, b0, b1);
+            mma_bf16_16816(o[t * 16 + 2 * c + 1], p4_low, b2, b3);
+          }
         }
     }
     __syncwarp();
@@ -585,12 +612,12 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float* dst = reinterpret_cast<float*>(wbuf) + (i * kMapRows + r) * kPartStride + quad * 2;
+          float* dst = reinterpret_cast<float*>(wbuf) + (i * kMapRows + rt) * kPartStride + quad * 2;
 #pragma unroll
           for (int n = 0; n < 32; ++n)
             *reinterpret_cast<float2*>(dst + n * 8) =
                 make_float2(o[n][2 * i] * inv[i], o[n][2 * i + 1] * inv[i]);
-          if (quad == 0) part_lse[warp][i * kMapRows + r] = lse[i];
+          if (quad == 0) part_lse[warp][i * kMapRows + rt] = lse[i];
         }
       } else if (piece_b0 == 0 && cp.b == cp.nt - 1) {
         const int head = cp.h * G + r % G;
@@ -655,7 +682,13 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
               reinterpret_cast<const float*>(smem + k * kDStages * kDStage) +
               (i * kMapRows + row) * kPartStride + lane * 8);
           const float4 a0 = src[0], a1 = src[1];
-          const float ao[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+          float ao[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+          if constexpr (kWeights == kTwin) {  // what the weights' lower halves gave
+            const float4 b0 = src[kPartStride], b1 = src[kPartStride + 1];
+            const float bo[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ao[j] += bo[j];
+          }
           join(x[i], part_lse[k][i * kMapRows + row], 1.f, ao);
         }
       }
@@ -797,6 +830,16 @@ bool make_pair_map(CUtensorMap* map, const void* pool, int64_t rows) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+typedef void (*DiffKernel)(const CUtensorMap, const CUtensorMap, const DiffArgs);
+
+DiffKernel diff_kernel(bool whole, int weights) {
+  if (whole)
+    return weights == kTwin ? paged_diff_kernel<true, kTwin>
+           : weights == kSplit ? paged_diff_kernel<true, kSplit>
+                               : paged_diff_kernel<true, kRounded>;
+  return weights == kRounded ? paged_diff_kernel<false, kRounded> : paged_diff_kernel<false, kSplit>;
+}
+
 struct DiffGeometry {
   int grid = 0, workers = 0, npairs_cap = 0;
   size_t smem = 0, ws_desc = 0, ws_lse = 0, ws_o = 0, ws_bytes = 0;
@@ -818,10 +861,11 @@ int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int64_t longest, Dif
   const size_t plan = sizeof(int) * ((size_t)g->npairs_cap + 1 + 3 * (size_t)S + 2);
   g->smem = 1024 + (size_t)kDWarps * kDStages * kDStage + kDWarps * kDStages * 8 + plan;
   if (g->smem + kDiffDim * 4 > (size_t)dev.max_smem_optin) return PA_ERR_UNSUPPORTED;
-  if (!raise_smem_limit(reinterpret_cast<const void*>(paged_diff_kernel<false>), kDiffDim * 4) ||
-      !raise_smem_limit(reinterpret_cast<const void*>(paged_diff_kernel<true>),
-                        2 * 1024))  // (the ring's alignment rounds 1.3 KB up)
-    return PA_ERR_CUDA;
+  for (int weights = kRounded; weights <= kTwin; ++weights)
+    for (int whole = 0; whole < 2; ++whole)
+      if (!raise_smem_limit(reinterpret_cast<const void*>(diff_kernel(whole, weights)),
+                            whole ? 2 * 1024 : kDiffDim * 4))  // (the ring's alignment rounds 1.3 KB up)
+        return PA_ERR_CUDA;
   g->ws_desc = round_up(sizeof(int) * kDDesc * (size_t)g->workers, 256);
   g->ws_lse = round_up(sizeof(float) * 2 * kDRows * (size_t)g->workers, 256);
   g->ws_o = round_up(sizeof(float) * 2 * kDRows * kDiffDim * (size_t)g->workers, 256);
@@ -983,16 +1027,20 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
   a.part_o = reinterpret_cast<float*>(wws + g.ws_desc + g.ws_lse);
   // more than eight pieces to a segment on average (if the batch fills its contexts)
   const int64_t segments = (int64_t)g.npairs_cap * (a.Hkv / 2);
-  if (whole_segments(segments, a.max_blocks, g.grid))
-    return launch_dependent(paged_diff_kernel<true>, dim3((unsigned)segments), dim3(kDWarps * 32),
+  const bool whole = whole_segments(segments, a.max_blocks, g.grid);
+  // single queries: four rows or fewer twice, where that is not the merge's to add
+  const int weights = max_q_len > 1 ? kRounded : whole && a.G <= kMapRows / 2 ? kTwin : kSplit;
+  const DiffKernel kern = diff_kernel(whole, weights);
+  if (whole)
+    return launch_dependent(kern, dim3((unsigned)segments), dim3(kDWarps * 32),
                             g.smem, st, tmk, tmv, a) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
   const bool many = (int64_t)g.workers > 8 * segments;
   a.by_segment = many;
   a.segments = many ? (int)segments : 0;
-  if (launch_dependent(paged_diff_kernel<false>, dim3(g.grid), dim3(kDWarps * 32), g.smem, st, tmk, tmv,
-                       a) != cudaSuccess)
+  if (launch_dependent(kern, dim3(g.grid), dim3(kDWarps * 32), g.smem, st, tmk, tmv, a) !=
+      cudaSuccess)
     return PA_ERR_CUDA;
   const DiffMerge m = diff_merge(many, max_q_len, a.QT, a.G);
   // (a worker has two tiles at least: of a small call only the first ones work)
