@@ -90,3 +90,52 @@ def test_tiles_that_32_bits_do_not_count_are_refused():
     assert size(1, 16, 16, 1 << 26, 1, 1) == 0
     assert size(1000, 32, 32, 1 << 16, 64001, 64) == 0          # four query tiles to a window
     assert size(100, 32, 32, 1 << 16, 6401, 64) > 0
+
+
+@pytest.mark.parametrize("S,q,G", [(900, None, 16), (850, 20, 2), (860, 1, 40)])
+def test_a_long_plan_leaves_the_pair_kernel_two_stages(S, q, G):
+    # beyond some 830 windows the third stage of K and V gives way to the plan
+    lens = [(q or 0) + 7 * i % 300 for i in range(S)]
+    b = Batch(96, lens, None if q is None else [q] * S, 2, G).cuda()
+    out, lse = b.call(ws_fill=0xff)
+    ok()
+    b.check(out, lse)
+    again, _ = b.call(with_lse=False, ws_fill=0)
+    ok()
+    assert torch.equal(again[:b.T].view(torch.int16), out[:b.T].view(torch.int16))
+
+
+def most_sequences(words, pairs):
+    """The most sequences whose plan fits: a word a pair and one at the end, three a
+    sequence and two."""
+    return (words - 3) // (pairs + 3)
+
+
+def test_the_most_sequences_of_a_call():
+    def size(S, G, T, max_q):
+        sh = B.make_shape(num_seqs=S, num_q_heads=2 * G, num_kv_heads=2, head_dim=128,
+                          block_size=16, max_blocks_per_seq=4, num_blocks=1024)
+        return B.pa_decode_diff_workspace_size(sh, T, max_q)
+    props = torch.cuda.get_device_properties(0)
+    room = props.shared_memory_per_block_optin
+    # warp tiles: a ring of 160 KB with 10 barriers, its alignment, 1 KB of weights
+    words = (room - 160 * 1024 - 80 - 2048) // 4
+    for G, max_q, pairs in ((1, 1, 1), (8, 1, 1), (8, 3, 3), (2, 15, 4), (4, 7, 4)):
+        S = most_sequences(words, pairs)
+        assert size(S, G, S * max_q - (max_q > 1), max_q) > 0, (G, max_q)
+        S += 1
+        assert size(S, G, S * max_q - (max_q > 1), max_q) == 0, (G, max_q)
+    # pair kernel: two query tiles, two stages of 48 KB, 4864 bytes beside them, alignment; the
+    # cut's words, one a pair of SMs
+    words = (room - 1024 - 160 * 1024 - 4864) // 16 * 4 - props.multi_processor_count // 2 - 1
+    S = (words - 4) // 4
+    assert size(S, 16, S, 1) > 0 and size(S + 1, 16, S + 1, 1) == 0
+
+
+def test_a_call_of_the_most_sequences():
+    S = most_sequences((torch.cuda.get_device_properties(0).shared_memory_per_block_optin
+                        - 160 * 1024 - 80 - 2048) // 4, 1)
+    b = Batch(97, [5 * i % 37 for i in range(S)], None, 2, 1).cuda()
+    out, lse = b.call(ws_fill=0x7f)
+    ok()
+    b.check(out, lse)
