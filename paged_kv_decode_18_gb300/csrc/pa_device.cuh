@@ -463,9 +463,8 @@ __device__ inline void build_plan(const PlanInputs& in, PlanSmem& P, int* /*scra
     for (int s = tid; s < S; s += nthreads) {
       const int p0 = P.seq_pair[s], p1 = P.seq_pair[s + 1];
       if (p1 > npairs) continue;
-      const int c = P.ctx[s];
-      int q0, lq;
-      window(s, c, q0, lq);
+      const int c = P.ctx[s], q0 = in.cu_seqlens_q[s];
+      int lq = in.cu_seqlens_q[s + 1] - q0;
       if (bad_window(in, lq, q0, c)) lq = 0;
       if (lq < in.min_lq || lq > in.max_lq) lq = 0;
       for (int p = p0; p < p1; ++p)

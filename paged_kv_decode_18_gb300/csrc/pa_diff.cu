@@ -61,7 +61,6 @@ struct DiffArgs {
   int64_t num_q_tokens;
   int causal;
   int npairs_cap;
-  int num_workers;
   int max_lq;       // longer windows belong to the tcgen05 kernel
   int max_q_len;    // no window is longer than this
   float* part_o;    // [NW*2][16][256]
@@ -214,8 +213,8 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   P.qstart = P.ctx + S;
   // the norm's weights, in shared memory for the epilogue: from global memory its 32
   // loads a lane, few of them in flight beside 128 accumulators, cost a ragged batch of
-  // short contexts a third of its time
-  __shared__ float2 weights[kDiffDim / 2];
+  // short contexts a third of its time (a whole segment's rows are finished by finish_row)
+  __shared__ float2 weights[kWhole ? 1 : kDiffDim / 2];
   __shared__ float part_lse[kWhole ? kDWarps : 1][kDRows];
   if (kWhole && lane < kDRows) part_lse[warp][lane] = neg_inf();  // a warp without tiles
 
@@ -230,7 +229,7 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   static_assert(kDWarps * 32 >= kDiffDim / 2, "a pair of weights a thread");
   float2 mine = make_float2(1.f, 1.f);
-  if (a.o.weight && threadIdx.x < kDiffDim / 2)
+  if (!kWhole && a.o.weight && threadIdx.x < kDiffDim / 2)
     mine = reinterpret_cast<const float2*>(a.o.weight)[threadIdx.x];
   PlanInputs in;
   in.context_lens = a.context_lens;
@@ -246,8 +245,10 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
   in.announced = a.max_q_len;
   in.skip_empty = a.cu_seqlens_q == nullptr;
   build_plan(in, P, nullptr);
-  if (threadIdx.x < kDiffDim / 2) weights[threadIdx.x] = mine;
-  __syncthreads();
+  if (!kWhole) {
+    if (threadIdx.x < kDiffDim / 2) weights[threadIdx.x] = mine;
+    __syncthreads();
+  }
   const int W = P.total;
   // two tiles a warp at least: cutting a short batch further costs more in the merge
   // than it saves
@@ -845,6 +846,10 @@ struct DiffGeometry {
   size_t smem = 0, ws_desc = 0, ws_lse = 0, ws_o = 0, ws_bytes = 0;
 };
 
+// what the kernels declare themselves (the norm's weights, or a CTA's log-sum-exps), rounded
+// up by the ring's alignment
+constexpr int kDeclared = 1024;
+
 // longest: the longest window that comes here
 int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int64_t longest, DiffGeometry* g) {
   DeviceInfo dev;
@@ -860,11 +865,11 @@ int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int64_t longest, Dif
   g->workers = g->grid * kDWarps;
   const size_t plan = sizeof(int) * ((size_t)g->npairs_cap + 1 + 3 * (size_t)S + 2);
   g->smem = 1024 + (size_t)kDWarps * kDStages * kDStage + kDWarps * kDStages * 8 + plan;
-  if (g->smem + kDiffDim * 4 > (size_t)dev.max_smem_optin) return PA_ERR_UNSUPPORTED;
+  if (g->smem + kDeclared > (size_t)dev.max_smem_optin) return PA_ERR_UNSUPPORTED;
   for (int weights = kRounded; weights <= kTwin; ++weights)
     for (int whole = 0; whole < 2; ++whole)
       if (!raise_smem_limit(reinterpret_cast<const void*>(diff_kernel(whole, weights)),
-                            whole ? 2 * 1024 : kDiffDim * 4))  // (the ring's alignment rounds 1.3 KB up)
+                            kDeclared))
         return PA_ERR_CUDA;
   g->ws_desc = round_up(sizeof(int) * kDDesc * (size_t)g->workers, 256);
   g->ws_lse = round_up(sizeof(float) * 2 * kDRows * (size_t)g->workers, 256);
@@ -873,24 +878,27 @@ int diff_geometry(const pa_shape* sh, int64_t num_q_tokens, int64_t longest, Dif
   return PA_OK;
 }
 
-// The kernels of a call. A window whose rows of a KV head (query tokens x group) are
-// fewer than kTcMinRows goes through warp tiles of eight rows, the others through
-// tcgen05 tiles of 256; more than eight query heads to a KV head always do. Measured,
-// warp tiles against tcgen05, two heads to a KV head: 32 x 4096 keys 16 rows 163 against
-// 184 us, 24 rows 214 against 185, 32 rows 263 against 182; 4 x 2048 keys 22 against 33,
-// 29 against 33, 31 against 33, 48 rows 38 against 33; 64 x 512 keys 47 against 90, 62
-// against 91, 77 against 90, 48 rows 100 against 92.
 constexpr int kMaxGroup = 128;
 
+// The kernels of a call. A window whose rows of a KV head (query tokens x group) are
+// fewer than this goes through warp tiles of eight rows, the others through tcgen05 tiles
+// of 256; more than eight query heads to a KV head always do. Measured, warp tiles
+// against tcgen05, two heads to a KV head: 32 x 4096 keys 16 rows 163 against 184 us, 24
+// rows 214 against 185, 32 rows 263 against 182; 4 x 2048 keys 22 against 33, 29 against
+// 33, 31 against 33, 48 rows 38 against 33; 64 x 512 keys 47 against 90, 62 against 91, 77
+// against 90, 48 rows 100 against 92. One number for all lengths: at 24 rows it costs long
+// contexts 14 % and spares short ones a third.
+constexpr int kTcMinRows = 32;
+
 // Whether every segment gets a CTA, which ends in one grid, in the place of a cut over all
-// warps and a second grid. Without: 12.4 us for 16 segments of 24 blocks, 13.1 for 32
-// blocks, 13.7 for 64, 22.6 and 32.2 for 128 segments of 32 and 64; with: 10.4, 13.6, 20.3,
-// 18.0 and 27.4. The bound on the table keeps a batch whose contexts differ from waiting
-// long for one of them.
+// warps and a second grid. Without: 14.1 us for 16 segments of 24 blocks, 14.2 for 32
+// blocks, 15.7 for 64, 23.0 and 33.0 for 128 segments of 32 and 64; with: 11.9, 14.3, 21.0,
+// 18.1 and 27.3. The bound on the table keeps a batch whose contexts differ from waiting
+// long for one of them. (The host knows the table's width, not the contexts: the same
+// four short ones under a table of 2048 blocks are cut over all warps.)
 bool whole_segments(int64_t segments, int max_blocks, int sms) {
   return segments <= sms && max_blocks <= (3 * segments >= 2 * sms ? 64 : 28);
 }
-constexpr int kTcMinRows = 32;
 
 struct DiffPlan {
   bool warp = false;  // some window may be short
@@ -1018,7 +1026,6 @@ extern "C" int pa_decode_diff(const pa_bf16* q, const pa_bf16* k_cache, const pa
   a.num_q_tokens = num_q_tokens;
   a.causal = causal;
   a.npairs_cap = g.npairs_cap;
-  a.num_workers = g.workers;
   a.max_lq = p.tc.enabled ? p.tc.min_lq - 1 : 0x7fffffff;
   a.max_q_len = max_q_len;
   char* wws = ws + p.tc.ws_bytes;
