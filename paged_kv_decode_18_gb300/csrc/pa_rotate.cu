@@ -254,9 +254,13 @@ struct RowsArgs {
 // sines and cosines. Measured: 16,200 x 16 rows 22.5 us, 5.9 TB/s; 12,000 tokens of 16 + 8
 // + 8 rows into the cache 32.1 us, 6.2 TB/s. (Eight rows a warp: 23.5 and 37.8; twelve: 26.9
 // and 34.9; twenty: 23.1 and 37.8. At a decode step's 256 tokens all take the 4 us of a
-// launch.)
-// kAny's sines and cosines of 16 values want 128 registers: 46.6 us for 16,200 x 16 rows of
-// r = 72 with two CTAs to an SM, 49.3 with three, where the other layouts take 23.
+// launch.) 8,100 such tokens: bf16 22.8 us, FP8 24.5, int8 25.8, of which their bytes are
+// 19.6, 17.2 and 17.2: the quantiser's instructions, 1.9 a clock in all (12 bytes of
+// registers spill). A token of few rows leaves its warp's others empty: 65,536 tokens of
+// one, two or four heads take 37 to 39 us, their bytes 5, 10 and 20.
+// kAny's sines and cosines of 16 values (each side of a pair makes its own) want 128
+// registers: 46.6 us for 16,200 x 16 rows of r = 72 with two CTAs to an SM, 49.3 with three,
+// where the other layouts take 23.
 constexpr int kIter = 4;
 
 template <int MODE, int FMT>
@@ -378,9 +382,13 @@ struct CachedArgs {
 // Measured: 8 x 24,000..28,700 keys of 8 heads by a shift 143 us (6.0 TB/s); 32 x 1024
 // behind an eviction 26 us, of which some 7 us is the chain launch, lengths, block
 // ids and turns, first rows. (Loads of the next eight keys held ahead of the present
-// ones: 33 us, for the registers that it takes.)
+// ones: 33 us, for the registers that it takes.) 16 x 4096 keys of 8 heads by a shift: bf16
+// 47 us, FP8 35.4, int8 41.6, behind an eviction 47.6, 43 and 51; the 8-bit ones, 20 us
+// by their bytes, issue 2.4 and 2.5 instructions a clock with a third of the warp slots
+// filled. kAny: bf16 70 us (68 bytes spilled), FP8 54, int8 59 with two CTAs to an SM; three,
+// at 80 registers and 900 bytes of spill loads a thread, 70 and 76.
 template <int MODE, int FMT>
-__global__ void __launch_bounds__(kRotWarps * 32, MODE == kAny && FMT == kFmtBf16 ? 2 : 3)
+__global__ void __launch_bounds__(kRotWarps * 32, MODE == kAny ? 2 : 3)
     rotate_cached_kernel(const __grid_constant__ CachedArgs a) {
   extern __shared__ __align__(16) int area[];  // turns, kAny: the exchange, the plan
   unsigned long long* turns = reinterpret_cast<unsigned long long*>(area);
