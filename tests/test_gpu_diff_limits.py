@@ -92,7 +92,7 @@ def test_tiles_that_32_bits_do_not_count_are_refused():
     assert size(100, 32, 32, 1 << 16, 6401, 64) > 0
 
 
-@pytest.mark.parametrize("S,q,G", [(900, None, 16), (850, 20, 2), (860, 1, 40)])
+@pytest.mark.parametrize("S,q,G", [(900, None, 16), (850, 20, 2), (860, 1, 12)])
 def test_a_long_plan_leaves_the_pair_kernel_two_stages(S, q, G):
     # beyond some 830 windows the third stage of K and V gives way to the plan
     lens = [(q or 0) + 7 * i % 300 for i in range(S)]
