@@ -77,7 +77,7 @@ typedef enum pa_status {
 #define PA_DEVERR_SLOT_RANGE 0x1u    /* slot_mapping[t] >= num_blocks * block_size */
 #define PA_DEVERR_BLOCK_RANGE 0x2u   /* a used block_tables entry outside [0, num_blocks) */
 #define PA_DEVERR_CONTEXT_RANGE 0x4u /* context_len < 0 or > max_blocks_per_seq * block_size */
-#define PA_DEVERR_QLEN_RANGE 0x8u    /* q_len < 0, q_len > context_len (causal, or context 0), or cu_seqlens_q inconsistent */
+#define PA_DEVERR_QLEN_RANGE 0x8u    /* q_len < 0, q_len > context_len (causal, or context 0), q_len > max_q_len (where a call says so), or cu_seqlens_q inconsistent */
 #define PA_DEVERR_PIPE_TIMEOUT 0x10u /* an asynchronous copy did not land within its time limit */
 #define PA_DEVERR_PLAN_OVERFLOW 0x20u /* work list larger than the launch was sized for */
 #define PA_DEVERR_TREE_RANGE 0x40u   /* a tree parent or an accepted path outside its rules */

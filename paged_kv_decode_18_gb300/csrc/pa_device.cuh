@@ -364,7 +364,8 @@ __device__ __forceinline__ int pair_tiles(int c, int lq, int qt, int qtile, int 
 // other queries see the whole (non-empty) context whatever their number. What
 // the host sized a launch by bounds it too.
 __device__ __forceinline__ bool bad_window(const PlanInputs& in, int lq, int q0, int c) {
-  return lq < 0 || lq > in.announced || (lq > c && (in.causal || in.max_window > 0 || c == 0)) || q0 < 0 ||
+  return lq < 0 || lq > in.announced ||
+         (lq > c && (in.causal || in.max_window > 0 || c == 0)) || q0 < 0 ||
          (in.max_window > 0 && lq > in.max_window) || (int64_t)q0 + lq > in.num_q_rows;
 }
 

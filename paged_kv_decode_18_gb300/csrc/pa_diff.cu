@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(kDWarps * 32, 1)
     // beside it. Of single queries a weight is two such numbers, its upper half and what
     // that leaves, off by 2^-15 of it together (1.5 us of the calls above); of windows, as
     // elsewhere, it is one, off by 2^-8 at most: their tiles are full, and a second product
-    // takes 46.7 to 53.1 us for 64 windows of 16 rows over 512 keys. The sums of the weights, and with them lse, are of the unrounded ones.
+    // takes 46.7 to 53.1 us for 64 windows of 16 rows over 512 keys. The sums of the weights,
+    // and with them lse, are of the unrounded ones.
     uint32_t p4[4], p4_low[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
